@@ -34,12 +34,20 @@ QMM_OUT_BF16 = 1
 MAX_ROWS = 16
 MAX_BANKS = 64
 MAX_SPLITS = 16
+QMM_IN_F32 = 0
+QMM_IN_BF16 = 1
+KV_BAD_PAGE = 1
+KV_BAD_LENGTH = 2
+KV_BAD_POSITION = 4
+SAMPLE_MAX_VOCAB = 393216
 
 # Every entry point declared in include/qmm.h.
 EXPORTS = (
     "qmm_validate_desc", "qmm_workspace_bytes", "qmm_plan", "qmm_plan_get_info",
     "qmm_check_forward_args", "qmm_forward", "qmm_forward_banked", "qmm_unpack_codes",
     "qmm_plan_error", "qmm_destroy", "qmm_status_string", "qmm_forward_noalloc", "qmm_forward_swiglu",
+    "qmm_kv_validate_desc", "qmm_kv_workspace_bytes", "qmm_kv_plan", "qmm_kv_error", "qmm_kv_destroy",
+    "qmm_check_qk_norm_rope_args", "qmm_qk_norm_rope", "qmm_check_attention_args", "qmm_attention", "qmm_sample",
 )
 
 
@@ -53,6 +61,26 @@ class QmmPlanInfo(ctypes.Structure):
     _fields_ = [("splits", ctypes.c_int32), ("chunks", ctypes.c_int32), ("stages", ctypes.c_int32 * 2),
                 ("smem_bytes", ctypes.c_int32 * 2), ("num_sms", ctypes.c_int32), ("device", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class QmmKvDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "page_size", "max_seqs", "max_rows",
+                                              "max_pages", "window", "sinks", "rot_dim", "interleaved")] + \
+               [("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class QmmKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64)] + \
+               [(f"{s}_{d}_stride", ctypes.c_int64) for s in "kv" for d in ("page", "head", "slot")]
+
+
+class QmmAppendArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("rope_len", ctypes.c_int64), ("lengths", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("in_dtype", ctypes.c_int32)]
 
 
 class QmmError(RuntimeError):
@@ -82,10 +110,24 @@ def _load() -> ctypes.CDLL:
     lib.qmm_plan_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.qmm_destroy.argtypes = [vp]
     lib.qmm_destroy.restype = None
+    kvd, kvc, kva = ctypes.POINTER(QmmKvDesc), ctypes.POINTER(QmmKvCache), ctypes.POINTER(QmmAppendArgs)
+    lib.qmm_kv_validate_desc.argtypes = [kvd]
+    lib.qmm_kv_workspace_bytes.argtypes = [kvd]
+    lib.qmm_kv_workspace_bytes.restype = sz
+    lib.qmm_kv_plan.argtypes = [ctypes.POINTER(vp), kvd, vp, sz]
+    lib.qmm_kv_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+    lib.qmm_kv_destroy.argtypes = [vp]
+    lib.qmm_kv_destroy.restype = None
+    lib.qmm_check_qk_norm_rope_args.argtypes = [kvd, kvc, kva]
+    lib.qmm_qk_norm_rope.argtypes = [vp, kvc, kva, vp]
+    lib.qmm_check_attention_args.argtypes = [kvd, kvc, vp, i64, vp, vp, i32, i32, vp, i64]
+    lib.qmm_attention.argtypes = [vp, kvc, vp, i64, vp, vp, i32, i32, vp, i64, vp]
+    lib.qmm_sample.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.qmm_status_string.argtypes = [i32]
     lib.qmm_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
-        if name not in ("qmm_workspace_bytes", "qmm_destroy", "qmm_status_string"):
+        if name not in ("qmm_workspace_bytes", "qmm_destroy", "qmm_status_string", "qmm_kv_workspace_bytes",
+                        "qmm_kv_destroy"):
             getattr(lib, name).restype = i32
     return lib
 
@@ -280,3 +322,175 @@ def unpack_codes(w, K: int, N: int, bits: int, stream=None):
     if st != QMM_OK:
         raise QmmError(st, "qmm_unpack_codes")
     return codes
+
+
+def make_kv_desc(q_heads, kv_heads, head_dim, page_size, max_seqs, max_rows, max_pages, window=0, sinks=0, rot_dim=None,
+                 interleaved=False, scale=None, eps=1e-6) -> QmmKvDesc:
+    """Descriptor of a KVPlan; rot_dim defaults to head_dim and scale to head_dim ** -0.5."""
+    return QmmKvDesc(int(q_heads), int(kv_heads), int(head_dim), int(page_size), int(max_seqs), int(max_rows),
+                     int(max_pages), int(window), int(sinks), int(head_dim if rot_dim is None else rot_dim),
+                     int(bool(interleaved)), float(head_dim ** -0.5 if scale is None else scale), float(eps))
+
+
+def kv_validate_desc(desc: QmmKvDesc) -> int:
+    return int(_lib().qmm_kv_validate_desc(ctypes.byref(desc)))
+
+
+def kv_workspace_bytes(desc: QmmKvDesc) -> int:
+    return int(_lib().qmm_kv_workspace_bytes(ctypes.byref(desc)))
+
+
+class KVPlan:
+    """A plan of the cache operators (qmm_kv_plan / qmm_kv_destroy) for one kind of attention layer. Its workspace
+    is a PyTorch-allocated device buffer unless ``torch_workspace=False``. Arguments as for `make_kv_desc`."""
+
+    def __init__(self, *args, torch_workspace: bool = True, device=None, **kwargs):
+        import torch
+        self.desc = d = make_kv_desc(*args, **kwargs)
+        st = kv_validate_desc(d)
+        if st != QMM_OK:
+            raise QmmError(st, "qmm_kv_validate_desc")
+        self._handle = ctypes.c_void_p()
+        self.workspace = None
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(dev):
+            ws, nbytes = None, 0
+            if torch_workspace:
+                nbytes = kv_workspace_bytes(d)
+                self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
+                ws = (self.workspace.data_ptr() + 255) // 256 * 256
+            st = _lib().qmm_kv_plan(ctypes.byref(self._handle), ctypes.byref(d), ws, nbytes)
+        if st != QMM_OK:
+            raise QmmError(st, "qmm_kv_plan")
+        self.device = dev
+        self.q_width, self.kv_width = d.q_heads * d.head_dim, d.kv_heads * d.head_dim
+        self.page_shape = (d.kv_heads, d.page_size, d.head_dim)
+        self.max_pages = d.max_pages
+
+    @property
+    def handle(self):
+        return self._handle
+
+    def error_flags(self) -> int:
+        """The KV_BAD_* bits of the calls since the last read (synchronizes), cleared."""
+        v = ctypes.c_uint32(0)
+        st = _lib().qmm_kv_error(self._handle, ctypes.byref(v))
+        if st not in (QMM_OK, QMM_ERR_INVALID_ARG):
+            raise QmmError(st, "qmm_kv_error")
+        return int(v.value)
+
+    def close(self):
+        if self._handle is not None and self._handle.value:
+            _lib().qmm_kv_destroy(self._handle)
+            self._handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """The pages of keys and values as the cache operators take them: two bfloat16 tensors
+    [pages, kv_heads, page_size, head_dim] of any strides with adjacent elements in the last dimension (a pool laid
+    out [pages, page_size, kv_heads, head_dim] is passed as its transpose(1, 2))."""
+
+    def __init__(self, k, v):
+        import torch
+        for t in (k, v):
+            if t.dim() != 4 or t.dtype != torch.bfloat16 or t.shape != k.shape or t.stride(3) != 1:
+                raise ValueError("k and v are bfloat16 tensors [pages, kv_heads, page_size, head_dim] of the same shape")
+        self.k, self.v = k, v
+        self.page_shape = tuple(k.shape[1:])
+        self.struct = QmmKvCache(k.data_ptr(), v.data_ptr(), k.shape[0], *k.stride()[:3], *v.stride()[:3])
+        self.ref = ctypes.byref(self.struct)
+
+
+def _rows(t, width, dtype, what):
+    """Elements between the rows of a tensor [tokens, width] or [tokens, heads, head_dim] of adjacent heads."""
+    if t.dtype != dtype or t.numel() != t.shape[0] * width or t.stride(-1) != 1 or \
+            (t.dim() == 3 and t.stride(1) != t.shape[2]) or not 2 <= t.dim() <= 3:
+        raise ValueError(f"{what}: {dtype} rows of {width} adjacent elements are needed")
+    return t.stride(0)
+
+
+def _check_step(plan, cache, page_table, lengths, tokens):
+    import torch
+    if cache.page_shape != plan.page_shape:
+        raise ValueError("the cache's pages are not the plan's [kv_heads, page_size, head_dim]")
+    if lengths.dtype != torch.int32 or page_table.dtype != torch.int32 or not page_table.is_contiguous() or \
+            not lengths.is_contiguous() or page_table.shape != (lengths.shape[0], plan.max_pages):
+        raise ValueError("lengths [seqs] and page_table [seqs, max_pages] are contiguous int32 tensors")
+    seqs = lengths.shape[0]
+    if tokens % max(seqs, 1) != 0:
+        raise ValueError("every sequence has the same number of rows")
+    return seqs, tokens // max(seqs, 1)
+
+
+def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_table, cache: KVCache, out,
+                 positions=None, stream=None) -> None:
+    """Norms of q and k for each head, rotation, and the append of k and v to the cache (qmm_qk_norm_rope). q, k, v:
+    [tokens, heads * head_dim] of float32 or bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and
+    k_weight: float32 [head_dim] or None; rope: float32 [positions, rot_dim], cosines then sines."""
+    import torch
+    tokens = q.shape[0]
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
+    if q.dtype not in (torch.float32, torch.bfloat16) or k.shape[0] != tokens or v.shape[0] != tokens or \
+            out.shape[0] != tokens:
+        raise ValueError("q, k and v are float32 or bfloat16 rows of the same tokens, as out is")
+    for w, n in ((q_weight, plan.desc.head_dim), (k_weight, plan.desc.head_dim)):
+        if w is not None and (w.dtype != torch.float32 or w.numel() != n or not w.is_contiguous()):
+            raise ValueError("q_weight and k_weight are float32 [head_dim] or None")
+    if plan.desc.rot_dim and (rope is None or rope.dtype != torch.float32 or not rope.is_contiguous() or
+                              rope.shape[-1] != plan.desc.rot_dim):
+        raise ValueError("rope is a float32 tensor [positions, rot_dim]")
+    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != tokens or
+                                  not positions.is_contiguous()):
+        raise ValueError("positions is an int32 tensor [tokens]")
+    a = QmmAppendArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, plan.q_width, q.dtype, "q"),
+                      _rows(k, plan.kv_width, q.dtype, "k"), _rows(v, plan.kv_width, q.dtype, "v"), _ptr(q_weight),
+                      _ptr(k_weight), _ptr(rope), rope.shape[0] if rope is not None else 0, lengths.data_ptr(),
+                      _ptr(positions), page_table.data_ptr(), out.data_ptr(),
+                      _rows(out, plan.q_width, torch.bfloat16, "out"), seqs, rows,
+                      QMM_IN_F32 if q.dtype is torch.float32 else QMM_IN_BF16)
+    st = _lib().qmm_qk_norm_rope(plan.handle, cache.ref, ctypes.byref(a), _stream_handle(stream))
+    if st != QMM_OK:
+        raise QmmError(st, "qmm_qk_norm_rope")
+
+
+def attention(plan: KVPlan, q, cache: KVCache, page_table, lengths, out, stream=None) -> None:
+    """Attention of the new tokens over the cache (qmm_attention): q and out [tokens, q_heads, head_dim] bfloat16 (or
+    [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
+    import torch
+    tokens = q.shape[0]
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
+    if out.shape[0] != tokens:
+        raise ValueError("out has q's rows")
+    st = _lib().qmm_attention(plan.handle, cache.ref, q.data_ptr(), _rows(q, plan.q_width, torch.bfloat16, "q"),
+                              page_table.data_ptr(), lengths.data_ptr(), seqs, rows, out.data_ptr(),
+                              _rows(out, plan.q_width, torch.bfloat16, "out"), _stream_handle(stream))
+    if st != QMM_OK:
+        raise QmmError(st, "qmm_attention")
+
+
+def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stream=None) -> None:
+    """Draw a token for each row of logits [M, vocab] (float32 or bfloat16, rows of any stride) from the uniform
+    numbers u (qmm_sample): tokens int32 [M], probs float32 [M] or None. temperature, top_p, min_p: float32 [M];
+    top_k: int32 [M]."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or logits.stride(1) != 1:
+        raise ValueError("logits are float32 or bfloat16 rows of adjacent elements")
+    M = logits.shape[0]
+    for t, dtype in ((temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32),
+                     (min_p, torch.float32), (u, torch.float32), (tokens, torch.int32)):
+        if t.dtype != dtype or t.numel() != M or not t.is_contiguous():
+            raise ValueError("temperature, top_p, min_p and u are float32 [M], top_k and tokens int32 [M]")
+    if probs is not None and (probs.dtype != torch.float32 or probs.numel() != M or not probs.is_contiguous()):
+        raise ValueError("probs is float32 [M] or None")
+    st = _lib().qmm_sample(logits.data_ptr(), M, logits.shape[1], logits.stride(0),
+                           QMM_IN_F32 if logits.dtype is torch.float32 else QMM_IN_BF16, temperature.data_ptr(),
+                           top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), u.data_ptr(), tokens.data_ptr(),
+                           _ptr(probs), _stream_handle(stream))
+    if st != QMM_OK:
+        raise QmmError(st, "qmm_sample")

@@ -263,6 +263,165 @@ int qmm_forward_noalloc(const void* x_bf16, int M, const uint32_t* packed_w, con
 /* Free the plan and any workspace it allocated. NULL is accepted. */
 void qmm_destroy(qmm_plan_t* p);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Between two projections of a decode or verification step: query/key norms
+ * with the position rotation and the append to a paged key/value cache,
+ * attention of the new tokens over that cache, and the draw of the next token
+ * from the output head's logits.
+ *
+ * A step has `seqs` sequences of `rows` new tokens each; token t = s * rows + r
+ * is row r of sequence s. lengths[s] (device int32) counts the tokens of
+ * sequence s with the new ones, so row r has the cache position
+ *   pos(s, r) = lengths[s] - rows + r.
+ * A row with pos < 0 is padding: nothing is appended for it, and it attends to
+ * nothing (its output is zeros).
+ *
+ * The cache is a pool of pages of page_size positions. Position j of sequence s
+ * is slot j % page_size of page page_table[s * max_pages + j / page_size]
+ * (device int32). Entries of positions that no row reads or writes are never
+ * used and may hold anything. Elements are bfloat16 at
+ *   base + page * page_stride + head * head_stride + slot * slot_stride + d.
+ */
+
+#define QMM_KV_MAX_SEQS 65536
+#define QMM_KV_MAX_ROWS 16
+#define QMM_KV_MAX_GROUP 64
+
+/* Types of the values that qmm_qk_norm_rope and qmm_sample read. */
+enum { QMM_IN_F32 = 0, QMM_IN_BF16 = 1 };
+
+/* Error bits of qmm_kv_error. */
+enum {
+    QMM_KV_BAD_PAGE = 1,     /* a page table entry in use lies outside 0..num_pages-1 */
+    QMM_KV_BAD_LENGTH = 2,   /* a length above max_pages * page_size: what is past the page table was left out */
+    QMM_KV_BAD_POSITION = 4  /* a rotation position outside the rope table: the row was not rotated */
+};
+
+/* What a plan for the cache operators fixes. */
+typedef struct qmm_kv_desc {
+    int32_t q_heads;      /* query heads, a multiple of kv_heads (at most QMM_KV_MAX_GROUP times as many) */
+    int32_t kv_heads;     /* heads of the cache */
+    int32_t head_dim;     /* 64, 128 or 256 */
+    int32_t page_size;    /* positions of a page: a power of two, 1..1024 */
+    int32_t max_seqs;     /* largest number of sequences of a call */
+    int32_t max_rows;     /* largest rows of an attention call, 1..16 */
+    int32_t max_pages;    /* entries of a page table row (the table is [seqs, max_pages]) */
+    int32_t window;       /* 0: every earlier position is visible; W: those with pos - j < W ... */
+    int32_t sinks;        /* ... and the first `sinks` positions */
+    int32_t rot_dim;      /* rotated elements of a head: 0 or a multiple of 16, at most head_dim */
+    int32_t interleaved;  /* 0: element i turns with i + rot_dim/2; 1: element 2i with 2i + 1 */
+    float scale;          /* factor of the attention scores */
+    float eps;            /* added to the mean square in the norms */
+} qmm_kv_desc;
+
+/* The cache: bases, pages, and strides in elements (multiples of 8). */
+typedef struct qmm_kv_cache {
+    void* k;              /* bfloat16, 16-byte aligned */
+    void* v;
+    int64_t num_pages;
+    int64_t k_page_stride, k_head_stride, k_slot_stride;
+    int64_t v_page_stride, v_head_stride, v_slot_stride;
+} qmm_kv_cache;
+
+typedef struct qmm_kv_plan qmm_kv_plan_t;
+
+/* Validate a descriptor on the host (no CUDA call): QMM_OK, QMM_ERR_INVALID_ARG or QMM_ERR_UNSUPPORTED. */
+int qmm_kv_validate_desc(const qmm_kv_desc* d);
+
+/* Device workspace of a plan for `d` (error word, join counters and partial results); 0 if d is invalid. */
+size_t qmm_kv_workspace_bytes(const qmm_kv_desc* d);
+
+/*
+ * Create a plan on the current device; the workspace is handled as in
+ * qmm_plan (NULL: the plan allocates it). A plan is used by one stream at a
+ * time; qmm_qk_norm_rope and qmm_attention may share one.
+ */
+int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, size_t ws_bytes);
+
+/* Read (synchronously) and clear the plan's device error word; QMM_ERR_INVALID_ARG if a bit was set. */
+int qmm_kv_error(const qmm_kv_plan_t* p, uint32_t* flags);
+
+/* Free the plan and any workspace it allocated. NULL is accepted. */
+void qmm_kv_destroy(qmm_kv_plan_t* p);
+
+/* What qmm_qk_norm_rope reads and writes. All pointers are device pointers. */
+typedef struct qmm_append_args {
+    const void* q;            /* [seqs*rows, q_heads*head_dim], in_dtype, 16-byte aligned rows */
+    const void* k;            /* [seqs*rows, kv_heads*head_dim] */
+    const void* v;            /* [seqs*rows, kv_heads*head_dim] */
+    int64_t q_stride, k_stride, v_stride;   /* elements from row to row (multiples of 16 bytes) */
+    const float* q_weight;    /* [head_dim] norm weights, 16-byte aligned; NULL: queries are not normalised */
+    const float* k_weight;    /* [head_dim]; NULL: keys are not normalised */
+    const float* rope;        /* [rope_len, rot_dim]: rot_dim/2 cosines, then rot_dim/2 sines; 16-byte aligned */
+    int64_t rope_len;
+    const int32_t* lengths;   /* [seqs] */
+    const int32_t* positions; /* [seqs*rows] rotation positions; NULL: the cache positions */
+    const int32_t* page_table;/* [seqs, max_pages] */
+    void* q_out;              /* [seqs*rows, q_heads*head_dim] bfloat16, 16-byte aligned rows */
+    int64_t q_out_stride;
+    int32_t seqs;             /* <= max_seqs */
+    int32_t rows;             /* any number: prompts too */
+    int32_t in_dtype;         /* QMM_IN_F32 or QMM_IN_BF16 (a projection's output type) */
+} qmm_append_args;
+
+/*
+ * For every new token and head: y = x * rsqrt(mean(x^2) + eps) * weight for
+ * queries and keys, the first rot_dim elements rotated by the token's position,
+ * all in float32, rounded once to bfloat16; queries go to q_out, keys and the
+ * (only rounded) values to their cache slots. One launch. q_out rows of padding
+ * are zeros. q_out must not overlap the inputs.
+ * The host-only check makes no CUDA call.
+ */
+int qmm_check_qk_norm_rope_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_append_args* a);
+int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_append_args* a, void* stream);
+
+/*
+ * out[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j over the positions j
+ * that token t sees: j <= pos, and with a window pos - j < window or j < sinks.
+ * Query head h reads cache head h / (q_heads / kv_heads). q and out are
+ * [seqs*rows, q_heads*head_dim] bfloat16 with 16-byte aligned rows. The scores,
+ * the softmax's maximum and sum and the output are held in float32. A row that
+ * sees nothing gives zeros, and no value at a position that a row does not see
+ * reaches that row, infinities and NaN among them.
+ *
+ * The work of all sequences is cut into equal shares for the GPU whatever their
+ * lengths; the parts of one head are joined in a fixed order, so a call with
+ * the same lengths gives the same bits. The cut depends on all lengths of the
+ * call: the same sequence in another batch may differ by rounding.
+ */
+int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const void* q, int64_t q_stride,
+                             const int32_t* page_table, const int32_t* lengths, int seqs, int rows, void* out,
+                             int64_t out_stride);
+int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const void* q, int64_t q_stride,
+                  const int32_t* page_table, const int32_t* lengths, int seqs, int rows, void* out,
+                  int64_t out_stride, void* stream);
+
+/* Largest vocabulary of qmm_sample. */
+#define QMM_SAMPLE_MAX_VOCAB 393216
+
+/*
+ * Draw one token for each of M rows of logits [M, vocab] (rows `stride`
+ * elements apart; naturally aligned) from the given uniform numbers u[M].
+ * With the row's temperature T, top_k, top_p and min_p (device arrays [M]):
+ *   w_i = exp((l_i - max l) / T), held as the whole number floor(2^40 w_i);
+ *   tokens are ranked by falling logit, equal ones by rising index, and kept if
+ *     rank < top_k                      (top_k <= 0: no limit),
+ *     the mass ranked before it < top_p * the mass of the top_k  (top_p >= 1: no limit),
+ *     w_i >= min_p                      (min_p <= 0: no limit);
+ *   the token of rank 0 is always kept;
+ *   token = the first index whose sum of kept mass up to itself exceeds
+ *     floor(u * kept mass), and prob = its mass / the kept mass.
+ * The masses are whole numbers, so no order of summation changes a result. T
+ * not above 0 takes the token of rank 0. NaN logits count as -infinity; a row
+ * without any logit above that gives token -1 and prob 0. u outside [0, 1) is
+ * brought to the nearest kept mass. probs may be NULL. 1 <= vocab <=
+ * QMM_SAMPLE_MAX_VOCAB. M = 0 is a no-op. One launch, no plan, no workspace.
+ */
+int qmm_sample(const void* logits, int M, int vocab, int64_t stride, int in_dtype, const float* temperature,
+               const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+               float* probs, void* stream);
+
 /* Static description of a status code; never NULL. */
 const char* qmm_status_string(int status);
 
