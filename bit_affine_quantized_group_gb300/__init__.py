@@ -36,9 +36,10 @@ MAX_BANKS = 64
 MAX_SPLITS = 16
 QMM_IN_F32 = 0
 QMM_IN_BF16 = 1
-KV_BAD_PAGE = 1
-KV_BAD_LENGTH = 2
-KV_BAD_POSITION = 4
+KV_TIMEOUT = 7
+KV_BAD_PAGE = 16
+KV_BAD_LENGTH = 32
+KV_BAD_POSITION = 64
 SAMPLE_MAX_VOCAB = 393216
 
 # Every entry point declared in include/qmm.h.
@@ -375,7 +376,7 @@ class KVPlan:
         """The KV_BAD_* bits of the calls since the last read (synchronizes), cleared."""
         v = ctypes.c_uint32(0)
         st = _lib().qmm_kv_error(self._handle, ctypes.byref(v))
-        if st not in (QMM_OK, QMM_ERR_INVALID_ARG):
+        if st not in (QMM_OK, QMM_ERR_INVALID_ARG, QMM_ERR_TIMEOUT):
             raise QmmError(st, "qmm_kv_error")
         return int(v.value)
 

@@ -10,17 +10,13 @@ namespace qmmk {
 
 constexpr size_t kKvErrBytes = 256;        // error word at the start of the workspace
 constexpr int kAttnMaxCtas = 320;          // largest grid of the attention kernel (2 CTAs on each of 152 SMs, and room)
-constexpr size_t kAttnCounterBytes = 4096; // one join counter per CTA
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnTile = 16;              // positions of one warp's step
-constexpr int kAttnUnit = kAttnTile * kAttnWarps;
+constexpr size_t kAttnCounterBytes = 4096; // two join counters per CTA
 
-static_assert(kAttnMaxCtas * 4 <= kAttnCounterBytes, "join counters");
+static_assert(2 * kAttnMaxCtas * 4 <= kAttnCounterBytes, "join counters");
 
-// Query rows (tokens x heads of a group) that one CTA holds: one or two 16-row
-// MMA tiles a warp. 256-wide heads have registers for one.
-constexpr int attn_row_tiles(int head_dim, int rows) { return head_dim < 256 && rows > 16 ? 2 : 1; }
+// Warps that share a key and value tile with 16 query rows (tokens x heads of a
+// group) each. A CTA holds 16 rows for each of them.
+constexpr int attn_row_warps(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 // Strides in elements.
 struct KvSide {
@@ -34,13 +30,19 @@ struct AttnParams {
     uint16_t* out;
     const int32_t* page_table;
     const int32_t* lengths;
-    float* part;            // [2 * ctas][16 * MT][D] unnormalised outputs of cut heads
-    float* part_ml;         // [2 * ctas][16 * MT][2] their maxima (in powers of two) and sums
-    uint32_t* counters;     // [ctas] parts that have arrived, by the CTA that a head starts in; left at zero
+    float* part;            // [2 * ctas][16 * row warps][D] unnormalised outputs of cut heads
+    float* part_ml;         // [2 * ctas][16 * row warps][2] their maxima (in powers of two) and sums
+    uint32_t* counters;     // [2][kAttnMaxCtas] parts that have arrived, by the CTA that a head, or a run of its
+                            // parts, starts in; left at zero
+    int4* joins;            // [ctas] for the join kernel: parts, sequence, cache head and first row of the cut head that
+                            // begins in a CTA; no parts for none
     uint32_t* err;
     int64_t q_stride, out_stride, num_pages;
     int32_t seqs, rows, group, kv_heads, row_groups, max_pages, page_shift, window, sinks;
-    float scale_log2;       // scale * log2(e)
+    int32_t group_inverse;  // ceil(2^20 / group): rows (fewer than 1024) divide by the group (64 at most) exactly
+    int32_t min_unit;
+    uint32_t query_sign;    // flips the signs of two query elements where the scale is negative
+    float scale_log2;       // |scale| * log2(e)
 };
 
 struct AppendParams {
@@ -62,14 +64,15 @@ struct AppendParams {
 };
 
 struct AttnWorkspace {
-    size_t counters, part, part_ml, bytes;   // offsets
+    size_t counters, joins, part, part_ml, bytes;   // offsets
 };
 
 constexpr AttnWorkspace attn_workspace(int head_dim, int rows) {
-    const size_t slots = 2 * static_cast<size_t>(kAttnMaxCtas) * 16 * attn_row_tiles(head_dim, rows);
+    const size_t slots = 2 * static_cast<size_t>(kAttnMaxCtas) * 16 * attn_row_warps(rows);
     AttnWorkspace w{};
     w.counters = kKvErrBytes;
-    w.part_ml = w.counters + kAttnCounterBytes;
+    w.joins = w.counters + kAttnCounterBytes;
+    w.part_ml = w.joins + kAttnMaxCtas * sizeof(int4);
     w.part = w.part_ml + slots * 2 * sizeof(float);
     w.bytes = w.part + slots * head_dim * sizeof(float);
     return w;

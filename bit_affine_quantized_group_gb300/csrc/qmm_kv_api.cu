@@ -31,7 +31,7 @@ int log2_of(int v) {
 int check_cache(const qmm_kv_cache* c) {
     if (c == nullptr || c->k == nullptr || c->v == nullptr) return QMM_ERR_INVALID_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QMM_ERR_INVALID_ARG;
-    if (c->num_pages < 0 || c->num_pages > (1LL << 31)) return QMM_ERR_INVALID_ARG;
+    if (c->num_pages < 0 || c->num_pages > 0x7FFFFFFF) return QMM_ERR_INVALID_ARG;
     const int64_t strides[6] = {c->k_page_stride, c->k_head_stride, c->k_slot_stride,
                                 c->v_page_stride, c->v_head_stride, c->v_slot_stride};
     for (int64_t s : strides)
@@ -115,7 +115,8 @@ int qmm_kv_error(const qmm_kv_plan_t* p, uint32_t* flags) {
     if (cudaMemcpy(&v, p->ws, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return QMM_ERR_CUDA;
     if (v != 0 && cudaMemset(p->ws, 0, sizeof(v)) != cudaSuccess) return QMM_ERR_CUDA;
     *flags = v;
-    return v == 0 ? QMM_OK : QMM_ERR_INVALID_ARG;
+    if (v == 0) return QMM_OK;
+    return v & QMM_KV_TIMEOUT ? QMM_ERR_TIMEOUT : QMM_ERR_INVALID_ARG;
 }
 
 void qmm_kv_destroy(qmm_kv_plan_t* p) {
@@ -194,6 +195,8 @@ int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, co
     if (seqs < 0 || seqs > d->max_seqs || rows < 0 || rows > d->max_rows) return QMM_ERR_INVALID_ARG;
     const int64_t tokens = static_cast<int64_t>(seqs) * rows;
     if (tokens == 0) return QMM_OK;
+    const int64_t row_tiles = (static_cast<int64_t>(rows) * (d->q_heads / d->kv_heads) + 15) / 16;
+    if (static_cast<int64_t>(seqs) * d->kv_heads * row_tiles >= (1LL << 30)) return QMM_ERR_UNSUPPORTED;
     const int64_t dq = static_cast<int64_t>(d->q_heads) * d->head_dim;
     if (!rows_ok(q, q_stride, dq, 2, tokens) || !rows_ok(out, out_stride, dq, 2, tokens)) return QMM_ERR_INVALID_ARG;
     if (page_table == nullptr || !aligned(page_table, 4) || lengths == nullptr || !aligned(lengths, 4))
@@ -220,6 +223,7 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const void*
     ap.lengths = lengths;
     ap.err = reinterpret_cast<uint32_t*>(p->ws);
     ap.counters = reinterpret_cast<uint32_t*>(p->ws + w.counters);
+    ap.joins = reinterpret_cast<int4*>(p->ws + w.joins);
     ap.part = reinterpret_cast<float*>(p->ws + w.part);
     ap.part_ml = reinterpret_cast<float*>(p->ws + w.part_ml);
     ap.q_stride = q_stride;
@@ -229,12 +233,16 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const void*
     ap.rows = rows;
     ap.group = group;
     ap.kv_heads = d.kv_heads;
-    ap.row_groups = 0;   // set by the launcher for the rows that one CTA holds
+    ap.group_inverse = ((1 << 20) + group - 1) / group;
+    ap.row_groups = ap.min_unit = 0;   // set by the launcher for the rows that one CTA holds
     ap.max_pages = d.max_pages;
     ap.page_shift = log2_of(d.page_size);
-    ap.window = d.window;
+    // a window that no position leaves is none
+    ap.window = d.window >= static_cast<int64_t>(d.max_pages) * d.page_size ? 0 : d.window;
     ap.sinks = d.sinks;
-    ap.scale_log2 = d.scale * 1.4426950408889634f;
+    ap.query_sign = d.scale < 0.0f ? 0x80008000u : 0u;
+    // a scale of 0 would make masked scores of -infinity NaN; one that moves no score does not
+    ap.scale_log2 = std::fmax(std::fabs(d.scale), 1e-30f) * 1.4426950408889634f;
     return launch_attention(d.head_dim, ap, p->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QMM_OK
                                                                                                         : QMM_ERR_CUDA;
 }

@@ -293,9 +293,10 @@ enum { QMM_IN_F32 = 0, QMM_IN_BF16 = 1 };
 
 /* Error bits of qmm_kv_error. */
 enum {
-    QMM_KV_BAD_PAGE = 1,     /* a page table entry in use lies outside 0..num_pages-1 */
-    QMM_KV_BAD_LENGTH = 2,   /* a length above max_pages * page_size: what is past the page table was left out */
-    QMM_KV_BAD_POSITION = 4  /* a rotation position outside the rope table: the row was not rotated */
+    QMM_KV_TIMEOUT = 7,       /* a kernel gave up a bounded wait (any of three bits) */
+    QMM_KV_BAD_PAGE = 16,     /* a page table entry in use lies outside 0..num_pages-1: read as zeros, not written */
+    QMM_KV_BAD_LENGTH = 32,   /* a length above max_pages * page_size: what is past the page table was left out */
+    QMM_KV_BAD_POSITION = 64  /* a rotation position outside the rope table: the row was not rotated */
 };
 
 /* What a plan for the cache operators fixes. */
@@ -339,7 +340,7 @@ size_t qmm_kv_workspace_bytes(const qmm_kv_desc* d);
  */
 int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, size_t ws_bytes);
 
-/* Read (synchronously) and clear the plan's device error word; QMM_ERR_INVALID_ARG if a bit was set. */
+/* Read (synchronously) and clear the plan's device error word: QMM_ERR_TIMEOUT or QMM_ERR_INVALID_ARG if a bit was set. */
 int qmm_kv_error(const qmm_kv_plan_t* p, uint32_t* flags);
 
 /* Free the plan and any workspace it allocated. NULL is accepted. */
