@@ -11,10 +11,16 @@
 // A row is one cluster's: its CTAs read it once from memory, keep it in shared
 // memory and exchange maxima, histograms and sums through distributed shared
 // memory. top-k and top-p are thresholds in the order (logit falling, index
-// rising). One histogram of count and mass over (max l - l) / T finds the bin
-// that a threshold lies in; its few members are then ranked against one
-// another. Only where a bin holds too many are they parted further: by the next
-// bits of the same distance, then by the bits of the logit, last by index.
+// rising), and what lies above one is nearly always few tokens:
+//   - top_k: the largest logit of every thread is counted in a histogram. The
+//     bin where the count reaches k bounds the k largest of all from below, and
+//     little more than k logits lie above it.
+//   - top_p alone: w_i > (1 - p) * (sum of w) / vocabulary for every kept token
+//     (what ranks from it on has mass above 1 - p, in at most `vocabulary`
+//     parts of at most w_i), so only those enter a histogram of mass.
+// The first CTA sorts these candidates and draws among them. Rows where a
+// threshold leaves too many candidates (flat ones, many equal logits) are
+// resolved bin by bin, then bit by bit, then by index.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -29,13 +35,17 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSampleThreads = 1024;
+constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = kSampleThreads;      // one thread of the first CTA joins one bin
-constexpr int kCap = 1024;                 // members of a bin that are ranked one by one
-constexpr int kMaxCluster = 8;
+constexpr int kBins = 1024;
+constexpr int kBinsEach = kBins / kSampleThreads;
+constexpr int kList = 2048;                // candidates that the first CTA sorts
+constexpr int kRanks = 16;                 // CTAs of a cluster at most
+constexpr int kPortableRanks = 8;
+constexpr int kCounted = 256;              // candidates that are ranked by counting; more are sorted
 constexpr float kWeightOne = 1099511627776.0f;   // 2^40
 constexpr float kBinsPerUnit = 32.0f;      // bins for one unit of (max l - l) / T: mass ends at 27.7 units
+constexpr int kWeightBinShift = 18;        // bits of a weight below its bin: 32 bins an octave
 
 typedef unsigned long long u64;
 
@@ -67,15 +77,13 @@ struct Threshold {   // kept: key > key, or key == key and index <= index
 };
 
 struct SampleShared {
-    u64 best[kMaxCluster];
-    u64 sum[kMaxCluster];
+    u64 sum[kRanks];
+    float top[kRanks], level[kRanks], above[kRanks];
     u64 warp_mass[kSampleWarps];
-    u64 mass[kBins];
-    uint32_t count[kBins];
+    alignas(16) u64 mass[kBins];
+    alignas(16) uint32_t count[kBins];
     uint32_t warp_count[kSampleWarps];
-    uint32_t list_key[kCap];
-    uint32_t list_index[kCap];
-    u64 list_mass[kCap];
+    u64 list[kList];
     uint32_t list_size;
     Decision decision;
     Threshold threshold;
@@ -89,6 +97,10 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+// (logit, index) as one number that falls along the ranks.
+__device__ __forceinline__ u64 entry_of(uint32_t key, uint32_t index) {
+    return static_cast<u64>(key) << 32 | (0xFFFFFFFFu - index);
 }
 
 template <class T>
@@ -107,30 +119,264 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {
     return v;
 }
 
+// Sorts v[0..kList) falling by the whole CTA. Every thread holds neighbours; partners a warp apart meet by shuffles, the
+// others in shared memory.
+__device__ __forceinline__ void sort_falling(u64* v) {
+    constexpr int kEach = kList / kSampleThreads;
+    const int tid = threadIdx.x, first = tid * kEach;
+    u64 e[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) e[j] = v[first + j];
+    auto keep = [](u64 a, u64 b, bool larger) -> u64 { return (a > b) == larger ? a : b; };
+    for (int size = 2; size <= kList; size *= 2) {
+        for (int step = size / 2; step > 0; step /= 2) {
+            if (step >= 32 * kEach) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) v[first + j] = e[j];
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const int i = first + j;
+                    e[j] = keep(e[j], v[i ^ step], ((i & step) == 0) == ((i & size) == 0));
+                }
+            } else if (step >= kEach) {
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const int i = first + j;
+                    e[j] = keep(e[j], __shfl_xor_sync(0xFFFFFFFFu, e[j], step / kEach), ((i & step) == 0) == ((i & size) == 0));
+                }
+            } else {
+#pragma unroll
+                for (int st = kEach / 2; st > 0; st /= 2) {   // constant indices
+                    if (st != step) continue;
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) {
+                        if (j & st) continue;
+                        const bool falls = ((first + j) & size) == 0;
+                        const u64 a = e[j], b = e[j | st];
+                        e[j] = keep(a, b, falls);
+                        e[j | st] = keep(a, b, !falls);
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) v[first + j] = e[j];
+    __syncthreads();
+}
+
+// Sum of v over the threads before this one; `all`: over all. scratch: kSampleWarps numbers.
+__device__ __forceinline__ u64 block_before(u64 v, u64* scratch, u64& all) {
+    static_assert(kSampleWarps == 16, "half a warp scans the warps");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u64 upto = warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) scratch[warp] = upto;
+    __syncthreads();
+    const u64 mine = scratch[lane & 15];
+    u64 w = mine;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+        const u64 a = __shfl_up_sync(0xFFFFFFFFu, w, o, 16);
+        if ((lane & 15) >= o) w += a;
+    }
+    all = __shfl_sync(0xFFFFFFFFu, w, 15);
+    return upto - v + __shfl_sync(0xFFFFFFFFu, w - mine, warp);
+}
+
+// 64-bit sums of two 32-bit atomics each: a 64-bit one in shared memory is a loop of compare-and-swaps (37 a thread of
+// 512 took 12,000 cycles, these 3,500).
+__device__ __forceinline__ void add_mass(u64* sum, u64 m) {
+    uint32_t* const w = reinterpret_cast<uint32_t*>(sum);
+    const uint32_t lo = static_cast<uint32_t>(m), old = atomicAdd(&w[0], lo);
+    const uint32_t hi = static_cast<uint32_t>(m >> 32) + (old + lo < old ? 1u : 0u);
+    if (hi != 0) atomicAdd(&w[1], hi);
+}
+
 template <class T>
 struct RowSampler {
     SampleShared& sh;
-    const T* x;            // this CTA's slots
+    float* x;              // this CTA's slots: the logits, and later their weights
+    const T* src;          // the row
     int lo, hi;            // the slots that hold logits
-    int64_t shift;         // index of slot 0
+    int shift;             // index of slot 0
     int rank, ranks;
     float top, temperature;
     Threshold thr;
 
-    __device__ __forceinline__ float logit(int i) const {
+    __device__ __forceinline__ float logit_at(uint32_t index) const {   // from memory
         if constexpr (sizeof(T) == 2)
-            return clean(__uint_as_float(static_cast<uint32_t>(x[i]) << 16));
+            return clean(__uint_as_float(static_cast<uint32_t>(src[index]) << 16));
         else
-            return clean(x[i]);
+            return clean(src[index]);
     }
     __device__ __forceinline__ uint32_t index(int i) const { return static_cast<uint32_t>(shift + i); }
-    __device__ __forceinline__ float depth(float l) const { return l == top ? 0.0f : __fdiv_rn(l - top, temperature); }
+    __device__ __forceinline__ float depth(float l) const { return temperature == 1.0f || l == top ? l == top ? 0.0f : l - top : __fdiv_rn(l - top, temperature); }
     __device__ __forceinline__ float weight(float l, float z) const { return l == top ? 1.0f : expf(z); }
+    __device__ __forceinline__ float weight(float l) const { return weight(l, depth(l)); }
     // (not above 0 also where an infinite temperature or logit leaves no number)
-    __device__ __forceinline__ u64 mass(float w) const { return w > 0.0f ? static_cast<u64>(w * kWeightOne) : 0ull; }
+    __device__ __forceinline__ static u64 mass(float w) { return w > 0.0f ? static_cast<u64>(w * kWeightOne) : 0ull; }
     __device__ __forceinline__ bool under(uint32_t key, uint32_t idx) const {
         return key > thr.key || (key == thr.key && idx <= thr.index);
     }
+
+    // ---- candidates ------------------------------------------------------------------------------------------------
+
+    __device__ __forceinline__ void clear_list() {
+        if (threadIdx.x == 0) sh.list_size = 0u;
+    }
+    __device__ __forceinline__ void add(uint32_t key, uint32_t index) {
+        const uint32_t at = atomicAdd(&sh.list_size, 1u);
+        if (at < kList) sh.list[at] = entry_of(key, index);
+    }
+
+    // Brings all CTAs' lists to the first one. Every CTA returns the number of entries; more than kList: nothing came.
+    __device__ int collect() {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        uint32_t sizes[kRanks], n = 0;   // all loads in flight at once: each takes as long as hundreds of instructions
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) sizes[r] = r < ranks ? cluster.map_shared_rank(&sh, r)->list_size : 0u;
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) n += sizes[r];
+        if (rank == 0 && n <= kList) {
+            for (uint32_t i = sizes[0] + threadIdx.x; i < n; i += kSampleThreads) {
+                uint32_t at = i;
+                int r = 0;
+#pragma unroll
+                for (int k = 0; k < kRanks - 1; ++k) {
+                    if (r == k && at >= sizes[k]) {
+                        at -= sizes[k];
+                        r = k + 1;
+                    }
+                }
+                sh.list[i] = cluster.map_shared_rank(&sh, r)->list[at];
+            }
+        }
+        cluster.sync();   // the other CTAs' lists have been read
+        return static_cast<int>(n);
+    }
+
+    __device__ __forceinline__ void sort_list(int n) {
+        for (int i = n + threadIdx.x; i < kList; i += kSampleThreads) sh.list[i] = 0ull;
+        __syncthreads();
+        sort_falling(sh.list);
+    }
+
+    // The draw among the n candidates of the list, which hold everything that may be kept; by the first CTA. `total`: the
+    // mass that top_p is a share of, 0 where it is that of the top_k candidates.
+    __device__ void finish(const SampleParams& p, int row, int n, int top_k, float top_p, float min_p, u64 total) {
+        const int k = top_k > 0 && top_k < n ? top_k : n;
+        __syncthreads();
+        if (n <= kCounted) {
+            // every candidate counts those that rank before it, and later those of lower indices; sh.mass is free
+            const int tid = threadIdx.x;
+            const u64 e = tid < n ? sh.list[tid] : 0ull;
+            const float w = tid < n ? weight(value_of(static_cast<uint32_t>(e >> 32))) : 0.0f;
+            u64 m = mass(w), all;
+            if (tid < kCounted) sh.mass[tid] = m;
+            __syncthreads();
+            int place = 0;
+            u64 before = 0;
+            if (tid < n) {
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) {
+                    const bool first = sh.list[j] > e;
+                    place += first ? 1 : 0;
+                    before += first ? sh.mass[j] : 0ull;
+                }
+            }
+            if (place >= k) m = 0;
+            if (total == 0) {
+                (void)block_before(tid < n ? m : 0ull, sh.warp_mass, all);
+                total = all;
+            }
+            const double limit = static_cast<double>(top_p) * static_cast<double>(total);
+            const bool keep = tid < n && place < k && (!(top_p < 1.0f) || static_cast<double>(before) < limit) && !(w < min_p);
+            m = keep ? m : 0ull;
+            __syncthreads();
+            if (tid < kCounted) sh.mass[tid] = m;
+            (void)block_before(m, sh.warp_mass, all);
+            const u64 target = target_of(p.u[row], all);
+            if (m == 0) return;
+            const uint32_t index = 0xFFFFFFFFu - static_cast<uint32_t>(e);
+            before = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) before += 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[j]) < index ? sh.mass[j] : 0ull;
+            if (target >= before && target < before + m) {
+                p.tokens[row] = static_cast<int32_t>(index);
+                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(m), static_cast<float>(all));
+            }
+            return;
+        }
+        sort_list(n);
+        constexpr int kEach = kList / kSampleThreads;
+        const int first = threadIdx.x * kEach;
+        float w[kEach];
+        u64 m[kEach], own = 0, all;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            w[j] = 0.0f;
+            m[j] = 0;
+            if (first + j < k) {
+                w[j] = weight(value_of(static_cast<uint32_t>(sh.list[first + j] >> 32)));
+                m[j] = mass(w[j]);
+                own += m[j];
+            }
+        }
+        u64 before = block_before(own, sh.warp_mass, all);
+        const double limit = static_cast<double>(top_p) * static_cast<double>(total != 0 ? total : all);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const bool keep = first + j < k && (!(top_p < 1.0f) || static_cast<double>(before) < limit) && !(w[j] < min_p);
+            before += m[j];
+            // packed as (index, mass) for the order of the indices; others go last
+            const uint32_t index = 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[first + j]);
+            sh.list[first + j] = keep ? ~(static_cast<u64>(index) << 41 | m[j]) : 0ull;
+        }
+        __syncthreads();
+        sort_falling(sh.list);   // the first indices first
+        own = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const u64 e = sh.list[first + j];
+            m[j] = e != 0 ? ~e & ((1ull << 41) - 1) : 0ull;
+            own += m[j];
+        }
+        before = block_before(own, sh.warp_mass, all);
+        const u64 target = target_of(p.u[row], all);
+        if (target < before || target >= before + own) return;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            if (target >= before && target < before + m[j]) {
+                p.tokens[row] = static_cast<int32_t>(~sh.list[first + j] >> 41);
+                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(m[j]), static_cast<float>(all));
+            }
+            before += m[j];
+        }
+    }
+
+    __device__ __forceinline__ static u64 target_of(float u, u64 total) {
+        const double want = static_cast<double>(u) * static_cast<double>(total);
+        const u64 target = want > 0.0 ? static_cast<u64>(want) : 0ull;
+        return target >= total ? total - 1 : target;
+    }
+
+    __device__ __forceinline__ uint32_t block_total(uint32_t v) {
+        v = __reduce_add_sync(0xFFFFFFFFu, v);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) sh.warp_count[threadIdx.x >> 5] = v;
+        __syncthreads();
+        uint32_t all = 0;
+        for (int w = 0; w < kSampleWarps; ++w) all += sh.warp_count[w];
+        return all;
+    }
+
+    // ---- selection in general --------------------------------------------------------------------------------------
+
     __device__ __forceinline__ static float bins(float z) { return fminf(-z * kBinsPerUnit, static_cast<float>(kBins - 1)); }
 
     // Elements that the levels before `level` left over: same bin0, same bin1, same leading key bits.
@@ -158,59 +404,98 @@ struct RowSampler {
         return kBins - 1 - ((key >> key_shift(level)) & (kBins - 1));   // the largest keys first
     }
 
-    // One level: which bin holds the last kept element. By count: rank < limit. By mass: mass before < limit.
-    __device__ Decision level_pass(int level, bool by_mass, u64 limit_count, float top_p, double limit_mass,
-                                   u64 count_before, u64 mass_before) {
-        cg::cluster_group cluster = cg::this_cluster();
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        sh.count[tid] = 0u;
-        sh.mass[tid] = 0ull;
-        __syncthreads();
-        for (int i = lo + tid; i < hi; i += kSampleThreads) {
-            const float l = logit(i);
-            const uint32_t key = key_of(l);
-            if (!under(key, index(i))) continue;
-            const float z = depth(l);
-            if (!member(level, z, key)) continue;
-            const uint32_t d = digit(level, z, key);
-            atomicAdd(&sh.count[d], 1u);
-            const u64 m = mass(weight(l, z));
-            if (m != 0) atomicAdd(&sh.mass[d], m);
+    __device__ __forceinline__ void clear_bins() {
+        for (int b = threadIdx.x; b < kBins; b += kSampleThreads) {
+            sh.count[b] = 0u;
+            sh.mass[b] = 0ull;
         }
+        __syncthreads();
+    }
+
+    // Joins the CTAs' histograms (every CTA does) and finds the bin of the last kept element: by count, rank < limit_count;
+    // by mass, mass before < limit_mass. The counts and masses before the histogram are given. Ends the CTAs' use of the
+    // histograms with a cluster barrier.
+    __device__ Decision join_bins(bool by_mass, u64 limit_count, double limit_mass, u64 count_before, u64 mass_before,
+                                  float top_p_of_total, bool with_mass = true) {
+        cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
-        if (rank == 0) {
-            u64 c = 0, m = 0;
-            for (int r = 0; r < ranks; ++r) {
-                const SampleShared* o = cluster.map_shared_rank(&sh, r);
-                c += o->count[tid];
-                m += o->mass[tid];
+        u64 c[kBinsEach], m[kBinsEach], own_c = 0, own_m = 0, all_c, all_m;
+        static_assert(kBinsEach == 2, "pairs of bins");
+        {
+            uint2 rc[kRanks];   // all loads in flight at once
+#pragma unroll
+            for (int r = 0; r < kRanks; ++r)
+                rc[r] = r < ranks ? reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh, r)->count)[threadIdx.x]
+                                  : make_uint2(0u, 0u);
+            c[0] = c[1] = m[0] = m[1] = 0;
+#pragma unroll
+            for (int r = 0; r < kRanks; ++r) c[0] += rc[r].x, c[1] += rc[r].y;
+        }
+        if (with_mass) {
+#pragma unroll
+            for (int h = 0; h < kRanks; h += 8) {
+                ulonglong2 rm[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    rm[r] = h + r < ranks
+                                ? reinterpret_cast<const ulonglong2*>(cluster.map_shared_rank(&sh, h + r)->mass)[threadIdx.x]
+                                : make_ulonglong2(0, 0);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) m[0] += rm[r].x, m[1] += rm[r].y;
             }
-            const u64 c_in = warp_scan(c, lane), m_in = warp_scan(m, lane);
-            if (lane == 31) {
-                sh.warp_count[warp] = static_cast<uint32_t>(c_in);
-                sh.warp_mass[warp] = m_in;
-            }
-            __syncthreads();
-            u64 c_off = count_before, m_off = mass_before, total = 0;
-            for (int w = 0; w < kSampleWarps; ++w) {
-                if (w < warp) c_off += sh.warp_count[w], m_off += sh.warp_mass[w];
-                total += sh.warp_mass[w];
-            }
-            const u64 c1 = c_off + c_in, m1 = m_off + m_in, c0 = c1 - c, m0 = m1 - m;
-            bool here;
-            if (by_mass) {
-                const double limit = level == 0 ? static_cast<double>(top_p) * static_cast<double>(total) : limit_mass;
-                here = c != 0 && static_cast<double>(m0) < limit && !(static_cast<double>(m1) < limit);
-            } else {
-                here = c0 < limit_count && c1 >= limit_count;
-            }
-            if (here) {
-                const Decision d{m0, total, static_cast<uint32_t>(c0), static_cast<uint32_t>(tid), static_cast<uint32_t>(c)};
-                for (int r = 0; r < ranks; ++r) cluster.map_shared_rank(&sh, r)->decision = d;
-            }
+        }
+        own_c = c[0] + c[1];
+        own_m = m[0] + m[1];
+        u64 c0 = count_before + block_before(own_c, sh.warp_mass, all_c);
+        u64 m0 = mass_before + block_before(own_m, sh.warp_mass, all_m);
+        if (top_p_of_total > 0.0f) limit_mass = static_cast<double>(top_p_of_total) * static_cast<double>(all_m);
+        if (threadIdx.x == 0) sh.decision.members = 0xFFFFFFFFu;   // none: everything lies above the threshold
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kBinsEach; ++j) {
+            const u64 c1 = c0 + c[j], m1 = m0 + m[j];
+            const bool here = by_mass ? c[j] != 0 && static_cast<double>(m0) < limit_mass && !(static_cast<double>(m1) < limit_mass)
+                                      : c0 < limit_count && c1 >= limit_count;
+            if (here)
+                sh.decision = Decision{m0, all_m, static_cast<uint32_t>(c0),
+                                       static_cast<uint32_t>(threadIdx.x * kBinsEach + j), static_cast<uint32_t>(c[j])};
+            c0 = c1;
+            m0 = m1;
         }
         cluster.sync();
         return sh.decision;
+    }
+
+    // The threshold among the members of one bin, collected in the first CTA's list: the last kept one.
+    __device__ void threshold_of_list(int n, bool by_mass, u64 limit_count, double limit, const Decision& d) {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (rank == 0) {
+            sort_list(n);
+            constexpr int kEach = kList / kSampleThreads;
+            const int first = threadIdx.x * kEach;
+            u64 m[kEach], own = 0, all;
+            uint32_t kept = 0;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                m[j] = first + j < n ? mass(weight(value_of(static_cast<uint32_t>(sh.list[first + j] >> 32)))) : 0ull;
+                own += m[j];
+            }
+            u64 before = d.mass + block_before(own, sh.warp_mass, all);
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                const int i = first + j;
+                if (i < n && (by_mass ? static_cast<double>(before) < limit : d.count + static_cast<u64>(i) < limit_count)) ++kept;
+                before += m[j];
+            }
+            const int last = static_cast<int>(block_total(kept)) - 1;
+            if (threadIdx.x < ranks && last >= 0) {
+                const u64 e = sh.list[last];
+                cluster.map_shared_rank(&sh, threadIdx.x)->threshold =
+                    Threshold{static_cast<uint32_t>(e >> 32), 0xFFFFFFFFu - static_cast<uint32_t>(e)};
+            }
+        }
+        cluster.sync();
+        thr = sh.threshold;
     }
 
     // Lower the threshold to the last element kept by the rank limit (by count) or by top_p (by mass).
@@ -222,7 +507,19 @@ struct RowSampler {
         bin0 = bin1 = prefix = 0;
         int level = 0;
         for (;;) {
-            d = level_pass(level, by_mass, limit_count, top_p, limit, d.count, d.mass);
+            clear_bins();
+            for (int i = lo + tid; i < hi; i += kSampleThreads) {
+                const float l = x[i];
+                const uint32_t key = key_of(l);
+                if (!under(key, index(i))) continue;
+                const float z = depth(l);
+                if (!member(level, z, key)) continue;
+                const uint32_t b = digit(level, z, key);
+                atomicAdd(&sh.count[b], 1u);
+                const u64 m = mass(weight(l, z));
+                if (m != 0) add_mass(&sh.mass[b], m);
+            }
+            d = join_bins(by_mass, limit_count, limit, d.count, d.mass, level == 0 ? top_p : 0.0f);
             if (level == 0) limit = static_cast<double>(top_p) * static_cast<double>(d.total);
             if (level == 0) bin0 = d.bin;
             if (level == 1) bin1 = d.bin;
@@ -231,58 +528,23 @@ struct RowSampler {
                 prefix = level == 2 ? dig : level == 5 ? (prefix << 2) | dig : (prefix << 10) | dig;
             }
             ++level;
-            if (d.members <= kCap || level == 6) break;
+            if (d.members <= kList || level == 6) break;
         }
-        if (d.members <= kCap) {
-            // rank the members against one another in the first CTA
-            SampleShared* first = cluster.map_shared_rank(&sh, 0);
-            if (rank == 0 && tid == 0) sh.list_size = 0u;
-            cluster.sync();
+        if (d.members <= kList) {
+            clear_list();
+            __syncthreads();
             for (int i = lo + tid; i < hi; i += kSampleThreads) {
-                const float l = logit(i);
+                const float l = x[i];
                 const uint32_t key = key_of(l);
-                if (!under(key, index(i))) continue;
-                const float z = depth(l);
-                if (!member(level, z, key)) continue;
-                const uint32_t at = atomicAdd(&first->list_size, 1u);
-                if (at < kCap) {
-                    first->list_key[at] = key;
-                    first->list_index[at] = index(i);
-                    first->list_mass[at] = mass(weight(l, z));
-                }
+                if (under(key, index(i)) && member(level, depth(l), key)) add(key, index(i));
             }
-            cluster.sync();
-            if (rank == 0) {
-                const int n = static_cast<int>(d.members);
-                bool kept = false;
-                u64 before = d.mass;
-                uint32_t place = 0, key = 0, idx = 0;
-                if (tid < n) {
-                    key = sh.list_key[tid];
-                    idx = sh.list_index[tid];
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t k2 = sh.list_key[j], i2 = sh.list_index[j];
-                        if (k2 > key || (k2 == key && i2 < idx)) {
-                            ++place;
-                            before += sh.list_mass[j];
-                        }
-                    }
-                    kept = by_mass ? static_cast<double>(before) < limit : d.count + place < limit_count;
-                }
-                const int keep = __syncthreads_count(kept);
-                if (kept && place == static_cast<uint32_t>(keep - 1)) {
-                    const Threshold t{key, idx};
-                    for (int r = 0; r < ranks; ++r) cluster.map_shared_rank(&sh, r)->threshold = t;
-                }
-            }
-            cluster.sync();
-            thr = sh.threshold;
+            const int n = collect();
+            threshold_of_list(n, by_mass, limit_count, limit, d);
             return;
         }
         // more equal logits than the list holds: the first `keep` of them by index
         const uint32_t key = prefix;
-        const float l0 = value_of(key);
-        const u64 m = mass(weight(l0, depth(l0)));
+        const u64 m = mass(weight(value_of(key)));
         u64 keep = d.members;
         if (by_mass) {
             u64 a = 0, b = d.members;   // the first i whose mass before is not below the limit
@@ -299,10 +561,10 @@ struct RowSampler {
         const int s0 = lo + warp * seg, s1 = s0 + seg < hi ? s0 + seg : hi;
         uint32_t equal = 0;
         for (int i = s0 + lane; i < s1; i += 32) {
-            const uint32_t k2 = key_of(logit(i));
+            const uint32_t k2 = key_of(x[i]);
             equal += k2 == key && under(k2, index(i)) ? 1u : 0u;
         }
-        equal = warp_add(equal);
+        equal = __reduce_add_sync(0xFFFFFFFFu, equal);
         if (lane == 0) sh.warp_count[warp] = equal;
         __syncthreads();
         u64 mine = 0, at = 0;
@@ -316,7 +578,7 @@ struct RowSampler {
         if (at < keep && at + equal >= keep) {
             for (int i0 = s0; i0 < s1; i0 += 32) {
                 const int i = i0 + lane;
-                const bool in = i < s1 && key_of(logit(i)) == key && under(key, index(i));
+                const bool in = i < s1 && key_of(x[i]) == key && under(key, index(i));
                 const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in);
                 const u64 place = at + __popc(votes & ((1u << lane) - 1u));
                 if (in && place == keep - 1) {
@@ -332,8 +594,8 @@ struct RowSampler {
 };
 
 template <class T>
-__global__ void __launch_bounds__(kSampleThreads) qmm_sample_kernel(const __grid_constant__ SampleParams p) {
-    extern __shared__ __align__(16) uint8_t slots[];
+__global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __grid_constant__ SampleParams p) {
+    extern __shared__ __align__(16) float slots[];
     __shared__ SampleShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     constexpr int kVec = 16 / sizeof(T);
@@ -348,76 +610,246 @@ __global__ void __launch_bounds__(kSampleThreads) qmm_sample_kernel(const __grid
     const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
     const int chunks = (lead + p.vocab + kVec - 1) / kVec;
     const int per_cta = (chunks + ranks - 1) / ranks;
-    const int64_t shift = static_cast<int64_t>(rank) * per_cta * kVec - lead;   // index of slot 0
-    const int64_t left = p.vocab - shift;
-    T* const x = reinterpret_cast<T*>(slots);
-    RowSampler<T> s{sh, x};
-    s.shift = shift;
-    s.lo = shift < 0 ? static_cast<int>(-shift) : 0;
-    s.hi = left < per_cta * kVec ? (left > s.lo ? static_cast<int>(left) : s.lo) : per_cta * kVec;
+    RowSampler<T> s{sh, slots, src};
+    s.shift = rank * per_cta * kVec - lead;
+    const int left = p.vocab - s.shift;
+    s.lo = s.shift < 0 ? -s.shift : 0;
+    s.hi = left < per_cta * kVec ? (left > s.lo ? left : s.lo) : per_cta * kVec;
     s.rank = rank;
     s.ranks = ranks;
-
-    u64 best = 0;
-    for (int c = tid; c < per_cta; c += kSampleThreads) {
-        const int at = c * kVec;
-        if (at >= s.lo && at + kVec <= s.hi) {
-            *reinterpret_cast<uint4*>(x + at) = __ldg(reinterpret_cast<const uint4*>(src + shift + at));
-        } else {
-            for (int j = at; j < at + kVec; ++j)
-                if (j >= s.lo && j < s.hi) x[j] = src[shift + j];
-        }
-        for (int j = at; j < at + kVec; ++j) {
-            if (j < s.lo || j >= s.hi) continue;
-            const u64 v = static_cast<u64>(key_of(s.logit(j))) << 32 | (0xFFFFFFFFu - s.index(j));
-            best = v > best ? v : best;
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const u64 v = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-        best = v > best ? v : best;
-    }
-    if (lane == 0) sh.warp_mass[warp] = best;
-    __syncthreads();
-    if (tid < ranks) {
-        for (int w = 0; w < kSampleWarps; ++w) best = sh.warp_mass[w] > best ? sh.warp_mass[w] : best;
-        cluster.map_shared_rank(&sh, tid)->best[rank] = best;
-    }
-    cluster.sync();
-    best = 0;
-    for (int r = 0; r < ranks; ++r) best = sh.best[r] > best ? sh.best[r] : best;
-    s.top = value_of(static_cast<uint32_t>(best >> 32));
-    const uint32_t top_index = 0xFFFFFFFFu - static_cast<uint32_t>(best);
     s.temperature = p.temperature[row];
     const int top_k = p.top_k[row];
     const float top_p = p.top_p[row], min_p = p.min_p[row];
 
-    const bool none = s.top == -INFINITY;
-    if (none || !(s.temperature > 0.0f) || top_k == 1 || top_p <= 0.0f) {
+    // the logits to shared memory, and every thread's largest
+    float best = -INFINITY;
+    for (int c0 = tid; c0 < per_cta; c0 += 4 * kSampleThreads) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // four loads in flight
+            const int at = (c0 + j * kSampleThreads) * kVec;
+            if (at >= s.lo && at + kVec <= s.hi) v[j] = __ldg(reinterpret_cast<const uint4*>(src + s.shift + at));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + j * kSampleThreads, at = c * kVec;
+            if (c >= per_cta) continue;
+            if (at >= s.lo && at + kVec <= s.hi) {
+                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                float f[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    if constexpr (sizeof(T) == 2)
+                        f[e] = clean(__uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16));
+                    else
+                        f[e] = clean(__uint_as_float(w[e]));
+                    best = fmaxf(best, f[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < kVec; e += 4)
+                    *reinterpret_cast<float4*>(slots + at + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            } else {
+                for (int i = at; i < at + kVec; ++i) {
+                    if (i < s.lo || i >= s.hi) continue;
+                    slots[i] = s.logit_at(s.index(i));
+                    best = fmaxf(best, slots[i]);
+                }
+            }
+        }
+    }
+    // The row's largest logit, and the mean of the threads' largest ones (those of numbers in use, not of masks).
+    {
+        const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, key_of(best));
+        const bool in_use = best > -1e30f && best < 1e30f;
+        const float sum = warp_add(in_use ? best : 0.0f);
+        const uint32_t some = __popc(__ballot_sync(0xFFFFFFFFu, in_use));
+        if (lane == 0) {
+            sh.warp_count[warp] = key;
+            sh.warp_mass[warp] = static_cast<u64>(__float_as_uint(sum)) << 32 | some;
+        }
+        __syncthreads();
+        if (tid < ranks) {
+            uint32_t k = 0, n = 0;
+            float f = 0.0f;
+            for (int w = 0; w < kSampleWarps; ++w) {
+                k = sh.warp_count[w] > k ? sh.warp_count[w] : k;
+                f += __uint_as_float(static_cast<uint32_t>(sh.warp_mass[w] >> 32));
+                n += static_cast<uint32_t>(sh.warp_mass[w]);
+            }
+            SampleShared* o = cluster.map_shared_rank(&sh, tid);
+            o->top[rank] = value_of(k);
+            o->level[rank] = f;
+            o->above[rank] = static_cast<float>(n);
+        }
+    }
+    for (int b = tid; b < kBins; b += kSampleThreads) {
+        sh.count[b] = 0u;
+        sh.mass[b] = 0ull;
+    }
+    s.clear_list();
+    cluster.sync();
+    float level = 0.0f, above = 0.0f;
+    s.top = sh.top[0];
+    for (int r = 0; r < ranks; ++r) {
+        s.top = fmaxf(s.top, sh.top[r]);
+        level += sh.level[r];
+        above += sh.above[r];
+    }
+    s.thr = Threshold{0u, 0xFFFFFFFFu};
+    if (s.top == -INFINITY) {
         if (rank == 0 && tid == 0) {
-            p.tokens[row] = none ? -1 : static_cast<int32_t>(top_index);
-            if (p.probs != nullptr) p.probs[row] = none ? 0.0f : 1.0f;
+            p.tokens[row] = -1;
+            if (p.probs != nullptr) p.probs[row] = 0.0f;
         }
         return;
     }
 
-    s.thr = Threshold{0u, 0xFFFFFFFFu};
-    if (top_k > 0 && top_k < p.vocab) s.select(false, static_cast<u64>(top_k), 1.0f);
-    if (top_p < 1.0f) s.select(true, 0, top_p);
+    const bool by_count = top_k > 0 && top_k < p.vocab;
+    const bool by_mass = top_p < 1.0f;
+    if (!(s.temperature > 0.0f) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f) {
+        // the first of the largest
+        uint32_t first = 0xFFFFFFFFu;
+        for (int i = s.lo + tid; i < s.hi; i += kSampleThreads)
+            if (slots[i] == s.top) first = min(first, s.index(i));
+        first = __reduce_min_sync(0xFFFFFFFFu, first);
+        if (lane == 0) sh.warp_count[warp] = first;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 0; w < kSampleWarps; ++w) first = min(first, sh.warp_count[w]);
+            cluster.map_shared_rank(&sh, 0)->sum[rank] = first;
+        }
+        cluster.sync();
+        if (rank == 0 && tid == 0) {
+            for (int r = 0; r < ranks; ++r) first = min(first, static_cast<uint32_t>(sh.sum[r]));
+            p.tokens[row] = static_cast<int32_t>(first);
+            if (p.probs != nullptr) p.probs[row] = 1.0f;
+        }
+        return;
+    }
+
+    if (by_count && top_k <= kList * 3 / 4 && s.top < 1e30f) {
+        // The bin of the k-th of the threads' largest logits, or of all logits where k is a large part of the threads.
+        const bool largest = top_k <= ranks * kSampleThreads / 4;
+        const float range = above > 0.0f ? (largest ? 1.5f : 4.0f) * (s.top - level / above) : 0.0f;
+        const float per_unit = range > 0.0f ? kBins / range : 1.0f;
+        auto bin_of = [&](float l) -> int { return static_cast<int>(fminf((s.top - l) * per_unit, kBins - 1.0f)); };
+        if (largest) {
+            if (best > -INFINITY) atomicAdd(&sh.count[bin_of(best)], 1u);
+        } else {
+            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) atomicAdd(&sh.count[bin_of(slots[i])], 1u);
+        }
+        const Decision d = s.join_bins(false, static_cast<u64>(top_k), 0.0, 0, 0, 0.0f, false);
+        if (d.members != 0xFFFFFFFFu && d.bin < kBins - 1) {
+            const float below = static_cast<float>(d.bin + 1);
+            if ((s.top - best) * per_unit < below) {   // else this thread's chunks have none
+                for (int c = tid; c < per_cta; c += kSampleThreads) {
+                    for (int i = max(c * kVec, s.lo); i < min((c + 1) * kVec, s.hi); ++i)
+                        if ((s.top - slots[i]) * per_unit < below) s.add(key_of(slots[i]), s.index(i));
+                }
+            }
+            const int n = s.collect();
+            if (n <= kList) {
+                if (rank == 0) s.finish(p, row, n, top_k, top_p, min_p, 0);
+                return;
+            }
+        }
+    }
+
+    // weights in the logits' place, segment by segment of a warp, and their masses
+    const int seg = ((s.hi - s.lo + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;
+    const int s0 = s.lo + warp * seg, s1 = s0 + seg < s.hi ? s0 + seg : s.hi;
+    bool general = by_count;   // thresholds by logit and index, the logits still in their place
+    u64 own = 0;
+    if (!general) {
+        __syncthreads();
+        for (int i = s0 + lane; i < s1; i += 32) {
+            const float w = s.weight(slots[i]);
+            const u64 m = s.mass(w);
+            slots[i] = m != 0 ? w : 0.0f;
+            if (by_mass || !(w < min_p)) own += m;
+        }
+    }
+    uint32_t edge = 0;           // weights of this many bits or more lie in bins before the threshold's
+    uint32_t edge_end = 0;       // and below this in bins after it
+    if (!general && by_mass) {
+        u64 all;
+        (void)block_before(own, sh.warp_mass, all);
+        if (tid < ranks) cluster.map_shared_rank(&sh, tid)->sum[rank] = all;
+        cluster.sync();
+        u64 total = 0;
+        for (int r = 0; r < ranks; ++r) total += sh.sum[r];
+        // no kept token weighs less (a little off for the roundings of this line)
+        const float least = 0.999f * (1.0f - top_p) * static_cast<float>(total) / kWeightOne / static_cast<float>(p.vocab);
+        for (int b = tid; b < kBins; b += kSampleThreads) {
+            sh.count[b] = 0u;
+            sh.mass[b] = 0ull;
+        }
+        s.clear_list();
+        __syncthreads();
+        auto bin_of = [](float w) -> uint32_t {
+            return min((0x3F800000u - __float_as_uint(w)) >> kWeightBinShift, static_cast<uint32_t>(kBins - 1));
+        };
+        for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) {
+            const float w = slots[i];
+            if (w >= least && w > 0.0f) {
+                atomicAdd(&sh.count[bin_of(w)], 1u);
+                add_mass(&sh.mass[bin_of(w)], s.mass(w));
+            }
+        }
+        const double limit = static_cast<double>(top_p) * static_cast<double>(total);
+        const Decision d = s.join_bins(true, 0, limit, 0, 0, 0.0f);
+        general = d.members == 0xFFFFFFFFu || d.bin == kBins - 1;
+        if (!general) {
+            const bool whole = d.count + d.members <= kList;   // everything down to this bin: the draw is the first CTA's
+            if (whole || d.members <= kList) {
+                for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) {
+                    const float w = slots[i];
+                    if (w > 0.0f && (whole ? bin_of(w) <= d.bin : bin_of(w) == d.bin)) s.add(key_of(s.logit_at(s.index(i))), s.index(i));
+                }
+                const int n = s.collect();
+                if (whole) {
+                    if (rank == 0) s.finish(p, row, n, 0, top_p, min_p, total);
+                    return;
+                }
+                s.threshold_of_list(n, true, 0, limit, d);
+                edge = 0x3F800000u - (d.bin << kWeightBinShift) + 1;
+                edge_end = 0x3F800000u - ((d.bin + 1) << kWeightBinShift) + 1;
+            } else {
+                general = true;
+            }
+        }
+        if (general) {   // the logits again
+            __syncthreads();
+            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) slots[i] = s.logit_at(s.index(i));
+            __syncthreads();
+        }
+    }
+    if (general) {
+        if (by_count) s.select(false, static_cast<u64>(top_k), 0.0f);
+        if (by_mass) s.select(true, 0, top_p);
+    }
 
     // the draw: kept masses in the order of the indices
     auto kept = [&](int i) -> u64 {
-        const float l = s.logit(i);
-        const uint32_t idx = s.index(i);
-        if (!s.under(key_of(l), idx)) return 0;
-        const float w = s.weight(l, s.depth(l));
-        return w < min_p && idx != top_index ? 0 : s.mass(w);
+        if (general) {
+            const float l = slots[i];
+            if (!s.under(key_of(l), s.index(i))) return 0;
+            const float w = s.weight(l);
+            return w < min_p ? 0 : s.mass(w);
+        }
+        const float w = slots[i];
+        if (w < min_p) return 0;
+        if (by_mass) {
+            const uint32_t bits = __float_as_uint(w);
+            if (bits < edge_end) return 0;
+            if (bits < edge && !s.under(key_of(s.logit_at(s.index(i))), s.index(i))) return 0;
+        }
+        return s.mass(w);
     };
-    const int seg = ((s.hi - s.lo + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;
-    const int s0 = s.lo + warp * seg, s1 = s0 + seg < s.hi ? s0 + seg : s.hi;
-    u64 own = 0;
-    for (int i = s0 + lane; i < s1; i += 32) own += kept(i);
+    if (general || by_mass) {
+        own = 0;
+        for (int i = s0 + lane; i < s1; i += 32) own += kept(i);
+    }
     own = warp_add(own);
     __syncthreads();
     if (lane == 0) sh.warp_mass[warp] = own;
@@ -434,9 +866,7 @@ __global__ void __launch_bounds__(kSampleThreads) qmm_sample_kernel(const __grid
         if (r < rank) before += sh.sum[r];
         total += sh.sum[r];
     }
-    const double want = static_cast<double>(p.u[row]) * static_cast<double>(total);
-    u64 target = want > 0.0 ? static_cast<u64>(want) : 0ull;
-    if (target >= total) target = total - 1;
+    const u64 target = s.target_of(p.u[row], total);
     if (target < before || target >= before + own) return;
     for (int i0 = s0; i0 < s1; i0 += 32) {
         const int i = i0 + lane;
@@ -455,7 +885,8 @@ __global__ void __launch_bounds__(kSampleThreads) qmm_sample_kernel(const __grid
 }
 
 // A CTA's share of a row in shared memory: at most this many bytes.
-constexpr int kSampleSmem = 16 * ((QMM_SAMPLE_MAX_VOCAB * 4 / 16 + 1 + kMaxCluster - 1) / kMaxCluster);
+constexpr int kSampleSmem = 4 * 8 * ((QMM_SAMPLE_MAX_VOCAB / 8 + 1 + kPortableRanks - 1) / kPortableRanks);
+static_assert(kSampleSmem + sizeof(SampleShared) <= 227 * 1024, "the largest row fits its cluster");
 
 template <class T>
 int launch(const SampleParams& p, int M, cudaStream_t stream) {
@@ -463,11 +894,12 @@ int launch(const SampleParams& p, int M, cudaStream_t stream) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
     if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(qmm_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(qmm_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(qmm_sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return QMM_ERR_CUDA;
         if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    int ranks = kMaxCluster;
+    int ranks = M <= 9 ? kRanks : kPortableRanks;             // few rows leave SMs for more CTAs each
     while (ranks > 1 && p.vocab / ranks < 2048) ranks /= 2;   // shorter shares cost more exchange than they save
     const int vec = 16 / static_cast<int>(sizeof(T));
     const int chunks = (p.vocab + vec - 1) / vec + 1;         // one more where the row starts inside a chunk
@@ -480,7 +912,7 @@ int launch(const SampleParams& p, int M, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M) * ranks);
     cfg.blockDim = dim3(kSampleThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>((chunks + ranks - 1) / ranks) * 16;
+    cfg.dynamicSmemBytes = static_cast<size_t>((chunks + ranks - 1) / ranks) * vec * 4;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
