@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <utility>
 
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
@@ -37,15 +38,14 @@ namespace cg = cooperative_groups;
 
 constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kBinsEach = kBins / kSampleThreads;
+constexpr int kBins = 256;                 // few: every CTA reads every other's histogram, at shared memory's remote rate
 constexpr int kList = 2048;                // candidates that the first CTA sorts
 constexpr int kRanks = 16;                 // CTAs of a cluster at most
 constexpr int kPortableRanks = 8;
-constexpr int kCounted = 256;              // candidates that are ranked by counting; more are sorted
+constexpr int kCounted = 256;              // candidates that are ranked by counting; more are sorted (kBins at most)
 constexpr float kWeightOne = 1099511627776.0f;   // 2^40
-constexpr float kBinsPerUnit = 32.0f;      // bins for one unit of (max l - l) / T: mass ends at 27.7 units
-constexpr int kWeightBinShift = 18;        // bits of a weight below its bin: 32 bins an octave
+constexpr float kBinsPerUnit = 8.0f;       // bins for one unit of (max l - l) / T: mass ends at 27.7 units
+constexpr int kWeightBinShift = 20;        // bits of a weight below its bin: 8 bins an octave
 
 typedef unsigned long long u64;
 
@@ -84,7 +84,8 @@ struct SampleShared {
     alignas(16) uint32_t count[kBins];
     uint32_t warp_count[kSampleWarps];
     u64 list[kList];
-    uint32_t list_size;
+    u64 scalar;
+    uint32_t list_size, sizes[kRanks];
     Decision decision;
     Threshold threshold;
 };
@@ -119,16 +120,19 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {
     return v;
 }
 
-// Sorts v[0..kList) falling by the whole CTA. Every thread holds neighbours; partners a warp apart meet by shuffles, the
-// others in shared memory.
+// Sorts v[0 .. kEach * kSampleThreads) falling by the whole CTA. Every thread holds kEach neighbours; partners a warp apart
+// meet by shuffles, the others in shared memory.
+template <int kEach>
 __device__ __forceinline__ void sort_falling(u64* v) {
-    constexpr int kEach = kList / kSampleThreads;
+    constexpr int kAll = kEach * kSampleThreads;
     const int tid = threadIdx.x, first = tid * kEach;
     u64 e[kEach];
 #pragma unroll
     for (int j = 0; j < kEach; ++j) e[j] = v[first + j];
     auto keep = [](u64 a, u64 b, bool larger) -> u64 { return (a > b) == larger ? a : b; };
-    for (int size = 2; size <= kList; size *= 2) {
+#pragma unroll 1
+    for (int size = 2; size <= kAll; size *= 2) {
+#pragma unroll 1
         for (int step = size / 2; step > 0; step /= 2) {
             if (step >= 32 * kEach) {
                 __syncthreads();
@@ -196,6 +200,20 @@ __device__ __forceinline__ void add_mass(u64* sum, u64 m) {
     if (hi != 0) atomicAdd(&w[1], hi);
 }
 
+// The least whole number whose double is not below `limit`: `(double)a < limit` for whole a is `a < bound`. One thread's
+// work (double arithmetic is slow on this GPU).
+__device__ __forceinline__ u64 bound_of(double limit) {
+    u64 a = static_cast<u64>(limit);
+    if (a < (1ull << 53)) return static_cast<double>(a) < limit ? a + 1 : a;
+    u64 lo = a - 4096, hi = a + 4096;   // conversions of numbers below 2^60 are off by 64 at most
+    while (lo < hi) {
+        const u64 mid = lo + (hi - lo) / 2;
+        if (static_cast<double>(mid) < limit) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
 template <class T>
 struct RowSampler {
     SampleShared& sh;
@@ -225,120 +243,152 @@ struct RowSampler {
 
     // ---- candidates ------------------------------------------------------------------------------------------------
 
+    // Every CTA has a part of the first one's list for its own candidates.
     __device__ __forceinline__ void clear_list() {
         if (threadIdx.x == 0) sh.list_size = 0u;
     }
     __device__ __forceinline__ void add(uint32_t key, uint32_t index) {
-        const uint32_t at = atomicAdd(&sh.list_size, 1u);
-        if (at < kList) sh.list[at] = entry_of(key, index);
+        const uint32_t room = kList / ranks, at = atomicAdd(&sh.list_size, 1u);
+        if (at < room) cg::this_cluster().map_shared_rank(&sh, 0)->list[rank * room + at] = entry_of(key, index);
     }
 
-    // Brings all CTAs' lists to the first one. Every CTA returns the number of entries; more than kList: nothing came.
+    // The number of candidates of all CTAs, which the first one then has in its list; more than kList where a CTA had more
+    // than fit its part. All CTAs call it, and are done with one another's memory after it.
     __device__ int collect() {
         cg::cluster_group cluster = cg::this_cluster();
+        __syncthreads();
+        if (threadIdx.x < ranks) cluster.map_shared_rank(&sh, threadIdx.x)->sizes[rank] = sh.list_size;
         cluster.sync();
-        uint32_t sizes[kRanks], n = 0;   // all loads in flight at once: each takes as long as hundreds of instructions
+        const uint32_t room = kList / ranks;
+        uint32_t n = 0;
+        bool fits = true;
 #pragma unroll
-        for (int r = 0; r < kRanks; ++r) sizes[r] = r < ranks ? cluster.map_shared_rank(&sh, r)->list_size : 0u;
+        for (int r = 0; r < kRanks; ++r) {
+            const uint32_t size = r < ranks ? sh.sizes[r] : 0u;
+            n += size;
+            fits &= size <= room;
+        }
+        if (!fits) return kList + 1;
+        if (rank == 0 && ranks > 1) {   // close the gaps
+            u64 e[kList / kSampleThreads];
 #pragma unroll
-        for (int r = 0; r < kRanks; ++r) n += sizes[r];
-        if (rank == 0 && n <= kList) {
-            for (uint32_t i = sizes[0] + threadIdx.x; i < n; i += kSampleThreads) {
+            for (int k = 0; k < kList / kSampleThreads; ++k) {
+                const uint32_t i = threadIdx.x + k * kSampleThreads;
+                if (i >= n) break;
                 uint32_t at = i;
                 int r = 0;
+                while (at >= sh.sizes[r]) at -= sh.sizes[r++];
+                e[k] = sh.list[r * room + at];
+            }
+            __syncthreads();
 #pragma unroll
-                for (int k = 0; k < kRanks - 1; ++k) {
-                    if (r == k && at >= sizes[k]) {
-                        at -= sizes[k];
-                        r = k + 1;
-                    }
-                }
-                sh.list[i] = cluster.map_shared_rank(&sh, r)->list[at];
+            for (int k = 0; k < kList / kSampleThreads; ++k) {
+                const uint32_t i = threadIdx.x + k * kSampleThreads;
+                if (i < n) sh.list[i] = e[k];
             }
         }
-        cluster.sync();   // the other CTAs' lists have been read
+        __syncthreads();
         return static_cast<int>(n);
     }
 
-    __device__ __forceinline__ void sort_list(int n) {
-        for (int i = n + threadIdx.x; i < kList; i += kSampleThreads) sh.list[i] = 0ull;
+    // One thread's result for all; a barrier before and after.
+    template <class F>
+    __device__ __forceinline__ u64 by_one(F f) {
         __syncthreads();
-        sort_falling(sh.list);
+        if (threadIdx.x == 0) sh.scalar = f();
+        __syncthreads();
+        return sh.scalar;
+    }
+    __device__ __forceinline__ static u64 mass_limit(float top_p, u64 total) {
+        return bound_of(static_cast<double>(top_p) * static_cast<double>(total));
+    }
+    __device__ __forceinline__ static u64 target_of(float u, u64 total) {
+        const double want = static_cast<double>(u) * static_cast<double>(total);
+        const u64 target = want > 0.0 ? static_cast<u64>(want) : 0ull;
+        return target >= total ? total - 1 : target;
     }
 
     // The draw among the n candidates of the list, which hold everything that may be kept; by the first CTA. `total`: the
     // mass that top_p is a share of, 0 where it is that of the top_k candidates.
     __device__ void finish(const SampleParams& p, int row, int n, int top_k, float top_p, float min_p, u64 total) {
         const int k = top_k > 0 && top_k < n ? top_k : n;
+        if (n <= kCounted) finish_counted(p, row, n, k, top_p, min_p, total);
+        else if (n <= kSampleThreads) finish_sorted<1>(p, row, n, k, top_p, min_p, total);
+        else finish_sorted<kList / kSampleThreads>(p, row, n, k, top_p, min_p, total);
+    }
+
+    // Every candidate counts those that rank before it, and then those of lower indices.
+    __device__ __forceinline__ void finish_counted(const SampleParams& p, int row, int n, int k, float top_p, float min_p,
+                                                   u64 total) {
+        const int tid = threadIdx.x;
+        const u64 e = tid < n ? sh.list[tid] : 0ull;
+        const float w = tid < n ? weight(value_of(static_cast<uint32_t>(e >> 32))) : 0.0f;
+        u64 m = mass(w), all;
+        if (tid < kCounted) sh.mass[tid] = m;   // the histogram is used up
         __syncthreads();
-        if (n <= kCounted) {
-            // every candidate counts those that rank before it, and later those of lower indices; sh.mass is free
-            const int tid = threadIdx.x;
-            const u64 e = tid < n ? sh.list[tid] : 0ull;
-            const float w = tid < n ? weight(value_of(static_cast<uint32_t>(e >> 32))) : 0.0f;
-            u64 m = mass(w), all;
-            if (tid < kCounted) sh.mass[tid] = m;
-            __syncthreads();
-            int place = 0;
-            u64 before = 0;
-            if (tid < n) {
+        int place = 0;
+        u64 before = 0;
+        if (tid < n) {
 #pragma unroll 4
-                for (int j = 0; j < n; ++j) {
-                    const bool first = sh.list[j] > e;
-                    place += first ? 1 : 0;
-                    before += first ? sh.mass[j] : 0ull;
-                }
+            for (int j = 0; j < n; ++j) {
+                const bool first = sh.list[j] > e;
+                place += first ? 1 : 0;
+                before += first ? sh.mass[j] : 0ull;
             }
-            if (place >= k) m = 0;
-            if (total == 0) {
-                (void)block_before(tid < n ? m : 0ull, sh.warp_mass, all);
-                total = all;
-            }
-            const double limit = static_cast<double>(top_p) * static_cast<double>(total);
-            const bool keep = tid < n && place < k && (!(top_p < 1.0f) || static_cast<double>(before) < limit) && !(w < min_p);
-            m = keep ? m : 0ull;
-            __syncthreads();
-            if (tid < kCounted) sh.mass[tid] = m;
-            (void)block_before(m, sh.warp_mass, all);
-            const u64 target = target_of(p.u[row], all);
-            if (m == 0) return;
-            const uint32_t index = 0xFFFFFFFFu - static_cast<uint32_t>(e);
-            before = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) before += 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[j]) < index ? sh.mass[j] : 0ull;
-            if (target >= before && target < before + m) {
-                p.tokens[row] = static_cast<int32_t>(index);
-                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(m), static_cast<float>(all));
-            }
-            return;
         }
-        sort_list(n);
-        constexpr int kEach = kList / kSampleThreads;
+        bool keep = tid < n && place < k && !(w < min_p);
+        if (top_p < 1.0f) {
+            if (total == 0) (void)block_before(place < k ? m : 0ull, sh.warp_mass, total);
+            keep &= before < by_one([&] { return mass_limit(top_p, total); });
+        }
+        m = keep ? m : 0ull;
+        __syncthreads();
+        if (tid < kCounted) sh.mass[tid] = m;
+        (void)block_before(m, sh.warp_mass, all);
+        const u64 target = by_one([&] { return target_of(p.u[row], all); });
+        if (m == 0) return;
+        const uint32_t low = static_cast<uint32_t>(e);   // falls with the index
+        before = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) before += static_cast<uint32_t>(sh.list[j]) > low ? sh.mass[j] : 0ull;
+        if (target >= before && target < before + m) {
+            p.tokens[row] = static_cast<int32_t>(0xFFFFFFFFu - low);
+            if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(m), static_cast<float>(all));
+        }
+    }
+
+    template <int kEach>
+    __device__ __forceinline__ void sort_list(int n) {
+        for (int i = n + threadIdx.x; i < kEach * kSampleThreads; i += kSampleThreads) sh.list[i] = 0ull;
+        __syncthreads();
+        sort_falling<kEach>(sh.list);
+    }
+
+    template <int kEach>
+    __device__ __forceinline__ void finish_sorted(const SampleParams& p, int row, int n, int k, float top_p, float min_p,
+                                                  u64 total) {
+        sort_list<kEach>(n);
         const int first = threadIdx.x * kEach;
         float w[kEach];
         u64 m[kEach], own = 0, all;
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            w[j] = 0.0f;
-            m[j] = 0;
-            if (first + j < k) {
-                w[j] = weight(value_of(static_cast<uint32_t>(sh.list[first + j] >> 32)));
-                m[j] = mass(w[j]);
-                own += m[j];
-            }
+            w[j] = first + j < k ? weight(value_of(static_cast<uint32_t>(sh.list[first + j] >> 32))) : 0.0f;
+            m[j] = mass(w[j]);
+            own += m[j];
         }
         u64 before = block_before(own, sh.warp_mass, all);
-        const double limit = static_cast<double>(top_p) * static_cast<double>(total != 0 ? total : all);
+        const u64 limit = by_one([&] { return top_p < 1.0f ? mass_limit(top_p, total != 0 ? total : all) : ~0ull; });
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            const bool keep = first + j < k && (!(top_p < 1.0f) || static_cast<double>(before) < limit) && !(w[j] < min_p);
+            const bool keep = first + j < k && before < limit && !(w[j] < min_p);
             before += m[j];
             // packed as (index, mass) for the order of the indices; others go last
             const uint32_t index = 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[first + j]);
             sh.list[first + j] = keep ? ~(static_cast<u64>(index) << 41 | m[j]) : 0ull;
         }
         __syncthreads();
-        sort_falling(sh.list);   // the first indices first
+        sort_falling<kEach>(sh.list);   // the first indices first
         own = 0;
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
@@ -347,7 +397,7 @@ struct RowSampler {
             own += m[j];
         }
         before = block_before(own, sh.warp_mass, all);
-        const u64 target = target_of(p.u[row], all);
+        const u64 target = by_one([&] { return target_of(p.u[row], all); });
         if (target < before || target >= before + own) return;
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
@@ -357,12 +407,6 @@ struct RowSampler {
             }
             before += m[j];
         }
-    }
-
-    __device__ __forceinline__ static u64 target_of(float u, u64 total) {
-        const double want = static_cast<double>(u) * static_cast<double>(total);
-        const u64 target = want > 0.0 ? static_cast<u64>(want) : 0ull;
-        return target >= total ? total - 1 : target;
     }
 
     __device__ __forceinline__ uint32_t block_total(uint32_t v) {
@@ -394,7 +438,7 @@ struct RowSampler {
         // t - b is exact; the last bin is open and has no parts
         return b == kBins - 1 ? 0u : static_cast<uint32_t>((t - static_cast<float>(b)) * kBins);
     }
-    __device__ __forceinline__ static int key_shift(int level) { return level == 2 ? 22 : level == 3 ? 12 : level == 4 ? 2 : 0; }
+    __device__ __forceinline__ static int key_shift(int level) { return 8 * (5 - level); }
     __device__ __forceinline__ uint32_t digit(int level, float z, uint32_t key) const {
         if (level <= 1) {
             const float t = bins(z);
@@ -405,108 +449,117 @@ struct RowSampler {
     }
 
     __device__ __forceinline__ void clear_bins() {
-        for (int b = threadIdx.x; b < kBins; b += kSampleThreads) {
-            sh.count[b] = 0u;
-            sh.mass[b] = 0ull;
+        if (threadIdx.x < kBins) {
+            sh.count[threadIdx.x] = 0u;
+            sh.mass[threadIdx.x] = 0ull;
         }
         __syncthreads();
     }
 
-    // Joins the CTAs' histograms (every CTA does) and finds the bin of the last kept element: by count, rank < limit_count;
-    // by mass, mass before < limit_mass. The counts and masses before the histogram are given. Ends the CTAs' use of the
-    // histograms with a cluster barrier.
-    __device__ Decision join_bins(bool by_mass, u64 limit_count, double limit_mass, u64 count_before, u64 mass_before,
-                                  float top_p_of_total, bool with_mass = true) {
+    // Joins the CTAs' histograms (every CTA does) and finds the bin of the last kept element: by count, rank < limit; by
+    // mass, mass before < limit. The counts and masses before the histogram are given. With top_p_of_total the limit is that
+    // share of the histogram's mass. The CTAs may still read one another's histograms when it returns.
+    __device__ Decision join_bins(bool by_mass, u64 limit, u64 count_before, u64 mass_before, float top_p_of_total,
+                                  bool with_mass = true) {
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
-        u64 c[kBinsEach], m[kBinsEach], own_c = 0, own_m = 0, all_c, all_m;
-        static_assert(kBinsEach == 2, "pairs of bins");
-        {
-            uint2 rc[kRanks];   // all loads in flight at once
+        const int b = threadIdx.x;   // a bin for each of the first threads
+        uint32_t c = 0;
+        u64 m = 0, all_c, all_m = 0, m0 = 0;
+        if (b < kBins) {
+            uint32_t rc[kRanks];   // all loads in flight at once
 #pragma unroll
-            for (int r = 0; r < kRanks; ++r)
-                rc[r] = r < ranks ? reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh, r)->count)[threadIdx.x]
-                                  : make_uint2(0u, 0u);
-            c[0] = c[1] = m[0] = m[1] = 0;
+            for (int r = 0; r < kRanks; ++r) rc[r] = r < ranks ? cluster.map_shared_rank(&sh, r)->count[b] : 0u;
 #pragma unroll
-            for (int r = 0; r < kRanks; ++r) c[0] += rc[r].x, c[1] += rc[r].y;
+            for (int r = 0; r < kRanks; ++r) c += rc[r];
         }
         if (with_mass) {
+            if (b < kBins) {
+                u64 rm[kRanks];
 #pragma unroll
-            for (int h = 0; h < kRanks; h += 8) {
-                ulonglong2 rm[8];
+                for (int r = 0; r < kRanks; ++r) rm[r] = r < ranks ? cluster.map_shared_rank(&sh, r)->mass[b] : 0ull;
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    rm[r] = h + r < ranks
-                                ? reinterpret_cast<const ulonglong2*>(cluster.map_shared_rank(&sh, h + r)->mass)[threadIdx.x]
-                                : make_ulonglong2(0, 0);
-#pragma unroll
-                for (int r = 0; r < 8; ++r) m[0] += rm[r].x, m[1] += rm[r].y;
+                for (int r = 0; r < kRanks; ++r) m += rm[r];
             }
+            m0 = mass_before + block_before(m, sh.warp_mass, all_m);
+            if (top_p_of_total > 0.0f) limit = by_one([&] { return mass_limit(top_p_of_total, all_m); });
         }
-        own_c = c[0] + c[1];
-        own_m = m[0] + m[1];
-        u64 c0 = count_before + block_before(own_c, sh.warp_mass, all_c);
-        u64 m0 = mass_before + block_before(own_m, sh.warp_mass, all_m);
-        if (top_p_of_total > 0.0f) limit_mass = static_cast<double>(top_p_of_total) * static_cast<double>(all_m);
+        const u64 c0 = count_before + block_before(c, sh.warp_mass, all_c);
         if (threadIdx.x == 0) sh.decision.members = 0xFFFFFFFFu;   // none: everything lies above the threshold
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kBinsEach; ++j) {
-            const u64 c1 = c0 + c[j], m1 = m0 + m[j];
-            const bool here = by_mass ? c[j] != 0 && static_cast<double>(m0) < limit_mass && !(static_cast<double>(m1) < limit_mass)
-                                      : c0 < limit_count && c1 >= limit_count;
-            if (here)
-                sh.decision = Decision{m0, all_m, static_cast<uint32_t>(c0),
-                                       static_cast<uint32_t>(threadIdx.x * kBinsEach + j), static_cast<uint32_t>(c[j])};
-            c0 = c1;
-            m0 = m1;
-        }
-        cluster.sync();
+        const bool here = by_mass ? c != 0 && m0 < limit && m0 + m >= limit : c0 < limit && c0 + c >= limit;
+        if (b < kBins && here) sh.decision = Decision{m0, all_m, static_cast<uint32_t>(c0), static_cast<uint32_t>(b), c};
+        __syncthreads();
         return sh.decision;
     }
 
     // The threshold among the members of one bin, collected in the first CTA's list: the last kept one.
-    __device__ void threshold_of_list(int n, bool by_mass, u64 limit_count, double limit, const Decision& d) {
-        cg::cluster_group cluster = cg::this_cluster();
+    __device__ void threshold_of_list(int n, bool by_mass, u64 limit, const Decision& d) {
         if (rank == 0) {
-            sort_list(n);
-            constexpr int kEach = kList / kSampleThreads;
-            const int first = threadIdx.x * kEach;
-            u64 m[kEach], own = 0, all;
-            uint32_t kept = 0;
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                m[j] = first + j < n ? mass(weight(value_of(static_cast<uint32_t>(sh.list[first + j] >> 32)))) : 0ull;
-                own += m[j];
-            }
-            u64 before = d.mass + block_before(own, sh.warp_mass, all);
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                const int i = first + j;
-                if (i < n && (by_mass ? static_cast<double>(before) < limit : d.count + static_cast<u64>(i) < limit_count)) ++kept;
-                before += m[j];
-            }
-            const int last = static_cast<int>(block_total(kept)) - 1;
-            if (threadIdx.x < ranks && last >= 0) {
-                const u64 e = sh.list[last];
-                cluster.map_shared_rank(&sh, threadIdx.x)->threshold =
-                    Threshold{static_cast<uint32_t>(e >> 32), 0xFFFFFFFFu - static_cast<uint32_t>(e)};
+            if (n <= kCounted) {
+                const int tid = threadIdx.x;
+                const u64 e = tid < n ? sh.list[tid] : 0ull;
+                if (tid < kCounted) sh.mass[tid] = tid < n ? mass(weight(value_of(static_cast<uint32_t>(e >> 32)))) : 0ull;
+                __syncthreads();
+                uint32_t place = 0;
+                u64 before = d.mass;
+                if (tid < n) {
+#pragma unroll 4
+                    for (int j = 0; j < n; ++j) {
+                        const bool first = sh.list[j] > e;
+                        place += first ? 1u : 0u;
+                        before += first ? sh.mass[j] : 0ull;
+                    }
+                }
+                const bool keep = tid < n && (by_mass ? before < limit : d.count + static_cast<u64>(place) < limit);
+                const uint32_t kept = block_total(keep ? 1u : 0u);
+                if (keep && place == kept - 1) tell_threshold(e);
+            } else if (n <= kSampleThreads) {
+                threshold_of_sorted<1>(n, by_mass, limit, d);
+            } else {
+                threshold_of_sorted<kList / kSampleThreads>(n, by_mass, limit, d);
             }
         }
-        cluster.sync();
+        cg::this_cluster().sync();
         thr = sh.threshold;
+    }
+    __device__ __forceinline__ void tell_threshold(u64 e) {
+        cg::cluster_group cluster = cg::this_cluster();
+        for (int r = 0; r < ranks; ++r)
+            cluster.map_shared_rank(&sh, r)->threshold =
+                Threshold{static_cast<uint32_t>(e >> 32), 0xFFFFFFFFu - static_cast<uint32_t>(e)};
+    }
+    template <int kEach>
+    __device__ __forceinline__ void threshold_of_sorted(int n, bool by_mass, u64 limit, const Decision& d) {
+        sort_list<kEach>(n);
+        const int first = threadIdx.x * kEach;
+        u64 m[kEach], own = 0, all;
+        uint32_t kept = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            m[j] = first + j < n ? mass(weight(value_of(static_cast<uint32_t>(sh.list[first + j] >> 32)))) : 0ull;
+            own += m[j];
+        }
+        u64 before = d.mass + block_before(own, sh.warp_mass, all);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int i = first + j;
+            if (i < n && (by_mass ? before < limit : d.count + static_cast<u64>(i) < limit)) ++kept;
+            before += m[j];
+        }
+        const uint32_t all_kept = block_total(kept);
+        if (threadIdx.x == 0 && all_kept > 0) tell_threshold(sh.list[all_kept - 1]);
     }
 
     // Lower the threshold to the last element kept by the rank limit (by count) or by top_p (by mass).
-    __device__ void select(bool by_mass, u64 limit_count, float top_p) {
+    __device__ void select(bool by_mass, u64 limit, float top_p) {
         cg::cluster_group cluster = cg::this_cluster();
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        double limit = 0.0;
         Decision d{0, 0, 0, 0, 0};
         bin0 = bin1 = prefix = 0;
         int level = 0;
         for (;;) {
+            cluster.sync();   // no CTA reads another's histogram any more
             clear_bins();
             for (int i = lo + tid; i < hi; i += kSampleThreads) {
                 const float l = x[i];
@@ -519,30 +572,52 @@ struct RowSampler {
                 const u64 m = mass(weight(l, z));
                 if (m != 0) add_mass(&sh.mass[b], m);
             }
-            d = join_bins(by_mass, limit_count, limit, d.count, d.mass, level == 0 ? top_p : 0.0f);
-            if (level == 0) limit = static_cast<double>(top_p) * static_cast<double>(d.total);
+            d = join_bins(by_mass, limit, d.count, d.mass, level == 0 ? top_p : 0.0f);
+            if (level == 0 && by_mass) limit = by_one([&] { return mass_limit(top_p, d.total); });
             if (level == 0) bin0 = d.bin;
             if (level == 1) bin1 = d.bin;
             if (level >= 2) {
                 const uint32_t dig = kBins - 1 - d.bin;
-                prefix = level == 2 ? dig : level == 5 ? (prefix << 2) | dig : (prefix << 10) | dig;
+                prefix = level == 2 ? dig : prefix << 8 | dig;
             }
             ++level;
             if (d.members <= kList || level == 6) break;
         }
         if (d.members <= kList) {
-            clear_list();
             __syncthreads();
+            clear_list();
+            cluster.sync();   // the first CTA's list is free
             for (int i = lo + tid; i < hi; i += kSampleThreads) {
                 const float l = x[i];
                 const uint32_t key = key_of(l);
                 if (under(key, index(i)) && member(level, depth(l), key)) add(key, index(i));
             }
             const int n = collect();
-            threshold_of_list(n, by_mass, limit_count, limit, d);
-            return;
+            if (n <= kList) {
+                threshold_of_list(n, by_mass, limit, d);
+                return;
+            }
+            // all members in the part of one CTA: on to single logits
+            for (; level < 6; ++level) {
+                cluster.sync();
+                clear_bins();
+                for (int i = lo + tid; i < hi; i += kSampleThreads) {
+                    const float l = x[i];
+                    const uint32_t key = key_of(l);
+                    const float z = depth(l);
+                    if (!under(key, index(i)) || !member(level, z, key)) continue;
+                    atomicAdd(&sh.count[digit(level, z, key)], 1u);
+                    add_mass(&sh.mass[digit(level, z, key)], mass(weight(l, z)));
+                }
+                d = join_bins(by_mass, limit, d.count, d.mass, 0.0f);
+                if (level == 1) bin1 = d.bin;
+                if (level >= 2) {
+                    const uint32_t dig = kBins - 1 - d.bin;
+                    prefix = level == 2 ? dig : prefix << 8 | dig;
+                }
+            }
         }
-        // more equal logits than the list holds: the first `keep` of them by index
+        // equal logits, more than the list holds: the first `keep` of them by index
         const uint32_t key = prefix;
         const u64 m = mass(weight(value_of(key)));
         u64 keep = d.members;
@@ -550,12 +625,12 @@ struct RowSampler {
             u64 a = 0, b = d.members;   // the first i whose mass before is not below the limit
             while (a < b) {
                 const u64 mid = (a + b) / 2;
-                if (static_cast<double>(d.mass + mid * m) < limit) a = mid + 1;
+                if (d.mass + mid * m < limit) a = mid + 1;
                 else b = mid;
             }
             keep = a;
         } else {
-            keep = limit_count - d.count;
+            keep = limit - d.count;
         }
         const int seg = ((hi - lo + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;
         const int s0 = lo + warp * seg, s1 = s0 + seg < hi ? s0 + seg : hi;
@@ -602,6 +677,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / ranks;
+    auto started = cluster.barrier_arrive();   // waited for before the first access to another CTA's memory
     griddep_launch_dependents();
     griddep_wait();
 
@@ -668,6 +744,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
             sh.warp_mass[warp] = static_cast<u64>(__float_as_uint(sum)) << 32 | some;
         }
         __syncthreads();
+        cluster.barrier_wait(std::move(started));
         if (tid < ranks) {
             uint32_t k = 0, n = 0;
             float f = 0.0f;
@@ -682,15 +759,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
             o->above[rank] = static_cast<float>(n);
         }
     }
-    for (int b = tid; b < kBins; b += kSampleThreads) {
-        sh.count[b] = 0u;
-        sh.mass[b] = 0ull;
+    if (tid < kBins) {
+        sh.count[tid] = 0u;
+        sh.mass[tid] = 0ull;
     }
     s.clear_list();
     cluster.sync();
     float level = 0.0f, above = 0.0f;
     s.top = sh.top[0];
-    for (int r = 0; r < ranks; ++r) {
+#pragma unroll
+    for (int r = 0; r < kRanks; ++r) {
+        if (r >= ranks) continue;
         s.top = fmaxf(s.top, sh.top[r]);
         level += sh.level[r];
         above += sh.above[r];
@@ -727,7 +806,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         return;
     }
 
-    if (by_count && top_k <= kList * 3 / 4 && s.top < 1e30f) {
+    if (by_count && top_k <= kList / 2 && s.top < 1e30f) {
         // The bin of the k-th of the threads' largest logits, or of all logits where k is a large part of the threads.
         const bool largest = top_k <= ranks * kSampleThreads / 4;
         const float range = above > 0.0f ? (largest ? 1.5f : 4.0f) * (s.top - level / above) : 0.0f;
@@ -738,7 +817,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         } else {
             for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) atomicAdd(&sh.count[bin_of(slots[i])], 1u);
         }
-        const Decision d = s.join_bins(false, static_cast<u64>(top_k), 0.0, 0, 0, 0.0f, false);
+        const Decision d = s.join_bins(false, static_cast<u64>(top_k), 0, 0, 0.0f, false);
         if (d.members != 0xFFFFFFFFu && d.bin < kBins - 1) {
             const float below = static_cast<float>(d.bin + 1);
             if ((s.top - best) * per_unit < below) {   // else this thread's chunks have none
@@ -780,12 +859,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         for (int r = 0; r < ranks; ++r) total += sh.sum[r];
         // no kept token weighs less (a little off for the roundings of this line)
         const float least = 0.999f * (1.0f - top_p) * static_cast<float>(total) / kWeightOne / static_cast<float>(p.vocab);
-        for (int b = tid; b < kBins; b += kSampleThreads) {
-            sh.count[b] = 0u;
-            sh.mass[b] = 0ull;
-        }
         s.clear_list();
-        __syncthreads();
+        s.clear_bins();
         auto bin_of = [](float w) -> uint32_t {
             return min((0x3F800000u - __float_as_uint(w)) >> kWeightBinShift, static_cast<uint32_t>(kBins - 1));
         };
@@ -796,26 +871,48 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
                 add_mass(&sh.mass[bin_of(w)], s.mass(w));
             }
         }
-        const double limit = static_cast<double>(top_p) * static_cast<double>(total);
-        const Decision d = s.join_bins(true, 0, limit, 0, 0, 0.0f);
+        const u64 limit = s.by_one([&] { return s.mass_limit(top_p, total); });
+        Decision d = s.join_bins(true, limit, 0, 0, 0.0f);
         general = d.members == 0xFFFFFFFFu || d.bin == kBins - 1;
+        const bool whole = !general && d.count + d.members <= kCounted;   // few in all: the draw is the first CTA's
+        const uint32_t bin = d.bin;
+        auto bits_below = [](float w) -> uint32_t { return 0x3F800000u - __float_as_uint(w); };
+        uint32_t sub = 0xFFFFFFFFu;                                       // part of the bin
+        constexpr int kSubShift = kWeightBinShift - 8;
+        if (!general && !whole && d.members > kCounted) {
+            // the next bits part the bin's members
+            cluster.sync();
+            s.clear_bins();
+            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) {
+                const float w = slots[i];
+                if (!(w > 0.0f) || bin_of(w) != bin) continue;
+                const uint32_t b = bits_below(w) >> kSubShift & (kBins - 1);
+                atomicAdd(&sh.count[b], 1u);
+                add_mass(&sh.mass[b], s.mass(w));
+            }
+            d = s.join_bins(true, limit, d.count, d.mass, 0.0f);
+            sub = d.bin;
+            general = d.members == 0xFFFFFFFFu || d.members > kList;
+        }
         if (!general) {
-            const bool whole = d.count + d.members <= kList;   // everything down to this bin: the draw is the first CTA's
-            if (whole || d.members <= kList) {
-                for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) {
-                    const float w = slots[i];
-                    if (w > 0.0f && (whole ? bin_of(w) <= d.bin : bin_of(w) == d.bin)) s.add(key_of(s.logit_at(s.index(i))), s.index(i));
-                }
-                const int n = s.collect();
-                if (whole) {
-                    if (rank == 0) s.finish(p, row, n, 0, top_p, min_p, total);
-                    return;
-                }
-                s.threshold_of_list(n, true, 0, limit, d);
-                edge = 0x3F800000u - (d.bin << kWeightBinShift) + 1;
-                edge_end = 0x3F800000u - ((d.bin + 1) << kWeightBinShift) + 1;
-            } else {
+            auto member = [&](float w) -> bool {
+                if (!(w > 0.0f)) return false;
+                if (whole) return bin_of(w) <= bin;
+                return bin_of(w) == bin && (sub == 0xFFFFFFFFu || (bits_below(w) >> kSubShift & (kBins - 1)) == sub);
+            };
+            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads)
+                if (member(slots[i])) s.add(key_of(s.logit_at(s.index(i))), s.index(i));
+            const int n = s.collect();
+            if (n > kList) {
                 general = true;
+            } else if (whole) {
+                if (rank == 0) s.finish(p, row, n, 0, top_p, min_p, total);
+                return;
+            } else {
+                s.threshold_of_list(n, true, limit, d);
+                const uint32_t from = sub == 0xFFFFFFFFu ? bin << kWeightBinShift : bin << kWeightBinShift | sub << kSubShift;
+                edge = 0x3F800000u - from + 1;
+                edge_end = edge - (sub == 0xFFFFFFFFu ? 1u << kWeightBinShift : 1u << kSubShift);
             }
         }
         if (general) {   // the logits again
@@ -866,7 +963,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         if (r < rank) before += sh.sum[r];
         total += sh.sum[r];
     }
-    const u64 target = s.target_of(p.u[row], total);
+    const u64 target = s.by_one([&] { return s.target_of(p.u[row], total); });
     if (target < before || target >= before + own) return;
     for (int i0 = s0; i0 < s1; i0 += 32) {
         const int i = i0 + lane;
@@ -899,7 +996,7 @@ int launch(const SampleParams& p, int M, cudaStream_t stream) {
             return QMM_ERR_CUDA;
         if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    int ranks = M <= 9 ? kRanks : kPortableRanks;             // few rows leave SMs for more CTAs each
+    int ranks = M <= 16 ? kRanks : kPortableRanks;             // few rows leave SMs for more CTAs each
     while (ranks > 1 && p.vocab / ranks < 2048) ranks /= 2;   // shorter shares cost more exchange than they save
     const int vec = 16 / static_cast<int>(sizeof(T));
     const int chunks = (p.vocab + vec - 1) / vec + 1;         // one more where the row starts inside a chunk

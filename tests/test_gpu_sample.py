@@ -112,6 +112,19 @@ def test_modes(q, dtype, V, mode):
     _check(q, torch, logits, T, k, p, min_p, V)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 2, 10, 17, 40])
+def test_rows(q, dtype, M):
+    """One row and many: the number of rows decides how many CTAs share one."""
+    import torch
+    gen = torch.Generator().manual_seed(M)
+    logits = (torch.randn((M, 50021), generator=gen) * 2.5).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    l = logits.double().numpy()
+    k = [(0, 30)[r % 2] for r in range(M)]
+    p = [_top_p_between(l[r], 1.0, k[r], (900, 12)[r % 2]) for r in range(M)]
+    _check(q, torch, logits, [1.0] * M, k, p, [0.0] * M, M)
+
+
 @pytest.mark.parametrize("V", [5000, 30001])
 @pytest.mark.parametrize("spread", [0.0, 1e-6, 0.01, 0.3])
 def test_flat_rows(q, V, spread):
