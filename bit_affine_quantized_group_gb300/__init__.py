@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libqmm.so")
@@ -75,6 +76,12 @@ class QmmKvCache(ctypes.Structure):
                [(f"{s}_{d}_stride", ctypes.c_int64) for s in "kv" for d in ("page", "head", "slot")]
 
 
+class QmmAttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
 class QmmAppendArgs(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
@@ -111,7 +118,7 @@ def _load() -> ctypes.CDLL:
     lib.qmm_plan_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.qmm_destroy.argtypes = [vp]
     lib.qmm_destroy.restype = None
-    kvd, kvc, kva = ctypes.POINTER(QmmKvDesc), ctypes.POINTER(QmmKvCache), ctypes.POINTER(QmmAppendArgs)
+    kvd, kvc = ctypes.POINTER(QmmKvDesc), ctypes.POINTER(QmmKvCache)
     lib.qmm_kv_validate_desc.argtypes = [kvd]
     lib.qmm_kv_workspace_bytes.argtypes = [kvd]
     lib.qmm_kv_workspace_bytes.restype = sz
@@ -119,10 +126,10 @@ def _load() -> ctypes.CDLL:
     lib.qmm_kv_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.qmm_kv_destroy.argtypes = [vp]
     lib.qmm_kv_destroy.restype = None
-    lib.qmm_check_qk_norm_rope_args.argtypes = [kvd, kvc, kva]
-    lib.qmm_qk_norm_rope.argtypes = [vp, kvc, kva, vp]
-    lib.qmm_check_attention_args.argtypes = [kvd, kvc, vp, i64, vp, vp, i32, i32, vp, i64]
-    lib.qmm_attention.argtypes = [vp, kvc, vp, i64, vp, vp, i32, i32, vp, i64, vp]
+    lib.qmm_check_qk_norm_rope_args.argtypes = [kvd, kvc, vp]
+    lib.qmm_qk_norm_rope.argtypes = [vp, kvc, vp, vp]
+    lib.qmm_check_attention_args.argtypes = [kvd, kvc, vp]
+    lib.qmm_attention.argtypes = [vp, kvc, vp, vp]
     lib.qmm_sample.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.qmm_status_string.argtypes = [i32]
     lib.qmm_status_string.restype = ctypes.c_char_p
@@ -188,6 +195,16 @@ def _stream_handle(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_on(stream, device: int) -> int:
+    """_stream_handle without a Stream object for the current stream: calls of a few microseconds notice it."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device >= 0:
+            return raw(device)
+    return _stream_handle(stream)
 
 
 class Plan:
@@ -354,6 +371,8 @@ class KVPlan:
         self._handle = ctypes.c_void_p()
         self.workspace = None
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
         with torch.cuda.device(dev):
             ws, nbytes = None, 0
             if torch_workspace:
@@ -366,7 +385,10 @@ class KVPlan:
         self.device = dev
         self.q_width, self.kv_width = d.q_heads * d.head_dim, d.kv_heads * d.head_dim
         self.page_shape = (d.kv_heads, d.page_size, d.head_dim)
-        self.max_pages = d.max_pages
+        self.max_pages, self.head_dim, self.rot_dim = d.max_pages, d.head_dim, d.rot_dim
+        # what a call passes to the library: a plan is used by one call at a time
+        self._args = ctypes.create_string_buffer(max(_APPEND_ARGS.size, _ATTENTION_ARGS.size))
+        self._args_at = ctypes.addressof(self._args)
 
     @property
     def handle(self):
@@ -408,25 +430,31 @@ class KVCache:
         self.ref = ctypes.byref(self.struct)
 
 
-def _rows(t, width, dtype, what):
+_APPEND_ARGS = struct.Struct("@3P3q3Pq4Pq3i4x")      # QmmAppendArgs
+_ATTENTION_ARGS = struct.Struct("@4P2q2i")           # QmmAttentionArgs
+assert _APPEND_ARGS.size == ctypes.sizeof(QmmAppendArgs) and _ATTENTION_ARGS.size == ctypes.sizeof(QmmAttentionArgs)
+
+
+def _rows(t, tokens, width, dtype, what):
     """Elements between the rows of a tensor [tokens, width] or [tokens, heads, head_dim] of adjacent heads."""
-    if t.dtype != dtype or t.numel() != t.shape[0] * width or t.stride(-1) != 1 or \
-            (t.dim() == 3 and t.stride(1) != t.shape[2]) or not 2 <= t.dim() <= 3:
-        raise ValueError(f"{what}: {dtype} rows of {width} adjacent elements are needed")
-    return t.stride(0)
+    st = t.stride()
+    if t.dtype is not dtype or t.numel() != tokens * width or st[-1] != 1 or \
+            (len(st) != 2 and (len(st) != 3 or st[1] != t.shape[2])):
+        raise ValueError(f"{what}: {tokens} {dtype} rows of {width} adjacent elements are needed")
+    return st[0]
 
 
-def _check_step(plan, cache, page_table, lengths, tokens):
-    import torch
+def _check_step(plan, cache, page_table, lengths, tokens, int32):
+    seqs = lengths.numel()
     if cache.page_shape != plan.page_shape:
         raise ValueError("the cache's pages are not the plan's [kv_heads, page_size, head_dim]")
-    if lengths.dtype != torch.int32 or page_table.dtype != torch.int32 or not page_table.is_contiguous() or \
-            not lengths.is_contiguous() or page_table.shape != (lengths.shape[0], plan.max_pages):
+    if lengths.dtype is not int32 or page_table.dtype is not int32 or not page_table.is_contiguous() or \
+            not lengths.is_contiguous() or page_table.shape != (seqs, plan.max_pages):
         raise ValueError("lengths [seqs] and page_table [seqs, max_pages] are contiguous int32 tensors")
-    seqs = lengths.shape[0]
-    if tokens % max(seqs, 1) != 0:
+    rows, rest = divmod(tokens, seqs) if seqs else (0, tokens)
+    if rest:
         raise ValueError("every sequence has the same number of rows")
-    return seqs, tokens // max(seqs, 1)
+    return seqs, rows
 
 
 def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_table, cache: KVCache, out,
@@ -435,27 +463,25 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
     [tokens, heads * head_dim] of float32 or bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and
     k_weight: float32 [head_dim] or None; rope: float32 [positions, rot_dim], cosines then sines."""
     import torch
-    tokens = q.shape[0]
-    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
-    if q.dtype not in (torch.float32, torch.bfloat16) or k.shape[0] != tokens or v.shape[0] != tokens or \
-            out.shape[0] != tokens:
-        raise ValueError("q, k and v are float32 or bfloat16 rows of the same tokens, as out is")
-    for w, n in ((q_weight, plan.desc.head_dim), (k_weight, plan.desc.head_dim)):
-        if w is not None and (w.dtype != torch.float32 or w.numel() != n or not w.is_contiguous()):
+    f32, bf16, dtype, tokens = torch.float32, torch.bfloat16, q.dtype, q.shape[0]
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, torch.int32)
+    if dtype is not f32 and dtype is not bf16:
+        raise ValueError("q, k and v are float32 or bfloat16")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not f32 or w.numel() != plan.head_dim or not w.is_contiguous()):
             raise ValueError("q_weight and k_weight are float32 [head_dim] or None")
-    if plan.desc.rot_dim and (rope is None or rope.dtype != torch.float32 or not rope.is_contiguous() or
-                              rope.shape[-1] != plan.desc.rot_dim):
+    if plan.rot_dim and (rope is None or rope.dtype is not f32 or not rope.is_contiguous() or rope.shape[-1] != plan.rot_dim):
         raise ValueError("rope is a float32 tensor [positions, rot_dim]")
-    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != tokens or
+    if positions is not None and (positions.dtype is not torch.int32 or positions.numel() != tokens or
                                   not positions.is_contiguous()):
         raise ValueError("positions is an int32 tensor [tokens]")
-    a = QmmAppendArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, plan.q_width, q.dtype, "q"),
-                      _rows(k, plan.kv_width, q.dtype, "k"), _rows(v, plan.kv_width, q.dtype, "v"), _ptr(q_weight),
-                      _ptr(k_weight), _ptr(rope), rope.shape[0] if rope is not None else 0, lengths.data_ptr(),
-                      _ptr(positions), page_table.data_ptr(), out.data_ptr(),
-                      _rows(out, plan.q_width, torch.bfloat16, "out"), seqs, rows,
-                      QMM_IN_F32 if q.dtype is torch.float32 else QMM_IN_BF16)
-    st = _lib().qmm_qk_norm_rope(plan.handle, cache.ref, ctypes.byref(a), _stream_handle(stream))
+    _APPEND_ARGS.pack_into(
+        plan._args, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, tokens, plan.q_width, dtype, "q"),
+        _rows(k, tokens, plan.kv_width, dtype, "k"), _rows(v, tokens, plan.kv_width, dtype, "v"), _ptr(q_weight),
+        _ptr(k_weight), _ptr(rope), 0 if rope is None else rope.shape[0], lengths.data_ptr(), _ptr(positions),
+        page_table.data_ptr(), out.data_ptr(), _rows(out, tokens, plan.q_width, bf16, "out"), seqs, rows,
+        QMM_IN_F32 if dtype is f32 else QMM_IN_BF16)
+    st = _lib().qmm_qk_norm_rope(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan.device.index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_qk_norm_rope")
 
@@ -464,13 +490,12 @@ def attention(plan: KVPlan, q, cache: KVCache, page_table, lengths, out, stream=
     """Attention of the new tokens over the cache (qmm_attention): q and out [tokens, q_heads, head_dim] bfloat16 (or
     [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
     import torch
-    tokens = q.shape[0]
-    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
-    if out.shape[0] != tokens:
-        raise ValueError("out has q's rows")
-    st = _lib().qmm_attention(plan.handle, cache.ref, q.data_ptr(), _rows(q, plan.q_width, torch.bfloat16, "q"),
-                              page_table.data_ptr(), lengths.data_ptr(), seqs, rows, out.data_ptr(),
-                              _rows(out, plan.q_width, torch.bfloat16, "out"), _stream_handle(stream))
+    tokens, bf16 = q.shape[0], torch.bfloat16
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, torch.int32)
+    _ATTENTION_ARGS.pack_into(plan._args, 0, q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
+                              _rows(q, tokens, plan.q_width, bf16, "q"), _rows(out, tokens, plan.q_width, bf16, "out"),
+                              seqs, rows)
+    st = _lib().qmm_attention(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan.device.index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_attention")
 
@@ -480,18 +505,19 @@ def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stre
     numbers u (qmm_sample): tokens int32 [M], probs float32 [M] or None. temperature, top_p, min_p: float32 [M];
     top_k: int32 [M]."""
     import torch
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or logits.stride(1) != 1:
+    f32, i32, dtype = torch.float32, torch.int32, logits.dtype
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) != 2 or (dtype is not f32 and dtype is not torch.bfloat16) or strides[1] != 1:
         raise ValueError("logits are float32 or bfloat16 rows of adjacent elements")
-    M = logits.shape[0]
-    for t, dtype in ((temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32),
-                     (min_p, torch.float32), (u, torch.float32), (tokens, torch.int32)):
-        if t.dtype != dtype or t.numel() != M or not t.is_contiguous():
+    M = shape[0]
+    for t, want in ((temperature, f32), (top_k, i32), (top_p, f32), (min_p, f32), (u, f32), (tokens, i32)):
+        if t.dtype is not want or t.numel() != M or not t.is_contiguous():
             raise ValueError("temperature, top_p, min_p and u are float32 [M], top_k and tokens int32 [M]")
-    if probs is not None and (probs.dtype != torch.float32 or probs.numel() != M or not probs.is_contiguous()):
+    if probs is not None and (probs.dtype is not f32 or probs.numel() != M or not probs.is_contiguous()):
         raise ValueError("probs is float32 [M] or None")
-    st = _lib().qmm_sample(logits.data_ptr(), M, logits.shape[1], logits.stride(0),
-                           QMM_IN_F32 if logits.dtype is torch.float32 else QMM_IN_BF16, temperature.data_ptr(),
-                           top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), u.data_ptr(), tokens.data_ptr(),
-                           _ptr(probs), _stream_handle(stream))
+    st = _lib().qmm_sample(logits.data_ptr(), M, shape[1], strides[0], QMM_IN_F32 if dtype is f32 else QMM_IN_BF16,
+                           temperature.data_ptr(), top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), u.data_ptr(),
+                           tokens.data_ptr(), None if probs is None else probs.data_ptr(),
+                           _stream_on(stream, logits.get_device()))
     if st != QMM_OK:
         raise QmmError(st, "qmm_sample")

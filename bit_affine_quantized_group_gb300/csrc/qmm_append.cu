@@ -16,7 +16,11 @@ namespace qmmk {
 namespace {
 
 constexpr int kAppendWarps = 4;
-constexpr int kAppendSteps = 4;   // head vectors that a warp loads before it works on the first
+constexpr int64_t kManyWarps = 152 * 40;   // two rounds of the warps that run at once
+
+// Head vectors that a warp loads before it works on the last ones.
+template <bool F32>
+constexpr int kAppendSteps = F32 ? 2 : 4;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -28,47 +32,61 @@ __device__ __forceinline__ void unpack_bf16(uint32_t w, float& a, float& b) {
     b = __uint_as_float(w & 0xFFFF0000u);
 }
 
+// Eight elements as they lie in memory.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t elem, float (&x)[8]) {
-    if constexpr (F32) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-        const float4 a = s[0], b = s[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
-        unpack_bf16(a.x, x[0], x[1]);
-        unpack_bf16(a.y, x[2], x[3]);
-        unpack_bf16(a.z, x[4], x[5]);
-        unpack_bf16(a.w, x[6], x[7]);
+struct Raw {
+    uint4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* base, int64_t elem) {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + elem * (F32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = __ldg(s + i);
     }
-}
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        if constexpr (F32) {
+            x[0] = __uint_as_float(w[0].x), x[1] = __uint_as_float(w[0].y);
+            x[2] = __uint_as_float(w[0].z), x[3] = __uint_as_float(w[0].w);
+            x[4] = __uint_as_float(w[1].x), x[5] = __uint_as_float(w[1].y);
+            x[6] = __uint_as_float(w[1].z), x[7] = __uint_as_float(w[1].w);
+        } else {
+            unpack_bf16(w[0].x, x[0], x[1]);
+            unpack_bf16(w[0].y, x[2], x[3]);
+            unpack_bf16(w[0].z, x[4], x[5]);
+            unpack_bf16(w[0].w, x[6], x[7]);
+        }
+    }
+};
 
-// One warp takes kAppendSteps vectors of 32 / (D / 8) heads of one token.
+// One warp takes `span` heads of one token, kSteps vectors of 32 / (D / 8) heads at a time: position, page and rotation are
+// looked up once for all of them, and the next vectors are on their way while it works on the last.
 template <int D, bool F32>
-__global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __grid_constant__ AppendParams p, int span) {
     constexpr int kLanes = D / 8;
     constexpr int kHeads = 32 / kLanes;
-    constexpr int kPerWarp = kHeads * kAppendSteps;
+    constexpr int kSteps = kAppendSteps<F32>;
     const int lane = threadIdx.x & 31;
     const int heads = p.q_heads + 2 * p.kv_heads;
-    const int per_token = (heads + kPerWarp - 1) / kPerWarp;
+    const int per_token = (heads + span - 1) / span;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
     const int token = static_cast<int>(unit / per_token);
-    const int first = static_cast<int>(unit - static_cast<int64_t>(token) * per_token) * kPerWarp + lane / kLanes;
+    const int h0 = static_cast<int>(unit - static_cast<int64_t>(token) * per_token) * span;
+    const int h1 = h0 + span < heads ? h0 + span : heads;
     const int e = (lane % kLanes) * 8;   // this lane's elements of a head
     griddep_launch_dependents();
     griddep_wait();
     if (token >= p.tokens) return;
 
-    float x[kAppendSteps][8];
+    Raw<F32> next[kSteps];
+    auto load = [&](int h) {   // the vectors from head h on
 #pragma unroll
-    for (int i = 0; i < kAppendSteps; ++i) {
-        const int h = first + i * kHeads;
-        if (h >= heads) continue;
-        const int kind = h < p.q_heads ? 0 : h < p.q_heads + p.kv_heads ? 1 : 2;
-        const int hk = kind == 0 ? h : h - p.q_heads - (kind - 1) * p.kv_heads;
-        load8<F32>(p.in[kind], token * p.in_stride[kind] + static_cast<int64_t>(hk) * D + e, x[i]);
-    }
+        for (int i = 0; i < kSteps; ++i) {
+            const int hd = h + i * kHeads + lane / kLanes;
+            if (hd >= h1) continue;
+            const int kind = hd < p.q_heads ? 0 : hd < p.q_heads + p.kv_heads ? 1 : 2;
+            const int hk = kind == 0 ? hd : hd - p.q_heads - (kind - 1) * p.kv_heads;
+            next[i].load(p.in[kind], token * p.in_stride[kind] + static_cast<int64_t>(hk) * D + e);
+        }
+    };
+    load(h0);
 
     const int seq = token / p.rows;
     const int pos = p.lengths[seq] - p.rows + (token - seq * p.rows);
@@ -130,60 +148,71 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
     }
     const int other = !turns ? lane : e < half ? lane + half / 8 : lane - half / 8;
 
+#pragma unroll 1
+    for (int h = h0; h < h1; h += kSteps * kHeads) {
+        Raw<F32> now[kSteps];
 #pragma unroll
-    for (int i = 0; i < kAppendSteps; ++i) {
-        const int h = first + i * kHeads;
-        const bool in = h < heads;
-        const int kind = h < p.q_heads ? 0 : h < p.q_heads + p.kv_heads ? 1 : 2;
-        const int hk = kind == 0 ? h : h - p.q_heads - (kind - 1) * p.kv_heads;
-        float(&y)[8] = x[i];
-        if (!in) {
+        for (int i = 0; i < kSteps; ++i) now[i] = next[i];
+        load(h + kSteps * kHeads);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-        }
-        float sum = 0.0f;
+        for (int i = 0; i < kSteps; ++i) {
+            const int hd = h + i * kHeads + lane / kLanes;
+            const bool in = hd < h1;
+            const int kind = hd < p.q_heads ? 0 : hd < p.q_heads + p.kv_heads ? 1 : 2;
+            const int hk = kind == 0 ? hd : hd - p.q_heads - (kind - 1) * p.kv_heads;
+            float y[8];
+            now[i].values(y);
+            float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+            for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const float* weight = kind < 2 ? p.weight[kind] : nullptr;
-        if (weight != nullptr) {
-            const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
-            const float4 a = *reinterpret_cast<const float4*>(weight + e);
-            const float4 b = *reinterpret_cast<const float4*>(weight + e + 4);
-            y[0] *= inv * a.x, y[1] *= inv * a.y, y[2] *= inv * a.z, y[3] *= inv * a.w;
-            y[4] *= inv * b.x, y[5] *= inv * b.y, y[6] *= inv * b.z, y[7] *= inv * b.w;
-        }
-        if (rotate) {
-            float z[8];
-            if (p.interleaved) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = y[j ^ 1];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = __shfl_sync(0xFFFFFFFFu, y[j], other);
+            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            const float* weight = kind < 2 ? p.weight[kind] : nullptr;
+            if (weight != nullptr) {
+                const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
+                const float4 a = __ldg(reinterpret_cast<const float4*>(weight + e));
+                const float4 b = __ldg(reinterpret_cast<const float4*>(weight + e + 4));
+                y[0] *= inv * a.x, y[1] *= inv * a.y, y[2] *= inv * a.z, y[3] *= inv * a.w;
+                y[4] *= inv * b.x, y[5] *= inv * b.y, y[6] *= inv * b.z, y[7] *= inv * b.w;
             }
-            if (turns && kind < 2) {
+            if (rotate) {
+                float z[8];
+                if (p.interleaved) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = fmaf(y[j], c[j], z[j] * s[j]);
+                    for (int j = 0; j < 8; ++j) z[j] = y[j ^ 1];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] = __shfl_sync(0xFFFFFFFFu, y[j], other);
+                }
+                if (turns && kind < 2) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = fmaf(y[j], c[j], z[j] * s[j]);
+                }
             }
+            uint4 w = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+            uint16_t* dst = nullptr;
+            if (kind == 0) {
+                if (!live) w = make_uint4(0u, 0u, 0u, 0u);
+                dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(hk) * D + e;
+            } else if (store) {
+                dst = kind == 1 ? p.k.base + k_at + hk * p.k.head + e : p.v.base + v_at + hk * p.v.head + e;
+            }
+            if (in && dst != nullptr) *reinterpret_cast<uint4*>(dst) = w;
         }
-        uint4 w = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        uint16_t* dst = nullptr;
-        if (kind == 0) {
-            if (!live) w = make_uint4(0u, 0u, 0u, 0u);
-            dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(hk) * D + e;
-        } else if (store) {
-            dst = kind == 1 ? p.k.base + k_at + hk * p.k.head + e : p.v.base + v_at + hk * p.v.head + e;
-        }
-        if (in && dst != nullptr) *reinterpret_cast<uint4*>(dst) = w;
     }
 }
 
 template <int D, bool F32>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-    constexpr int kPerWarp = 32 / (D / 8) * kAppendSteps;
-    const int64_t per_token = (p.q_heads + 2 * p.kv_heads + kPerWarp - 1) / kPerWarp;
+    // few tokens: a warp for every load in flight; many: equal parts of a token, up to all of it
+    constexpr int kPerLoad = 32 / (D / 8) * kAppendSteps<F32>;
+    const int heads = p.q_heads + 2 * p.kv_heads;
+    const int64_t loads = (heads + kPerLoad - 1) / kPerLoad;
+    int64_t each = p.tokens * loads / kManyWarps;
+    each = each < 1 ? 1 : each > loads ? loads : each;
+    const int64_t parts = (loads + each - 1) / each;
+    const int span = static_cast<int>((loads + parts - 1) / parts) * kPerLoad;
+    const int64_t per_token = (heads + span - 1) / span;
     const int64_t blocks = (p.tokens * per_token + kAppendWarps - 1) / kAppendWarps;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -194,7 +223,7 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qmm_append_kernel<D, F32>, p);
+    return cudaLaunchKernelEx(&cfg, qmm_append_kernel<D, F32>, p, span);
 }
 
 }  // namespace

@@ -186,51 +186,48 @@ int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qm
                ? QMM_OK : QMM_ERR_CUDA;
 }
 
-int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const void* q, int64_t q_stride,
-                             const int32_t* page_table, const int32_t* lengths, int seqs, int rows, void* out,
-                             int64_t out_stride) {
-    if (d == nullptr) return QMM_ERR_INVALID_ARG;
+int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_attention_args* a) {
+    if (d == nullptr || a == nullptr) return QMM_ERR_INVALID_ARG;
     const int chk = check_cache(cache);
     if (chk != QMM_OK) return chk;
+    const int seqs = a->seqs, rows = a->rows;
     if (seqs < 0 || seqs > d->max_seqs || rows < 0 || rows > d->max_rows) return QMM_ERR_INVALID_ARG;
     const int64_t tokens = static_cast<int64_t>(seqs) * rows;
     if (tokens == 0) return QMM_OK;
     const int64_t row_tiles = (static_cast<int64_t>(rows) * (d->q_heads / d->kv_heads) + 15) / 16;
     if (static_cast<int64_t>(seqs) * d->kv_heads * row_tiles >= (1LL << 30)) return QMM_ERR_UNSUPPORTED;
     const int64_t dq = static_cast<int64_t>(d->q_heads) * d->head_dim;
-    if (!rows_ok(q, q_stride, dq, 2, tokens) || !rows_ok(out, out_stride, dq, 2, tokens)) return QMM_ERR_INVALID_ARG;
-    if (page_table == nullptr || !aligned(page_table, 4) || lengths == nullptr || !aligned(lengths, 4))
+    if (!rows_ok(a->q, a->q_stride, dq, 2, tokens) || !rows_ok(a->out, a->out_stride, dq, 2, tokens)) return QMM_ERR_INVALID_ARG;
+    if (a->page_table == nullptr || !aligned(a->page_table, 4) || a->lengths == nullptr || !aligned(a->lengths, 4))
         return QMM_ERR_INVALID_ARG;
     return QMM_OK;
 }
 
-int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const void* q, int64_t q_stride,
-                  const int32_t* page_table, const int32_t* lengths, int seqs, int rows, void* out,
-                  int64_t out_stride, void* stream) {
+int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_attention_args* a, void* stream) {
     if (p == nullptr) return QMM_ERR_INVALID_ARG;
-    const int chk = qmm_check_attention_args(&p->d, cache, q, q_stride, page_table, lengths, seqs, rows, out, out_stride);
+    const int chk = qmm_check_attention_args(&p->d, cache, a);
     if (chk != QMM_OK) return chk;
-    if (seqs == 0 || rows == 0) return QMM_OK;
+    if (a->seqs == 0 || a->rows == 0) return QMM_OK;
     const qmm_kv_desc& d = p->d;
     const int group = d.q_heads / d.kv_heads;
     const AttnWorkspace w = attn_workspace(d.head_dim, d.max_rows * group);
     AttnParams ap;
     ap.k = side(cache->k, cache->k_page_stride, cache->k_head_stride, cache->k_slot_stride);
     ap.v = side(cache->v, cache->v_page_stride, cache->v_head_stride, cache->v_slot_stride);
-    ap.q = static_cast<const uint16_t*>(q);
-    ap.out = static_cast<uint16_t*>(out);
-    ap.page_table = page_table;
-    ap.lengths = lengths;
+    ap.q = static_cast<const uint16_t*>(a->q);
+    ap.out = static_cast<uint16_t*>(a->out);
+    ap.page_table = a->page_table;
+    ap.lengths = a->lengths;
     ap.err = reinterpret_cast<uint32_t*>(p->ws);
     ap.counters = reinterpret_cast<uint32_t*>(p->ws + w.counters);
     ap.joins = reinterpret_cast<int4*>(p->ws + w.joins);
     ap.part = reinterpret_cast<float*>(p->ws + w.part);
     ap.part_ml = reinterpret_cast<float*>(p->ws + w.part_ml);
-    ap.q_stride = q_stride;
-    ap.out_stride = out_stride;
+    ap.q_stride = a->q_stride;
+    ap.out_stride = a->out_stride;
     ap.num_pages = cache->num_pages;
-    ap.seqs = seqs;
-    ap.rows = rows;
+    ap.seqs = a->seqs;
+    ap.rows = a->rows;
     ap.group = group;
     ap.kv_heads = d.kv_heads;
     ap.group_inverse = ((1 << 20) + group - 1) / group;

@@ -377,12 +377,22 @@ typedef struct qmm_append_args {
 int qmm_check_qk_norm_rope_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_append_args* a);
 int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_append_args* a, void* stream);
 
+/* What qmm_attention reads and writes. All pointers are device pointers. */
+typedef struct qmm_attention_args {
+    const void* q;             /* [seqs*rows, q_heads*head_dim] bfloat16, 16-byte aligned rows */
+    void* out;                 /* as q */
+    const int32_t* lengths;    /* [seqs] */
+    const int32_t* page_table; /* [seqs, max_pages] */
+    int64_t q_stride, out_stride;   /* elements from row to row (multiples of 16 bytes) */
+    int32_t seqs;              /* <= max_seqs */
+    int32_t rows;              /* <= max_rows */
+} qmm_attention_args;
+
 /*
  * out[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j over the positions j
  * that token t sees: j <= pos, and with a window pos - j < window or j < sinks.
- * Query head h reads cache head h / (q_heads / kv_heads). q and out are
- * [seqs*rows, q_heads*head_dim] bfloat16 with 16-byte aligned rows. The scores,
- * the softmax's maximum and sum and the output are held in float32. A row that
+ * Query head h reads cache head h / (q_heads / kv_heads). The scores, the
+ * softmax's maximum and sum and the output are held in float32. A row that
  * sees nothing gives zeros, and no value at a position that a row does not see
  * reaches that row, infinities and NaN among them.
  *
@@ -391,12 +401,8 @@ int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qm
  * the same lengths gives the same bits. The cut depends on all lengths of the
  * call: the same sequence in another batch may differ by rounding.
  */
-int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const void* q, int64_t q_stride,
-                             const int32_t* page_table, const int32_t* lengths, int seqs, int rows, void* out,
-                             int64_t out_stride);
-int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const void* q, int64_t q_stride,
-                  const int32_t* page_table, const int32_t* lengths, int seqs, int rows, void* out,
-                  int64_t out_stride, void* stream);
+int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_attention_args* a);
+int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_attention_args* a, void* stream);
 
 /* Largest vocabulary of qmm_sample. */
 #define QMM_SAMPLE_MAX_VOCAB 393216

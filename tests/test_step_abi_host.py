@@ -40,7 +40,7 @@ def test_null_handles(q):
     assert lib.qmm_kv_plan(None, None, None, 0) == q.QMM_ERR_INVALID_ARG
     assert lib.qmm_kv_error(None, None) == q.QMM_ERR_INVALID_ARG
     assert lib.qmm_qk_norm_rope(None, None, None, None) == q.QMM_ERR_INVALID_ARG
-    assert lib.qmm_attention(None, None, None, 0, None, None, 1, 1, None, 0, None) == q.QMM_ERR_INVALID_ARG
+    assert lib.qmm_attention(None, None, None, None) == q.QMM_ERR_INVALID_ARG
     lib.qmm_kv_destroy(None)   # accepted
     out = ctypes.c_void_p(1)
     bad = q.make_kv_desc(**{**GOOD, "head_dim": 96})
@@ -67,26 +67,27 @@ CACHE_FAULTS = [{"k": 0}, {"v": 0}, {"k": 0x100008}, {"v": 0x200002}, {"num_page
 @pytest.mark.parametrize("kw,expect", [
     ({}, 0), ({"seqs": 0, "q": 0, "out": 0}, 0), ({"rows": 0, "q": 0}, 0), ({"rows": 8}, 0),
     ({"rows": 9}, 1), ({"rows": -1}, 1), ({"seqs": 5}, 1), ({"seqs": -1}, 1), ({"q": 0}, 1), ({"q": 0x3008}, 1),
-    ({"out": 0}, 1), ({"out": 0x4002}, 1), ({"table": 0}, 1), ({"table": 0x5002}, 1), ({"lengths": 0}, 1),
+    ({"out": 0}, 1), ({"out": 0x4002}, 1), ({"page_table": 0}, 1), ({"page_table": 0x5002}, 1), ({"lengths": 0}, 1),
     ({"q_stride": 4095}, 1), ({"q_stride": 4104}, 0), ({"q_stride": 4100}, 1), ({"out_stride": 4088}, 1),
     ({"seqs": 1, "rows": 1, "q_stride": 0}, 0),
 ])
 def test_attention_args(q, kw, expect):
-    a = dict(q=0x3000, q_stride=4096, table=0x5000, lengths=0x6000, seqs=2, rows=1, out=0x4000, out_stride=4096)
+    a = dict(q=0x3000, q_stride=4096, page_table=0x5000, lengths=0x6000, seqs=2, rows=1, out=0x4000, out_stride=4096)
     a.update(kw)
-    d, c = q.make_kv_desc(**GOOD), _cache(q)
-    st = q.lib.qmm_check_attention_args(ctypes.byref(d), ctypes.byref(c), a["q"], a["q_stride"], a["table"], a["lengths"],
-                                        a["seqs"], a["rows"], a["out"], a["out_stride"])
-    assert st == expect
+    d, c, args = q.make_kv_desc(**GOOD), _cache(q), q.QmmAttentionArgs(**a)
+    assert q.lib.qmm_check_attention_args(ctypes.byref(d), ctypes.byref(c), ctypes.byref(args)) == expect
 
 
 @pytest.mark.parametrize("fault", CACHE_FAULTS)
 def test_cache_faults(q, fault):
     d, c = q.make_kv_desc(**GOOD), _cache(q, **fault)
-    args = (ctypes.byref(d), ctypes.byref(c), 0x3000, 4096, 0x5000, 0x6000, 2, 1, 0x4000, 4096)
+    a = q.QmmAttentionArgs(q=0x3000, q_stride=4096, page_table=0x5000, lengths=0x6000, seqs=2, rows=1, out=0x4000,
+                           out_stride=4096)
+    args = (ctypes.byref(d), ctypes.byref(c), ctypes.byref(a))
     assert q.lib.qmm_check_attention_args(*args) == q.QMM_ERR_INVALID_ARG
     assert q.lib.qmm_check_attention_args(None, *args[1:]) == q.QMM_ERR_INVALID_ARG
-    assert q.lib.qmm_check_attention_args(args[0], None, *args[2:]) == q.QMM_ERR_INVALID_ARG
+    assert q.lib.qmm_check_attention_args(args[0], None, args[2]) == q.QMM_ERR_INVALID_ARG
+    assert q.lib.qmm_check_attention_args(*args[:2], None) == q.QMM_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("kw,expect", [
