@@ -15,12 +15,11 @@
 //   - top_k: the largest logit of every thread is counted in a histogram. The
 //     bin where the count reaches k bounds the k largest of all from below, and
 //     little more than k logits lie above it.
-//   - top_p alone: w_i > (1 - p) * (sum of w) / vocabulary for every kept token
-//     (what ranks from it on has mass above 1 - p, in at most `vocabulary`
-//     parts of at most w_i), so only those enter a histogram of mass.
-// The first CTA sorts these candidates and draws among them. Rows where a
-// threshold leaves too many candidates (flat ones, many equal logits) are
-// resolved bin by bin, then bit by bit, then by index.
+//   - top_p alone: a histogram of the masses by the leading bits of the weights,
+//     and one by the next bits inside the bin that the threshold lies in.
+// The first CTA ranks these candidates and draws among them, or tells the others
+// the threshold. Rows where too many candidates are left (flat ones, many equal
+// logits) are resolved bin by bin, then bit by bit, then by index.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -189,6 +188,20 @@ __device__ __forceinline__ u64 block_before(u64 v, u64* scratch, u64& all) {
     }
     all = __shfl_sync(0xFFFFFFFFu, w, 15);
     return upto - v + __shfl_sync(0xFFFFFFFFu, w - mine, warp);
+}
+
+// f(i, x[i]) for i = from, from + step, ... below end, four values read at a time.
+template <class F>
+__device__ __forceinline__ void for_each(const float* x, int from, int end, int step, F f) {
+    for (int i = from; i < end; i += 4 * step) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * step < end) v[j] = x[i + j * step];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * step < end) f(i + j * step, v[j]);
+    }
 }
 
 // 64-bit sums of two 32-bit atomics each: a 64-bit one in shared memory is a loop of compare-and-swaps (37 a thread of
@@ -815,7 +828,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         if (largest) {
             if (best > -INFINITY) atomicAdd(&sh.count[bin_of(best)], 1u);
         } else {
-            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) atomicAdd(&sh.count[bin_of(slots[i])], 1u);
+            for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int, float l) { atomicAdd(&sh.count[bin_of(l)], 1u); });
         }
         const Decision d = s.join_bins(false, static_cast<u64>(top_k), 0, 0, 0.0f, false);
         if (d.members != 0xFFFFFFFFu && d.bin < kBins - 1) {
@@ -834,62 +847,57 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         }
     }
 
-    // weights in the logits' place, segment by segment of a warp, and their masses
+    // Weights in the logits' place, and a histogram of their masses or their sums by warps, which have segments of the row.
     const int seg = ((s.hi - s.lo + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;
     const int s0 = s.lo + warp * seg, s1 = s0 + seg < s.hi ? s0 + seg : s.hi;
-    bool general = by_count;   // thresholds by logit and index, the logits still in their place
+    bool general = by_count;     // thresholds by logit and index, the logits still in their place
     u64 own = 0;
-    if (!general) {
-        __syncthreads();
-        for (int i = s0 + lane; i < s1; i += 32) {
-            const float w = s.weight(slots[i]);
-            const u64 m = s.mass(w);
-            slots[i] = m != 0 ? w : 0.0f;
-            if (by_mass || !(w < min_p)) own += m;
-        }
-    }
     uint32_t edge = 0;           // weights of this many bits or more lie in bins before the threshold's
     uint32_t edge_end = 0;       // and below this in bins after it
-    if (!general && by_mass) {
-        u64 all;
-        (void)block_before(own, sh.warp_mass, all);
-        if (tid < ranks) cluster.map_shared_rank(&sh, tid)->sum[rank] = all;
-        cluster.sync();
-        u64 total = 0;
-        for (int r = 0; r < ranks; ++r) total += sh.sum[r];
-        // no kept token weighs less (a little off for the roundings of this line)
-        const float least = 0.999f * (1.0f - top_p) * static_cast<float>(total) / kWeightOne / static_cast<float>(p.vocab);
-        s.clear_list();
-        s.clear_bins();
-        auto bin_of = [](float w) -> uint32_t {
-            return min((0x3F800000u - __float_as_uint(w)) >> kWeightBinShift, static_cast<uint32_t>(kBins - 1));
-        };
-        for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) {
-            const float w = slots[i];
-            if (w >= least && w > 0.0f) {
-                atomicAdd(&sh.count[bin_of(w)], 1u);
-                add_mass(&sh.mass[bin_of(w)], s.mass(w));
+    auto bits_below = [](float w) -> uint32_t { return 0x3F800000u - __float_as_uint(w); };
+    auto bin_of = [&](float w) -> uint32_t { return min(bits_below(w) >> kWeightBinShift, static_cast<uint32_t>(kBins - 1)); };
+    if (!general) {
+        __syncthreads();
+        // four logits at a time, so that the chains of their exponentials overlap
+        for (int i0 = s0 + lane; i0 < s1; i0 += 4 * 32) {
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = i0 + j * 32 < s1 ? slots[i0 + j * 32] : -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = s.weight(w[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (i0 + j * 32 >= s1) continue;
+                const u64 m = s.mass(w[j]);
+                slots[i0 + j * 32] = m != 0 ? w[j] : 0.0f;
+                if (m == 0) continue;
+                if (by_mass) {
+                    atomicAdd(&sh.count[bin_of(w[j])], 1u);
+                    add_mass(&sh.mass[bin_of(w[j])], m);
+                } else if (!(w[j] < min_p)) {
+                    own += m;
+                }
             }
         }
-        const u64 limit = s.by_one([&] { return s.mass_limit(top_p, total); });
-        Decision d = s.join_bins(true, limit, 0, 0, 0.0f);
+    }
+    if (!general && by_mass) {
+        Decision d = s.join_bins(true, 0, 0, 0, top_p);
+        const u64 total = d.total, limit = s.by_one([&] { return s.mass_limit(top_p, total); });
         general = d.members == 0xFFFFFFFFu || d.bin == kBins - 1;
         const bool whole = !general && d.count + d.members <= kCounted;   // few in all: the draw is the first CTA's
         const uint32_t bin = d.bin;
-        auto bits_below = [](float w) -> uint32_t { return 0x3F800000u - __float_as_uint(w); };
         uint32_t sub = 0xFFFFFFFFu;                                       // part of the bin
         constexpr int kSubShift = kWeightBinShift - 8;
         if (!general && !whole && d.members > kCounted) {
             // the next bits part the bin's members
             cluster.sync();
             s.clear_bins();
-            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) {
-                const float w = slots[i];
-                if (!(w > 0.0f) || bin_of(w) != bin) continue;
+            for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int, float w) {
+                if (!(w > 0.0f) || bin_of(w) != bin) return;
                 const uint32_t b = bits_below(w) >> kSubShift & (kBins - 1);
                 atomicAdd(&sh.count[b], 1u);
                 add_mass(&sh.mass[b], s.mass(w));
-            }
+            });
             d = s.join_bins(true, limit, d.count, d.mass, 0.0f);
             sub = d.bin;
             general = d.members == 0xFFFFFFFFu || d.members > kList;
@@ -900,8 +908,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
                 if (whole) return bin_of(w) <= bin;
                 return bin_of(w) == bin && (sub == 0xFFFFFFFFu || (bits_below(w) >> kSubShift & (kBins - 1)) == sub);
             };
-            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads)
-                if (member(slots[i])) s.add(key_of(s.logit_at(s.index(i))), s.index(i));
+            for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int i, float w) {
+                if (member(w)) s.add(key_of(s.logit_at(s.index(i))), s.index(i));
+            });
             const int n = s.collect();
             if (n > kList) {
                 general = true;
@@ -927,25 +936,23 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
 
     // the draw: kept masses in the order of the indices
-    auto kept = [&](int i) -> u64 {
+    auto kept = [&](int i, float v) -> u64 {
         if (general) {
-            const float l = slots[i];
-            if (!s.under(key_of(l), s.index(i))) return 0;
-            const float w = s.weight(l);
+            if (!s.under(key_of(v), s.index(i))) return 0;
+            const float w = s.weight(v);
             return w < min_p ? 0 : s.mass(w);
         }
-        const float w = slots[i];
-        if (w < min_p) return 0;
+        if (v < min_p) return 0;
         if (by_mass) {
-            const uint32_t bits = __float_as_uint(w);
+            const uint32_t bits = __float_as_uint(v);
             if (bits < edge_end) return 0;
             if (bits < edge && !s.under(key_of(s.logit_at(s.index(i))), s.index(i))) return 0;
         }
-        return s.mass(w);
+        return s.mass(v);
     };
     if (general || by_mass) {
         own = 0;
-        for (int i = s0 + lane; i < s1; i += 32) own += kept(i);
+        for_each(slots, s0 + lane, s1, 32, [&](int i, float v) { own += kept(i, v); });
     }
     own = warp_add(own);
     __syncthreads();
@@ -967,7 +974,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     if (target < before || target >= before + own) return;
     for (int i0 = s0; i0 < s1; i0 += 32) {
         const int i = i0 + lane;
-        const u64 m = i < s1 ? kept(i) : 0;
+        const u64 m = i < s1 ? kept(i, slots[i]) : 0;
         const u64 upto = before + warp_scan(m, lane);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > target);
         if (past != 0) {
