@@ -65,6 +65,7 @@ struct SampleParams {
 struct Decision {
     u64 mass;        // mass ranked before the bin
     u64 total;       // mass of everything that takes part
+    u64 limit;       // what the mass before a kept element is below
     uint32_t count;  // elements ranked before the bin
     uint32_t bin;
     uint32_t members;
@@ -83,6 +84,7 @@ struct SampleShared {
     alignas(16) uint32_t count[kBins];
     uint32_t warp_count[kSampleWarps];
     u64 list[kList];
+    uint16_t own[kList];   // slots of this CTA's candidates
     u64 scalar;
     uint32_t list_size, sizes[kRanks];
     Decision decision;
@@ -90,7 +92,7 @@ struct SampleShared {
 };
 
 // Unsigned numbers in the order of the floats; NaN is -infinity, and -0 is 0.
-__device__ __forceinline__ float clean(float l) { return l != l ? -INFINITY : l + 0.0f; }
+__device__ __forceinline__ float clean(float l) { return fmaxf(l, -INFINITY) + 0.0f; }
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t b = __float_as_uint(l);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -172,18 +174,19 @@ __device__ __forceinline__ void sort_falling(u64* v) {
 }
 
 // Sum of v over the threads before this one; `all`: over all. scratch: kSampleWarps numbers.
-__device__ __forceinline__ u64 block_before(u64 v, u64* scratch, u64& all) {
+template <class N>
+__device__ __forceinline__ N block_before(N v, N* scratch, N& all) {
     static_assert(kSampleWarps == 16, "half a warp scans the warps");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u64 upto = warp_scan(v, lane);
+    const N upto = warp_scan(v, lane);
     __syncthreads();
     if (lane == 31) scratch[warp] = upto;
     __syncthreads();
-    const u64 mine = scratch[lane & 15];
-    u64 w = mine;
+    const N mine = scratch[lane & 15];
+    N w = mine;
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) {
-        const u64 a = __shfl_up_sync(0xFFFFFFFFu, w, o, 16);
+        const N a = __shfl_up_sync(0xFFFFFFFFu, w, o, 16);
         if ((lane & 15) >= o) w += a;
     }
     all = __shfl_sync(0xFFFFFFFFu, w, 15);
@@ -272,15 +275,9 @@ struct RowSampler {
         __syncthreads();
         if (threadIdx.x < ranks) cluster.map_shared_rank(&sh, threadIdx.x)->sizes[rank] = sh.list_size;
         cluster.sync();
-        const uint32_t room = kList / ranks;
-        uint32_t n = 0;
-        bool fits = true;
-#pragma unroll
-        for (int r = 0; r < kRanks; ++r) {
-            const uint32_t size = r < ranks ? sh.sizes[r] : 0u;
-            n += size;
-            fits &= size <= room;
-        }
+        const uint32_t room = kList / ranks, lane = threadIdx.x & 31;
+        const uint32_t size = lane < ranks ? sh.sizes[lane] : 0u, n = __reduce_add_sync(0xFFFFFFFFu, size);
+        const bool fits = __all_sync(0xFFFFFFFFu, size <= room);
         if (!fits) return kList + 1;
         if (rank == 0 && ranks > 1) {   // close the gaps
             u64 e[kList / kSampleThreads];
@@ -478,30 +475,39 @@ struct RowSampler {
         cluster.sync();
         const int b = threadIdx.x;   // a bin for each of the first threads
         uint32_t c = 0;
-        u64 m = 0, all_c, all_m = 0, m0 = 0;
+        uint32_t all_c;
+        u64 m = 0, all_m = 0, m0 = 0;
         if (b < kBins) {
-            uint32_t rc[kRanks];   // all loads in flight at once
 #pragma unroll
-            for (int r = 0; r < kRanks; ++r) rc[r] = r < ranks ? cluster.map_shared_rank(&sh, r)->count[b] : 0u;
+            for (int h = 0; h < kRanks; h += 8) {
+                if (h >= ranks) break;
+                uint32_t rc[8];   // eight loads in flight at once
 #pragma unroll
-            for (int r = 0; r < kRanks; ++r) c += rc[r];
+                for (int r = 0; r < 8; ++r) rc[r] = h + r < ranks ? cluster.map_shared_rank(&sh, h + r)->count[b] : 0u;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) c += rc[r];
+            }
         }
         if (with_mass) {
             if (b < kBins) {
-                u64 rm[kRanks];
 #pragma unroll
-                for (int r = 0; r < kRanks; ++r) rm[r] = r < ranks ? cluster.map_shared_rank(&sh, r)->mass[b] : 0ull;
+                for (int h = 0; h < kRanks; h += 8) {
+                    if (h >= ranks) break;
+                    u64 rm[8];
 #pragma unroll
-                for (int r = 0; r < kRanks; ++r) m += rm[r];
+                    for (int r = 0; r < 8; ++r) rm[r] = h + r < ranks ? cluster.map_shared_rank(&sh, h + r)->mass[b] : 0ull;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) m += rm[r];
+                }
             }
             m0 = mass_before + block_before(m, sh.warp_mass, all_m);
             if (top_p_of_total > 0.0f) limit = by_one([&] { return mass_limit(top_p_of_total, all_m); });
         }
-        const u64 c0 = count_before + block_before(c, sh.warp_mass, all_c);
+        const u64 c0 = count_before + block_before(c, sh.warp_count, all_c);
         if (threadIdx.x == 0) sh.decision.members = 0xFFFFFFFFu;   // none: everything lies above the threshold
         __syncthreads();
         const bool here = by_mass ? c != 0 && m0 < limit && m0 + m >= limit : c0 < limit && c0 + c >= limit;
-        if (b < kBins && here) sh.decision = Decision{m0, all_m, static_cast<uint32_t>(c0), static_cast<uint32_t>(b), c};
+        if (b < kBins && here) sh.decision = Decision{m0, all_m, limit, static_cast<uint32_t>(c0), static_cast<uint32_t>(b), c};
         __syncthreads();
         return sh.decision;
     }
@@ -568,7 +574,7 @@ struct RowSampler {
     __device__ void select(bool by_mass, u64 limit, float top_p) {
         cg::cluster_group cluster = cg::this_cluster();
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        Decision d{0, 0, 0, 0, 0};
+        Decision d{0, 0, 0, 0, 0, 0};
         bin0 = bin1 = prefix = 0;
         int level = 0;
         for (;;) {
@@ -586,7 +592,7 @@ struct RowSampler {
                 if (m != 0) add_mass(&sh.mass[b], m);
             }
             d = join_bins(by_mass, limit, d.count, d.mass, level == 0 ? top_p : 0.0f);
-            if (level == 0 && by_mass) limit = by_one([&] { return mass_limit(top_p, d.total); });
+            if (level == 0 && by_mass) limit = d.limit;
             if (level == 0) bin0 = d.bin;
             if (level == 1) bin1 = d.bin;
             if (level >= 2) {
@@ -778,14 +784,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
     s.clear_list();
     cluster.sync();
-    float level = 0.0f, above = 0.0f;
-    s.top = sh.top[0];
-#pragma unroll
-    for (int r = 0; r < kRanks; ++r) {
-        if (r >= ranks) continue;
-        s.top = fmaxf(s.top, sh.top[r]);
-        level += sh.level[r];
-        above += sh.above[r];
+    float level, above;
+    {
+        const bool in = lane < ranks;
+        s.top = value_of(__reduce_max_sync(0xFFFFFFFFu, in ? key_of(sh.top[lane]) : 0u));
+        level = warp_add(in ? sh.level[lane] : 0.0f);
+        above = warp_add(in ? sh.above[lane] : 0.0f);
     }
     s.thr = Threshold{0u, 0xFFFFFFFFu};
     if (s.top == -INFINITY) {
@@ -852,8 +856,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     const int s0 = s.lo + warp * seg, s1 = s0 + seg < s.hi ? s0 + seg : s.hi;
     bool general = by_count;     // thresholds by logit and index, the logits still in their place
     u64 own = 0;
-    uint32_t edge = 0;           // weights of this many bits or more lie in bins before the threshold's
-    uint32_t edge_end = 0;       // and below this in bins after it
+    uint32_t edge = 0;           // weights of fewer bits lie in bins after the threshold's
     auto bits_below = [](float w) -> uint32_t { return 0x3F800000u - __float_as_uint(w); };
     auto bin_of = [&](float w) -> uint32_t { return min(bits_below(w) >> kWeightBinShift, static_cast<uint32_t>(kBins - 1)); };
     if (!general) {
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
     if (!general && by_mass) {
         Decision d = s.join_bins(true, 0, 0, 0, top_p);
-        const u64 total = d.total, limit = s.by_one([&] { return s.mass_limit(top_p, total); });
+        const u64 total = d.total, limit = d.limit;
         general = d.members == 0xFFFFFFFFu || d.bin == kBins - 1;
         const bool whole = !general && d.count + d.members <= kCounted;   // few in all: the draw is the first CTA's
         const uint32_t bin = d.bin;
@@ -908,9 +911,18 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
                 if (whole) return bin_of(w) <= bin;
                 return bin_of(w) == bin && (sub == 0xFFFFFFFFu || (bits_below(w) >> kSubShift & (kBins - 1)) == sub);
             };
+            // their slots first: the logits come from memory again, all at once
             for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int i, float w) {
-                if (member(w)) s.add(key_of(s.logit_at(s.index(i))), s.index(i));
+                if (!member(w)) return;
+                const uint32_t at = atomicAdd(&sh.list_size, 1u);
+                if (at < kList) sh.own[at] = static_cast<uint16_t>(i);
             });
+            __syncthreads();
+            const int mine = static_cast<int>(min(sh.list_size, static_cast<uint32_t>(kList / ranks)));
+            for (int k = tid; k < mine; k += kSampleThreads) {
+                const uint32_t index = s.index(sh.own[k]);
+                cluster.map_shared_rank(&sh, 0)->list[rank * (kList / ranks) + k] = entry_of(key_of(s.logit_at(index)), index);
+            }
             const int n = s.collect();
             if (n > kList) {
                 general = true;
@@ -919,9 +931,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
                 return;
             } else {
                 s.threshold_of_list(n, true, limit, d);
-                const uint32_t from = sub == 0xFFFFFFFFu ? bin << kWeightBinShift : bin << kWeightBinShift | sub << kSubShift;
-                edge = 0x3F800000u - from + 1;
-                edge_end = edge - (sub == 0xFFFFFFFFu ? 1u << kWeightBinShift : 1u << kSubShift);
+                // members past the threshold lose their weight
+                for (int k = tid; k < mine; k += kSampleThreads) {
+                    const uint32_t index = s.index(sh.own[k]);
+                    if (!s.under(key_of(s.logit_at(index)), index)) slots[sh.own[k]] = 0.0f;
+                }
+                __syncthreads();
+                const uint32_t end = sub == 0xFFFFFFFFu ? (bin + 1) << kWeightBinShift : (bin << kWeightBinShift) + ((sub + 1) << kSubShift);
+                edge = 0x3F800000u - end + 1;
             }
         }
         if (general) {   // the logits again
@@ -943,12 +960,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
             return w < min_p ? 0 : s.mass(w);
         }
         if (v < min_p) return 0;
-        if (by_mass) {
-            const uint32_t bits = __float_as_uint(v);
-            if (bits < edge_end) return 0;
-            if (bits < edge && !s.under(key_of(s.logit_at(s.index(i))), s.index(i))) return 0;
-        }
-        return s.mass(v);
+        return __float_as_uint(v) < edge ? 0 : s.mass(v);
     };
     if (general || by_mass) {
         own = 0;
@@ -972,15 +984,26 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
     const u64 target = s.by_one([&] { return s.target_of(p.u[row], total); });
     if (target < before || target >= before + own) return;
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-        const int i = i0 + lane;
-        const u64 m = i < s1 ? kept(i, slots[i]) : 0;
-        const u64 upto = before + warp_scan(m, lane);
+    for (int i0 = s0; i0 < s1; i0 += 4 * 32) {
+        u64 m[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 4 * lane + j;
+            m[j] = i < s1 ? kept(i, slots[i]) : 0;
+            sum += m[j];
+        }
+        u64 upto = before + warp_scan(sum, lane);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > target);
         if (past != 0) {
             if (lane == __ffs(past) - 1) {
-                p.tokens[row] = static_cast<int32_t>(s.index(i));
-                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(m), static_cast<float>(total));
+                upto -= sum;
+                int j = 0;
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (j == k && upto + m[k] <= target) upto += m[k], ++j;
+                const u64 own_mass = j == 0 ? m[0] : j == 1 ? m[1] : j == 2 ? m[2] : m[3];
+                p.tokens[row] = static_cast<int32_t>(s.index(i0 + 4 * lane + j));
+                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(own_mass), static_cast<float>(total));
             }
             return;
         }
@@ -1003,7 +1026,7 @@ int launch(const SampleParams& p, int M, cudaStream_t stream) {
             return QMM_ERR_CUDA;
         if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    int ranks = M <= 16 ? kRanks : kPortableRanks;             // few rows leave SMs for more CTAs each
+    int ranks = M <= 8 ? kRanks : kPortableRanks;             // few rows leave SMs for more CTAs each
     while (ranks > 1 && p.vocab / ranks < 2048) ranks /= 2;   // shorter shares cost more exchange than they save
     const int vec = 16 / static_cast<int>(sizeof(T));
     const int chunks = (p.vocab + vec - 1) / vec + 1;         // one more where the row starts inside a chunk
