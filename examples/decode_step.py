@@ -54,7 +54,7 @@ def rms_norm(x):
 
 
 class Decoder:
-    def __init__(self, sequences=8, layers=2, hidden=2048, q_heads=16, kv_heads=4, head_dim=128, ffn=4096, vocab=32000,
+    def __init__(self, sequences=8, layers=2, hidden=2048, q_heads=16, kv_heads=8, head_dim=128, ffn=4096, vocab=32000,
                  max_len=512, page=16, window=0, sinks=0, seed=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         S, D = sequences, head_dim
