@@ -31,8 +31,6 @@ namespace qmmk {
 namespace {
 
 constexpr int kStep = 64;       // positions of a step
-constexpr int kCoarse = 8;      // steps that a CTA takes at once where that leaves none without a CTA: about as long as
-                                // joining parts takes
 constexpr int kJoin = 40;       // parts of a head that one CTA joins at once
 constexpr int kJoinRun = 16;    // more of them: runs of this many first
 constexpr int kJoinWarps = 8;   // of a CTA of the join kernel
@@ -50,6 +48,7 @@ struct AttnCfg {
     static constexpr int kParts = kTeamWarps / RW;                 // parts of a step's positions
     static constexpr int kTiles = 4 / kParts;                      // 16-position tiles of a part
     static constexpr int kGroups = kTeams * kParts;                // sets of positions of a row
+    static constexpr bool kScaled = kGroups == 8;                  // groups join outputs of a common scale
     static constexpr int kThreads = 32 * (kCompute + 4);           // and a group of four that starts the copies
     // registers a thread: at launch, and then of the computing and the copying group, out of the same sum
     static constexpr int kLaunchRegs = D == 256 ? 168 : 128;
@@ -57,6 +56,8 @@ struct AttnCfg {
     static constexpr int kCopyRegs = 72;
     static_assert(kCompute * kComputeRegs + 4 * kCopyRegs <= (kCompute + 4) * kLaunchRegs, "registers of a CTA");
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+    // steps of the shortest share: about as long as joining parts takes, and work for every team
+    static constexpr int kShortShare = RW == 1 && D < 256 ? 4 : RW == 4 ? kTeams : 2;
     static constexpr int kSideBytes = kStep * D * 2;               // the keys or the values of a step
     // Every team has a ring of its own: in a common one, a team that only steps over the other's sides could take a
     // barrier's phase for one two rounds away.
@@ -71,7 +72,8 @@ struct AttnCfg {
     static constexpr int kJoinAt = kTeams * kRingBytes;
     static constexpr int kQueryAt = kJoinAt + kJoinBytes;
     static constexpr int kMlAt = kQueryAt + (kQueryRegs ? 0 : RW * kQueryBytes);
-    static constexpr int kBarsAt = kMlAt + kGroups * 16 * RW * 8;
+    static constexpr int kSumAt = kMlAt + kGroups * 16 * RW * 8;
+    static constexpr int kBarsAt = kSumAt + (kScaled ? 16 * RW * 8 : 0);
     static constexpr int kLastAt = kBarsAt + 2 * kTeams * kSides * 8;
     static constexpr int kSmem = kLastAt + 16;
     static_assert((kJoin + 2) * 16 * 4 <= kJoinBytes, "the weights of a join fit its buffer");
@@ -205,21 +207,42 @@ struct Share {
     int ctas, unit, items, seq, lane_len;
 
     // Whole warps. False: nothing for this CTA.
-    __device__ __forceinline__ bool init(const AttnParams& p, int lane) {
-        // units are steps (or p.min_unit of them), or kCoarse of them where that leaves a CTA for every unit
+    __device__ __forceinline__ bool init(const AttnParams& p, int short_share, int lane) {
+        const int most = gridDim.x;
         items = p.kv_heads * p.row_groups;
         lane_len = length_of(p, lane);
-        int fine = 0, coarse = 0;
-        for (int s = lane; s < p.seqs; s += 32) {
-            const SeqSpan span = span_of(p, s < 32 ? lane_len : length_of(p, s));
-            fine += span.units(p.min_unit);
-            coarse += span.units(kCoarse * p.min_unit);
+        // Units of one step (p.min_unit steps). Where items are few, units of so many more that every CTA has one unit at
+        // most, for a second item costs a CTA several steps: n of them if that makes the longest share at most 2/5 longer.
+        // Shares of fewer steps than short_share are not worth the joining of more parts, nor two such shares that of two.
+        int n = 1, low = 0, high = 0;   // units of `low` are too many
+        for (;;) {
+            int sum = 0, longest = 0;
+            for (int s = lane; s < p.seqs; s += 32) {
+                const SeqSpan span = span_of(p, s < 32 ? lane_len : length_of(p, s));
+                sum += span.units(n * p.min_unit);
+                longest = max(longest, span.steps);
+            }
+            sum = __reduce_add_sync(0xFFFFFFFFu, sum) * items;
+            const bool first = high == 0;
+            if (first || sum <= most) {
+                high = n;
+                unit = n * p.min_unit;
+                total = sum;
+            } else {
+                low = n;
+            }
+            if (first) {
+                if (p.seqs * items > most) break;
+                n = static_cast<uint32_t>(sum + most - 1) / static_cast<uint32_t>(most);
+                if (n < short_share)
+                    n = __reduce_max_sync(0xFFFFFFFFu, longest) <= 2 * short_share ? 2 * short_share : short_share;
+                low = n - 1;
+                high = n * 7 / 5 + 1;
+            } else {
+                if (high - low <= 1) break;
+                n = (low + high) / 2;
+            }
         }
-        fine = __reduce_add_sync(0xFFFFFFFFu, fine) * items;
-        coarse = __reduce_add_sync(0xFFFFFFFFu, coarse) * items;
-        const bool few = coarse <= static_cast<int>(gridDim.x);
-        unit = few ? kCoarse * p.min_unit : p.min_unit;
-        total = few ? coarse : fine;
         ctas = total < static_cast<int>(gridDim.x) ? total : static_cast<int>(gridDim.x);
         const int cta = blockIdx.x;
         if (cta >= ctas) return false;
@@ -543,7 +566,7 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
     griddep_wait();
 
     Share share;
-    const bool any = share.init(p, lane);
+    const bool any = share.init(p, Cfg::kShortShare, lane);
     float* const s_join = reinterpret_cast<float*>(smem + Cfg::kJoinAt);
     uint32_t* const s_last = reinterpret_cast<uint32_t*>(smem + Cfg::kLastAt);
     if (RW > 1 && threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -562,6 +585,7 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
     const int quad = lane & 3, gid = lane >> 2;
     const uint32_t q_smem = ring + Cfg::kQueryAt + wr * Cfg::kQueryBytes;
     float* const s_ml = reinterpret_cast<float*>(smem + Cfg::kMlAt);     // [kGroups][kRows][2]
+    float* const s_sum = reinterpret_cast<float*>(smem + Cfg::kSumAt);   // [kRows][2]
 
     // fragment addresses in a side: the row of the lane's part, and the places of its four chunks of 64 elements
     const int kr = (lane & 7) + ((lane >> 4) << 3), vr = (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -858,15 +882,15 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
         }
 
         // join the groups
+        float sum[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float sum = l[h];
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            if (quad == 0)
-                *reinterpret_cast<float2*>(s_ml + (grp * kRows + wr * 16 + h * 8 + gid) * 2) = make_float2(m[h], sum);
+            sum[h] = l[h];
+            sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 2);
+            if (kGroups > 1 && quad == 0)
+                *reinterpret_cast<float2*>(s_ml + (grp * kRows + wr * 16 + h * 8 + gid) * 2) = make_float2(m[h], sum[h]);
         }
-        __syncwarp();
         auto store_out = [&](int r, int d, const float4& acc, float sum) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             *reinterpret_cast<uint2*>(p.out + row_offset(r, p.out_stride) + d) =
@@ -882,9 +906,8 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
             for (int h = 0; h < 2; ++h) {
                 const int row = wr * 16 + h * 8 + gid;
                 if (row >= rows) continue;
-                const float sum = s_ml[row * 2 + 1];
                 if (!cut) {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    const float inv = sum[h] == 0.0f ? 0.0f : 1.0f / sum[h];
                     uint16_t* const dst = p.out + row_offset(row, p.out_stride) + quad * 2;
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n)
@@ -895,10 +918,35 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
                     for (int n = 0; n < D / 8; ++n)
                         *reinterpret_cast<float2*>(p.part + at * D + n * 8 + quad * 2) =
                             make_float2(o[n][2 * h], o[n][2 * h + 1]);
-                    if (quad == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[h], sum);
+                    if (quad == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[h], sum[h]);
                 }
             }
         } else {
+            // The outputs of many groups are brought to the rows' common maxima, and then only add up.
+            float scale[2] = {1.0f, 1.0f};
+            if constexpr (Cfg::kScaled) {
+                named_barrier(1, kThreads);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = wr * 16 + h * 8 + gid;
+                    float2 ml[kGroups / 4];   // a lane of the row's four looks at these groups
+                    float top = -INFINITY, total = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kGroups / 4; ++k) {
+                        ml[k] = *reinterpret_cast<const float2*>(s_ml + ((k * 4 + quad) * kRows + row) * 2);
+                        top = fmaxf(top, ml[k].x);
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                    for (int k = 0; k < kGroups / 4; ++k) total = fmaf(ml[k].y, exp2_approx(ml[k].x - ref), total);
+                    total += __shfl_xor_sync(0xFFFFFFFFu, total, 1);
+                    total += __shfl_xor_sync(0xFFFFFFFFu, total, 2);
+                    scale[h] = exp2_approx(m[h] - ref);
+                    if (grp == 0 && quad == 0) *reinterpret_cast<float2*>(s_sum + row * 2) = make_float2(top, total);
+                }
+            }
             // as many columns at a time as the rows leave room for
             constexpr int kCols = Cfg::kJoinCols;
             int wide = kCols;   // a power of two
@@ -914,9 +962,9 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
                     if (row < rows) {
                         float* const at = s_join + (grp * rows + row) * wide + in_round + quad * 2;
 #pragma unroll
-                        for (int n = 0; n < kCols / 8; ++n)
-                            *reinterpret_cast<float2*>(at + n * 8) =
-                                make_float2(o[col / 8 + n][2 * h], o[col / 8 + n][2 * h + 1]);
+                        for (int n = 0; n < kCols / 8; ++n)   // eight columns at place n ^ (row % 4): no bank conflicts
+                            *reinterpret_cast<float2*>(at + (n ^ (gid & 3)) * 8) =
+                                make_float2(o[col / 8 + n][2 * h] * scale[h], o[col / 8 + n][2 * h + 1] * scale[h]);
                     }
                 }
                 if (in_round + kCols != wide) continue;
@@ -924,32 +972,45 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
                 named_barrier(1, kThreads);
                 for (int e = threadIdx.x; e < rows * per_row; e += kThreads) {
                     const int row = e >> row_shift, d = (e & (per_row - 1)) * 4;
-                    float2 ml[kGroups];
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kGroups; ++w) {
-                        ml[w] = *reinterpret_cast<const float2*>(s_ml + (w * kRows + row) * 2);
-                        top = fmaxf(top, ml[w].x);
-                    }
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    float sum = 0.0f;
+                    const float* const from = s_join + row * wide + (d ^ ((row & 3) << 3));
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float2 sums;   // maximum and sum
+                    if constexpr (Cfg::kScaled) {
+                        sums = *reinterpret_cast<const float2*>(s_sum + row * 2);
 #pragma unroll
-                    for (int w = 0; w < kGroups; ++w) {
-                        const float a = exp2_approx(ml[w].x - ref);
-                        sum = fmaf(ml[w].y, a, sum);
-                        const float4 v = *reinterpret_cast<const float4*>(s_join + (w * rows + row) * wide + d);
-                        acc.x = fmaf(v.x, a, acc.x);
-                        acc.y = fmaf(v.y, a, acc.y);
-                        acc.z = fmaf(v.z, a, acc.z);
-                        acc.w = fmaf(v.w, a, acc.w);
+                        for (int w = 0; w < kGroups; ++w) {
+                            const float4 v = *reinterpret_cast<const float4*>(from + w * rows * wide);
+                            acc.x += v.x;
+                            acc.y += v.y;
+                            acc.z += v.z;
+                            acc.w += v.w;
+                        }
+                    } else {
+                        float2 ml[kGroups];
+                        sums = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                        for (int w = 0; w < kGroups; ++w) {
+                            ml[w] = *reinterpret_cast<const float2*>(s_ml + (w * kRows + row) * 2);
+                            sums.x = fmaxf(sums.x, ml[w].x);
+                        }
+                        const float ref = sums.x == -INFINITY ? 0.0f : sums.x;
+#pragma unroll
+                        for (int w = 0; w < kGroups; ++w) {
+                            const float a = exp2_approx(ml[w].x - ref);
+                            sums.y = fmaf(ml[w].y, a, sums.y);
+                            const float4 v = *reinterpret_cast<const float4*>(from + w * rows * wide);
+                            acc.x = fmaf(v.x, a, acc.x);
+                            acc.y = fmaf(v.y, a, acc.y);
+                            acc.z = fmaf(v.z, a, acc.z);
+                            acc.w = fmaf(v.w, a, acc.w);
+                        }
                     }
                     if (!cut) {
-                        store_out(row, col0 + d, acc, sum);
+                        store_out(row, col0 + d, acc, sums.y);
                     } else {
                         const int64_t at = parts.row(cta - c0, row);
                         *reinterpret_cast<float4*>(p.part + at * D + col0 + d) = acc;
-                        if (col0 + d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, sum);
+                        if (col0 + d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = sums;
                     }
                 }
             }
