@@ -8,18 +8,21 @@
 // than 2^59), so histograms with atomics, any split of the row and any order of
 // arrival give the same token.
 //
-// A row is one cluster's: its CTAs read it once from memory, keep it in shared
-// memory and exchange maxima, histograms and sums through distributed shared
-// memory. top-k and top-p are thresholds in the order (logit falling, index
-// rising), and what lies above one is nearly always few tokens:
-//   - top_k: the largest logit of every thread is counted in a histogram. The
-//     bin where the count reaches k bounds the k largest of all from below, and
-//     little more than k logits lie above it.
-//   - top_p alone: a histogram of the masses by the leading bits of the weights,
-//     and one by the next bits inside the bin that the threshold lies in.
-// The first CTA ranks these candidates and draws among them, or tells the others
-// the threshold. Rows where too many candidates are left (flat ones, many equal
-// logits) are resolved bin by bin, then bit by bit, then by index.
+// A row is one cluster's: its CTAs exchange maxima, histograms and sums through distributed shared memory. top-k and top-p
+// are thresholds in the order (logit falling, index rising), and what lies above one is nearly always few tokens:
+//   - top_k: the largest logit of every thread is counted in a histogram. The bin where the count reaches k bounds the k
+//     largest of all from below, and little more than k logits lie above it.
+//   - top_p alone: a histogram of the masses by the leading bits of the weights, and one by the next bits inside the bin that
+//     the threshold lies in.
+// The first CTA ranks these candidates and draws among them, or tells the others the threshold. Rows where too many
+// candidates are left (flat ones, many equal logits) are resolved bin by bin, then bit by bit, then by index.
+//
+// The bound of few rows is latency: the exchanges, and instructions that run once and have to be fetched. 16 CTAs a row
+// (8 from 9 rows on) read it once and keep it in shared memory: 1 x 151,936 with top_k 50 8.7 us, 16 x 151,936 bfloat16
+// with top_p 0.9 38 us. The bound of many rows is the time that a row's steps hold an SM, so that the fewest CTAs that fill
+// the GPU take a row and read it again from the L2 cache where they need it, for parts of rows in shared memory leave no
+// room for other rows: 256 x 100,277 with top_k 50 in 34 us, 3.0 TB/s, where 8 CTAs each that keep the row took 85 us. What
+// top_p alone costs there (256 x 151,936 bfloat16 279 us) is an exponential and two additions in shared memory a logit.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -42,9 +45,9 @@ constexpr int kList = 2048;                // candidates of the first CTA
 constexpr int kEach = kList / kSampleThreads;
 constexpr int kRanks = 16;                 // CTAs of a cluster at most
 constexpr int kPortableRanks = 8;
+constexpr int kManyCtas = 2 * 152;         // CTAs that the GPU holds at once
 constexpr int kCounted = 256;              // candidates that are ranked by counting all others (kBins at most)
 constexpr int kFew = 64;                   // the same where more have been parted by histograms
-constexpr float kWeightOne = 1099511627776.0f;   // 2^40
 constexpr float kBinsPerUnit = 8.0f;       // bins for one unit of (max l - l) / T: mass ends at 27.7 units
 constexpr int kWeightBinShift = 20;        // bits of a weight below its bin: 8 bins an octave
 
@@ -87,7 +90,7 @@ struct SampleShared {
     uint32_t warp_count[kSampleWarps];
     u64 list[kList];
     u64 few[kFew], few_value[kFew], pick, pick_value;
-    uint16_t own[kList];   // slots of this CTA's candidates
+    uint32_t own[kList];   // slots of this CTA's candidates
     u64 scalar;
     uint32_t list_size, sizes[kRanks];
     Decision decision;
@@ -144,20 +147,6 @@ __device__ __forceinline__ N block_before(N v, N* scratch, N& all) {
     return upto - v + __shfl_sync(0xFFFFFFFFu, w - mine, warp);
 }
 
-// f(i, x[i]) for i = from, from + step, ... below end, four values read at a time.
-template <class F>
-__device__ __forceinline__ void for_each(const float* x, int from, int end, int step, F f) {
-    for (int i = from; i < end; i += 4 * step) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (i + j * step < end) v[j] = x[i + j * step];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (i + j * step < end) f(i + j * step, v[j]);
-    }
-}
-
 // 64-bit sums of two 32-bit atomics each: a 64-bit one in shared memory is a loop of compare-and-swaps (37 a thread of
 // 512 took 12,000 cycles, these 3,500).
 __device__ __forceinline__ void add_mass(u64* sum, u64 m) {
@@ -181,12 +170,17 @@ __device__ __forceinline__ u64 bound_of(double limit) {
     return lo;
 }
 
-template <class T>
+// HELD: the CTA keeps its part of the row in shared memory; else it reads it again in every pass.
+template <class T, bool HELD>
 struct RowSampler {
+    // slots of a chunk: 16 bytes of the row in memory, or of the slots in shared memory
+    static constexpr int kVec = HELD ? 4 : 16 / sizeof(T);
+    static constexpr int kPerRead = 16 / static_cast<int>(sizeof(T)) / kVec;   // chunks of 16 bytes in memory
     SampleShared& sh;
-    float* x;              // this CTA's slots: the logits, and later their weights
+    float* x;              // HELD: this CTA's slots, the logits and later their weights
     const T* src;          // the row
-    int lo, hi;            // the slots that hold logits
+    int lo, hi;            // the slots that hold logits; those before and after in the first and the last chunk are -infinity
+    int chunks;            // of the slots
     int shift;             // index of slot 0
     int rank, ranks;
     float top, temperature;
@@ -199,11 +193,114 @@ struct RowSampler {
             return clean(src[index]);
     }
     __device__ __forceinline__ uint32_t index(int i) const { return static_cast<uint32_t>(shift + i); }
+    __device__ __forceinline__ float slot(int i) const {
+        if constexpr (HELD) return x[i];
+        else return i >= lo && i < hi ? logit_at(index(i)) : -INFINITY;   // an index outside the row is not one of memory
+    }
+    __device__ __forceinline__ static float pick(const float (&v)[kVec], int e) {
+        float x = v[0];
+#pragma unroll
+        for (int k = 1; k < kVec; ++k) x = e == k ? v[k] : x;
+        return x;
+    }
+    __device__ __forceinline__ bool inside(int c) const { return c * kVec >= lo && (c + 1) * kVec <= hi; }
+    __device__ __forceinline__ uint4 raw(int c) const { return __ldg(reinterpret_cast<const uint4*>(src + shift + c * kVec)); }
+    __device__ __forceinline__ static void unpack(const uint4& r, float (&v)[kVec]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            if constexpr (sizeof(T) == 2)
+                v[e] = clean(__uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16));
+            else
+                v[e] = clean(__uint_as_float(w[e]));
+        }
+    }
+    // The slots of chunk c.
+    __device__ __forceinline__ void load(int c, float (&v)[kVec]) const {
+        if constexpr (HELD) {
+            const float4 f = *reinterpret_cast<const float4*>(x + c * kVec);
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else if (inside(c)) {
+            unpack(raw(c), v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int i = c * kVec + e;
+                v[e] = i >= lo && i < hi ? logit_at(index(i)) : -INFINITY;
+            }
+        }
+    }
+    // f(c, v) for chunks c = from, from + step, ... below end and their slots v.
+    template <class F>
+    __device__ __forceinline__ void each_chunk(int from, int end, int step, F f) const {
+        if constexpr (HELD) {
+            for (int c = from; c < end; c += step) {
+                float v[kVec];
+                load(c, v);
+                f(c, v);
+            }
+        } else {
+            for (int c0 = from; c0 < end; c0 += 4 * step) {   // four loads in flight
+                uint4 r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j * step < end && inside(c0 + j * step)) r[j] = raw(c0 + j * step);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = c0 + j * step;
+                    if (c >= end) continue;
+                    float v[kVec];
+                    if (inside(c)) unpack(r[j], v);
+                    else load(c, v);
+                    f(c, v);
+                }
+            }
+        }
+    }
+    // The chunks that the threads with `here` have read first (theirs are the 16 bytes at tid, tid + kSampleThreads, ...);
+    // where they are many, all lanes of a warp together for one thread's.
+    template <class F>
+    __device__ __forceinline__ void each_chunk_of(bool here, F f) const {
+        const int lane = threadIdx.x & 31, reads = chunks / kPerRead;
+        auto read = [&](int r) {
+#pragma unroll
+            for (int k = 0; k < kPerRead; ++k) {
+                float v[kVec];
+                load(r * kPerRead + k, v);
+                f(r * kPerRead + k, v);
+            }
+        };
+        if (reads <= 8 * kSampleThreads) {
+            if (here)
+                for (int r = threadIdx.x; r < reads; r += kSampleThreads) read(r);
+            return;
+        }
+        for (uint32_t votes = __ballot_sync(0xFFFFFFFFu, here); votes != 0; votes &= votes - 1) {
+            const int owner = static_cast<int>(threadIdx.x) - lane + __ffs(votes) - 1;
+            for (int r = owner + lane * kSampleThreads; r < reads; r += 32 * kSampleThreads) read(r);
+        }
+    }
     __device__ __forceinline__ float depth(float l) const { return temperature == 1.0f || l == top ? l == top ? 0.0f : l - top : __fdiv_rn(l - top, temperature); }
     __device__ __forceinline__ float weight(float l, float z) const { return l == top ? 1.0f : expf(z); }
     __device__ __forceinline__ float weight(float l) const { return weight(l, depth(l)); }
-    // (not above 0 also where an infinite temperature or logit leaves no number)
-    __device__ __forceinline__ static u64 mass(float w) { return w > 0.0f ? static_cast<u64>(w * kWeightOne) : 0ull; }
+    // floor(2^40 w) from the bits of w, for conversions to 64 bits run at the rate of double arithmetic. 0 also where an
+    // infinite temperature or logit leaves no number.
+    __device__ __forceinline__ static u64 mass(float w) {
+        const uint32_t b = __float_as_uint(w), at = 133u - (b >> 23);   // 6 for 1, 46 for 2^-40
+        const u64 m = (static_cast<u64>((b & 0x7FFFFFu) | 0x800000u) << 23) >> (at & 63u);
+        return at - 6u <= 40u ? m : 0ull;
+    }
+    // The weights of a chunk, without branches between its slots.
+    __device__ __forceinline__ void weights(const float (&v)[kVec], float (&w)[kVec]) const {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) w[e] = v[e] == top ? 0.0f : v[e] - top;
+        if (temperature != 1.0f) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) w[e] = __fdiv_rn(w[e], temperature);
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) w[e] = expf(w[e]);
+    }
     __device__ __forceinline__ bool under(uint32_t key, uint32_t idx) const {
         return key > thr.key || (key == thr.key && idx <= thr.index);
     }
@@ -600,7 +697,7 @@ struct RowSampler {
             cluster.sync();   // no CTA reads another's histogram any more
             clear_bins();
             for (int i = lo + tid; i < hi; i += kSampleThreads) {
-                const float l = x[i];
+                const float l = slot(i);
                 const uint32_t key = key_of(l);
                 if (!under(key, index(i))) continue;
                 const float z = depth(l);
@@ -626,7 +723,7 @@ struct RowSampler {
             clear_list();
             cluster.sync();   // the first CTA's list is free
             for (int i = lo + tid; i < hi; i += kSampleThreads) {
-                const float l = x[i];
+                const float l = slot(i);
                 const uint32_t key = key_of(l);
                 if (under(key, index(i)) && member(level, depth(l), key)) add(key, index(i));
             }
@@ -640,7 +737,7 @@ struct RowSampler {
                 cluster.sync();
                 clear_bins();
                 for (int i = lo + tid; i < hi; i += kSampleThreads) {
-                    const float l = x[i];
+                    const float l = slot(i);
                     const uint32_t key = key_of(l);
                     const float z = depth(l);
                     if (!under(key, index(i)) || !member(level, z, key)) continue;
@@ -674,7 +771,7 @@ struct RowSampler {
         const int s0 = lo + warp * seg, s1 = s0 + seg < hi ? s0 + seg : hi;
         uint32_t equal = 0;
         for (int i = s0 + lane; i < s1; i += 32) {
-            const uint32_t k2 = key_of(x[i]);
+            const uint32_t k2 = key_of(slot(i));
             equal += k2 == key && under(k2, index(i)) ? 1u : 0u;
         }
         equal = __reduce_add_sync(0xFFFFFFFFu, equal);
@@ -691,7 +788,7 @@ struct RowSampler {
         if (at < keep && at + equal >= keep) {
             for (int i0 = s0; i0 < s1; i0 += 32) {
                 const int i = i0 + lane;
-                const bool in = i < s1 && key_of(x[i]) == key && under(key, index(i));
+                const bool in = i < s1 && key_of(slot(i)) == key && under(key, index(i));
                 const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in);
                 const u64 place = at + __popc(votes & ((1u << lane) - 1u));
                 if (in && place == keep - 1) {
@@ -706,12 +803,13 @@ struct RowSampler {
     }
 };
 
-template <class T>
+template <class T, bool HELD>
 __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __grid_constant__ SampleParams p) {
     extern __shared__ __align__(16) float slots[];
     __shared__ SampleShared sh;
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int kVec = 16 / sizeof(T);
+    constexpr int kRead = 16 / sizeof(T);
+    constexpr int kVec = RowSampler<T, HELD>::kVec;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / ranks;
@@ -722,10 +820,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     // this CTA's 16-byte chunks of the row; slot 0 is the first element of its first chunk
     const T* src = static_cast<const T*>(p.logits) + row * p.stride;
     const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-    const int chunks = (lead + p.vocab + kVec - 1) / kVec;
-    const int per_cta = (chunks + ranks - 1) / ranks;
-    RowSampler<T> s{sh, slots, src};
-    s.shift = rank * per_cta * kVec - lead;
+    const int reads = (lead + p.vocab + kRead - 1) / kRead;
+    const int reads_here = (reads + ranks - 1) / ranks, per_cta = reads_here * (kRead / kVec);   // per_cta: chunks
+    RowSampler<T, HELD> s{sh, slots, src};
+    s.chunks = per_cta;
+    s.shift = rank * reads_here * kRead - lead;
     const int left = p.vocab - s.shift;
     s.lo = s.shift < 0 ? -s.shift : 0;
     s.hi = left < per_cta * kVec ? (left > s.lo ? left : s.lo) : per_cta * kVec;
@@ -735,42 +834,18 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     const int top_k = p.top_k[row];
     const float top_p = p.top_p[row], min_p = p.min_p[row];
 
-    // the logits to shared memory, and every thread's largest
+    // every thread's largest logit, and the logits to shared memory
     float best = -INFINITY;
-    for (int c0 = tid; c0 < per_cta; c0 += 4 * kSampleThreads) {
-        uint4 v[4];
+    RowSampler<T, false>{sh, nullptr, src, s.lo, s.hi, reads_here, s.shift}.each_chunk(
+        tid, reads_here, kSampleThreads, [&](int c, const float(&v)[kRead]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {   // four loads in flight
-            const int at = (c0 + j * kSampleThreads) * kVec;
-            if (at >= s.lo && at + kVec <= s.hi) v[j] = __ldg(reinterpret_cast<const uint4*>(src + s.shift + at));
-        }
+            for (int e = 0; e < kRead; ++e) best = fmaxf(best, v[e]);
+            if constexpr (HELD) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = c0 + j * kSampleThreads, at = c * kVec;
-            if (c >= per_cta) continue;
-            if (at >= s.lo && at + kVec <= s.hi) {
-                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                float f[kVec];
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    if constexpr (sizeof(T) == 2)
-                        f[e] = clean(__uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16));
-                    else
-                        f[e] = clean(__uint_as_float(w[e]));
-                    best = fmaxf(best, f[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < kVec; e += 4)
-                    *reinterpret_cast<float4*>(slots + at + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-            } else {
-                for (int i = at; i < at + kVec; ++i) {
-                    if (i < s.lo || i >= s.hi) continue;
-                    slots[i] = s.logit_at(s.index(i));
-                    best = fmaxf(best, slots[i]);
-                }
+                for (int e = 0; e < kRead; e += 4)
+                    *reinterpret_cast<float4*>(slots + c * kRead + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
-        }
-    }
+        });
     // The row's largest logit, and the mean of the threads' largest ones (those of numbers in use, not of masks).
     {
         const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, key_of(best));
@@ -824,8 +899,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     if (!(s.temperature > 0.0f) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f) {
         // the first of the largest
         uint32_t first = 0xFFFFFFFFu;
-        for (int i = s.lo + tid; i < s.hi; i += kSampleThreads)
-            if (slots[i] == s.top) first = min(first, s.index(i));
+        s.each_chunk_of(best == s.top, [&](int c, const float(&v)[kVec]) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (v[e] == s.top) first = min(first, s.index(c * kVec + e));
+        });
         first = __reduce_min_sync(0xFFFFFFFFu, first);
         if (lane == 0) sh.warp_count[warp] = first;
         __syncthreads();
@@ -843,25 +921,38 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
 
     if (by_count && top_k <= kList / 2 && s.top < 1e30f) {
-        // The bin of the k-th of the threads' largest logits, or of all logits where k is a large part of the threads.
-        const bool largest = top_k <= ranks * kSampleThreads / 4;
-        const float range = above > 0.0f ? (largest ? 1.5f : 4.0f) * (s.top - level / above) : 0.0f;
+        // The bin of the k-th of the threads' largest logits, or of the chunks' largest ones where k is a large part of the
+        // threads, or of all logits.
+        const bool of_threads = top_k <= ranks * kSampleThreads / 4, of_chunks = top_k <= reads / 4;
+        const float range = above > 0.0f ? (of_threads ? 1.5f : of_chunks ? 2.5f : 4.0f) * (s.top - level / above) : 0.0f;
         const float per_unit = range > 0.0f ? kBins / range : 1.0f;
         auto bin_of = [&](float l) -> int { return static_cast<int>(fminf((s.top - l) * per_unit, kBins - 1.0f)); };
-        if (largest) {
+        if (of_threads) {
             if (best > -INFINITY) atomicAdd(&sh.count[bin_of(best)], 1u);
         } else {
-            for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int, float l) { atomicAdd(&sh.count[bin_of(l)], 1u); });
+            s.each_chunk(tid, per_cta, kSampleThreads, [&](int c, const float(&v)[kVec]) {
+                float l = v[0];
+#pragma unroll
+                for (int e = 1; e < kVec; ++e) l = fmaxf(l, v[e]);
+                if (of_chunks) {
+                    if (l > -INFINITY) atomicAdd(&sh.count[bin_of(l)], 1u);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e)
+                        if (v[e] > -INFINITY) atomicAdd(&sh.count[bin_of(v[e])], 1u);
+                }
+            });
         }
         const Decision d = s.join_bins(false, static_cast<u64>(top_k), 0, 0, 0.0f, false);
         if (d.members != 0xFFFFFFFFu && d.bin < kBins - 1) {
             const float below = static_cast<float>(d.bin + 1);
-            if ((s.top - best) * per_unit < below) {   // else this thread's chunks have none
-                for (int c = tid; c < per_cta; c += kSampleThreads) {
-                    for (int i = max(c * kVec, s.lo); i < min((c + 1) * kVec, s.hi); ++i)
-                        if ((s.top - slots[i]) * per_unit < below) s.add(key_of(slots[i]), s.index(i));
-                }
-            }
+            auto add_above = [&](int c, const float(&v)[kVec]) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if ((s.top - v[e]) * per_unit < below) s.add(key_of(v[e]), s.index(c * kVec + e));
+            };
+            if (of_threads) s.each_chunk_of((s.top - best) * per_unit < below, add_above);
+            else s.each_chunk(tid, per_cta, kSampleThreads, add_above);
             const int n = s.collect();
             if (n <= kList) {
                 if (rank == 0) s.finish(p, row, n, top_k, top_p, min_p, 0);
@@ -870,38 +961,63 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
         }
     }
 
-    // Weights in the logits' place, and a histogram of their masses or their sums by warps, which have segments of the row.
-    const int seg = ((s.hi - s.lo + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;
-    const int s0 = s.lo + warp * seg, s1 = s0 + seg < s.hi ? s0 + seg : s.hi;
+    // The weights (HELD: in the logits' place), and a histogram of their masses or their sums by warps, which have segments
+    // of the row.
+    const int seg = (per_cta + kSampleWarps - 1) / kSampleWarps;
+    const int s0 = warp * seg, s1 = s0 + seg < per_cta ? s0 + seg : per_cta;   // in chunks
     bool general = by_count;     // thresholds by logit and index, the logits still in their place
     u64 own = 0;
-    uint32_t edge = 0;           // weights of fewer bits lie in bins after the threshold's
+    uint32_t edge = 0;           // HELD: weights of fewer bits lie in bins after the threshold's
     auto bits_below = [](float w) -> uint32_t { return 0x3F800000u - __float_as_uint(w); };
     auto bin_of = [&](float w) -> uint32_t { return min(bits_below(w) >> kWeightBinShift, static_cast<uint32_t>(kBins - 1)); };
     if (!general) {
         __syncthreads();
-        // four logits at a time, so that the chains of their exponentials overlap
-        for (int i0 = s0 + lane; i0 < s1; i0 += 4 * 32) {
-            float w[4];
+        s.each_chunk(s0 + lane, s1, 32, [&](int c, const float(&v)[kVec]) {
+            float w[kVec];
+            s.weights(v, w);
+            u64 m[kVec];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = i0 + j * 32 < s1 ? slots[i0 + j * 32] : -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = s.weight(w[j]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (i0 + j * 32 >= s1) continue;
-                const u64 m = s.mass(w[j]);
-                slots[i0 + j * 32] = m != 0 ? w[j] : 0.0f;
-                if (m == 0) continue;
-                if (by_mass) {
-                    atomicAdd(&sh.count[bin_of(w[j])], 1u);
-                    add_mass(&sh.mass[bin_of(w[j])], m);
-                } else if (!(w[j] < min_p)) {
-                    own += m;
-                }
+            for (int e = 0; e < kVec; ++e) {
+                m[e] = s.mass(w[e]);
+                w[e] = m[e] != 0 ? w[e] : 0.0f;
             }
-        }
+            if (by_mass) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    if (m[e] == 0) continue;
+                    atomicAdd(&sh.count[bin_of(w[e])], 1u);
+                    add_mass(&sh.mass[bin_of(w[e])], m[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) own += w[e] < min_p ? 0 : m[e];
+            }
+            if constexpr (HELD) {
+                *reinterpret_cast<float4*>(slots + c * kVec) = make_float4(w[0], w[1], w[2], w[3]);
+            }
+        });
     }
+    // f(i, w) for the slots whose weights have bits_below in [from, to]. Unless they are HELD, a range of logits a little wider
+    // (by the rounding of all between logit and weight) says which weights to look at.
+    auto each_between = [&](uint32_t from, uint32_t to, auto f) {
+        float low = __uint_as_float(0x3F800000u - to), high = __uint_as_float(0x3F800000u - from);
+        if constexpr (!HELD) {
+            const float slack = fabsf(s.top) * 2.5e-7f;
+            low = fmaf(logf(low) - 1e-3f, s.temperature, s.top) - slack;
+            high = fmaf(logf(high) + 1e-3f, s.temperature, s.top) + slack;
+        }
+        s.each_chunk(tid, per_cta, kSampleThreads, [&](int c, const float(&v)[kVec]) {
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) hits |= v[e] < low || v[e] > high ? 0u : 1u << e;   // all if no numbers
+            for (; hits != 0; hits &= hits - 1) {
+                const int e = __ffs(hits) - 1, i = c * kVec + e;
+                float w = s.pick(v, e);
+                if constexpr (!HELD) w = s.weight(w);
+                if (w > 0.0f && s.mass(w) != 0 && bits_below(w) - from <= to - from) f(i, w);
+            }
+        });
+    };
     if (!general && by_mass) {
         Decision d = s.join_bins(true, 0, 0, 0, top_p);
         const u64 total = d.total, limit = d.limit;
@@ -914,8 +1030,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
             // the next bits part the bin's members
             cluster.sync();
             s.clear_bins();
-            for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int, float w) {
-                if (!(w > 0.0f) || bin_of(w) != bin) return;
+            each_between(bin << kWeightBinShift, (bin + 1 << kWeightBinShift) - 1, [&](int, float w) {
                 const uint32_t b = bits_below(w) >> kSubShift & (kBins - 1);
                 atomicAdd(&sh.count[b], 1u);
                 add_mass(&sh.mass[b], s.mass(w));
@@ -925,16 +1040,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
             general = d.members == 0xFFFFFFFFu || d.members > kList;
         }
         if (!general) {
-            auto member = [&](float w) -> bool {
-                if (!(w > 0.0f)) return false;
-                if (whole) return bin_of(w) <= bin;
-                return bin_of(w) == bin && (sub == 0xFFFFFFFFu || (bits_below(w) >> kSubShift & (kBins - 1)) == sub);
-            };
+            const bool parted = sub != 0xFFFFFFFFu;
+            const uint32_t from = (bin << kWeightBinShift) + (parted ? sub << kSubShift : 0u);
+            const uint32_t past = from + (1u << (parted ? kSubShift : kWeightBinShift));
             // their slots first: the logits come from memory again, all at once
-            for_each(slots, s.lo + tid, s.hi, kSampleThreads, [&](int i, float w) {
-                if (!member(w)) return;
+            each_between(whole ? 0u : from, past - 1, [&](int i, float) {
                 const uint32_t at = atomicAdd(&sh.list_size, 1u);
-                if (at < kList) sh.own[at] = static_cast<uint16_t>(i);
+                if (at < kList) sh.own[at] = static_cast<uint32_t>(i);
             });
             __syncthreads();
             const int mine = static_cast<int>(min(sh.list_size, static_cast<uint32_t>(kList / ranks)));
@@ -950,19 +1062,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
                 return;
             } else {
                 s.threshold_of_list(n, true, limit, d);
-                // members past the threshold lose their weight
-                for (int k = tid; k < mine; k += kSampleThreads) {
-                    const uint32_t index = s.index(sh.own[k]);
-                    if (!s.under(key_of(s.logit_at(index)), index)) slots[sh.own[k]] = 0.0f;
+                if constexpr (HELD) {   // members past the threshold lose their weight
+                    for (int k = tid; k < mine; k += kSampleThreads) {
+                        const uint32_t index = s.index(sh.own[k]);
+                        if (!s.under(key_of(s.logit_at(index)), index)) slots[sh.own[k]] = 0.0f;
+                    }
+                    __syncthreads();
+                    edge = 0x3F800000u - past + 1;
                 }
-                __syncthreads();
-                const uint32_t end = sub == 0xFFFFFFFFu ? (bin + 1) << kWeightBinShift : (bin << kWeightBinShift) + ((sub + 1) << kSubShift);
-                edge = 0x3F800000u - end + 1;
             }
         }
-        if (general) {   // the logits again
+        if (HELD && general) {   // the logits again
             __syncthreads();
-            for (int i = s.lo + tid; i < s.hi; i += kSampleThreads) slots[i] = s.logit_at(s.index(i));
+            for (int i = tid; i < per_cta * kVec; i += kSampleThreads)
+                slots[i] = i >= s.lo && i < s.hi ? s.logit_at(s.index(i)) : -INFINITY;
             __syncthreads();
         }
     }
@@ -972,18 +1085,35 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
 
     // the draw: kept masses in the order of the indices
+    const bool by_logit = !HELD || general;
     auto kept = [&](int i, float v) -> u64 {
-        if (general) {
+        if (by_logit) {
             if (!s.under(key_of(v), s.index(i))) return 0;
-            const float w = s.weight(v);
-            return w < min_p ? 0 : s.mass(w);
+            v = s.weight(v);
+        } else if (__float_as_uint(v) < edge) {
+            return 0;
         }
-        if (v < min_p) return 0;
-        return __float_as_uint(v) < edge ? 0 : s.mass(v);
+        return v < min_p ? 0 : s.mass(v);
+    };
+    auto kept_of = [&](int c, const float(&v)[kVec]) -> u64 {
+        u64 sum = 0;
+        if (by_logit) {
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) hits |= v[e] > -INFINITY && s.under(key_of(v[e]), s.index(c * kVec + e)) ? 1u << e : 0u;
+            for (; hits != 0; hits &= hits - 1) {
+                const int e = __ffs(hits) - 1;
+                sum += kept(c * kVec + e, s.pick(v, e));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) sum += v[e] < min_p || __float_as_uint(v[e]) < edge ? 0ull : s.mass(v[e]);
+        }
+        return sum;
     };
     if (general || by_mass) {
         own = 0;
-        for_each(slots, s0 + lane, s1, 32, [&](int i, float v) { own += kept(i, v); });
+        s.each_chunk(s0 + lane, s1, 32, [&](int c, const float(&v)[kVec]) { own += kept_of(c, v); });
     }
     own = warp_add(own);
     __syncthreads();
@@ -996,33 +1126,56 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
     }
     if (tid < ranks) cluster.map_shared_rank(&sh, tid)->sum[rank] = all;
     cluster.sync();
-    u64 total = 0;
+    u64 total = 0, before_cta = 0;
     for (int r = 0; r < ranks; ++r) {
-        if (r < rank) before += sh.sum[r];
+        if (r < rank) before_cta += sh.sum[r];
         total += sh.sum[r];
     }
+    before += before_cta;
     const u64 target = s.by_one([&] { return s.target_of(p.u[row], total); });
+    if (target < before_cta || target >= before_cta + all) return;
+    int c0 = s0, c1 = s1;
+    if (seg > 4 * 32) {   // all warps part the segment of the one that has it
+        if (lane == 0 && target >= before && target < before + own) {
+            sh.pick = before;
+            sh.decision.bin = static_cast<uint32_t>(warp);
+        }
+        __syncthreads();
+        const int first = static_cast<int>(sh.decision.bin) * seg, part = (seg + kSampleWarps - 1) / kSampleWarps;
+        const int end = first + seg < per_cta ? first + seg : per_cta;
+        c0 = first + warp * part;
+        c1 = c0 + part < end ? c0 + part : end;
+        own = 0;
+        s.each_chunk(c0 + lane, c1, 32, [&](int c, const float(&v)[kVec]) { own += kept_of(c, v); });
+        own = warp_add(own);
+        if (lane == 0) sh.warp_mass[warp] = own;
+        __syncthreads();
+        before = sh.pick;
+        for (int w = 0; w < warp; ++w) before += sh.warp_mass[w];
+    }
     if (target < before || target >= before + own) return;
-    for (int i0 = s0; i0 < s1; i0 += 4 * 32) {
-        u64 m[4], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = i0 + 4 * lane + j;
-            m[j] = i < s1 ? kept(i, slots[i]) : 0;
-            sum += m[j];
+    for (; c0 < c1; c0 += 32) {
+        const int c = c0 + lane;
+        u64 sum = 0;
+        if (c < c1) {
+            float v[kVec];
+            s.load(c, v);
+            sum = kept_of(c, v);
         }
         u64 upto = before + warp_scan(sum, lane);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > target);
         if (past != 0) {
             if (lane == __ffs(past) - 1) {
                 upto -= sum;
-                int j = 0;
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (j == k && upto + m[k] <= target) upto += m[k], ++j;
-                const u64 own_mass = j == 0 ? m[0] : j == 1 ? m[1] : j == 2 ? m[2] : m[3];
-                p.tokens[row] = static_cast<int32_t>(s.index(i0 + 4 * lane + j));
-                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(own_mass), static_cast<float>(total));
+                int i = c * kVec;
+                u64 m = kept(i, s.slot(i));
+                while (upto + m <= target && i < c * kVec + kVec - 1) {
+                    upto += m;
+                    ++i;
+                    m = kept(i, s.slot(i));
+                }
+                p.tokens[row] = static_cast<int32_t>(s.index(i));
+                if (p.probs != nullptr) p.probs[row] = __fdiv_rn(static_cast<float>(m), static_cast<float>(total));
             }
             return;
         }
@@ -1034,18 +1187,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) qmm_sample_kernel(const __g
 constexpr int kSampleSmem = 4 * 8 * ((QMM_SAMPLE_MAX_VOCAB / 8 + 1 + kPortableRanks - 1) / kPortableRanks);
 static_assert(kSampleSmem + sizeof(SampleShared) <= 227 * 1024, "the largest row fits its cluster");
 
-template <class T>
-int launch(const SampleParams& p, int M, cudaStream_t stream) {
-    static std::atomic<u64> configured{0};   // one bit for each device
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
-    if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(qmm_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(qmm_sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return QMM_ERR_CUDA;
-        if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
+template <class T, bool HELD>
+int launch(const SampleParams& p, int M, int ranks, cudaStream_t stream) {
+    if (HELD) {
+        static std::atomic<u64> configured{0};   // one bit for each device
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
+        if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
+            const void* kernel = reinterpret_cast<const void*>(&qmm_sample_kernel<T, HELD>);
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem) != cudaSuccess ||
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                return QMM_ERR_CUDA;
+            if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
+        }
     }
-    int ranks = M <= 8 ? kRanks : kPortableRanks;             // few rows leave SMs for more CTAs each
     while (ranks > 1 && p.vocab / ranks < 2048) ranks /= 2;   // shorter shares cost more exchange than they save
     const int vec = 16 / static_cast<int>(sizeof(T));
     const int chunks = (p.vocab + vec - 1) / vec + 1;         // one more where the row starts inside a chunk
@@ -1058,11 +1213,21 @@ int launch(const SampleParams& p, int M, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M) * ranks);
     cfg.blockDim = dim3(kSampleThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>((chunks + ranks - 1) / ranks) * vec * 4;
+    cfg.dynamicSmemBytes = HELD ? static_cast<size_t>((chunks + ranks - 1) / ranks) * vec * 4 : 0;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, qmm_sample_kernel<T>, p) == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, qmm_sample_kernel<T, HELD>, p) == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+// Few rows are split over many CTAs, which keep them. Where those would not all fit the GPU at once, as few CTAs a row as
+// fill it read the row again from the L2 cache when they need it: their exchanges cost less, and none waits for others.
+template <class T>
+int launch_rows(const SampleParams& p, int M, cudaStream_t stream) {
+    if (M * kPortableRanks <= kManyCtas) return launch<T, true>(p, M, M <= 8 ? kRanks : kPortableRanks, stream);
+    int ranks = kPortableRanks / 2;
+    while (ranks > 1 && M * ranks > kManyCtas) ranks /= 2;
+    return launch<T, false>(p, M, ranks, stream);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1097,5 +1262,5 @@ extern "C" int qmm_sample(const void* logits, int M, int vocab, int64_t stride, 
     sp.probs = probs;
     sp.vocab = vocab;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return in_dtype == QMM_IN_F32 ? launch<float>(sp, M, st) : launch<uint16_t>(sp, M, st);
+    return in_dtype == QMM_IN_F32 ? launch_rows<float>(sp, M, st) : launch_rows<uint16_t>(sp, M, st);
 }

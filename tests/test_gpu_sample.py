@@ -256,3 +256,42 @@ def test_graph_and_stream(q):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(tokens, eager[0]) and torch.equal(probs, eager[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1003, 33001])
+@pytest.mark.parametrize("M", [39, 80, 153, 310])
+def test_batches_agree(q, dtype, V, M):
+    """A row's token and probability do not depend on how many rows share the call: the masses are whole numbers, and their
+    sums the same for one CTA as for sixteen. Rows of every kind, next to one another."""
+    import torch
+    gen = torch.Generator().manual_seed(V + M)
+    R = 22
+    base = torch.randn((R, V + 3), generator=gen) * 2.2
+    base[1] = 1.5                                    # equal logits
+    base[2, ::2] = -float("inf")
+    base[3] = torch.round(base[3])                   # many ties
+    base[4] = -float("inf")                          # nothing to draw from
+    base[5, 17:] = -float("inf")
+    base[6] *= 1e-5
+    base[7, 40] = float("nan")
+    base[8, :V // 3] += 9.0                          # the likely ones in one part of the row
+    base = base.to(torch.float32 if dtype == "f32" else torch.bfloat16).to(DEV)[:, 1:V + 1]
+    T = [(1.0, 0.7, 1.3)[r % 3] for r in range(R)]
+    k = [(0, 50, 0, 1000, 3)[r % 5] for r in range(R)]
+    p = [(1.0, 0.9, 0.6, 1.0)[r % 4] for r in range(R)]
+    min_p = [(0.0, 0.0, 0.02)[r % 3] for r in range(R)]
+    T[9], k[10] = 0.0, 1
+    u = torch.rand(M, generator=gen).tolist()
+    rows = [r % R for r in range(M)]
+    col = lambda v, t: torch.tensor([v[r] for r in rows], dtype=t).to(DEV)  # noqa: E731
+    args = [col(T, torch.float32), col(k, torch.int32), col(p, torch.float32), col(min_p, torch.float32), torch.tensor(u).to(DEV)]
+    logits = base[torch.tensor(rows).to(DEV)]
+    tokens, probs = torch.full((M,), -9, dtype=torch.int32, device=DEV), torch.full((M,), -9.0, device=DEV)
+    q.sample(logits, *args, tokens, probs)
+    for i in range(0, M, 5):
+        few = slice(i, min(i + 5, M))
+        t, pr = torch.full((M,), -9, dtype=torch.int32, device=DEV)[few], torch.full((M,), -9.0, device=DEV)[few]
+        q.sample(logits[few], *(a[few] for a in args), t, pr)
+        assert torch.equal(t, tokens[few]), (i, t, tokens[few])
+        assert torch.equal(pr, probs[few])
