@@ -1,11 +1,20 @@
 // Norms of queries and keys, their rotation, and the append to the paged cache,
 // in one pass over the new tokens:
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> (a c - b s, b c + a s).
-// A head is spread over head_dim / 8 lanes with 8 neighbouring elements each
-// (16-byte accesses of bfloat16): the mean is a sum over those lanes, and the
-// other element of a half-split pair lies rot_dim / 16 lanes away. Everything
-// is float32 until the one rounding to bfloat16.
+// A head is spread over head_dim / 8 lanes with eight elements each, four a and
+// the four b that they turn with, so that a pair never leaves its lane: where
+// the halves of the rotated part turn with one another, a lane has four
+// neighbours of each half. The mean is a sum over the lanes. Everything is
+// float32 until the one rounding to bfloat16.
+//
+// The bound of many tokens is the bytes, but instructions are close to it: 4 x
+// 2048 tokens of 48 heads of 128 take 39.5 us, 5.2 TB/s, where pairs that met by
+// shuffles, single float32 operations and addresses computed for every vector
+// took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.1 us for
+// one), and a warp takes only as many heads as it can have in flight.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
@@ -18,9 +27,9 @@ namespace {
 constexpr int kAppendWarps = 4;
 constexpr int64_t kManyWarps = 152 * 40;   // two rounds of the warps that run at once
 
-// Head vectors that a warp loads before it works on the last ones.
-template <bool F32>
-constexpr int kAppendSteps = F32 ? 2 : 4;
+// Head vectors that a warp loads before it works on the last ones: with one the 4 x 2048 tokens take 45 us, with four 44, for
+// then fewer warps fit an SM.
+constexpr int kAppendSteps = 2;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -32,58 +41,117 @@ __device__ __forceinline__ void unpack_bf16(uint32_t w, float& a, float& b) {
     b = __uint_as_float(w & 0xFFFF0000u);
 }
 
-// Eight elements as they lie in memory.
-template <bool F32>
+// Two float32 operations at once.
+__device__ __forceinline__ uint64_t bits2(const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); }
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+
+// A lane's elements: a[j] turns with b[j].
+struct Pairs {
+    float2 a[2], b[2];
+};
+
+// Float32 elements x (four from e0 on, or the first of eight) and y: pairs of neighbours (NEAR), or of x and y.
+template <bool NEAR>
+__device__ __forceinline__ Pairs pairs_of(const float4& x, const float4& y) {
+    Pairs v;
+    if constexpr (NEAR) {
+        v.a[0] = make_float2(x.x, x.z), v.b[0] = make_float2(x.y, x.w);
+        v.a[1] = make_float2(y.x, y.z), v.b[1] = make_float2(y.y, y.w);
+    } else {
+        v.a[0] = make_float2(x.x, x.y), v.a[1] = make_float2(x.z, x.w);
+        v.b[0] = make_float2(y.x, y.y), v.b[1] = make_float2(y.z, y.w);
+    }
+    return v;
+}
+
+// A lane's eight elements as they lie in memory.
+template <bool F32, bool NEAR>
 struct Raw {
     uint4 w[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void* base, int64_t elem) {
-        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + elem * (F32 ? 4 : 2));
-#pragma unroll
-        for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = __ldg(s + i);
-    }
-    __device__ __forceinline__ void values(float (&x)[8]) const {
+    // the elements at `first`, and four more at `second` bytes from there
+    __device__ __forceinline__ void load(const uint8_t* first, int second) {
         if constexpr (F32) {
-            x[0] = __uint_as_float(w[0].x), x[1] = __uint_as_float(w[0].y);
-            x[2] = __uint_as_float(w[0].z), x[3] = __uint_as_float(w[0].w);
-            x[4] = __uint_as_float(w[1].x), x[5] = __uint_as_float(w[1].y);
-            x[6] = __uint_as_float(w[1].z), x[7] = __uint_as_float(w[1].w);
+            w[0] = __ldg(reinterpret_cast<const uint4*>(first));
+            w[1] = __ldg(reinterpret_cast<const uint4*>(first + second));
+        } else if constexpr (NEAR) {
+            w[0] = __ldg(reinterpret_cast<const uint4*>(first));
         } else {
-            unpack_bf16(w[0].x, x[0], x[1]);
-            unpack_bf16(w[0].y, x[2], x[3]);
-            unpack_bf16(w[0].z, x[4], x[5]);
-            unpack_bf16(w[0].w, x[6], x[7]);
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(first));
+            const uint2 y = __ldg(reinterpret_cast<const uint2*>(first + second));
+            w[0] = make_uint4(x.x, x.y, y.x, y.y);
         }
+    }
+    __device__ __forceinline__ Pairs values() const {
+        float4 x, y;
+        if constexpr (F32) {
+            x = make_float4(__uint_as_float(w[0].x), __uint_as_float(w[0].y), __uint_as_float(w[0].z), __uint_as_float(w[0].w));
+            y = make_float4(__uint_as_float(w[1].x), __uint_as_float(w[1].y), __uint_as_float(w[1].z), __uint_as_float(w[1].w));
+        } else {
+            unpack_bf16(w[0].x, x.x, x.y);
+            unpack_bf16(w[0].y, x.z, x.w);
+            unpack_bf16(w[0].z, y.x, y.y);
+            unpack_bf16(w[0].w, y.z, y.w);
+        }
+        return pairs_of<NEAR>(x, y);
     }
 };
 
+template <bool NEAR>
+__device__ __forceinline__ void store_pairs(uint16_t* dst, int second, const Pairs& v) {
+    if constexpr (NEAR) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v.a[0].x, v.b[0].x), pack_bf16(v.a[0].y, v.b[0].y),
+                                                    pack_bf16(v.a[1].x, v.b[1].x), pack_bf16(v.a[1].y, v.b[1].y));
+    } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.a[0].x, v.a[0].y), pack_bf16(v.a[1].x, v.a[1].y));
+        *reinterpret_cast<uint2*>(dst + second) = make_uint2(pack_bf16(v.b[0].x, v.b[0].y), pack_bf16(v.b[1].x, v.b[1].y));
+    }
+}
+
 // One warp takes `span` heads of one token, kSteps vectors of 32 / (D / 8) heads at a time: position, page and rotation are
 // looked up once for all of them, and the next vectors are on their way while it works on the last.
-template <int D, bool F32>
+template <int D, bool F32, bool NEAR>
 __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __grid_constant__ AppendParams p, int span) {
     constexpr int kLanes = D / 8;
     constexpr int kHeads = 32 / kLanes;
-    constexpr int kSteps = kAppendSteps<F32>;
+    constexpr int kSteps = kAppendSteps;
+    constexpr int kSize = F32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
-    const int heads = p.q_heads + 2 * p.kv_heads;
+    const int heads = p.q_heads + 2 * p.kv_heads, qk_heads = p.q_heads + p.kv_heads;
     const int per_token = (heads + span - 1) / span;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
     const int token = static_cast<int>(unit / per_token);
     const int h0 = static_cast<int>(unit - static_cast<int64_t>(token) * per_token) * span;
     const int h1 = h0 + span < heads ? h0 + span : heads;
-    const int e = (lane % kLanes) * 8;   // this lane's elements of a head
+    // this lane's elements of a head: four from e0 on, and four `second` elements later
+    const int l = lane % kLanes;
+    const bool turns = l < p.rot_dim / 8;
+    const bool split = !NEAR && turns;
+    const int e0 = split ? 4 * l : 8 * l, second = split ? p.rot_dim / 2 : 4;
     griddep_launch_dependents();
     griddep_wait();
     if (token >= p.tokens) return;
 
-    Raw<F32> next[kSteps];
+    // rows of the token, as if each held all heads
+    const uint8_t* src[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        src[k] = static_cast<const uint8_t*>(p.in[k]) +
+                 (token * p.in_stride[k] - (k == 0 ? 0 : k == 1 ? p.q_heads : qk_heads) * D + e0) * kSize;
+    Raw<F32, NEAR> next[kSteps];
     auto load = [&](int h) {   // the vectors from head h on
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int hd = h + i * kHeads + lane / kLanes;
-            if (hd >= h1) continue;
-            const int kind = hd < p.q_heads ? 0 : hd < p.q_heads + p.kv_heads ? 1 : 2;
-            const int hk = kind == 0 ? hd : hd - p.q_heads - (kind - 1) * p.kv_heads;
-            next[i].load(p.in[kind], token * p.in_stride[kind] + static_cast<int64_t>(hk) * D + e);
+            if (hd < h1) next[i].load((hd < p.q_heads ? src[0] : hd < qk_heads ? src[1] : src[2]) + hd * (D * kSize), second * kSize);
         }
     };
     load(h0);
@@ -92,8 +160,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
     const int pos = p.lengths[seq] - p.rows + (token - seq * p.rows);
     const bool live = pos >= 0;
 
-    // the cache slot
-    int64_t k_at = 0, v_at = 0;
+    // where head 0 would lie, and from head to head
+    uint16_t* dst[3] = {p.q_out + token * p.q_out_stride + e0, nullptr, nullptr};
+    const int64_t step[3] = {D, p.k.head, p.v.head};
     bool store = live;
     if (live) {
         const int slot = pos & ((1 << p.page_shift) - 1);
@@ -107,18 +176,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
                 if (lane == 0) atomicOr(p.err, QMM_KV_BAD_PAGE);
                 store = false;
             } else {
-                k_at = page * p.k.page + slot * p.k.slot;
-                v_at = page * p.v.page + slot * p.v.slot;
+                dst[1] = p.k.base + page * p.k.page + slot * p.k.slot - p.q_heads * p.k.head + e0;
+                dst[2] = p.v.base + page * p.v.page + slot * p.v.slot - qk_heads * p.v.head + e0;
             }
         }
     }
 
-    // this lane's cosines and sines: element pairs (e + j, e + j +- rot/2), or (2i, 2i + 1)
-    const int half = p.rot_dim >> 1;
-    const bool turns = e < p.rot_dim;
-    float c[8], s[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+    // this lane's cosines and sines
+    float2 c[2], s[2], neg[2];
     bool rotate = p.rot_dim > 0 && live;
     if (rotate) {
         const int at = p.positions != nullptr ? p.positions[token] : pos;
@@ -126,86 +191,71 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
             if (lane == 0) atomicOr(p.err, QMM_KV_BAD_POSITION);
             rotate = false;
         } else if (turns) {
-            const float* row = p.rope + static_cast<int64_t>(at) * p.rot_dim;
-            if (p.interleaved) {
-                const float4 cc = *reinterpret_cast<const float4*>(row + e / 2);
-                const float4 ss = *reinterpret_cast<const float4*>(row + half + e / 2);
-                c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
-                s[0] = -ss.x, s[1] = ss.x, s[2] = -ss.y, s[3] = ss.y;
-                s[4] = -ss.z, s[5] = ss.z, s[6] = -ss.w, s[7] = ss.w;
-            } else {
-                const int i0 = e < half ? e : e - half;
-                const float sign = e < half ? -1.0f : 1.0f;
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const float4 cc = *reinterpret_cast<const float4*>(row + i0 + j);
-                    const float4 ss = *reinterpret_cast<const float4*>(row + half + i0 + j);
-                    c[j] = cc.x, c[j + 1] = cc.y, c[j + 2] = cc.z, c[j + 3] = cc.w;
-                    s[j] = sign * ss.x, s[j + 1] = sign * ss.y, s[j + 2] = sign * ss.z, s[j + 3] = sign * ss.w;
-                }
-            }
+            const float* row = p.rope + static_cast<int64_t>(at) * p.rot_dim + 4 * l;
+            const float4 cc = *reinterpret_cast<const float4*>(row), ss = *reinterpret_cast<const float4*>(row + p.rot_dim / 2);
+            c[0] = make_float2(cc.x, cc.y), c[1] = make_float2(cc.z, cc.w);
+            s[0] = make_float2(ss.x, ss.y), s[1] = make_float2(ss.z, ss.w);
+            neg[0] = make_float2(-ss.x, -ss.y), neg[1] = make_float2(-ss.z, -ss.w);
         }
     }
-    const int other = !turns ? lane : e < half ? lane + half / 8 : lane - half / 8;
+    rotate = rotate && turns;
 
 #pragma unroll 1
     for (int h = h0; h < h1; h += kSteps * kHeads) {
-        Raw<F32> now[kSteps];
+        Raw<F32, NEAR> now[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) now[i] = next[i];
         load(h + kSteps * kHeads);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int hd = h + i * kHeads + lane / kLanes;
-            const bool in = hd < h1;
-            const int kind = hd < p.q_heads ? 0 : hd < p.q_heads + p.kv_heads ? 1 : 2;
-            const int hk = kind == 0 ? hd : hd - p.q_heads - (kind - 1) * p.kv_heads;
-            float y[8];
-            now[i].values(y);
-            float sum = 0.0f;
+            const int first = h + i * kHeads, hd = first + lane / kLanes;   // the first lane's head, and this one's
+            Pairs y = now[i].values();
+            if (first < qk_heads) {   // else nothing but values
+                float2 sq = mul2(y.a[0], y.a[0]);
+                sq = fma2(y.a[1], y.a[1], sq);
+                sq = fma2(y.b[0], y.b[0], sq);
+                sq = fma2(y.b[1], y.b[1], sq);
+                float sum = sq.x + sq.y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+                for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                if (hd < qk_heads) {
+                    const float* weight = hd < p.q_heads ? p.weight[0] : p.weight[1];
+                    if (weight != nullptr) {
+                        const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
+                        const Pairs w = pairs_of<NEAR>(__ldg(reinterpret_cast<const float4*>(weight + e0)),
+                                                       __ldg(reinterpret_cast<const float4*>(weight + e0 + second)));
+                        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            const float* weight = kind < 2 ? p.weight[kind] : nullptr;
-            if (weight != nullptr) {
-                const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
-                const float4 a = __ldg(reinterpret_cast<const float4*>(weight + e));
-                const float4 b = __ldg(reinterpret_cast<const float4*>(weight + e + 4));
-                y[0] *= inv * a.x, y[1] *= inv * a.y, y[2] *= inv * a.z, y[3] *= inv * a.w;
-                y[4] *= inv * b.x, y[5] *= inv * b.y, y[6] *= inv * b.z, y[7] *= inv * b.w;
-            }
-            if (rotate) {
-                float z[8];
-                if (p.interleaved) {
+                        for (int j = 0; j < 2; ++j) {
+                            y.a[j] = mul2(y.a[j], mul2(w.a[j], inv2));
+                            y.b[j] = mul2(y.b[j], mul2(w.b[j], inv2));
+                        }
+                    }
+                    if (rotate) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) z[j] = y[j ^ 1];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) z[j] = __shfl_sync(0xFFFFFFFFu, y[j], other);
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 a = fma2(y.a[j], c[j], mul2(y.b[j], neg[j]));
+                            y.b[j] = fma2(y.b[j], c[j], mul2(y.a[j], s[j]));
+                            y.a[j] = a;
+                        }
+                    }
                 }
-                if (turns && kind < 2) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = fmaf(y[j], c[j], z[j] * s[j]);
-                }
             }
-            uint4 w = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-            uint16_t* dst = nullptr;
-            if (kind == 0) {
-                if (!live) w = make_uint4(0u, 0u, 0u, 0u);
-                dst = p.q_out + token * p.q_out_stride + static_cast<int64_t>(hk) * D + e;
-            } else if (store) {
-                dst = kind == 1 ? p.k.base + k_at + hk * p.k.head + e : p.v.base + v_at + hk * p.v.head + e;
+            if (hd < p.q_heads && !live)
+                y.a[0] = y.a[1] = y.b[0] = y.b[1] = make_float2(0.0f, 0.0f);
+            const int kind = hd < p.q_heads ? 0 : hd < qk_heads ? 1 : 2;
+            if (hd < h1 && (kind == 0 || store)) {
+                uint16_t* const base = kind == 0 ? dst[0] : kind == 1 ? dst[1] : dst[2];
+                store_pairs<NEAR>(base + hd * (kind == 0 ? step[0] : kind == 1 ? step[1] : step[2]), second, y);
             }
-            if (in && dst != nullptr) *reinterpret_cast<uint4*>(dst) = w;
         }
     }
 }
 
-template <int D, bool F32>
+template <int D, bool F32, bool NEAR>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
     // few tokens: a warp for every load in flight; many: equal parts of a token, up to all of it
-    constexpr int kPerLoad = 32 / (D / 8) * kAppendSteps<F32>;
+    constexpr int kPerLoad = 32 / (D / 8) * kAppendSteps;
     const int heads = p.q_heads + 2 * p.kv_heads;
     const int64_t loads = (heads + kPerLoad - 1) / kPerLoad;
     int64_t each = p.tokens * loads / kManyWarps;
@@ -223,15 +273,22 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qmm_append_kernel<D, F32>, p, span);
+    return cudaLaunchKernelEx(&cfg, qmm_append_kernel<D, F32, NEAR>, p, span);
 }
 
 }  // namespace
 
 cudaError_t launch_append(int head_dim, bool in_f32, const AppendParams& p, cudaStream_t stream) {
-    if (head_dim == 64) return in_f32 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
-    if (head_dim == 128) return in_f32 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
-    return in_f32 ? launch<256, true>(p, stream) : launch<256, false>(p, stream);
+    auto with = [&](auto f32, auto near) -> cudaError_t {
+        constexpr bool F32 = decltype(f32)::value, NEAR = decltype(near)::value;
+        if (head_dim == 64) return launch<64, F32, NEAR>(p, stream);
+        if (head_dim == 128) return launch<128, F32, NEAR>(p, stream);
+        return launch<256, F32, NEAR>(p, stream);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (in_f32) return p.interleaved ? with(yes, yes) : with(yes, no);
+    return p.interleaved ? with(no, yes) : with(no, no);
 }
 
 }  // namespace qmmk
