@@ -21,8 +21,8 @@
 // (8 from 9 rows on) read it once and keep it in shared memory: 1 x 151,936 with top_k 50 8.7 us, 16 x 151,936 bfloat16
 // with top_p 0.9 38 us. The bound of many rows is the time that a row's steps hold an SM, so that the fewest CTAs that fill
 // the GPU take a row and read it again from the L2 cache where they need it, for parts of rows in shared memory leave no
-// room for other rows: 256 x 100,277 with top_k 50 in 34 us, 3.0 TB/s, where 8 CTAs each that keep the row took 85 us. What
-// top_p alone costs there (256 x 151,936 bfloat16 279 us) is an exponential and two additions in shared memory a logit.
+// room for other rows: 256 x 100,277 with top_k 50 in 30 us, 3.4 TB/s, where 8 CTAs each that keep the row took 85 us. What
+// top_p alone costs there (256 x 151,936 bfloat16 275 us) is an exponential and two additions in shared memory a logit.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -92,7 +92,8 @@ struct SampleShared {
     u64 few[kFew], few_value[kFew], pick, pick_value;
     uint32_t own[kList];   // slots of this CTA's candidates
     u64 scalar;
-    uint32_t list_size, sizes[kRanks];
+    uint32_t list_size, sizes[kRanks], hit_count;
+    uint16_t hits[kSampleThreads];
     Decision decision;
     Threshold threshold;
 };
@@ -257,28 +258,28 @@ struct RowSampler {
             }
         }
     }
-    // The chunks that the threads with `here` have read first (theirs are the 16 bytes at tid, tid + kSampleThreads, ...);
-    // where they are many, all lanes of a warp together for one thread's.
+    // The chunks that the threads with `here` have read first (theirs are the 16 bytes at tid, tid + kSampleThreads, ...). All
+    // threads call it, with sh.hit_count zero; where many chunks come from memory, a warp takes one such thread's at a time.
     template <class F>
     __device__ __forceinline__ void each_chunk_of(bool here, F f) const {
-        const int lane = threadIdx.x & 31, reads = chunks / kPerRead;
-        auto read = [&](int r) {
+        const int reads = chunks / kPerRead;
+        if (HELD || reads <= 8 * kSampleThreads) {
+            if (!here) return;
+            for (int r = threadIdx.x; r < reads; r += kSampleThreads) {
 #pragma unroll
-            for (int k = 0; k < kPerRead; ++k) {
-                float v[kVec];
-                load(r * kPerRead + k, v);
-                f(r * kPerRead + k, v);
+                for (int k = 0; k < kPerRead; ++k) {
+                    float v[kVec];
+                    load(r * kPerRead + k, v);
+                    f(r * kPerRead + k, v);
+                }
             }
-        };
-        if (reads <= 8 * kSampleThreads) {
-            if (here)
-                for (int r = threadIdx.x; r < reads; r += kSampleThreads) read(r);
             return;
         }
-        for (uint32_t votes = __ballot_sync(0xFFFFFFFFu, here); votes != 0; votes &= votes - 1) {
-            const int owner = static_cast<int>(threadIdx.x) - lane + __ffs(votes) - 1;
-            for (int r = owner + lane * kSampleThreads; r < reads; r += 32 * kSampleThreads) read(r);
-        }
+        if (here) sh.hits[atomicAdd(&sh.hit_count, 1u)] = static_cast<uint16_t>(threadIdx.x);
+        __syncthreads();
+        const int hits = static_cast<int>(sh.hit_count), lane = threadIdx.x & 31;
+        for (int h = threadIdx.x >> 5; h < hits; h += kSampleWarps)
+            each_chunk(sh.hits[h] + lane * kSampleThreads, reads, 32 * kSampleThreads, f);
     }
     __device__ __forceinline__ float depth(float l) const { return temperature == 1.0f || l == top ? l == top ? 0.0f : l - top : __fdiv_rn(l - top, temperature); }
     __device__ __forceinline__ float weight(float l, float z) const { return l == top ? 1.0f : expf(z); }
@@ -309,7 +310,7 @@ struct RowSampler {
 
     // Every CTA has a part of the first one's list for its own candidates.
     __device__ __forceinline__ void clear_list() {
-        if (threadIdx.x == 0) sh.list_size = 0u;
+        if (threadIdx.x == 0) sh.list_size = sh.hit_count = 0u;
     }
     __device__ __forceinline__ void add(uint32_t key, uint32_t index) {
         const uint32_t room = kList / ranks, at = atomicAdd(&sh.list_size, 1u);
