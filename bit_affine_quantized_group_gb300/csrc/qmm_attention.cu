@@ -215,8 +215,10 @@ struct Share {
         // most, for a second item costs a CTA several steps: n of them if that makes the longest share at most 2/5 longer.
         // Shares of fewer steps than short_share are not worth the joining of more parts, nor two such shares that of two.
         int n = 1, low = 0, high = 0;   // units of `low` are too many
+#pragma unroll 1
         for (;;) {
             int sum = 0, longest = 0;
+#pragma unroll 1
             for (int s = lane; s < p.seqs; s += 32) {
                 const SeqSpan span = span_of(p, s < 32 ? lane_len : length_of(p, s));
                 sum += span.units(n * p.min_unit);
