@@ -318,12 +318,24 @@ struct Parts {
 };
 
 // Join parts first, first + step, ... (n of them, at most kJoin) of `rows` query rows in that order; store(row, d,
-// values, m, l) takes the sums. `weights` is shared memory for (n + 2) * rows floats. The four copying warps do it.
+// values, m, l) takes the sums. `weights` is shared memory for (n + 2) * rows floats, `room` for `room_bytes` of parts:
+// loads to registers were six at a time and took 5 us for the 38 parts of 4 rows of 131,072 positions. The four copying
+// warps do it.
 template <int D, class Store>
 __device__ __forceinline__ void join_parts(const Parts& parts, int first, int step, int n, int rows, float* weights,
-                                           int tid, Store store) {
+                                           const float* room, int room_bytes, int tid, Store store) {
     const int warp = tid >> 5, lane = tid & 31;
     float* const sums = weights + n * rows;
+    const int most = room_bytes / (n * D * 4);   // rows that have room at once
+    const int together = rows < most ? rows : most;
+    auto fetch = [&](int r0, int count) {
+        for (int i = warp; i < n; i += 4) {
+            const float* src = parts.o + parts.row(first + i * step, r0) * D;
+            const uint32_t dst = smem_u32(room) + i * count * (D * 4);
+            for (int e = lane; e < count * (D / 4); e += 32) cp_async_16(dst + e * 16, src + e * 4);
+        }
+    };
+    fetch(0, together);
     for (int r = warp; r < rows; r += 4) {
         constexpr int kSets = (kJoin + 31) / 32;
         float2 ml[kSets];
@@ -354,28 +366,29 @@ __device__ __forceinline__ void join_parts(const Parts& parts, int first, int st
             sums[2 * r + 1] = sum;
         }
     }
-    named_barrier(3, 128);
-    for (int e = tid; e < rows * (D / 4); e += 128) {
-        const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        constexpr int kAtOnce = 6;   // loads in flight, also for the rest
-        for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-            float4 v[kAtOnce];
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                if (i0 + i < n)
-                    v[i] = __ldcg(reinterpret_cast<const float4*>(parts.o + parts.row(first + (i0 + i) * step, r) * D + d));
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                if (i0 + i >= n) continue;
-                const float a = weights[(i0 + i) * rows + r];
-                acc.x = fmaf(v[i].x, a, acc.x);
-                acc.y = fmaf(v[i].y, a, acc.y);
-                acc.z = fmaf(v[i].z, a, acc.z);
-                acc.w = fmaf(v[i].w, a, acc.w);
-            }
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += together) {
+        const int count = rows - r0 < together ? rows - r0 : together;
+        if (r0 > 0) {
+            named_barrier(3, 128);
+            fetch(r0, count);
         }
-        store(r, d, acc, sums[2 * r], sums[2 * r + 1]);
+        cp_async_wait_all();
+        named_barrier(3, 128);
+        for (int e = tid; e < count * (D / 4); e += 128) {
+            const int r = r0 + e / (D / 4), d = e % (D / 4) * 4;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(room + (i * count * (D / 4) + e) * 4);
+                const float a = weights[i * rows + r];
+                acc.x = fmaf(v.x, a, acc.x);
+                acc.y = fmaf(v.y, a, acc.y);
+                acc.z = fmaf(v.z, a, acc.z);
+                acc.w = fmaf(v.w, a, acc.w);
+            }
+            store(r, d, acc, sums[2 * r], sums[2 * r + 1]);
+        }
     }
 }
 
@@ -387,7 +400,10 @@ struct Cut {
 // The end of a cut head of up to 16 rows, by the four copying warps: the CTA that arrives last joins the parts, kJoin of
 // them at once, more first in runs of kJoinRun.
 template <int D, int RW>
-__device__ __forceinline__ void join_cut(const AttnParams& p, const Cut& cut, float* weights, uint32_t* s_last, int tid) {
+__device__ __forceinline__ void join_cut(const AttnParams& p, const Cut& cut, float* weights, const float* room,
+                                         uint32_t* s_last, int tid) {
+    constexpr int kRoom = AttnCfg<D, RW>::kTeams * AttnCfg<D, RW>::kRingBytes;
+    static_assert(kRoom >= kJoin * D * 4, "room for a row of every part");
     const int cta = blockIdx.x;
     const Parts parts{p.part, p.part_ml, 16 * RW, cut.c0};
     auto arrive = [&](uint32_t* counter, int of) -> bool {
@@ -408,7 +424,7 @@ __device__ __forceinline__ void join_cut(const AttnParams& p, const Cut& cut, fl
         const int size = cut.n - run < kJoinRun ? cut.n - run : kJoinRun;
         if (!arrive(p.counters + kAttnMaxCtas + cut.c0 + run, size)) return;
         if (size > 1) {
-            join_parts<D>(parts, run, 1, size, cut.rows, weights, tid,
+            join_parts<D>(parts, run, 1, size, cut.rows, weights, room, kRoom, tid,
                           [&](int r, int d, const float4& acc, float top, float sum) {
                               const int64_t at = parts.row(run, r);
                               *reinterpret_cast<float4*>(p.part + at * D + d) = acc;
@@ -418,7 +434,7 @@ __device__ __forceinline__ void join_cut(const AttnParams& p, const Cut& cut, fl
     }
     const int left = runs ? (cut.n + kJoinRun - 1) / kJoinRun : cut.n;
     if (!arrive(p.counters + cut.c0, left)) return;
-    join_parts<D>(parts, 0, runs ? kJoinRun : 1, left, cut.rows, weights, tid,
+    join_parts<D>(parts, 0, runs ? kJoinRun : 1, left, cut.rows, weights, room, kRoom, tid,
                   [&](int r, int d, const float4& acc, float, float sum) {
                       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                       const int row = cut.row0 + r, tok = (row * p.group_inverse) >> 20;
@@ -435,7 +451,8 @@ __device__ __forceinline__ void join_cut(const AttnParams& p, const Cut& cut, fl
 // zeros. (Tensor copies of the same boxes came to 35 GB/s for one CTA; these to over 80.)
 template <int D, int RW>
 __device__ __forceinline__ void copy_share(const AttnParams& p, Share share, uint32_t rings, uint64_t* full,
-                                           uint64_t* empty, float* weights, uint32_t* s_last, int warp, int lane) {
+                                           uint64_t* empty, float* weights, const float* room, uint32_t* s_last, int warp,
+                                           int lane) {
     using Cfg = AttnCfg<D, RW>;
     constexpr int kChunks = D / 8;              // 16-byte chunks of a row
     constexpr int kRowsPerCopy = 32 / kChunks;  // rows that one copy instruction of a warp covers
@@ -535,9 +552,9 @@ __device__ __forceinline__ void copy_share(const AttnParams& p, Share share, uin
     }
     cp_async_wait_all();   // no copy lands after the CTA has ended, not even where the computing warps gave up waiting
     if constexpr (RW == 1) {
-        named_barrier(2, Cfg::kThreads);   // this share's parts are written
-        if (first.n > 0) join_cut<D, RW>(p, first, weights, s_last, warp * 32 + lane);
-        if (last.n > 0) join_cut<D, RW>(p, last, weights, s_last, warp * 32 + lane);
+        named_barrier(2, Cfg::kThreads);   // this share's parts are written, and its rings read
+        if (first.n > 0) join_cut<D, RW>(p, first, weights, room, s_last, warp * 32 + lane);
+        if (last.n > 0) join_cut<D, RW>(p, last, weights, room, s_last, warp * 32 + lane);
     }
 }
 
@@ -575,7 +592,8 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
     if (!any) return;
     if (warp >= Cfg::kCompute) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kCopyRegs));
-        copy_share<D, RW>(p, share, ring, full, empty, s_join, s_last, warp - Cfg::kCompute, lane);
+        copy_share<D, RW>(p, share, ring, full, empty, s_join, reinterpret_cast<const float*>(smem), s_last, warp - Cfg::kCompute,
+                          lane);
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kComputeRegs));
