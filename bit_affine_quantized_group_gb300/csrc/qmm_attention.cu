@@ -422,8 +422,9 @@ __device__ __forceinline__ void join_cut(const AttnParams& p, const Cut& cut, fl
     if (runs) {
         const int run = (cta - cut.c0) / kJoinRun * kJoinRun;
         const int size = cut.n - run < kJoinRun ? cut.n - run : kJoinRun;
-        if (!arrive(p.counters + kAttnMaxCtas + cut.c0 + run, size)) return;
+        // a last run of one part has nothing to wait for, and the next head may begin in its CTA and count there
         if (size > 1) {
+            if (!arrive(p.counters + kAttnMaxCtas + cut.c0 + run, size)) return;
             join_parts<D>(parts, run, 1, size, cut.rows, weights, room, kRoom, tid,
                           [&](int r, int d, const float4& acc, float top, float sum) {
                               const int64_t at = parts.row(run, r);

@@ -435,3 +435,17 @@ def test_append_then_attend(q):
     assert plan.error_flags() == 0
     assert torch.equal(k.view(torch.int16), k1.view(torch.int16))
     assert torch.allclose(one.float(), whole.float(), rtol=2 ** -7, atol=2 ** -12)
+
+
+def test_long_neighbours_joined_in_runs(q):
+    """Two long sequences among many short ones, which a GPU of 152 SMs cuts into 49 and 216 parts that meet in one CTA: the
+    49th part of the first is a run of its own there, where the second's first run begins."""
+    import torch
+    lengths = [388 * 64, 1724 * 64] + [1] * 320
+    plan, qt, k, v, table, lens, out = _attend(q, torch, lengths, 2, 1, 64, page=128, seed=5)
+    dev, cache = qt.to(DEV), q.KVCache(k, v)
+    for _ in range(30):
+        again = torch.full_like(out, 77.0)
+        q.attention(plan, dev, cache, table, lens, again)
+        assert torch.equal(again, out)
+    assert plan.error_flags() == 0
