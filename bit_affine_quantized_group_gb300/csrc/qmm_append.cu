@@ -8,9 +8,9 @@
 // float32 until the one rounding to bfloat16.
 //
 // The bound of many tokens is the bytes, but instructions are close to it: 4 x
-// 2048 tokens of 48 heads of 128 take 39.5 us, 5.2 TB/s, where pairs that met by
+// 2048 tokens of 48 heads of 128 take 35.7 us, 5.7 TB/s, where pairs that met by
 // shuffles, single float32 operations and addresses computed for every vector
-// took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.1 us for
+// took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.3 us for
 // one), and a warp takes only as many heads as it can have in flight.
 #include <cuda_bf16.h>
 
@@ -25,12 +25,12 @@ namespace qmmk {
 namespace {
 
 constexpr int kAppendWarps = 4;
-// Parts of tokens that are worth it: a few more than the warps that run at once. (Three times as many: 42 us for the 4 x
-// 2048 tokens instead of 39.5, for what a warp looks up for a token takes longer than its last round lasts.)
+// Parts of tokens that are worth it: a few more than the warps that run at once. (Three times as many took a
+// fifteenth longer for the 4 x 2048 tokens, for what a warp looks up for a token outweighs a fuller last round.)
 constexpr int64_t kManyWarps = 152 * 40;
 
-// Head vectors that a warp loads before it works on the last ones: with one the 4 x 2048 tokens take 45 us, with four 44, for
-// then fewer warps fit an SM.
+// Head vectors that a warp loads before it works on the last ones: with one or four the 4 x 2048 tokens took about a tenth
+// longer: less in flight, or fewer warps on an SM.
 constexpr int kAppendSteps = 2;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -160,33 +160,34 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
 
     const int seq = token / p.rows;
     const int pos = p.lengths[seq] - p.rows + (token - seq * p.rows);
-    const bool live = pos >= 0;
+    if (pos < 0) {   // a token before the sequence's first: its queries are zero
+        for (int hd = h0 + lane / kLanes; hd < h1 && hd < p.q_heads; hd += kHeads)
+            *reinterpret_cast<uint4*>(p.q_out + token * p.q_out_stride + static_cast<int64_t>(hd) * D + 8 * l) =
+                make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
 
     // where head 0 would lie, and from head to head
     uint16_t* dst[3] = {p.q_out + token * p.q_out_stride + e0, nullptr, nullptr};
     const int64_t step[3] = {D, p.k.head, p.v.head};
-    bool store = live;
-    if (live) {
-        const int slot = pos & ((1 << p.page_shift) - 1);
-        const int index = pos >> p.page_shift;
-        if (index >= p.max_pages) {
-            if (lane == 0) atomicOr(p.err, QMM_KV_BAD_LENGTH);
-            store = false;
+    bool store = false;
+    const int slot = pos & ((1 << p.page_shift) - 1), index = pos >> p.page_shift;
+    if (index >= p.max_pages) {
+        if (lane == 0) atomicOr(p.err, QMM_KV_BAD_LENGTH);
+    } else {
+        const int64_t page = p.page_table[static_cast<int64_t>(seq) * p.max_pages + index];
+        if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) atomicOr(p.err, QMM_KV_BAD_PAGE);
         } else {
-            const int64_t page = p.page_table[static_cast<int64_t>(seq) * p.max_pages + index];
-            if (page < 0 || page >= p.num_pages) {
-                if (lane == 0) atomicOr(p.err, QMM_KV_BAD_PAGE);
-                store = false;
-            } else {
-                dst[1] = p.k.base + page * p.k.page + slot * p.k.slot - p.q_heads * p.k.head + e0;
-                dst[2] = p.v.base + page * p.v.page + slot * p.v.slot - qk_heads * p.v.head + e0;
-            }
+            dst[1] = p.k.base + page * p.k.page + slot * p.k.slot - p.q_heads * p.k.head + e0;
+            dst[2] = p.v.base + page * p.v.page + slot * p.v.slot - qk_heads * p.v.head + e0;
+            store = true;
         }
     }
 
     // this lane's cosines and sines
     float2 c[2], s[2], neg[2];
-    bool rotate = p.rot_dim > 0 && live;
+    bool rotate = p.rot_dim > 0;
     if (rotate) {
         const int at = p.positions != nullptr ? p.positions[token] : pos;
         if (at < 0 || at >= p.rope_len) {
@@ -243,8 +244,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
                     }
                 }
             }
-            if (hd < p.q_heads && !live)
-                y.a[0] = y.a[1] = y.b[0] = y.b[1] = make_float2(0.0f, 0.0f);
             const int kind = hd < p.q_heads ? 0 : hd < qk_heads ? 1 : 2;
             if (hd < h1 && (kind == 0 || store)) {
                 uint16_t* const base = kind == 0 ? dst[0] : kind == 1 ? dst[1] : dst[2];
