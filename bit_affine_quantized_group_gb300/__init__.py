@@ -197,13 +197,21 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# What calls of a few microseconds take from torch, looked up once (torch is imported when it is first needed).
+_F32 = _BF16 = _I32 = _RAW_STREAM = None
+
+
+def _bind_torch() -> None:
+    global _F32, _BF16, _I32, _RAW_STREAM
+    import torch
+    _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+    _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_on(stream, device: int) -> int:
     """_stream_handle without a Stream object for the current stream: calls of a few microseconds notice it."""
-    if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and device >= 0:
-            return raw(device)
+    if stream is None and _RAW_STREAM is not None and device >= 0:
+        return _RAW_STREAM(device)
     return _stream_handle(stream)
 
 
@@ -364,6 +372,7 @@ class KVPlan:
 
     def __init__(self, *args, torch_workspace: bool = True, device=None, **kwargs):
         import torch
+        _bind_torch()
         self.desc = d = make_kv_desc(*args, **kwargs)
         st = kv_validate_desc(d)
         if st != QMM_OK:
@@ -382,7 +391,7 @@ class KVPlan:
             st = _lib().qmm_kv_plan(ctypes.byref(self._handle), ctypes.byref(d), ws, nbytes)
         if st != QMM_OK:
             raise QmmError(st, "qmm_kv_plan")
-        self.device = dev
+        self.device, self._device_index = dev, dev.index
         self.q_width, self.kv_width = d.q_heads * d.head_dim, d.kv_heads * d.head_dim
         self.page_shape = (d.kv_heads, d.page_size, d.head_dim)
         self.max_pages, self.head_dim, self.rot_dim = d.max_pages, d.head_dim, d.rot_dim
@@ -444,11 +453,11 @@ def _rows(t, tokens, width, dtype, what):
     return st[0]
 
 
-def _check_step(plan, cache, page_table, lengths, tokens, int32):
+def _check_step(plan, cache, page_table, lengths, tokens):
     seqs = lengths.numel()
     if cache.page_shape != plan.page_shape:
         raise ValueError("the cache's pages are not the plan's [kv_heads, page_size, head_dim]")
-    if lengths.dtype is not int32 or page_table.dtype is not int32 or not page_table.is_contiguous() or \
+    if lengths.dtype is not _I32 or page_table.dtype is not _I32 or not page_table.is_contiguous() or \
             not lengths.is_contiguous() or page_table.shape != (seqs, plan.max_pages):
         raise ValueError("lengths [seqs] and page_table [seqs, max_pages] are contiguous int32 tensors")
     rows, rest = divmod(tokens, seqs) if seqs else (0, tokens)
@@ -462,26 +471,26 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
     """Norms of q and k for each head, rotation, and the append of k and v to the cache (qmm_qk_norm_rope). q, k, v:
     [tokens, heads * head_dim] of float32 or bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and
     k_weight: float32 [head_dim] or None; rope: float32 [positions, rot_dim], cosines then sines."""
-    import torch
-    f32, bf16, dtype, tokens = torch.float32, torch.bfloat16, q.dtype, q.shape[0]
-    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, torch.int32)
-    if dtype is not f32 and dtype is not bf16:
+    dtype, tokens = q.dtype, q.shape[0]
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
+    if dtype is not _F32 and dtype is not _BF16:
         raise ValueError("q, k and v are float32 or bfloat16")
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not f32 or w.numel() != plan.head_dim or not w.is_contiguous()):
+        if w is not None and (w.dtype is not _F32 or w.numel() != plan.head_dim or not w.is_contiguous()):
             raise ValueError("q_weight and k_weight are float32 [head_dim] or None")
-    if plan.rot_dim and (rope is None or rope.dtype is not f32 or not rope.is_contiguous() or rope.shape[-1] != plan.rot_dim):
+    if plan.rot_dim and (rope is None or rope.dtype is not _F32 or not rope.is_contiguous() or rope.shape[-1] != plan.rot_dim):
         raise ValueError("rope is a float32 tensor [positions, rot_dim]")
-    if positions is not None and (positions.dtype is not torch.int32 or positions.numel() != tokens or
+    if positions is not None and (positions.dtype is not _I32 or positions.numel() != tokens or
                                   not positions.is_contiguous()):
         raise ValueError("positions is an int32 tensor [tokens]")
     _APPEND_ARGS.pack_into(
         plan._args, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, tokens, plan.q_width, dtype, "q"),
-        _rows(k, tokens, plan.kv_width, dtype, "k"), _rows(v, tokens, plan.kv_width, dtype, "v"), _ptr(q_weight),
-        _ptr(k_weight), _ptr(rope), 0 if rope is None else rope.shape[0], lengths.data_ptr(), _ptr(positions),
-        page_table.data_ptr(), out.data_ptr(), _rows(out, tokens, plan.q_width, bf16, "out"), seqs, rows,
-        QMM_IN_F32 if dtype is f32 else QMM_IN_BF16)
-    st = _lib().qmm_qk_norm_rope(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan.device.index))
+        _rows(k, tokens, plan.kv_width, dtype, "k"), _rows(v, tokens, plan.kv_width, dtype, "v"),
+        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+        0 if rope is None else rope.data_ptr(), 0 if rope is None else rope.shape[0], lengths.data_ptr(),
+        0 if positions is None else positions.data_ptr(), page_table.data_ptr(), out.data_ptr(),
+        _rows(out, tokens, plan.q_width, _BF16, "out"), seqs, rows, QMM_IN_F32 if dtype is _F32 else QMM_IN_BF16)
+    st = _LIB.qmm_qk_norm_rope(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_qk_norm_rope")
 
@@ -489,13 +498,12 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
 def attention(plan: KVPlan, q, cache: KVCache, page_table, lengths, out, stream=None) -> None:
     """Attention of the new tokens over the cache (qmm_attention): q and out [tokens, q_heads, head_dim] bfloat16 (or
     [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
-    import torch
-    tokens, bf16 = q.shape[0], torch.bfloat16
-    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, torch.int32)
+    tokens = q.shape[0]
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
     _ATTENTION_ARGS.pack_into(plan._args, 0, q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
-                              _rows(q, tokens, plan.q_width, bf16, "q"), _rows(out, tokens, plan.q_width, bf16, "out"),
+                              _rows(q, tokens, plan.q_width, _BF16, "q"), _rows(out, tokens, plan.q_width, _BF16, "out"),
                               seqs, rows)
-    st = _lib().qmm_attention(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan.device.index))
+    st = _LIB.qmm_attention(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_attention")
 
@@ -504,10 +512,11 @@ def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stre
     """Draw a token for each row of logits [M, vocab] (float32 or bfloat16, rows of any stride) from the uniform
     numbers u (qmm_sample): tokens int32 [M], probs float32 [M] or None. temperature, top_p, min_p: float32 [M];
     top_k: int32 [M]."""
-    import torch
-    f32, i32, dtype = torch.float32, torch.int32, logits.dtype
+    if _F32 is None:
+        _bind_torch()
+    f32, i32, dtype = _F32, _I32, logits.dtype
     shape, strides = logits.shape, logits.stride()
-    if len(shape) != 2 or (dtype is not f32 and dtype is not torch.bfloat16) or strides[1] != 1:
+    if len(shape) != 2 or (dtype is not f32 and dtype is not _BF16) or strides[1] != 1:
         raise ValueError("logits are float32 or bfloat16 rows of adjacent elements")
     M = shape[0]
     for t, want in ((temperature, f32), (top_k, i32), (top_p, f32), (min_p, f32), (u, f32), (tokens, i32)):
