@@ -8,7 +8,7 @@
 // float32 until the one rounding to bfloat16.
 //
 // The bound of many tokens is the bytes, but instructions are close to it: 4 x
-// 2048 tokens of 48 heads of 128 take 35.7 us, 5.7 TB/s, where pairs that met by
+// 2048 tokens of 48 heads of 128 take 35.1 us, 5.8 TB/s, where pairs that met by
 // shuffles, single float32 operations and addresses computed for every vector
 // took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.3 us for
 // one), and a warp takes only as many heads as it can have in flight.
@@ -129,9 +129,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
     const int lane = threadIdx.x & 31;
     const int heads = p.q_heads + 2 * p.kv_heads, qk_heads = p.q_heads + p.kv_heads;
     const int per_token = (heads + span - 1) / span;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-    const int token = static_cast<int>(unit / per_token);
-    const int h0 = static_cast<int>(unit - static_cast<int64_t>(token) * per_token) * span;
+    // (32 bits: tokens have 384 bytes or more for each part, so that the memory holds fewer than 2^30 parts)
+    const uint32_t unit = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int token = static_cast<int>(unit / static_cast<uint32_t>(per_token));
+    const int h0 = static_cast<int>(unit - static_cast<uint32_t>(token) * per_token) * span;
     const int h1 = h0 + span < heads ? h0 + span : heads;
     // this lane's elements of a head: four from e0 on, and four `second` elements later
     const int l = lane % kLanes;
