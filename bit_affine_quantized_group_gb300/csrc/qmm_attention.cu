@@ -5,7 +5,7 @@
 // tensor-core products, and one pass over the cache keeps each row's running
 // maximum m and sum l:
 //   m' = max(m, S),  P = 2^(S - m'),  l = l 2^(m - m') + sum P,  O = O 2^(m - m') + P V.
-// P enters the second product as two bfloat16 terms (P = hi + lo to 2^-17), so
+// P enters the second product as two bfloat16 terms (P = hi + lo to 2^-16), so
 // its rounding stays below that of the bfloat16 output.
 //
 // The bound is the cache's bytes: 4 D per position and cache head against
@@ -120,11 +120,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// a and b as bfloat16 pairs: their upper halves, and the rounded remainders (hi + lo is within 2^-17).
+// Weights a and b, at least 0, as bfloat16 pairs: their upper halves, and the rounded remainders (hi + lo is within 2^-16).
+// The remainders get 2^-24 of the upper halves more, so that no weight from 2^-109 on has a lo of 0: that times an infinite
+// value were NaN where the weight times it is infinite. (Below, weights of no more than 8 bits still have one.)
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+    constexpr float kLess = 1.0f - 0x1p-24f;
     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
     hi = __byte_perm(ua, ub, 0x7632);
-    lo = pack_bf16(a - __uint_as_float(ua & 0xFFFF0000u), b - __uint_as_float(ub & 0xFFFF0000u));
+    lo = pack_bf16(fmaf(__uint_as_float(ua & 0xFFFF0000u), -kLess, a), fmaf(__uint_as_float(ub & 0xFFFF0000u), -kLess, b));
 }
 
 __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
