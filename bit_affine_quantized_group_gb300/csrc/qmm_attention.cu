@@ -819,9 +819,9 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
             bool apart = false;
             if (!whole && p.rows > 1) {
                 bool bad = false;
-                auto look = [&](int first, int end) {   // positions [first, end) of the part
-                    first = first > 0 ? first : 0;
-                    end = end < kPartRows ? end : kPartRows;
+                auto look = [&](int first, int end) {   // positions [first, end) of the part; they may be far from it
+                    first = min(max(first, 0), kPartRows);
+                    end = min(max(end, 0), kPartRows);
                     for (int c = first * (D / 8) + lane; c < end * (D / 8); c += 32) {
                         const uint32_t at = (part * kPartRows + c / (D / 8)) * 128 + ((c % (D / 8)) >> 3) * (kStep * 128);
                         const uint4 w = lds128(vst + at + ((c & 7) << 4));

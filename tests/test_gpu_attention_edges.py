@@ -141,3 +141,36 @@ def test_strange_values_reach_the_rows_that_see_them(q, d, hq, hkv, rows, window
             assert _near(got[rest], want[rest], tol[rest]), (j, keys)
             mine = got[see, own]
             assert (np.isnan(mine) if bad != bad else mine == bad).all(), (j, keys, mine)
+
+
+@pytest.mark.parametrize("rows,hq", [(2, 1), (3, 8)])
+def test_a_window_of_many_millions(q, rows, hq):
+    """Offsets of positions from a window's ends that pass 32 bits when they are multiplied by a row's size. All pages of the
+    table are the same one, so that a score's share of the softmax is the number of times that the window shows its slot."""
+    import torch
+    d, page, pages, window = 256, 1024, 65600, (1 << 26) + 1000
+    gen = torch.Generator().manual_seed(23)
+    k, v = (torch.randn((1, 1, page, d), generator=gen).to(torch.bfloat16) for _ in range(2))
+    qs = torch.randn((rows, hq, d), generator=gen).to(torch.bfloat16)
+    length = pages * page - 5
+    plan = q.KVPlan(hq, 1, d, page, max_seqs=1, max_rows=rows, max_pages=pages, window=window)
+    out = torch.full(qs.shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    q.attention(plan, qs.to(DEV), q.KVCache(k.to(DEV), v.to(DEV)), torch.zeros((1, pages), dtype=torch.int32, device=DEV),
+                torch.tensor([length], dtype=torch.int32, device=DEV), out)
+    got = out.double().cpu().numpy()
+    assert plan.error_flags() == 0
+    keys, values = k[0, 0].double().numpy(), v[0, 0].double().numpy()
+    slot = np.arange(page)
+    upto = lambda n: n // page + (slot < n % page)   # times that each slot lies before position n   # noqa: E731
+    for r in range(rows):
+        pos = length - rows + r
+        times = upto(pos + 1) - upto(pos + 1 - window)
+        for h in range(hq):
+            x = qs[r, h].double().numpy()
+            a = keys @ x * d ** -0.5
+            e = np.exp(a - a.max()) * times
+            want = (e / e.sum()) @ values
+            size = np.max(np.abs(keys) @ np.abs(x)) * d ** -0.5
+            # float32 sums over the 7,000 steps of a share, two additions each
+            tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -15 + 2.0 ** -19 * size + 2.0 ** -24 * 2 ** 14) * np.max(np.abs(values))
+            assert _near(got[r, h], want, tol)
