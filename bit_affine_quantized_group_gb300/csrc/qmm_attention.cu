@@ -156,6 +156,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
 // The steps of one sequence: those of the sinks, then from the window's first position to the end.
 struct SeqSpan {
     int len;        // positions in the cache, at most what the page table holds
+    int first;      // position of the first new token, by the length as it is given
     int low;        // first position that the window shows to any row
     int sink_steps;
     int low_step;
@@ -171,30 +172,29 @@ struct SeqSpan {
     }
 };
 
-// `len`: of the sequence, brought to what the page table holds.
+// `len`: of the sequence, 0 at least. Rows stand where it says even if it is more than the page table holds, as the append
+// puts them.
 __device__ __forceinline__ SeqSpan span_of(const AttnParams& p, int len) {
     SeqSpan s;
-    s.len = len;
+    s.len = min(len, p.positions);
+    s.first = len - p.rows;
     s.low = 0;
     s.low_step = 0;
     s.sink_steps = 0;
     if (p.window > 0) {
-        const int64_t low = static_cast<int64_t>(len) - p.rows - p.window + 1;
-        s.low = low > 0 ? static_cast<int>(low) : 0;
+        s.low = min(max(max(s.first, 0) - p.window + 1, 0), s.len);
         s.low_step = s.low / kStep;
-        const int64_t st = (static_cast<int64_t>(p.sinks) + kStep - 1) / kStep;
-        s.sink_steps = st < s.low_step ? static_cast<int>(st) : s.low_step;
+        s.sink_steps = min((p.sinks + kStep - 1) / kStep, s.low_step);
     }
-    s.steps = s.sink_steps + (len + kStep - 1) / kStep - s.low_step;
+    s.steps = s.sink_steps + (s.len + kStep - 1) / kStep - s.low_step;
     return s;
 }
 
 __device__ __forceinline__ int length_of(const AttnParams& p, int seq) {
     if (seq >= p.seqs) return 0;
-    const int most = p.max_pages << p.page_shift;
     const int len = p.lengths[seq];
-    if (len > most) atomicOr(p.err, QMM_KV_BAD_LENGTH);
-    return len > most ? most : len > 0 ? len : 0;
+    if (len > p.positions) atomicOr(p.err, QMM_KV_BAD_LENGTH);
+    return len > 0 ? len : 0;
 }
 
 // Floor of a * b / c; a 64-bit division takes as long as a load.
@@ -650,7 +650,8 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
         const int seq = it.seq, head = it.head, row0 = it.row0;
         const int rows_left = p.rows * p.group - row0;
         const int rows = rows_left < kRows ? rows_left : kRows;
-        const int first_pos = span.len - p.rows;   // the position of the sequence's first new token
+        const int first_pos = span.first;
+        auto seq_end = [&]() -> int { return min(first_pos + p.rows, p.positions); };   // span.len again
 
         // query row = (token, head of the group)
         auto token_of = [&](int i) -> int { return ((row0 + i) * p.group_inverse) >> 20; };   // (row0 + i) / group
@@ -754,8 +755,8 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
             side_done();
 
             // positions that every row sees need no mask
-            const bool whole = pos0 + 16 * kTiles - 1 <= first_pos &&
-                               (p.window == 0 || span.len - 1 - pos0 < p.window || pos0 + 16 * kTiles <= p.sinks);
+            const bool whole = pos0 + 16 * kTiles <= min(first_pos + 1, p.positions) &&
+                               (p.window == 0 || first_pos + p.rows - 1 - pos0 < p.window || pos0 + 16 * kTiles <= p.sinks);
             float alpha[2];
             float pr[kTiles][2][4];   // scores, then weights: [tile][row of the lane][position]
 #pragma unroll
@@ -771,10 +772,12 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
                         v[j] = x;
                     }
                     if (!whole) {
-                        // position s * 16 + (j >> 1) * 8 + (j & 1) of the lane's lies after its row, or before the window
-                        // and past the sinks
-                        const int last = row_pos[h] - pos0 - quad * 2;
-                        const int out = p.window == 0 ? -1 : last - p.window;
+                        // position s * 16 + (j >> 1) * 8 + (j & 1) of the lane's lies after its row or the table's end, or
+                        // before the window and past the sinks
+                        const int own = row_pos[h] - pos0 - quad * 2;
+                        const int last = min(own, seq_end() - 1 - pos0 - quad * 2);
+                        // (in 32 bits without a sign: wraps for rows without a position, which see nothing anyway)
+                        const int out = p.window == 0 ? -1 : static_cast<int>(static_cast<uint32_t>(own) - p.window);
                         const int sink = p.window == 0 ? -1 : p.sinks - pos0 - quad * 2;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(AttnCfg<D, RW>::kThreads, AttnCfg<D, RW>::kCta
                         bad |= nonfinite_pair(w.x) || nonfinite_pair(w.y) || nonfinite_pair(w.z) || nonfinite_pair(w.w);
                     }
                 };
-                look(first_pos + 1 - pos0, span.len - pos0);                                      // after some row
+                look(first_pos + 1 - pos0, seq_end() - pos0);                                      // after some row
                 if (p.window != 0) look(span.low - pos0, span.low + p.rows - 1 - pos0);           // before some window
                 apart = __any_sync(0xFFFFFFFFu, bad);
             }

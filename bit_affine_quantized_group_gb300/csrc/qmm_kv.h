@@ -39,6 +39,7 @@ struct AttnParams {
     uint32_t* err;
     int64_t q_stride, out_stride, num_pages;
     int32_t seqs, rows, group, kv_heads, row_groups, max_pages, page_shift, window, sinks;
+    int32_t positions;      // that the page table holds for a sequence
     int32_t group_inverse;  // ceil(2^20 / group): rows (fewer than 1024) divide by the group (64 at most) exactly
     int32_t min_unit;
     uint32_t query_sign;    // flips the signs of two query elements where the scale is negative

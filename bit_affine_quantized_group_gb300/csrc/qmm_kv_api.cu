@@ -234,9 +234,9 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_a
     ap.row_groups = ap.min_unit = 0;   // set by the launcher for the rows that one CTA holds
     ap.max_pages = d.max_pages;
     ap.page_shift = log2_of(d.page_size);
-    // a window that no position leaves is none
-    ap.window = d.window >= static_cast<int64_t>(d.max_pages) * d.page_size ? 0 : d.window;
-    ap.sinks = d.sinks;
+    ap.window = d.window == 0x7FFFFFFF ? 0 : d.window;   // a window that no position leaves is none
+    ap.positions = d.max_pages * d.page_size;
+    ap.sinks = d.sinks < ap.positions ? d.sinks : ap.positions;
     ap.query_sign = d.scale < 0.0f ? 0x80008000u : 0u;
     // a scale of 0 would make masked scores of -infinity NaN; one that moves no score does not
     ap.scale_log2 = std::fmax(std::fabs(d.scale), 1e-30f) * 1.4426950408889634f;

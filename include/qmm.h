@@ -295,7 +295,8 @@ enum { QMM_IN_F32 = 0, QMM_IN_BF16 = 1 };
 enum {
     QMM_KV_TIMEOUT = 7,       /* a kernel gave up a bounded wait (any of three bits) */
     QMM_KV_BAD_PAGE = 16,     /* a page table entry in use lies outside 0..num_pages-1: read as zeros, not written */
-    QMM_KV_BAD_LENGTH = 32,   /* a length above max_pages * page_size: what is past the page table was left out */
+    QMM_KV_BAD_LENGTH = 32,   /* a length above max_pages * page_size: rows stand where it says, and what is past the page
+                                 table was neither written nor seen */
     QMM_KV_BAD_POSITION = 64  /* a rotation position outside the rope table: the row was not rotated */
 };
 

@@ -1,5 +1,5 @@
-"""Attention where values are not finite, and where a window or the sinks end between drafted tokens, against plain float64
-computations.
+"""Attention where values are not finite, where a window or the sinks end between drafted tokens, and where a length is past
+the page table, against plain float64 computations.
 
 Tolerances, from the arithmetic: outputs are rounded once to bfloat16 (at most 2^-8 of the value between neighbours); a
 score's float32 sum of products is off by at most 2^-19 of the sum of their magnitudes, and the weights and their sums by
@@ -174,3 +174,17 @@ def test_a_window_of_many_millions(q, rows, hq):
             # float32 sums over the 7,000 steps of a share, two additions each
             tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -15 + 2.0 ** -19 * size + 2.0 ** -24 * 2 ** 14) * np.max(np.abs(values))
             assert _near(got[r, h], want, tol)
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d", [(1, 2, 1, 64), (8, 4, 2, 128), (8, 8, 1, 128), (5, 2, 1, 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 0), (20, 3), (70, 100), (2 ** 31 - 2, 0)])
+@pytest.mark.parametrize("over", [0, 1, 3, 7, 25, 200, 2 ** 31 - 1 - 128])
+def test_lengths_past_the_page_table(q, rows, hq, hkv, d, window, sinks, over):
+    """Rows stand where the length says, and see what the table holds."""
+    import torch
+    s = Sequence(torch, 128, hkv, d, seed=rows + d)
+    qs = s.queries(rows, hq, d)
+    got, flags = s.attend(q, qs, hkv, rows, 128 + over, window, sinks)
+    want, tol, _ = s.expected(qs, rows, 128 + over, window, sinks)
+    assert flags == (q.KV_BAD_LENGTH if over else 0)
+    assert _near(got, want, tol)
