@@ -215,6 +215,13 @@ def _stream_on(stream, device: int) -> int:
     return _stream_handle(stream)
 
 
+def _wait_for_block(dev) -> None:
+    """A block from the allocator may still be written by what was launched before on the current stream; the library clears a
+    workspace on another one."""
+    import torch
+    torch.cuda.current_stream(dev).synchronize()
+
+
 class Plan:
     """A qmm plan (qmm_plan / qmm_destroy). By default its workspace is a
     PyTorch-allocated device buffer (so PyTorch's allocator owns the memory);
@@ -388,6 +395,7 @@ class KVPlan:
                 nbytes = kv_workspace_bytes(d)
                 self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
                 ws = (self.workspace.data_ptr() + 255) // 256 * 256
+                _wait_for_block(dev)
             st = _lib().qmm_kv_plan(ctypes.byref(self._handle), ctypes.byref(d), ws, nbytes)
         if st != QMM_OK:
             raise QmmError(st, "qmm_kv_plan")

@@ -336,7 +336,9 @@ size_t qmm_kv_workspace_bytes(const qmm_kv_desc* d);
 
 /*
  * Create a plan on the current device; the workspace is handled as in
- * qmm_plan (NULL: the plan allocates it). A plan is used by one stream at a
+ * qmm_plan (NULL: the plan allocates it). Its head is cleared on the legacy
+ * default stream before the call returns, so nothing launched before, on any
+ * stream, may write the workspace any more. A plan is used by one stream at a
  * time; qmm_qk_norm_rope and qmm_attention may share one.
  */
 int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, size_t ws_bytes);

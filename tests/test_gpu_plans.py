@@ -1,0 +1,74 @@
+"""Plans next to other work on the GPU."""
+from __future__ import annotations
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+PAGE, MAX_PAGES = 16, 600
+
+
+@pytest.fixture(scope="module")
+def q():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_affine_quantized_group_gb300 import _build
+    _build.build()
+    import bit_affine_quantized_group_gb300 as q
+    return q
+
+
+def _busy(torch, n=80):
+    """Some tens of milliseconds of work on the current stream."""
+    room = torch.empty(1 << 31, dtype=torch.uint8, device=DEV)
+    for i in range(n):
+        room.fill_(i)
+
+
+class Step:
+    """Heads that are cut and joined: one sequence over all SMs."""
+
+    def __init__(self, q, torch, rows=1, seed=0):
+        self.q, self.torch = q, torch
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        normal = lambda *s: torch.randn(s, generator=gen, device=DEV).to(torch.bfloat16)  # noqa: E731
+        self.rows = rows
+        self.queries = normal(rows, 8, 128)
+        self.cache = q.KVCache(normal(MAX_PAGES, 2, PAGE, 128), normal(MAX_PAGES, 2, PAGE, 128))
+        self.table = torch.randperm(MAX_PAGES, generator=gen, device=DEV).int()[None]
+        self.lengths = torch.tensor([MAX_PAGES * PAGE - 3], dtype=torch.int32, device=DEV)
+
+    def plan(self, **kw):
+        return self.q.KVPlan(8, 2, 128, PAGE, max_seqs=1, max_rows=self.rows, max_pages=MAX_PAGES, **kw)
+
+    def __call__(self, plan, table=None):
+        out = self.torch.full_like(self.queries, 77.0)
+        self.q.attention(plan, self.queries, self.cache, self.table if table is None else table, self.lengths, out)
+        return out
+
+
+@pytest.mark.parametrize("rows", [1, 8])
+def test_a_plan_made_behind_a_late_write_to_its_block(q, rows):
+    """On a side stream, whose freed blocks are given out again at once."""
+    import torch
+    step = Step(q, torch, rows)
+    want = step(step.plan())
+    plan0 = step.plan()
+    nbytes = plan0.workspace.numel()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        block = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+        at = block.data_ptr()
+        _busy(torch)
+        block.fill_(255)
+        del block
+        plan = step.plan()
+        assert plan.workspace.data_ptr() == at   # the same block
+        outs = [step(plan) for _ in range(3)]
+        side.synchronize()
+        assert plan.error_flags() == 0
+    for out in outs:
+        assert torch.equal(out, want)
