@@ -246,6 +246,7 @@ class Plan:
                 self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
                 base = self.workspace.data_ptr()
                 aligned = (base + 255) // 256 * 256
+                _wait_for_block(dev)
                 st = _lib().qmm_plan(ctypes.byref(self._handle), ctypes.byref(self.desc), ctypes.c_void_p(aligned),
                                   ctypes.c_size_t(nbytes))
             else:

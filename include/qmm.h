@@ -135,7 +135,9 @@ size_t qmm_workspace_bytes(const qmm_desc* d);
  * qmm_workspace_bytes(d) bytes (freed by qmm_destroy); otherwise `workspace`
  * must be a device pointer, 256-byte aligned, of at least ws_bytes >=
  * qmm_workspace_bytes(d) bytes, owned by the caller and not used by anything
- * else while the plan is in use. On failure *plan is set to NULL.
+ * else while the plan is in use. Its error word is cleared on the legacy
+ * default stream before the call returns, so nothing launched before, on any
+ * stream, may write the workspace any more. On failure *plan is set to NULL.
  */
 int qmm_plan(qmm_plan_t** plan, const qmm_desc* d, void* workspace, size_t ws_bytes);
 

@@ -72,3 +72,38 @@ def test_a_plan_made_behind_a_late_write_to_its_block(q, rows):
         assert plan.error_flags() == 0
     for out in outs:
         assert torch.equal(out, want)
+
+
+def test_a_projection_plan_made_behind_a_late_write_to_its_block(q):
+    import torch
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    K, N, M = 4096, 1024, 8
+    x = torch.randn((M, K), generator=gen, device=DEV).to(torch.bfloat16)
+    w = torch.randint(-2 ** 31, 2 ** 31, (N, K * 4 // 32), generator=gen, device=DEV, dtype=torch.int32)
+    s = torch.full((N, K // 64), 0.01, dtype=torch.float16, device=DEV)
+    b = -7.5 * s
+
+    def make():
+        return q.Plan(K, N, 4, 64, max_M=M, out_dtype="f32", splits=4)
+
+    def run(plan):
+        out = torch.empty((M, N), device=DEV)
+        q.forward(plan, x, w, s, b, out)
+        return out
+
+    plan0 = make()
+    want = run(plan0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        block = torch.empty(plan0.workspace.numel(), dtype=torch.uint8, device=DEV)
+        at = block.data_ptr()
+        _busy(torch)
+        block.fill_(255)
+        del block
+        plan = make()
+        assert plan.workspace.data_ptr() == at   # the same block
+        got = run(plan)
+        side.synchronize()
+        assert plan.error_flags() == 0
+    assert torch.equal(got, want)
