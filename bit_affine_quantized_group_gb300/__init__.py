@@ -413,7 +413,7 @@ class KVPlan:
         return self._handle
 
     def error_flags(self) -> int:
-        """The KV_BAD_* bits of the calls since the last read (synchronizes), cleared."""
+        """The KV_BAD_* bits of the calls since the last read, cleared. Waits for the device, whatever streams they are on."""
         v = ctypes.c_uint32(0)
         st = _lib().qmm_kv_error(self._handle, ctypes.byref(v))
         if st not in (QMM_OK, QMM_ERR_INVALID_ARG, QMM_ERR_TIMEOUT):

@@ -112,8 +112,12 @@ int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, siz
 int qmm_kv_error(const qmm_kv_plan_t* p, uint32_t* flags) {
     if (p == nullptr || flags == nullptr) return QMM_ERR_INVALID_ARG;
     uint32_t v = 0;
+    // the plan's calls may be in flight on a stream that the legacy one does not wait for, and later ones must find the word
+    // cleared
+    if (cudaDeviceSynchronize() != cudaSuccess) return QMM_ERR_CUDA;
     if (cudaMemcpy(&v, p->ws, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return QMM_ERR_CUDA;
-    if (v != 0 && cudaMemset(p->ws, 0, sizeof(v)) != cudaSuccess) return QMM_ERR_CUDA;
+    if (v != 0 && (cudaMemset(p->ws, 0, sizeof(v)) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess))
+        return QMM_ERR_CUDA;
     *flags = v;
     if (v == 0) return QMM_OK;
     return v & QMM_KV_TIMEOUT ? QMM_ERR_TIMEOUT : QMM_ERR_INVALID_ARG;

@@ -345,7 +345,11 @@ size_t qmm_kv_workspace_bytes(const qmm_kv_desc* d);
  */
 int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, size_t ws_bytes);
 
-/* Read (synchronously) and clear the plan's device error word: QMM_ERR_TIMEOUT or QMM_ERR_INVALID_ARG if a bit was set. */
+/*
+ * Wait for the device, then read and clear the plan's error word, which is
+ * done when the call returns: QMM_ERR_TIMEOUT or QMM_ERR_INVALID_ARG if a bit
+ * was set. No call of the plan may be made meanwhile.
+ */
 int qmm_kv_error(const qmm_kv_plan_t* p, uint32_t* flags);
 
 /* Free the plan and any workspace it allocated. NULL is accepted. */

@@ -107,3 +107,27 @@ def test_a_projection_plan_made_behind_a_late_write_to_its_block(q):
         side.synchronize()
         assert plan.error_flags() == 0
     assert torch.equal(got, want)
+
+
+def test_error_flags_of_calls_in_flight(q):
+    """Asked for while the call with the fault still waits on a side stream, and not lost or kept by the clearing."""
+    import torch
+    step = Step(q, torch)
+    plan = step.plan()
+    want = step(plan)
+    wrong = step.table.clone()
+    wrong[0, 5] = MAX_PAGES
+    torch.cuda.synchronize()
+    assert plan.error_flags() == 0
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            _busy(torch, 20)
+            step(plan, wrong)
+            assert plan.error_flags() == q.KV_BAD_PAGE
+            out = step(plan)
+            assert plan.error_flags() == 0
+            assert torch.equal(out, want)
+            step(plan, wrong)   # right behind a clearing
+            assert plan.error_flags() == q.KV_BAD_PAGE
+
