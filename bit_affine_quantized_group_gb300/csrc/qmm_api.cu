@@ -403,8 +403,12 @@ int qmm_unpack_codes(const uint32_t* packed_w, int64_t K, int64_t N, int bits, u
 int qmm_plan_error(const qmm_plan_t* p, uint32_t* flags) {
     if (p == nullptr || flags == nullptr) return QMM_ERR_INVALID_ARG;
     uint32_t v = 0;
+    // the plan's calls may be in flight on a stream that the legacy one does not wait for, and later ones must find the word
+    // cleared
+    if (cudaDeviceSynchronize() != cudaSuccess) return QMM_ERR_CUDA;
     if (cudaMemcpy(&v, p->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return QMM_ERR_CUDA;
-    if (v != 0 && cudaMemset(p->err, 0, sizeof(v)) != cudaSuccess) return QMM_ERR_CUDA;
+    if (v != 0 && (cudaMemset(p->err, 0, sizeof(v)) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess))
+        return QMM_ERR_CUDA;
     *flags = v;
     return v == 0 ? QMM_OK : QMM_ERR_TIMEOUT;
 }

@@ -220,8 +220,9 @@ int qmm_unpack_codes(const uint32_t* packed_w, int64_t K, int64_t N, int bits, u
                      void* stream);
 
 /*
- * Read (synchronously) and clear the plan's device error word. Sets *flags to
- * 0 when every kernel since the last call finished normally; nonzero when a
+ * Wait for the device, then read and clear the plan's device error word, which
+ * is done when the call returns (no call of the plan may be made meanwhile).
+ * Sets *flags to 0 when every kernel since the last call finished normally; nonzero when a
  * kernel gave up a bounded wait (its output is then incomplete) and returns
  * QMM_ERR_TIMEOUT in that case.
  */

@@ -131,3 +131,18 @@ def test_error_flags_of_calls_in_flight(q):
             step(plan, wrong)   # right behind a clearing
             assert plan.error_flags() == q.KV_BAD_PAGE
 
+
+def test_error_flags_of_projections_in_flight(q):
+    """A bit that is set late, here by a write to the workspace, for no call sets one on purpose."""
+    import torch
+    plan = q.Plan(1024, 256, 4, 64, max_M=4)
+    word = (plan.workspace.data_ptr() + 255) // 256 * 256 - plan.workspace.data_ptr()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            _busy(torch, 20)
+            plan.workspace[word:word + 1].fill_(1)
+            assert plan.error_flags() == 1
+            plan.workspace[word:word + 1].fill_(2)   # right behind a clearing
+            assert plan.error_flags() == 2 and plan.error_flags() == 0
