@@ -404,9 +404,6 @@ class KVPlan:
         self.q_width, self.kv_width = d.q_heads * d.head_dim, d.kv_heads * d.head_dim
         self.page_shape = (d.kv_heads, d.page_size, d.head_dim)
         self.max_pages, self.head_dim, self.rot_dim = d.max_pages, d.head_dim, d.rot_dim
-        # what a call passes to the library: a plan is used by one call at a time
-        self._args = ctypes.create_string_buffer(max(_APPEND_ARGS.size, _ATTENTION_ARGS.size))
-        self._args_at = ctypes.addressof(self._args)
 
     @property
     def handle(self):
@@ -448,6 +445,7 @@ class KVCache:
         self.ref = ctypes.byref(self.struct)
 
 
+# What a call passes to the library, packed for each call: threads may share a plan.
 _APPEND_ARGS = struct.Struct("@3P3q3Pq4Pq3i4x")      # QmmAppendArgs
 _ATTENTION_ARGS = struct.Struct("@4P2q2i")           # QmmAttentionArgs
 assert _APPEND_ARGS.size == ctypes.sizeof(QmmAppendArgs) and _ATTENTION_ARGS.size == ctypes.sizeof(QmmAttentionArgs)
@@ -492,14 +490,14 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
     if positions is not None and (positions.dtype is not _I32 or positions.numel() != tokens or
                                   not positions.is_contiguous()):
         raise ValueError("positions is an int32 tensor [tokens]")
-    _APPEND_ARGS.pack_into(
-        plan._args, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, tokens, plan.q_width, dtype, "q"),
+    args = _APPEND_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, tokens, plan.q_width, dtype, "q"),
         _rows(k, tokens, plan.kv_width, dtype, "k"), _rows(v, tokens, plan.kv_width, dtype, "v"),
         0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
         0 if rope is None else rope.data_ptr(), 0 if rope is None else rope.shape[0], lengths.data_ptr(),
         0 if positions is None else positions.data_ptr(), page_table.data_ptr(), out.data_ptr(),
         _rows(out, tokens, plan.q_width, _BF16, "out"), seqs, rows, QMM_IN_F32 if dtype is _F32 else QMM_IN_BF16)
-    st = _LIB.qmm_qk_norm_rope(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan._device_index))
+    st = _LIB.qmm_qk_norm_rope(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_qk_norm_rope")
 
@@ -509,10 +507,10 @@ def attention(plan: KVPlan, q, cache: KVCache, page_table, lengths, out, stream=
     [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
     tokens = q.shape[0]
     seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
-    _ATTENTION_ARGS.pack_into(plan._args, 0, q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
-                              _rows(q, tokens, plan.q_width, _BF16, "q"), _rows(out, tokens, plan.q_width, _BF16, "out"),
-                              seqs, rows)
-    st = _LIB.qmm_attention(plan._handle, cache.ref, plan._args_at, _stream_on(stream, plan._device_index))
+    args = _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
+                                _rows(q, tokens, plan.q_width, _BF16, "q"), _rows(out, tokens, plan.q_width, _BF16, "out"),
+                                seqs, rows)
+    st = _LIB.qmm_attention(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_attention")
 

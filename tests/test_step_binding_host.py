@@ -1,0 +1,103 @@
+"""Host-only tests of the Python entry points of the cache operators and of sampling, with a library in the place of the real
+one that takes note of what it is passed. CPU tensors stand for those of the plan's device."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import threading
+
+import pytest
+
+HQ, HKV, D, PAGE, MAX_PAGES, SEQS = 4, 2, 64, 16, 3, 2
+KIND = {"qmm_attention": "QmmAttentionArgs", "qmm_qk_norm_rope": "QmmAppendArgs"}
+
+
+class Library:
+    """The real library, but for the calls that need a GPU."""
+
+    def __init__(self, q):
+        self.q, self.real, self.calls, self.inside = q, q.lib, [], lambda: None
+
+    def __getattr__(self, name):
+        if name == "qmm_kv_plan":
+            return lambda *a: 0
+        if name == "qmm_sample":
+            return lambda *a: self.calls.append(a) or 0
+        if name not in KIND:
+            return getattr(self.real, name)
+
+        def call(handle, cache, args, stream):
+            self.inside()   # what other threads do before the library has read the arguments
+            kind = getattr(self.q, KIND[name])
+            raw = args if isinstance(args, bytes) else ctypes.string_at(args, ctypes.sizeof(kind))
+            self.calls.append(kind.from_buffer_copy(raw))
+            return 0
+        return call
+
+
+@pytest.fixture
+def q(monkeypatch):
+    torch = pytest.importorskip("torch")
+    from bit_affine_quantized_group_gb300 import _build
+    _build.build()
+    import bit_affine_quantized_group_gb300 as q
+    monkeypatch.setattr(q, "_LIB", Library(q))
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return q
+
+
+@pytest.fixture
+def plan(q):
+    p = q.KVPlan(HQ, HKV, D, PAGE, max_seqs=SEQS, max_rows=4, max_pages=MAX_PAGES, torch_workspace=False, device="cpu:0")
+    p._device_index = -1   # what CPU tensors give for their device
+    return p
+
+
+class Args:
+    """Arguments of a step that fit; changed by name."""
+
+    def __init__(self, q, tokens=SEQS):
+        import torch
+        self.q_, self.tokens = q, tokens
+        cache = lambda: torch.zeros((5, HKV, PAGE, D), dtype=torch.bfloat16)  # noqa: E731
+        rows = lambda heads: torch.zeros((tokens, heads * D), dtype=torch.bfloat16)  # noqa: E731
+        seqs = 1 if tokens == 1 else SEQS
+        self.queries, self.keys, self.values, self.out = rows(HQ), rows(HKV), rows(HKV), rows(HQ)
+        self.cache = q.KVCache(cache(), cache())
+        self.weight = torch.ones(D)
+        self.rope = torch.zeros((50, D))
+        self.positions = None
+        self.lengths = torch.zeros(seqs, dtype=torch.int32)
+        self.table = torch.zeros((seqs, MAX_PAGES), dtype=torch.int32)
+
+    def append(self, plan, **kw):
+        a = {**self.__dict__, **kw}
+        self.q_.qk_norm_rope(plan, a["queries"], a["keys"], a["values"], a["weight"], a["weight"], a["rope"], a["lengths"],
+                             a["table"], a["cache"], a["out"], a["positions"], stream=0)
+
+    def attend(self, plan, **kw):
+        a = {**self.__dict__, **kw}
+        self.q_.attention(plan, a["queries"], a["cache"], a["table"], a["lengths"], a["out"], stream=0)
+
+
+def test_two_threads_share_a_plan(q, plan):
+    """Another thread's call, of either operator, between a call's packing of its arguments and the library's reading."""
+    one, two = Args(q), Args(q)
+    for mine in (one.attend, one.append):
+        for theirs in (two.attend, two.append):
+            q._LIB.calls.clear()
+
+            def other():
+                q._LIB.inside = lambda: None
+                t = threading.Thread(target=theirs, args=(plan,))
+                t.start()
+                t.join()
+
+            q._LIB.inside = other
+            mine(plan)
+            second, first = q._LIB.calls
+            assert type(first) is getattr(q, KIND["qmm_attention" if mine == one.attend else "qmm_qk_norm_rope"])
+            assert first.q == one.queries.data_ptr() and first.lengths == one.lengths.data_ptr()
+            assert second.q == two.queries.data_ptr() and second.lengths == two.lengths.data_ptr()
+            assert (first.seqs, first.rows) == (SEQS, 1)
