@@ -1,6 +1,7 @@
 // C ABI of the cache operators: descriptor and argument checks, plans, and the
 // calls of qmm_qk_norm_rope and qmm_attention. The contract is in include/qmm.h.
 #include <cuda_runtime.h>
+#include <pthread.h>
 
 #include <cmath>
 #include <cstring>
@@ -16,6 +17,9 @@ struct qmm_kv_plan {
     int num_sms;
     uint8_t* ws;
     bool owns_ws;
+    // held while an attention call launches: the kernel that joins parts reads what the one before it left in the workspace,
+    // and no other thread's call may come between the two
+    mutable pthread_mutex_t launches = PTHREAD_MUTEX_INITIALIZER;
 };
 
 namespace {
@@ -244,8 +248,10 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_a
     ap.query_sign = d.scale < 0.0f ? 0x80008000u : 0u;
     // a scale of 0 would make masked scores of -infinity NaN; one that moves no score does not
     ap.scale_log2 = std::fmax(std::fabs(d.scale), 1e-30f) * 1.4426950408889634f;
-    return launch_attention(d.head_dim, ap, p->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QMM_OK
-                                                                                                        : QMM_ERR_CUDA;
+    pthread_mutex_lock(&p->launches);
+    const cudaError_t e = launch_attention(d.head_dim, ap, p->num_sms, static_cast<cudaStream_t>(stream));
+    pthread_mutex_unlock(&p->launches);
+    return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -342,7 +342,8 @@ size_t qmm_kv_workspace_bytes(const qmm_kv_desc* d);
  * qmm_plan (NULL: the plan allocates it). Its head is cleared on the legacy
  * default stream before the call returns, so nothing launched before, on any
  * stream, may write the workspace any more. A plan is used by one stream at a
- * time; qmm_qk_norm_rope and qmm_attention may share one.
+ * time; qmm_qk_norm_rope and qmm_attention may share one, and host threads may
+ * that launch on the same stream.
  */
 int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, size_t ws_bytes);
 

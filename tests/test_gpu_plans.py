@@ -146,3 +146,33 @@ def test_error_flags_of_projections_in_flight(q):
             assert plan.error_flags() == 1
             plan.workspace[word:word + 1].fill_(2)   # right behind a clearing
             assert plan.error_flags() == 2 and plan.error_flags() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 8])
+def test_threads_share_a_plan_and_a_stream(q, rows):
+    """Calls of two threads give the bits of one, with parts that the call's own kernel joins or a second one."""
+    import threading
+
+    import torch
+    steps = [Step(q, torch, rows, seed=i) for i in range(2)]
+    plan = steps[0].plan()
+    want = [step(plan) for step in steps]
+    n = 200
+    outs = [[torch.full_like(w, 77.0) for _ in range(n)] for w in want]
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def run(step, out):
+        start.wait()
+        for o in out:
+            q.attention(plan, step.queries, step.cache, step.table, step.lengths, o)
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(steps, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert plan.error_flags() == 0
+    for w, out in zip(want, outs):
+        assert all(torch.equal(o, w) for o in out)
