@@ -485,7 +485,8 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype is not _F32 or w.numel() != plan.head_dim or not w.is_contiguous()):
             raise ValueError("q_weight and k_weight are float32 [head_dim] or None")
-    if plan.rot_dim and (rope is None or rope.dtype is not _F32 or not rope.is_contiguous() or rope.shape[-1] != plan.rot_dim):
+    if plan.rot_dim and (rope is None or rope.dtype is not _F32 or not rope.is_contiguous() or rope.dim() != 2 or
+                         rope.shape[1] != plan.rot_dim):
         raise ValueError("rope is a float32 tensor [positions, rot_dim]")
     if positions is not None and (positions.dtype is not _I32 or positions.numel() != tokens or
                                   not positions.is_contiguous()):
@@ -494,7 +495,7 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, tokens, plan.q_width, dtype, "q"),
         _rows(k, tokens, plan.kv_width, dtype, "k"), _rows(v, tokens, plan.kv_width, dtype, "v"),
         0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
-        0 if rope is None else rope.data_ptr(), 0 if rope is None else rope.shape[0], lengths.data_ptr(),
+        rope.data_ptr() if plan.rot_dim else 0, rope.shape[0] if plan.rot_dim else 0, lengths.data_ptr(),
         0 if positions is None else positions.data_ptr(), page_table.data_ptr(), out.data_ptr(),
         _rows(out, tokens, plan.q_width, _BF16, "out"), seqs, rows, QMM_IN_F32 if dtype is _F32 else QMM_IN_BF16)
     st = _LIB.qmm_qk_norm_rope(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))

@@ -101,3 +101,15 @@ def test_two_threads_share_a_plan(q, plan):
             assert first.q == one.queries.data_ptr() and first.lengths == one.lengths.data_ptr()
             assert second.q == two.queries.data_ptr() and second.lengths == two.lengths.data_ptr()
             assert (first.seqs, first.rows) == (SEQS, 1)
+
+
+@pytest.mark.parametrize("shape", [(D,), (50 * D,), (2, 25, D), (50, 1, D), (50, D // 2), ()])
+def test_the_rotation_table_has_two_dimensions(q, plan, shape):
+    """Its first is the number of positions that the kernel holds positions against."""
+    import torch
+    a = Args(q)
+    with pytest.raises(ValueError, match="rope"):
+        a.append(plan, rope=torch.zeros(shape))
+    assert not q._LIB.calls
+    a.append(plan)
+    assert q._LIB.calls[0].rope_len == 50
