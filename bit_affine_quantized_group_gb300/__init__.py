@@ -452,12 +452,18 @@ assert _APPEND_ARGS.size == ctypes.sizeof(QmmAppendArgs) and _ATTENTION_ARGS.siz
 
 
 def _rows(t, tokens, width, dtype, what):
-    """Elements between the rows of a tensor [tokens, width] or [tokens, heads, head_dim] of adjacent heads."""
-    st = t.stride()
-    if t.dtype is not dtype or t.numel() != tokens * width or st[-1] != 1 or \
-            (len(st) != 2 and (len(st) != 3 or st[1] != t.shape[2])):
-        raise ValueError(f"{what}: {tokens} {dtype} rows of {width} adjacent elements are needed")
-    return st[0]
+    """Elements between the rows of a tensor [tokens, width] or [tokens, heads, head_dim] of adjacent heads. One token's row may
+    be any contiguous tensor."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is dtype:
+        n = len(shape)
+        if n > 1 and shape[0] == tokens and st[-1] == 1 and \
+                (shape[1] == width if n == 2 else
+                 n == 3 and shape[1] * shape[2] == width and (st[1] == shape[2] or shape[1] == 1)):
+            return st[0]
+        if tokens == 1 and t.numel() == width and t.is_contiguous():
+            return width
+    raise ValueError(f"{what}: {tokens} {dtype} rows of {width} adjacent elements are needed")
 
 
 def _check_step(plan, cache, page_table, lengths, tokens):

@@ -113,3 +113,48 @@ def test_the_rotation_table_has_two_dimensions(q, plan, shape):
     assert not q._LIB.calls
     a.append(plan)
     assert q._LIB.calls[0].rope_len == 50
+
+
+def _wide(heads, tokens=None):
+    """Heads with gaps between them, as a slice of a wider tensor."""
+    import torch
+    shape = (heads, 2 * D) if tokens is None else (tokens, heads, 2 * D)
+    return torch.zeros(shape, dtype=torch.bfloat16)[..., :D]
+
+
+@pytest.mark.parametrize("name,heads", [("queries", HQ), ("keys", HKV), ("values", HKV), ("out", HQ)])
+def test_rows_hold_all_their_heads_side_by_side(q, plan, name, heads):
+    import torch
+    for tokens in (1, SEQS):
+        a = Args(q, tokens)
+        t = getattr(a, name)
+        wrong = [_wide(heads, tokens), t.view(tokens, heads, D).transpose(1, 2), torch.cat((t, t)), t[:, :-1], t.float(),
+                 t.view(tokens, heads, 2, D // 2), t.view(-1)]
+        if name != "queries":   # whose first dimension is the number of tokens
+            wrong += [_wide(heads), t.view(tokens * heads, D)[::tokens] if tokens > 1 else _wide(2 * heads)[::2], t.new_zeros((tokens * heads * 2, D))[::2]]
+        for w in wrong:
+            if tokens == 1 and w.is_contiguous() and w.dtype is t.dtype and w.numel() == t.numel() and (name != "queries" or w.shape[0] == 1):
+                continue   # one token's heads, whatever they are called
+            with pytest.raises((ValueError, q.QmmError)):
+                a.append(plan, **{name: w})
+            if name in ("queries", "out"):
+                with pytest.raises((ValueError, q.QmmError)):
+                    a.attend(plan, **{name: w})
+        assert not q._LIB.calls
+        for fits in (t, t.view(tokens, heads, D), torch.cat((t, t), 1)[:, :heads * D], torch.cat((t, t), 1).view(tokens, 2 * heads, D)[:, :heads]):
+            a.append(plan, **{name: fits})
+        q._LIB.calls.clear()
+
+
+def test_one_token_may_be_any_contiguous_tensor(q, plan):
+    import torch
+    a = Args(q, 1)
+    a.append(plan, keys=a.keys.view(HKV, D), values=a.values.view(HKV, D), out=a.out.view(HQ, D))
+    a.attend(plan, out=a.out.view(HQ, D))
+    one = torch.zeros((1, SEQS, D), dtype=torch.bfloat16).transpose(0, 1)   # one head a token: its stride says nothing
+    single = q.KVPlan(1, 1, D, PAGE, max_seqs=SEQS, max_rows=1, max_pages=MAX_PAGES, torch_workspace=False, device="cpu:0")
+    single._device_index = -1
+    b = Args(q)
+    pool = torch.zeros((5, 1, PAGE, D), dtype=torch.bfloat16)
+    b.attend(single, queries=one, out=one.clone(), cache=q.KVCache(pool, pool))
+    assert q._LIB.calls[-1].q_stride == D
