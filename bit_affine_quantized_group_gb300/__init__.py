@@ -437,9 +437,12 @@ class KVCache:
     def __init__(self, k, v):
         import torch
         for t in (k, v):
+            if t.get_device() != k.get_device():
+                raise ValueError("k and v are on the same device")
             if t.dim() != 4 or t.dtype != torch.bfloat16 or t.shape != k.shape or t.stride(3) != 1:
                 raise ValueError("k and v are bfloat16 tensors [pages, kv_heads, page_size, head_dim] of the same shape")
         self.k, self.v = k, v
+        self.device_index = k.get_device()
         self.page_shape = tuple(k.shape[1:])
         self.struct = QmmKvCache(k.data_ptr(), v.data_ptr(), k.shape[0], *k.stride()[:3], *v.stride()[:3])
         self.ref = ctypes.byref(self.struct)
@@ -466,7 +469,13 @@ def _rows(t, tokens, width, dtype, what):
     raise ValueError(f"{what}: {tokens} {dtype} rows of {width} adjacent elements are needed")
 
 
-def _check_step(plan, cache, page_table, lengths, tokens):
+def _check_step(plan, cache, page_table, lengths, tokens, *others):
+    device = plan._device_index
+    if cache.device_index != device or page_table.get_device() != device or lengths.get_device() != device:
+        raise ValueError(f"cache, page_table and lengths are on the plan's device {plan.device}")
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors are on the plan's device {plan.device}")
     seqs = lengths.numel()
     if cache.page_shape != plan.page_shape:
         raise ValueError("the cache's pages are not the plan's [kv_heads, page_size, head_dim]")
@@ -485,7 +494,7 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
     [tokens, heads * head_dim] of float32 or bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and
     k_weight: float32 [head_dim] or None; rope: float32 [positions, rot_dim], cosines then sines."""
     dtype, tokens = q.dtype, q.shape[0]
-    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, q, k, v, out, q_weight, k_weight, rope, positions)
     if dtype is not _F32 and dtype is not _BF16:
         raise ValueError("q, k and v are float32 or bfloat16")
     for w in (q_weight, k_weight):
@@ -513,7 +522,7 @@ def attention(plan: KVPlan, q, cache: KVCache, page_table, lengths, out, stream=
     """Attention of the new tokens over the cache (qmm_attention): q and out [tokens, q_heads, head_dim] bfloat16 (or
     [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
     tokens = q.shape[0]
-    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens)
+    seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, q, out)
     args = _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
                                 _rows(q, tokens, plan.q_width, _BF16, "q"), _rows(out, tokens, plan.q_width, _BF16, "out"),
                                 seqs, rows)
@@ -532,12 +541,17 @@ def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stre
     shape, strides = logits.shape, logits.stride()
     if len(shape) != 2 or (dtype is not f32 and dtype is not _BF16) or strides[1] != 1:
         raise ValueError("logits are float32 or bfloat16 rows of adjacent elements")
-    M = shape[0]
+    M, device = shape[0], logits.get_device()
     for t, want in ((temperature, f32), (top_k, i32), (top_p, f32), (min_p, f32), (u, f32), (tokens, i32)):
         if t.dtype is not want or t.numel() != M or not t.is_contiguous():
             raise ValueError("temperature, top_p, min_p and u are float32 [M], top_k and tokens int32 [M]")
-    if probs is not None and (probs.dtype is not f32 or probs.numel() != M or not probs.is_contiguous()):
-        raise ValueError("probs is float32 [M] or None")
+        if t.get_device() != device:
+            raise ValueError("all tensors are on the device of the logits")
+    if probs is not None and (probs.dtype is not f32 or probs.numel() != M or not probs.is_contiguous() or
+                              probs.get_device() != device):
+        raise ValueError("probs is float32 [M] on the device of the logits, or None")
+    if device < 0:
+        raise ValueError("logits are on a CUDA device")
     st = _lib().qmm_sample(logits.data_ptr(), M, shape[1], strides[0], QMM_IN_F32 if dtype is f32 else QMM_IN_BF16,
                            temperature.data_ptr(), top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), u.data_ptr(),
                            tokens.data_ptr(), None if probs is None else probs.data_ptr(),

@@ -158,3 +158,57 @@ def test_one_token_may_be_any_contiguous_tensor(q, plan):
     pool = torch.zeros((5, 1, PAGE, D), dtype=torch.bfloat16)
     b.attend(single, queries=one, out=one.clone(), cache=q.KVCache(pool, pool))
     assert q._LIB.calls[-1].q_stride == D
+
+
+def _elsewhere(t):
+    """t, as a tensor that says that it is on another device."""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 3
+    return t.as_subclass(Elsewhere)
+
+
+def test_tensors_of_another_device_are_refused(q, plan):
+    import torch
+    a = Args(q)
+    positions = torch.zeros(SEQS, dtype=torch.int32)
+    a.append(plan, positions=positions)
+    a.attend(plan)
+    q._LIB.calls.clear()
+    for name in ("queries", "keys", "values", "weight", "rope", "lengths", "table", "out"):
+        with pytest.raises(ValueError, match="device"):
+            a.append(plan, **{name: _elsewhere(getattr(a, name))})
+    with pytest.raises(ValueError, match="device"):
+        a.append(plan, positions=_elsewhere(positions))
+    for name in ("queries", "lengths", "table", "out"):
+        with pytest.raises(ValueError, match="device"):
+            a.attend(plan, **{name: _elsewhere(getattr(a, name))})
+    with pytest.raises(ValueError, match="device"):
+        q.KVCache(a.cache.k, _elsewhere(a.cache.v))
+    far = q.KVCache(_elsewhere(a.cache.k), _elsewhere(a.cache.v))
+    for call in (a.append, a.attend):
+        with pytest.raises(ValueError, match="device"):
+            call(plan, cache=far)
+    plan._device_index = 0   # a plan on a GPU, and tensors on the CPU
+    for call in (a.append, a.attend):
+        with pytest.raises(ValueError, match="device"):
+            call(plan)
+    assert not q._LIB.calls
+
+
+def test_sampling_refuses_tensors_of_another_device(q):
+    import torch
+    names = ("logits", "temperature", "top_k", "top_p", "min_p", "u", "tokens", "probs")
+    f, i = torch.zeros(2), torch.zeros(2, dtype=torch.int32)
+    plain = dict(zip(names, (torch.zeros((2, 10)), f, i, f, f, f, i, f)))
+    with pytest.raises(ValueError, match="device"):
+        q.sample(**plain, stream=0)
+    far = {n: _elsewhere(t) for n, t in plain.items()}
+    for name in names:
+        with pytest.raises(ValueError, match="device"):
+            q.sample(**{**far, name: plain[name]}, stream=0)
+    assert not q._LIB.calls
+    q.sample(**far, stream=0)
+    assert len(q._LIB.calls) == 1
