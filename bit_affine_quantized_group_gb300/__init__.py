@@ -198,14 +198,15 @@ def _stream_handle(stream) -> int:
 
 
 # What calls of a few microseconds take from torch, looked up once (torch is imported when it is first needed).
-_F32 = _BF16 = _I32 = _RAW_STREAM = None
+_F32 = _BF16 = _I32 = _RAW_STREAM = _CURRENT_DEVICE = None
 
 
 def _bind_torch() -> None:
-    global _F32, _BF16, _I32, _RAW_STREAM
+    global _F32, _BF16, _I32, _RAW_STREAM, _CURRENT_DEVICE
     import torch
     _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
     _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_on(stream, device: int) -> int:
@@ -552,9 +553,14 @@ def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stre
         raise ValueError("probs is float32 [M] on the device of the logits, or None")
     if device < 0:
         raise ValueError("logits are on a CUDA device")
-    st = _lib().qmm_sample(logits.data_ptr(), M, shape[1], strides[0], QMM_IN_F32 if dtype is f32 else QMM_IN_BF16,
-                           temperature.data_ptr(), top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), u.data_ptr(),
-                           tokens.data_ptr(), None if probs is None else probs.data_ptr(),
-                           _stream_on(stream, logits.get_device()))
+    args = (logits.data_ptr(), M, shape[1], strides[0], QMM_IN_F32 if dtype is f32 else QMM_IN_BF16,
+            temperature.data_ptr(), top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), u.data_ptr(),
+            tokens.data_ptr(), None if probs is None else probs.data_ptr(), _stream_on(stream, device))
+    if device == _CURRENT_DEVICE():
+        st = _lib().qmm_sample(*args)
+    else:
+        import torch
+        with torch.cuda.device(device):   # the library launches on the current one
+            st = _lib().qmm_sample(*args)
     if st != QMM_OK:
         raise QmmError(st, "qmm_sample")

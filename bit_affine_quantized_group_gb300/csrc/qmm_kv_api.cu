@@ -14,6 +14,7 @@ using namespace qmmk;
 
 struct qmm_kv_plan {
     qmm_kv_desc d;
+    int device;
     int num_sms;
     uint8_t* ws;
     bool owns_ws;
@@ -48,6 +49,28 @@ bool rows_ok(const void* p, int64_t stride, int64_t elems, int size, int64_t n) 
     if (p == nullptr || !aligned(p, 16)) return false;
     return n <= 1 || (stride >= elems && stride <= (1LL << 40) && (stride * size) % 16 == 0);
 }
+
+// Makes a plan's device the current one, and at the end of the call the one that was.
+class OnDevice {
+public:
+    explicit OnDevice(int device) {
+        int now = 0;
+        ok = cudaGetDevice(&now) == cudaSuccess;
+        if (ok && now != device) {
+            ok = cudaSetDevice(device) == cudaSuccess;
+            before_ = now;
+        }
+    }
+    ~OnDevice() {
+        if (before_ >= 0) cudaSetDevice(before_);
+    }
+    OnDevice(const OnDevice&) = delete;
+    OnDevice& operator=(const OnDevice&) = delete;
+    bool ok;
+
+private:
+    int before_ = -1;
+};
 
 KvSide side(void* base, int64_t page, int64_t head, int64_t slot) {
     return KvSide{static_cast<uint16_t*>(base), page, head, slot};
@@ -94,6 +117,7 @@ int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, siz
     struct qmm_kv_plan* p = new (std::nothrow) struct qmm_kv_plan();
     if (p == nullptr) return QMM_ERR_ALLOC;
     p->d = *d;
+    p->device = dev;
     p->num_sms = sms;
     p->owns_ws = workspace == nullptr;
     void* ws = workspace;
@@ -116,6 +140,8 @@ int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, siz
 int qmm_kv_error(const qmm_kv_plan_t* p, uint32_t* flags) {
     if (p == nullptr || flags == nullptr) return QMM_ERR_INVALID_ARG;
     uint32_t v = 0;
+    const OnDevice on(p->device);
+    if (!on.ok) return QMM_ERR_CUDA;
     // the plan's calls may be in flight on a stream that the legacy one does not wait for, and later ones must find the word
     // cleared
     if (cudaDeviceSynchronize() != cudaSuccess) return QMM_ERR_CUDA;
@@ -161,6 +187,8 @@ int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qm
     const int chk = qmm_check_qk_norm_rope_args(&p->d, cache, a);
     if (chk != QMM_OK) return chk;
     if (a->seqs == 0 || a->rows == 0) return QMM_OK;
+    const OnDevice on(p->device);
+    if (!on.ok) return QMM_ERR_CUDA;
     AppendParams ap;
     ap.k = side(cache->k, cache->k_page_stride, cache->k_head_stride, cache->k_slot_stride);
     ap.v = side(cache->v, cache->v_page_stride, cache->v_head_stride, cache->v_slot_stride);
@@ -216,6 +244,8 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_a
     const int chk = qmm_check_attention_args(&p->d, cache, a);
     if (chk != QMM_OK) return chk;
     if (a->seqs == 0 || a->rows == 0) return QMM_OK;
+    const OnDevice on(p->device);
+    if (!on.ok) return QMM_ERR_CUDA;
     const qmm_kv_desc& d = p->d;
     const int group = d.q_heads / d.kv_heads;
     const AttnWorkspace w = attn_workspace(d.head_dim, d.max_rows * group);

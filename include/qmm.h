@@ -338,12 +338,13 @@ int qmm_kv_validate_desc(const qmm_kv_desc* d);
 size_t qmm_kv_workspace_bytes(const qmm_kv_desc* d);
 
 /*
- * Create a plan on the current device; the workspace is handled as in
- * qmm_plan (NULL: the plan allocates it). Its head is cleared on the legacy
- * default stream before the call returns, so nothing launched before, on any
- * stream, may write the workspace any more. A plan is used by one stream at a
- * time; qmm_qk_norm_rope and qmm_attention may share one, and host threads may
- * that launch on the same stream.
+ * Create a plan on the current device, where its calls run whatever device is
+ * current then; the workspace is handled as in qmm_plan (NULL: the plan
+ * allocates it). Its head is cleared on the legacy default stream before the
+ * call returns, so nothing launched before, on any stream, may write the
+ * workspace any more. A plan is used by one stream at a time; qmm_qk_norm_rope
+ * and qmm_attention may share one, and so may host threads that launch on the
+ * same stream.
  */
 int qmm_kv_plan(qmm_kv_plan_t** plan, const qmm_kv_desc* d, void* workspace, size_t ws_bytes);
 
@@ -434,7 +435,8 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_a
  * not above 0 takes the token of rank 0. NaN logits count as -infinity; a row
  * without any logit above that gives token -1 and prob 0. u outside [0, 1) is
  * brought to the nearest kept mass. probs may be NULL. 1 <= vocab <=
- * QMM_SAMPLE_MAX_VOCAB. M = 0 is a no-op. One launch, no plan, no workspace.
+ * QMM_SAMPLE_MAX_VOCAB. M = 0 is a no-op. One launch, on the current
+ * device; no plan, no workspace.
  */
 int qmm_sample(const void* logits, int M, int vocab, int64_t stride, int in_dtype, const float* temperature,
                const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,

@@ -44,6 +44,8 @@ def q(monkeypatch):
     monkeypatch.setattr(q, "_LIB", Library(q))
     monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    q._bind_torch()
+    monkeypatch.setattr(q, "_CURRENT_DEVICE", lambda: 3, raising=False)
     return q
 
 
@@ -212,3 +214,25 @@ def test_sampling_refuses_tensors_of_another_device(q):
     assert not q._LIB.calls
     q.sample(**far, stream=0)
     assert len(q._LIB.calls) == 1
+
+
+def test_sampling_launches_on_the_logits_device(q, monkeypatch):
+    """Where another device is current, that of the logits is made the current one around the call."""
+    import torch
+    events = []
+
+    @contextlib.contextmanager
+    def device(d):
+        events.append(("enter", d))
+        yield
+        events.append(("exit", d))
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    f, i = _elsewhere(torch.zeros(2)), _elsewhere(torch.zeros(2, dtype=torch.int32))
+    logits = _elsewhere(torch.zeros((2, 10)))
+    q.sample(logits, f, i, f, f, f, i, stream=0)
+    assert events == [] and len(q._LIB.calls) == 1
+    monkeypatch.setattr(q, "_CURRENT_DEVICE", lambda: 1)
+    monkeypatch.setattr(q._LIB, "calls", events)   # in one list with the calls
+    q.sample(logits, f, i, f, f, f, i, stream=0)
+    assert [e[0] for e in events] == ["enter", logits.data_ptr(), "exit"] and events[0][1] == 3
