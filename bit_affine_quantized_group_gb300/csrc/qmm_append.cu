@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
     load(h0);
 
     const int seq = token / p.rows;
-    const int pos = p.lengths[seq] - p.rows + (token - seq * p.rows);
+    const int pos = max(p.lengths[seq], 0) - p.rows + (token - seq * p.rows);   // (no length wraps)
     if (pos < 0) {   // a token before the sequence's first: its queries are zero
         for (int hd = h0 + lane / kLanes; hd < h1 && hd < p.q_heads; hd += kHeads)
             *reinterpret_cast<uint4*>(p.q_out + token * p.q_out_stride + static_cast<int64_t>(hd) * D + 8 * l) =

@@ -188,3 +188,31 @@ def test_lengths_past_the_page_table(q, rows, hq, hkv, d, window, sinks, over):
     want, tol, _ = s.expected(qs, rows, 128 + over, window, sinks)
     assert flags == (q.KV_BAD_LENGTH if over else 0)
     assert _near(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_negative_lengths_are_padding(q, rows):
+    """However far below 0, in the append and in attention; the sequence between them is whole."""
+    import torch
+    lengths, hq, hkv, d = [-2 ** 31, 20, -1, -2 ** 31 + 2], 4, 2, 64
+    gen = torch.Generator().manual_seed(24)
+    k, v = (torch.full((8, hkv, PAGE, d), 3.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    cache = q.KVCache(k, v)
+    table = torch.arange(8, dtype=torch.int32, device=DEV).view(4, 2)
+    lens = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    x = torch.randn((4 * rows, (hq + 2 * hkv) * d), generator=gen).to(torch.bfloat16).to(DEV)
+    rope = torch.zeros((32, d), device=DEV)
+    rope[:, :d // 2] = 1.0   # turns nothing
+    plan = q.KVPlan(hq, hkv, d, PAGE, max_seqs=4, max_rows=rows, max_pages=2)
+    queries, out = (torch.full((4 * rows, hq, d), 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q.qk_norm_rope(plan, x[:, :hq * d], x[:, hq * d:(hq + hkv) * d], x[:, (hq + hkv) * d:], None, None, rope, lens, table, cache, queries)
+    q.attention(plan, queries, cache, table, lens, out)
+    assert plan.error_flags() == 0
+    whole = torch.arange(4 * rows, device=DEV) // rows == 1
+    assert (queries[~whole] == 0).all() and (out[~whole] == 0).all()
+    assert torch.equal(queries[whole].view(rows, -1), x[whole, :hq * d])
+    written = (k != 3.0).any(3).any(1).cpu()   # [page, slot]
+    at = torch.zeros_like(written)
+    for pos in range(20 - rows, 20):
+        at[2 + pos // PAGE, pos % PAGE] = True
+    assert torch.equal(written, at) and torch.isfinite(out.float()).all()
