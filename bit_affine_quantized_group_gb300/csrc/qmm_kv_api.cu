@@ -50,6 +50,47 @@ bool rows_ok(const void* p, int64_t stride, int64_t elems, int size, int64_t n) 
     return n <= 1 || (stride >= elems && stride <= (1LL << 40) && (stride * size) % 16 == 0);
 }
 
+// Arguments of a call, for a descriptor that is valid.
+int check_append(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_append_args* a) {
+    if (a == nullptr) return QMM_ERR_INVALID_ARG;
+    const int chk = check_cache(cache);
+    if (chk != QMM_OK) return chk;
+    if (a->in_dtype != QMM_IN_F32 && a->in_dtype != QMM_IN_BF16) return QMM_ERR_INVALID_ARG;
+    if (a->seqs < 0 || a->seqs > d->max_seqs || a->rows < 0) return QMM_ERR_INVALID_ARG;
+    const int64_t tokens = static_cast<int64_t>(a->seqs) * a->rows;
+    // the grid has one warp for every few heads of a token
+    if (tokens * (d->q_heads + 2 * d->kv_heads) > (1LL << 31)) return QMM_ERR_UNSUPPORTED;
+    if (tokens == 0) return QMM_OK;
+    const int size = a->in_dtype == QMM_IN_F32 ? 4 : 2;
+    const int64_t dq = static_cast<int64_t>(d->q_heads) * d->head_dim, dk = static_cast<int64_t>(d->kv_heads) * d->head_dim;
+    if (!rows_ok(a->q, a->q_stride, dq, size, tokens) || !rows_ok(a->k, a->k_stride, dk, size, tokens) ||
+        !rows_ok(a->v, a->v_stride, dk, size, tokens) || !rows_ok(a->q_out, a->q_out_stride, dq, 2, tokens))
+        return QMM_ERR_INVALID_ARG;
+    if (!aligned(a->q_weight, 16) || !aligned(a->k_weight, 16)) return QMM_ERR_INVALID_ARG;
+    if (d->rot_dim > 0 && (a->rope == nullptr || !aligned(a->rope, 16) || a->rope_len < 1)) return QMM_ERR_INVALID_ARG;
+    if (a->lengths == nullptr || !aligned(a->lengths, 4) || a->page_table == nullptr || !aligned(a->page_table, 4) ||
+        !aligned(a->positions, 4))
+        return QMM_ERR_INVALID_ARG;
+    return QMM_OK;
+}
+
+int check_attention(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_attention_args* a) {
+    if (a == nullptr) return QMM_ERR_INVALID_ARG;
+    const int chk = check_cache(cache);
+    if (chk != QMM_OK) return chk;
+    const int seqs = a->seqs, rows = a->rows;
+    if (seqs < 0 || seqs > d->max_seqs || rows < 0 || rows > d->max_rows) return QMM_ERR_INVALID_ARG;
+    const int64_t tokens = static_cast<int64_t>(seqs) * rows;
+    if (tokens == 0) return QMM_OK;
+    const int64_t row_tiles = (static_cast<int64_t>(rows) * (d->q_heads / d->kv_heads) + 15) / 16;
+    if (static_cast<int64_t>(seqs) * d->kv_heads * row_tiles >= (1LL << 30)) return QMM_ERR_UNSUPPORTED;
+    const int64_t dq = static_cast<int64_t>(d->q_heads) * d->head_dim;
+    if (!rows_ok(a->q, a->q_stride, dq, 2, tokens) || !rows_ok(a->out, a->out_stride, dq, 2, tokens)) return QMM_ERR_INVALID_ARG;
+    if (a->page_table == nullptr || !aligned(a->page_table, 4) || a->lengths == nullptr || !aligned(a->lengths, 4))
+        return QMM_ERR_INVALID_ARG;
+    return QMM_OK;
+}
+
 // Makes a plan's device the current one, and at the end of the call the one that was.
 class OnDevice {
 public:
@@ -160,31 +201,13 @@ void qmm_kv_destroy(qmm_kv_plan_t* p) {
 }
 
 int qmm_check_qk_norm_rope_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_append_args* a) {
-    if (d == nullptr || a == nullptr) return QMM_ERR_INVALID_ARG;
-    const int chk = check_cache(cache);
-    if (chk != QMM_OK) return chk;
-    if (a->in_dtype != QMM_IN_F32 && a->in_dtype != QMM_IN_BF16) return QMM_ERR_INVALID_ARG;
-    if (a->seqs < 0 || a->seqs > d->max_seqs || a->rows < 0) return QMM_ERR_INVALID_ARG;
-    const int64_t tokens = static_cast<int64_t>(a->seqs) * a->rows;
-    // the grid has one warp for every few heads of a token
-    if (tokens * (d->q_heads + 2 * d->kv_heads) > (1LL << 31)) return QMM_ERR_UNSUPPORTED;
-    if (tokens == 0) return QMM_OK;
-    const int size = a->in_dtype == QMM_IN_F32 ? 4 : 2;
-    const int64_t dq = static_cast<int64_t>(d->q_heads) * d->head_dim, dk = static_cast<int64_t>(d->kv_heads) * d->head_dim;
-    if (!rows_ok(a->q, a->q_stride, dq, size, tokens) || !rows_ok(a->k, a->k_stride, dk, size, tokens) ||
-        !rows_ok(a->v, a->v_stride, dk, size, tokens) || !rows_ok(a->q_out, a->q_out_stride, dq, 2, tokens))
-        return QMM_ERR_INVALID_ARG;
-    if (!aligned(a->q_weight, 16) || !aligned(a->k_weight, 16)) return QMM_ERR_INVALID_ARG;
-    if (d->rot_dim > 0 && (a->rope == nullptr || !aligned(a->rope, 16) || a->rope_len < 1)) return QMM_ERR_INVALID_ARG;
-    if (a->lengths == nullptr || !aligned(a->lengths, 4) || a->page_table == nullptr || !aligned(a->page_table, 4) ||
-        !aligned(a->positions, 4))
-        return QMM_ERR_INVALID_ARG;
-    return QMM_OK;
+    const int v = qmm_kv_validate_desc(d);
+    return v != QMM_OK ? v : check_append(d, cache, a);
 }
 
 int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_append_args* a, void* stream) {
     if (p == nullptr) return QMM_ERR_INVALID_ARG;
-    const int chk = qmm_check_qk_norm_rope_args(&p->d, cache, a);
+    const int chk = check_append(&p->d, cache, a);
     if (chk != QMM_OK) return chk;
     if (a->seqs == 0 || a->rows == 0) return QMM_OK;
     const OnDevice on(p->device);
@@ -223,25 +246,13 @@ int qmm_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qm
 }
 
 int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_attention_args* a) {
-    if (d == nullptr || a == nullptr) return QMM_ERR_INVALID_ARG;
-    const int chk = check_cache(cache);
-    if (chk != QMM_OK) return chk;
-    const int seqs = a->seqs, rows = a->rows;
-    if (seqs < 0 || seqs > d->max_seqs || rows < 0 || rows > d->max_rows) return QMM_ERR_INVALID_ARG;
-    const int64_t tokens = static_cast<int64_t>(seqs) * rows;
-    if (tokens == 0) return QMM_OK;
-    const int64_t row_tiles = (static_cast<int64_t>(rows) * (d->q_heads / d->kv_heads) + 15) / 16;
-    if (static_cast<int64_t>(seqs) * d->kv_heads * row_tiles >= (1LL << 30)) return QMM_ERR_UNSUPPORTED;
-    const int64_t dq = static_cast<int64_t>(d->q_heads) * d->head_dim;
-    if (!rows_ok(a->q, a->q_stride, dq, 2, tokens) || !rows_ok(a->out, a->out_stride, dq, 2, tokens)) return QMM_ERR_INVALID_ARG;
-    if (a->page_table == nullptr || !aligned(a->page_table, 4) || a->lengths == nullptr || !aligned(a->lengths, 4))
-        return QMM_ERR_INVALID_ARG;
-    return QMM_OK;
+    const int v = qmm_kv_validate_desc(d);
+    return v != QMM_OK ? v : check_attention(d, cache, a);
 }
 
 int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_attention_args* a, void* stream) {
     if (p == nullptr) return QMM_ERR_INVALID_ARG;
-    const int chk = qmm_check_attention_args(&p->d, cache, a);
+    const int chk = check_attention(&p->d, cache, a);
     if (chk != QMM_OK) return chk;
     if (a->seqs == 0 || a->rows == 0) return QMM_OK;
     const OnDevice on(p->device);

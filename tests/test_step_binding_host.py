@@ -236,3 +236,20 @@ def test_sampling_launches_on_the_logits_device(q, monkeypatch):
     monkeypatch.setattr(q._LIB, "calls", events)   # in one list with the calls
     q.sample(logits, f, i, f, f, f, i, stream=0)
     assert [e[0] for e in events] == ["enter", logits.data_ptr(), "exit"] and events[0][1] == 3
+
+
+@pytest.mark.parametrize("change", [{"kv_heads": 0}, {"kv_heads": -3}, {"q_heads": 0}, {"head_dim": 0}, {"head_dim": 96},
+                                    {"page_size": 24}, {"max_rows": 17}])
+def test_argument_checks_refuse_a_descriptor_that_is_not_valid(change):
+    """As the check of the descriptor does, whatever the arguments, and without a division by its fields."""
+    from bit_affine_quantized_group_gb300 import _build
+    _build.build()
+    import bit_affine_quantized_group_gb300 as q
+    d = q.make_kv_desc(HQ, HKV, D, PAGE, SEQS, 4, MAX_PAGES)
+    for name, value in change.items():
+        setattr(d, name, value)
+    want = q.kv_validate_desc(d)
+    assert want != q.QMM_OK
+    cache, attend, append = q.QmmKvCache(), q.QmmAttentionArgs(), q.QmmAppendArgs()
+    assert q.lib.qmm_check_attention_args(ctypes.byref(d), ctypes.byref(cache), ctypes.byref(attend)) == want
+    assert q.lib.qmm_check_qk_norm_rope_args(ctypes.byref(d), ctypes.byref(cache), ctypes.byref(append)) == want
