@@ -6,7 +6,10 @@
 //
 // Whole-number masses add up to the same sum in any order (a row holds less
 // than 2^59), so histograms with atomics, any split of the row and any order of
-// arrival give the same token.
+// arrival give the same token. What lies above a threshold is told by logit and
+// index in some variants, by the bits of the weights first in others: the same
+// set, for expf never falls as its argument rises (looked at for every float32
+// from -110 to 0) and the steps before it are rounded to nearest.
 //
 // A row is one cluster's: its CTAs exchange maxima, histograms and sums through distributed shared memory. top-k and top-p
 // are thresholds in the order (logit falling, index rising), and what lies above one is nearly always few tokens:
@@ -22,7 +25,8 @@
 // with top_p 0.9 38 us. The bound of many rows is the time that a row's steps hold an SM, so that the fewest CTAs that fill
 // the GPU take a row and read it again from the L2 cache where they need it, for parts of rows in shared memory leave no
 // room for other rows: 256 x 100,277 with top_k 50 in 30 us, 3.4 TB/s, where 8 CTAs each that keep the row took 85 us. What
-// top_p alone costs there (256 x 151,936 bfloat16 275 us) is an exponential and two additions in shared memory a logit.
+// top_p alone costs there (256 x 151,936 bfloat16 282 us, 107 without any limit) is an exponential and two additions in
+// shared memory a logit.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
