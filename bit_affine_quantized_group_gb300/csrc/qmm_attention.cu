@@ -23,10 +23,10 @@
 // does where there are more than 16 rows: one CTA would read them for too long.
 //
 // Measured with 8 cache heads of 128: 1 x 131,072 positions 88 us, 6.1 TB/s; 64
-// ragged sequences 187 us, 6.0 TB/s; 1 x 257 positions 8.1 us, latency. With 4
-// of them, 4 sequences x 8 tokens (64 rows) take 34 us, bound by the products;
-// 24 sequences with a window of 4,096 and 2 heads of 256 take 48 us, 4.1 TB/s, a
-// quarter of it start and join.
+// ragged sequences 186 us, 6.0 TB/s; 1 x 257 positions 8.0 us, latency. With 4
+// of them, 4 sequences x 8 tokens (64 rows) take 34 us, 14 of it products at
+// mma.sync's rate; 24 sequences with a window of 4,096 and 2 heads of 256 take
+// 48 us, 4.0 TB/s, a quarter of it start and join.
 #include <cuda_bf16.h>
 
 #include "../../include/qmm.h"
