@@ -377,7 +377,8 @@ def kv_workspace_bytes(desc: QmmKvDesc) -> int:
 
 class KVPlan:
     """A plan of the cache operators (qmm_kv_plan / qmm_kv_destroy) for one kind of attention layer. Its workspace
-    is a PyTorch-allocated device buffer unless ``torch_workspace=False``. Arguments as for `make_kv_desc`."""
+    is a PyTorch-allocated device buffer unless ``torch_workspace=False``; keep the plan until its calls have run.
+    Arguments as for `make_kv_desc`."""
 
     def __init__(self, *args, torch_workspace: bool = True, device=None, **kwargs):
         import torch

@@ -404,9 +404,11 @@ typedef struct qmm_attention_args {
  * out[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j over the positions j
  * that token t sees: j <= pos, and with a window pos - j < window or j < sinks.
  * Query head h reads cache head h / (q_heads / kv_heads). The scores, the
- * softmax's maximum and sum and the output are held in float32. A row that
- * sees nothing gives zeros, and no value at a position that a row does not see
- * reaches that row, infinities and NaN among them.
+ * softmax's maximum and sum and the output are held in float32, the output
+ * until its end as the sum before the division: values from 2^127 / positions
+ * on can overflow it. A row that sees nothing gives zeros, and no value at a
+ * position that a row does not see reaches that row, infinities and NaN among
+ * them.
  *
  * The work of all sequences is cut into equal shares for the GPU whatever their
  * lengths; the parts of one head are joined in a fixed order, so a call with
