@@ -10,7 +10,7 @@
 // The bound of many tokens is the bytes, but instructions are close to it: 4 x
 // 2048 tokens of 48 heads of 128 take 35.1 us, 5.8 TB/s, where pairs that met by
 // shuffles, single float32 operations and addresses computed for every vector
-// took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.3 us for
+// took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.2 us for
 // one), and a warp takes only as many heads as it can have in flight.
 #include <cuda_bf16.h>
 

@@ -21,10 +21,10 @@
 // candidates are left (flat ones, many equal logits) are resolved bin by bin, then bit by bit, then by index.
 //
 // The bound of few rows is latency: the exchanges, and instructions that run once and have to be fetched. 16 CTAs a row
-// (8 from 9 rows on) read it once and keep it in shared memory: 1 x 151,936 with top_k 50 8.7 us, 16 x 151,936 bfloat16
+// (8 from 9 rows on) read it once and keep it in shared memory: 1 x 151,936 with top_k 20 8.6 us, 16 x 151,936 bfloat16
 // with top_p 0.9 38 us. The bound of many rows is the time that a row's steps hold an SM, so that the fewest CTAs that fill
 // the GPU take a row and read it again from the L2 cache where they need it, for parts of rows in shared memory leave no
-// room for other rows: 256 x 100,277 with top_k 50 in 30 us, 3.4 TB/s, where 8 CTAs each that keep the row took 85 us. What
+// room for other rows: 256 x 100,277 with top_k 50 in 31 us, 3.3 TB/s, where 8 CTAs each that keep the row took 85 us. What
 // top_p alone costs there (256 x 151,936 bfloat16 282 us, 107 without any limit) is an exponential and two additions in
 // shared memory a logit.
 #include <cooperative_groups.h>
