@@ -41,7 +41,14 @@ KV_TIMEOUT = 7
 KV_BAD_PAGE = 16
 KV_BAD_LENGTH = 32
 KV_BAD_POSITION = 64
+KV_NOT_FINITE = 128
+KVQ_GROUP = 64
+KVQ_LARGEST = 65280.0
+ADAPTER_MAX_RANK = 128
+ADAPTER_MAX_ROWS = 1 << 20
+ADAPTER_BAD_ID = 1
 SAMPLE_MAX_VOCAB = 393216
+LOGPROBS_MAX_TOP = 32
 
 # Every entry point declared in include/qmm.h.
 EXPORTS = (
@@ -50,6 +57,10 @@ EXPORTS = (
     "qmm_plan_error", "qmm_destroy", "qmm_status_string", "qmm_forward_noalloc", "qmm_forward_swiglu",
     "qmm_kv_validate_desc", "qmm_kv_workspace_bytes", "qmm_kv_plan", "qmm_kv_error", "qmm_kv_destroy",
     "qmm_check_qk_norm_rope_args", "qmm_qk_norm_rope", "qmm_check_attention_args", "qmm_attention", "qmm_sample",
+    "qmm_check_kvq_qk_norm_rope_args", "qmm_kvq_qk_norm_rope", "qmm_check_kvq_attention_args", "qmm_kvq_attention",
+    "qmm_check_kvq_read_args", "qmm_kvq_read", "qmm_adapter_validate_desc", "qmm_adapter_workspace_bytes",
+    "qmm_adapter_plan", "qmm_adapter_error", "qmm_adapter_destroy", "qmm_check_adapter_args", "qmm_add_adapters",
+    "qmm_logprobs",
 )
 
 
@@ -89,6 +100,29 @@ class QmmAppendArgs(ctypes.Structure):
                 ("rope_len", ctypes.c_int64), ("lengths", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64),
                 ("seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("in_dtype", ctypes.c_int32)]
+
+
+class QmmKvqCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_affine", "v_affine")] + [("num_pages", ctypes.c_int64)] + \
+               [(f"{s}_{d}_stride", ctypes.c_int64) for s in ("k", "v", "ka", "va") for d in ("page", "head", "slot")] + \
+               [("bits", ctypes.c_int32)]
+
+
+class QmmReadArgs(ctypes.Structure):
+    _fields_ = [("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("k_seq_stride", ctypes.c_int64),
+                ("k_row_stride", ctypes.c_int64), ("v_seq_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class QmmAdapterDesc(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int64), ("N", ctypes.c_int64), ("rank", ctypes.c_int32), ("adapters", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class QmmAdapterArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "a", "b", "scale", "ids", "y", "out")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "y_stride", "out_stride")] + [("rows", ctypes.c_int32)]
 
 
 class QmmError(RuntimeError):
@@ -131,11 +165,29 @@ def _load() -> ctypes.CDLL:
     lib.qmm_check_attention_args.argtypes = [kvd, kvc, vp]
     lib.qmm_attention.argtypes = [vp, kvc, vp, vp]
     lib.qmm_sample.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    kvq = ctypes.POINTER(QmmKvqCache)
+    lib.qmm_check_kvq_qk_norm_rope_args.argtypes = [kvd, kvq, vp]
+    lib.qmm_kvq_qk_norm_rope.argtypes = [vp, kvq, vp, vp]
+    lib.qmm_check_kvq_attention_args.argtypes = [kvd, kvq, vp]
+    lib.qmm_kvq_attention.argtypes = [vp, kvq, vp, vp]
+    lib.qmm_check_kvq_read_args.argtypes = [kvd, kvq, vp]
+    lib.qmm_kvq_read.argtypes = [vp, kvq, vp, vp]
+    add = ctypes.POINTER(QmmAdapterDesc)
+    lib.qmm_adapter_validate_desc.argtypes = [add]
+    lib.qmm_adapter_workspace_bytes.argtypes = [add]
+    lib.qmm_adapter_workspace_bytes.restype = sz
+    lib.qmm_adapter_plan.argtypes = [ctypes.POINTER(vp), add, vp, sz]
+    lib.qmm_adapter_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+    lib.qmm_adapter_destroy.argtypes = [vp]
+    lib.qmm_adapter_destroy.restype = None
+    lib.qmm_check_adapter_args.argtypes = [add, vp]
+    lib.qmm_add_adapters.argtypes = [vp, vp, vp]
+    lib.qmm_logprobs.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, i32, vp, vp, vp]
     lib.qmm_status_string.argtypes = [i32]
     lib.qmm_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
         if name not in ("qmm_workspace_bytes", "qmm_destroy", "qmm_status_string", "qmm_kv_workspace_bytes",
-                        "qmm_kv_destroy"):
+                        "qmm_kv_destroy", "qmm_adapter_workspace_bytes", "qmm_adapter_destroy"):
             getattr(lib, name).restype = i32
     return lib
 
@@ -450,10 +502,44 @@ class KVCache:
         self.ref = ctypes.byref(self.struct)
 
 
+class QuantKVCache:
+    """A paged cache of group-wise affine codes, in the place of a KVCache: every 64 elements of a head as 8- or 4-bit codes c
+    with a float16 scale s and bias b, which stand for s * c + b. k and v: uint8 [pages, kv_heads, page_size, head_dim * bits
+    / 8], code j of a head in bits j * bits and on; k_affine and v_affine: float16 [pages, kv_heads, page_size, head_dim /
+    64, 2], the scales and biases. Any strides (of codes in multiples of 16 bytes) with adjacent heads' elements."""
+
+    def __init__(self, k, v, k_affine, v_affine, bits):
+        import torch
+        if bits not in (8, 4):
+            raise ValueError("bits is 8 or 4")
+        for t in (k, v, k_affine, v_affine):
+            if t.get_device() != k.get_device():
+                raise ValueError("codes, scales and biases are on the same device")
+        for t in (k, v):
+            if t.dim() != 4 or t.dtype != torch.uint8 or t.shape != k.shape or t.stride(3) != 1 or \
+                    t.shape[3] * 8 // bits % KVQ_GROUP:
+                raise ValueError("k and v are uint8 tensors [pages, kv_heads, page_size, head_dim * bits / 8] of the same shape")
+        head_dim = k.shape[3] * 8 // bits
+        for t in (k_affine, v_affine):
+            if t.dtype != torch.float16 or t.shape != (*k.shape[:3], head_dim // KVQ_GROUP, 2) or t.stride(4) != 1 or \
+                    (t.stride(3) != 2 and t.shape[3] > 1) or any(s % 2 for s in t.stride()[:3]):
+                raise ValueError("k_affine and v_affine are float16 tensors [pages, kv_heads, page_size, head_dim / 64, 2]")
+        self.k, self.v, self.k_affine, self.v_affine, self.bits = k, v, k_affine, v_affine, bits
+        self.device_index = k.get_device()
+        self.page_shape = (*k.shape[1:3], head_dim)
+        pairs = lambda t: (s // 2 for s in t.stride()[:3])  # noqa: E731
+        self.struct = QmmKvqCache(k.data_ptr(), v.data_ptr(), k_affine.data_ptr(), v_affine.data_ptr(), k.shape[0],
+                                  *k.stride()[:3], *v.stride()[:3], *pairs(k_affine), *pairs(v_affine), bits)
+        self.ref = ctypes.byref(self.struct)
+
+
 # What a call passes to the library, packed for each call: threads may share a plan.
 _APPEND_ARGS = struct.Struct("@3P3q3Pq4Pq3i4x")      # QmmAppendArgs
 _ATTENTION_ARGS = struct.Struct("@4P2q2i")           # QmmAttentionArgs
+_READ_ARGS = struct.Struct("@2P4q3P3i4x")            # QmmReadArgs
+_ADAPTER_ARGS = struct.Struct("@7P3qi4x")            # QmmAdapterArgs
 assert _APPEND_ARGS.size == ctypes.sizeof(QmmAppendArgs) and _ATTENTION_ARGS.size == ctypes.sizeof(QmmAttentionArgs)
+assert _READ_ARGS.size == ctypes.sizeof(QmmReadArgs) and _ADAPTER_ARGS.size == ctypes.sizeof(QmmAdapterArgs)
 
 
 def _rows(t, tokens, width, dtype, what):
@@ -490,9 +576,10 @@ def _check_step(plan, cache, page_table, lengths, tokens, *others):
     return seqs, rows
 
 
-def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_table, cache: KVCache, out,
-                 positions=None, stream=None) -> None:
-    """Norms of q and k for each head, rotation, and the append of k and v to the cache (qmm_qk_norm_rope). q, k, v:
+def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_table, cache, out, positions=None,
+                 stream=None) -> None:
+    """Norms of q and k for each head, rotation, and the append of k and v to the cache (qmm_qk_norm_rope, or
+    qmm_kvq_qk_norm_rope for a QuantKVCache, which quantises them). q, k, v:
     [tokens, heads * head_dim] of float32 or bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and
     k_weight: float32 [head_dim] or None; rope: float32 [positions, rot_dim], cosines then sines."""
     dtype, tokens = q.dtype, q.shape[0]
@@ -515,22 +602,149 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
         rope.data_ptr() if plan.rot_dim else 0, rope.shape[0] if plan.rot_dim else 0, lengths.data_ptr(),
         0 if positions is None else positions.data_ptr(), page_table.data_ptr(), out.data_ptr(),
         _rows(out, tokens, plan.q_width, _BF16, "out"), seqs, rows, QMM_IN_F32 if dtype is _F32 else QMM_IN_BF16)
-    st = _LIB.qmm_qk_norm_rope(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
+    call = _LIB.qmm_kvq_qk_norm_rope if isinstance(cache, QuantKVCache) else _LIB.qmm_qk_norm_rope
+    st = call(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_qk_norm_rope")
 
 
-def attention(plan: KVPlan, q, cache: KVCache, page_table, lengths, out, stream=None) -> None:
-    """Attention of the new tokens over the cache (qmm_attention): q and out [tokens, q_heads, head_dim] bfloat16 (or
+def attention(plan: KVPlan, q, cache, page_table, lengths, out, stream=None) -> None:
+    """Attention of the new tokens over the cache (qmm_attention, or qmm_kvq_attention for a QuantKVCache): q and out [tokens, q_heads, head_dim] bfloat16 (or
     [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
     tokens = q.shape[0]
     seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, q, out)
     args = _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
                                 _rows(q, tokens, plan.q_width, _BF16, "q"), _rows(out, tokens, plan.q_width, _BF16, "out"),
                                 seqs, rows)
-    st = _LIB.qmm_attention(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
+    call = _LIB.qmm_kvq_attention if isinstance(cache, QuantKVCache) else _LIB.qmm_attention
+    st = call(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
         raise QmmError(st, "qmm_attention")
+
+
+def _dense(t, seqs, plan, dtype, what):
+    """Strides from sequence to sequence and from row to row of a tensor [seqs, rows, kv_heads, head_dim]."""
+    shape, st, heads, d = t.shape, t.stride(), plan.page_shape[0], plan.head_dim
+    if t.dtype is not dtype or len(shape) != 4 or shape[0] != seqs or shape[2] != heads or shape[3] != d or st[3] != 1 or \
+            (st[2] != d and heads > 1):
+        raise ValueError(f"{what} is a {dtype} tensor [seqs, rows, kv_heads, head_dim] of adjacent heads")
+    return st[0], st[1]
+
+
+def kv_read(plan: KVPlan, cache: QuantKVCache, page_table, lengths, k_out, v_out, starts=None, stream=None) -> None:
+    """Keys and values of a cache of codes, back in float32 or bfloat16 (qmm_kvq_read): row j of sequence s of k_out and v_out
+    [seqs, rows, kv_heads, head_dim] is its position starts[s] + j (starts: int32 [seqs]; None: 0). Rows of positions
+    before 0 or from lengths[s] on are left as they were."""
+    if not isinstance(cache, QuantKVCache):
+        raise ValueError("cache is a QuantKVCache")
+    seqs, _ = _check_step(plan, cache, page_table, lengths, 0, k_out, v_out, starts)
+    dtype = k_out.dtype
+    if dtype is not _F32 and dtype is not _BF16:
+        raise ValueError("k_out and v_out are float32 or bfloat16")
+    if starts is not None and (starts.dtype is not _I32 or starts.numel() != seqs or not starts.is_contiguous()):
+        raise ValueError("starts is an int32 tensor [seqs]")
+    k_strides, v_strides = _dense(k_out, seqs, plan, dtype, "k_out"), _dense(v_out, seqs, plan, dtype, "v_out")
+    if k_out.shape[1] != v_out.shape[1]:
+        raise ValueError("k_out and v_out have the same number of rows")
+    args = _READ_ARGS.pack(k_out.data_ptr(), v_out.data_ptr(), *k_strides, *v_strides, lengths.data_ptr(),
+                           0 if starts is None else starts.data_ptr(), page_table.data_ptr(), seqs, k_out.shape[1],
+                           QMM_OUT_F32 if dtype is _F32 else QMM_OUT_BF16)
+    st = _LIB.qmm_kvq_read(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
+    if st != QMM_OK:
+        raise QmmError(st, "qmm_kvq_read")
+
+
+def make_adapter_desc(K, N, rank, adapters, max_rows, out_dtype="bf16") -> QmmAdapterDesc:
+    return QmmAdapterDesc(int(K), int(N), int(rank), int(adapters), int(max_rows), _out_code(out_dtype))
+
+
+def adapter_validate_desc(desc: QmmAdapterDesc) -> int:
+    return int(_lib().qmm_adapter_validate_desc(ctypes.byref(desc)))
+
+
+def adapter_workspace_bytes(desc: QmmAdapterDesc) -> int:
+    return int(_lib().qmm_adapter_workspace_bytes(ctypes.byref(desc)))
+
+
+class AdapterPlan:
+    """A plan of add_adapters (qmm_adapter_plan / qmm_adapter_destroy) beside projections from K to N. Its workspace is a
+    PyTorch-allocated device buffer unless ``torch_workspace=False``; keep the plan until its calls have run. Arguments as
+    for `make_adapter_desc`."""
+
+    def __init__(self, *args, torch_workspace: bool = True, device=None, **kwargs):
+        import torch
+        _bind_torch()
+        self.desc = d = make_adapter_desc(*args, **kwargs)
+        st = adapter_validate_desc(d)
+        if st != QMM_OK:
+            raise QmmError(st, "qmm_adapter_validate_desc")
+        self._handle = ctypes.c_void_p()
+        self.workspace = None
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
+        with torch.cuda.device(dev):
+            ws, nbytes = None, 0
+            if torch_workspace:
+                nbytes = adapter_workspace_bytes(d)
+                self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
+                ws = (self.workspace.data_ptr() + 255) // 256 * 256
+                _wait_for_block(dev)
+            st = _lib().qmm_adapter_plan(ctypes.byref(self._handle), ctypes.byref(d), ws, nbytes)
+        if st != QMM_OK:
+            raise QmmError(st, "qmm_adapter_plan")
+        self.device, self._device_index = dev, dev.index
+        self.K, self.N, self.rank, self.adapters = d.K, d.N, d.rank, d.adapters
+        self.out_dtype = torch.float32 if d.out_dtype == QMM_OUT_F32 else torch.bfloat16
+
+    @property
+    def handle(self):
+        return self._handle
+
+    def error_flags(self) -> int:
+        """ADAPTER_BAD_ID, if a call since the last read met one; cleared. Waits for the device."""
+        v = ctypes.c_uint32(0)
+        st = _lib().qmm_adapter_error(self._handle, ctypes.byref(v))
+        if st not in (QMM_OK, QMM_ERR_INVALID_ARG):
+            raise QmmError(st, "qmm_adapter_error")
+        return int(v.value)
+
+    def close(self):
+        if self._handle is not None and self._handle.value:
+            _lib().qmm_adapter_destroy(self._handle)
+            self._handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def add_adapters(plan: AdapterPlan, x, a, b, scale, ids, y, out, stream=None) -> None:
+    """out = y + scale[i] * (x a[i]^T) b[i]^T for each row, i = ids[row], -1 for none (qmm_add_adapters). x: bfloat16
+    [rows, K]; y and out: [rows, N] of the plan's out_dtype, which may be the same tensor; rows of any stride. a: bfloat16
+    [adapters, rank, K]; b: [adapters, N, rank]; scale: float32 [adapters] or None; ids: int32 [rows]."""
+    device = plan._device_index
+    for t in (x, a, b, scale, ids, y, out):
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors are on the plan's device {plan.device}")
+    if x.dim() != 2 or y.dim() != 2 or out.dim() != 2:
+        raise ValueError("x, y and out are [rows, width]")
+    rows, K, N = x.shape[0], plan.K, plan.N
+    if a.dtype is not _BF16 or b.dtype is not _BF16 or a.shape != (plan.adapters, plan.rank, K) or \
+            b.shape != (plan.adapters, N, plan.rank) or not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a [adapters, rank, K] and b [adapters, N, rank] are contiguous bfloat16 tensors")
+    if scale is not None and (scale.dtype is not _F32 or scale.numel() != plan.adapters or not scale.is_contiguous()):
+        raise ValueError("scale is float32 [adapters] or None")
+    if ids.dtype is not _I32 or ids.numel() != rows or not ids.is_contiguous():
+        raise ValueError("ids is an int32 tensor [rows]")
+    args = _ADAPTER_ARGS.pack(x.data_ptr(), a.data_ptr(), b.data_ptr(), 0 if scale is None else scale.data_ptr(),
+                              ids.data_ptr(), y.data_ptr(), out.data_ptr(), _rows(x, rows, K, _BF16, "x"),
+                              _rows(y, rows, N, plan.out_dtype, "y"), _rows(out, rows, N, plan.out_dtype, "out"), rows)
+    st = _LIB.qmm_add_adapters(plan._handle, args, _stream_on(stream, device))
+    if st != QMM_OK:
+        raise QmmError(st, "qmm_add_adapters")
 
 
 def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stream=None) -> None:
@@ -565,3 +779,47 @@ def sample(logits, temperature, top_k, top_p, min_p, u, tokens, probs=None, stre
             st = _lib().qmm_sample(*args)
     if st != QMM_OK:
         raise QmmError(st, "qmm_sample")
+
+
+def logprobs(logits, tokens, token_logprobs, entropy=None, top_tokens=None, top_logprobs=None, stream=None) -> None:
+    """Log probabilities of one given token for each row of logits [M, vocab] (float32 or bfloat16, rows of any stride), the
+    rows' entropy, and their likeliest tokens (qmm_logprobs). tokens: int32 [M] and token_logprobs float32 [M], or both
+    None; entropy: float32 [M] or None; top_tokens: int32 [M, n] and top_logprobs float32 [M, n] with n up to
+    LOGPROBS_MAX_TOP, or both None."""
+    if _F32 is None:
+        _bind_torch()
+    f32, i32, dtype = _F32, _I32, logits.dtype
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) != 2 or (dtype is not f32 and dtype is not _BF16) or strides[1] != 1:
+        raise ValueError("logits are float32 or bfloat16 rows of adjacent elements")
+    M, device = shape[0], logits.get_device()
+    if (tokens is None) != (token_logprobs is None) or (top_tokens is None) != (top_logprobs is None):
+        raise ValueError("tokens and token_logprobs, and top_tokens and top_logprobs, are given together")
+    top = 0
+    if top_tokens is not None:
+        if top_tokens.dim() != 2 or top_tokens.shape != top_logprobs.shape:
+            raise ValueError("top_tokens and top_logprobs are [M, n]")
+        top = top_tokens.shape[1]
+        if top == 0:
+            top_tokens = top_logprobs = None
+    for t, want, n in ((tokens, i32, M), (token_logprobs, f32, M), (entropy, f32, M), (top_tokens, i32, M * top),
+                       (top_logprobs, f32, M * top)):
+        if t is None:
+            continue
+        if t.dtype is not want or t.numel() != n or not t.is_contiguous():
+            raise ValueError("tokens are int32 and log probabilities and entropy float32, contiguous, for the M rows")
+        if t.get_device() != device:
+            raise ValueError("all tensors are on the device of the logits")
+    if device < 0:
+        raise ValueError("logits are on a CUDA device")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    args = (logits.data_ptr(), M, shape[1], strides[0], QMM_IN_F32 if dtype is f32 else QMM_IN_BF16, ptr(tokens),
+            ptr(token_logprobs), ptr(entropy), top, ptr(top_tokens), ptr(top_logprobs), _stream_on(stream, device))
+    if device == _CURRENT_DEVICE():
+        st = _lib().qmm_logprobs(*args)
+    else:
+        import torch
+        with torch.cuda.device(device):   # the library launches on the current one
+            st = _lib().qmm_logprobs(*args)
+    if st != QMM_OK:
+        raise QmmError(st, "qmm_logprobs")

@@ -12,6 +12,11 @@
 // shuffles, single float32 operations and addresses computed for every vector
 // took 45 at 66 % of the issue slots. Few tokens are bound by latency (2.2 us for
 // one), and a warp takes only as many heads as it can have in flight.
+//
+// For a cache of codes a head's float32 values pass through shared memory, after
+// which a lane has eight neighbours and eight lanes a group of 64, whose least
+// and largest they find by shuffles:
+//   b = f16(lo),  s = f16((hi - lo) / top),  c = round((x - b) (1 / s)).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -118,14 +123,57 @@ __device__ __forceinline__ void store_pairs(uint16_t* dst, int second, const Pai
     }
 }
 
+// Eight neighbouring values of a head as codes, of 8 or 4 bits in 8 or 4 bytes. The lanes of a group of 64 call it together;
+// `affine` gets their scale and bias. False: a value was not finite.
+template <int BITS>
+__device__ __forceinline__ bool quantise(float (&x)[8], uint32_t (&codes)[BITS / 4], uint32_t& affine) {
+    constexpr float kTop = (1 << BITS) - 1, kLargest = QMM_KVQ_LARGEST;
+    bool finite = true;
+    float lo = kLargest, hi = -kLargest;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        finite &= fabsf(x[i]) < INFINITY;
+        x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kLargest), kLargest) : 0.0f;
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    }
+    const __half scale = __float2half_rn(__fdiv_rn(hi - lo, kTop)), bias = __float2half_rn(lo);
+    const float s = __half2float(scale), b = __half2float(bias);
+    const float inverse = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    affine = static_cast<uint32_t>(__half_as_ushort(scale)) | static_cast<uint32_t>(__half_as_ushort(bias)) << 16;
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)   // the sum's last bits are the whole number, rounded to the nearest, ties to even
+        c[i] = __float_as_uint(fminf(fmaxf(__fmul_rn(x[i] - b, inverse), 0.0f), kTop) + 0x1p23f);
+    if constexpr (BITS == 8) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            codes[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040), __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040),
+                                   0x5410);
+    } else {
+        codes[0] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) codes[0] |= (c[i] & 15u) << (4 * i);
+    }
+    return finite;
+}
+
 // One warp takes `span` heads of one token, kSteps vectors of 32 / (D / 8) heads at a time: position, page and rotation are
 // looked up once for all of them, and the next vectors are on their way while it works on the last.
-template <int D, bool F32, bool NEAR>
+// BITS: of a cache of codes; 16 for one of bfloat16.
+template <int D, bool F32, bool NEAR, int BITS>
 __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __grid_constant__ AppendParams p, int span) {
     constexpr int kLanes = D / 8;
     constexpr int kHeads = 32 / kLanes;
     constexpr int kSteps = kAppendSteps;
     constexpr int kSize = F32 ? 4 : 2;
+    __shared__ __align__(16) float s_heads[BITS != 16 && !NEAR ? kAppendWarps * kHeads * D : 4];
+    float* const head_values = s_heads + (BITS != 16 && !NEAR ? (threadIdx.x >> 5) * kHeads * D : 0);
     const int lane = threadIdx.x & 31;
     const int heads = p.q_heads + 2 * p.kv_heads, qk_heads = p.q_heads + p.kv_heads;
     const int per_token = (heads + span - 1) / span;
@@ -168,7 +216,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
         return;
     }
 
-    // where head 0 would lie, and from head to head
+    // where head 0 would lie, and from head to head (codes: of this lane's eight neighbours, and their group's pair)
+    uint8_t *code[2] = {}, *pair[2] = {};
+    const int64_t code_step[2] = {p.k.head, p.v.head}, pair_step[2] = {p.ka.head, p.va.head};
     uint16_t* dst[3] = {p.q_out + token * p.q_out_stride + e0, nullptr, nullptr};
     const int64_t step[3] = {D, p.k.head, p.v.head};
     bool store = false;
@@ -180,8 +230,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
         if (page < 0 || page >= p.num_pages) {
             if (lane == 0) atomicOr(p.err, QMM_KV_BAD_PAGE);
         } else {
-            dst[1] = p.k.base + page * p.k.page + slot * p.k.slot - p.q_heads * p.k.head + e0;
-            dst[2] = p.v.base + page * p.v.page + slot * p.v.slot - qk_heads * p.v.head + e0;
+            if constexpr (BITS == 16) {
+                dst[1] = p.k.base + page * p.k.page + slot * p.k.slot - p.q_heads * p.k.head + e0;
+                dst[2] = p.v.base + page * p.v.page + slot * p.v.slot - qk_heads * p.v.head + e0;
+            } else {   // strides of bytes, and of pairs of 4 bytes
+                code[0] = reinterpret_cast<uint8_t*>(p.k.base) + page * p.k.page + slot * p.k.slot - p.q_heads * p.k.head + l * BITS;
+                code[1] = reinterpret_cast<uint8_t*>(p.v.base) + page * p.v.page + slot * p.v.slot - qk_heads * p.v.head + l * BITS;
+                pair[0] = reinterpret_cast<uint8_t*>(p.ka.base) +
+                          4 * (page * p.ka.page + slot * p.ka.slot - p.q_heads * p.ka.head + l / 8);
+                pair[1] = reinterpret_cast<uint8_t*>(p.va.base) +
+                          4 * (page * p.va.page + slot * p.va.slot - qk_heads * p.va.head + l / 8);
+            }
             store = true;
         }
     }
@@ -246,7 +305,36 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
                 }
             }
             const int kind = hd < p.q_heads ? 0 : hd < qk_heads ? 1 : 2;
-            if (hd < h1 && (kind == 0 || store)) {
+            if constexpr (BITS != 16) {
+                if (first + kHeads > p.q_heads && first < h1) {   // (the whole warp) keys or values among the heads
+                    float x[8];
+                    if constexpr (NEAR) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            x[4 * j] = y.a[j].x, x[4 * j + 1] = y.b[j].x, x[4 * j + 2] = y.a[j].y, x[4 * j + 3] = y.b[j].y;
+                    } else {
+                        float* const own = head_values + (lane / kLanes) * D;
+                        __syncwarp();
+                        *reinterpret_cast<float4*>(own + e0) = make_float4(y.a[0].x, y.a[0].y, y.a[1].x, y.a[1].y);
+                        *reinterpret_cast<float4*>(own + e0 + second) = make_float4(y.b[0].x, y.b[0].y, y.b[1].x, y.b[1].y);
+                        __syncwarp();
+                        const float4 u = *reinterpret_cast<const float4*>(own + 8 * l), w = *reinterpret_cast<const float4*>(own + 8 * l + 4);
+                        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+                    }
+                    uint32_t c[BITS / 4], affine;
+                    const bool finite = quantise<BITS>(x, c, affine);
+                    if (kind != 0 && hd < h1 && store) {
+                        uint8_t* const to = (kind == 1 ? code[0] : code[1]) + hd * (kind == 1 ? code_step[0] : code_step[1]);
+                        if constexpr (BITS == 8) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+                        else *reinterpret_cast<uint32_t*>(to) = c[0];
+                        if (l % 8 == 0)
+                            *reinterpret_cast<uint32_t*>((kind == 1 ? pair[0] : pair[1]) +
+                                                         4 * hd * (kind == 1 ? pair_step[0] : pair_step[1])) = affine;
+                        if (!finite) atomicOr(p.err, QMM_KV_NOT_FINITE);
+                    }
+                }
+                if (hd < h1 && kind == 0) store_pairs<NEAR>(dst[0] + hd * step[0], second, y);
+            } else if (hd < h1 && (kind == 0 || store)) {
                 uint16_t* const base = kind == 0 ? dst[0] : kind == 1 ? dst[1] : dst[2];
                 store_pairs<NEAR>(base + hd * (kind == 0 ? step[0] : kind == 1 ? step[1] : step[2]), second, y);
             }
@@ -254,7 +342,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
     }
 }
 
-template <int D, bool F32, bool NEAR>
+template <int D, bool F32, bool NEAR, int BITS>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
     // few tokens: a warp for every load in flight; many: equal parts of a token, up to all of it
     constexpr int kPerLoad = 32 / (D / 8) * kAppendSteps;
@@ -275,22 +363,28 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qmm_append_kernel<D, F32, NEAR>, p, span);
+    return cudaLaunchKernelEx(&cfg, qmm_append_kernel<D, F32, NEAR, BITS>, p, span);
 }
 
 }  // namespace
 
-cudaError_t launch_append(int head_dim, bool in_f32, const AppendParams& p, cudaStream_t stream) {
-    auto with = [&](auto f32, auto near) -> cudaError_t {
+cudaError_t launch_append(int head_dim, bool in_f32, int bits, const AppendParams& p, cudaStream_t stream) {
+    auto with = [&](auto f32, auto near, auto of) -> cudaError_t {
         constexpr bool F32 = decltype(f32)::value, NEAR = decltype(near)::value;
-        if (head_dim == 64) return launch<64, F32, NEAR>(p, stream);
-        if (head_dim == 128) return launch<128, F32, NEAR>(p, stream);
-        return launch<256, F32, NEAR>(p, stream);
+        constexpr int BITS = decltype(of)::value;
+        if (head_dim == 64) return launch<64, F32, NEAR, BITS>(p, stream);
+        if (head_dim == 128) return launch<128, F32, NEAR, BITS>(p, stream);
+        return launch<256, F32, NEAR, BITS>(p, stream);
     };
     const std::true_type yes;
     const std::false_type no;
-    if (in_f32) return p.interleaved ? with(yes, yes) : with(yes, no);
-    return p.interleaved ? with(no, yes) : with(no, no);
+    auto of_bits = [&](auto of) -> cudaError_t {
+        if (in_f32) return p.interleaved ? with(yes, yes, of) : with(yes, no, of);
+        return p.interleaved ? with(no, yes, of) : with(no, no, of);
+    };
+    if (bits == 8) return of_bits(std::integral_constant<int, 8>());
+    if (bits == 4) return of_bits(std::integral_constant<int, 4>());
+    return of_bits(std::integral_constant<int, 16>());
 }
 
 }  // namespace qmmk

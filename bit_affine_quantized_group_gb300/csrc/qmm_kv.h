@@ -25,7 +25,7 @@ struct KvSide {
 };
 
 struct AttnParams {
-    KvSide k, v;
+    KvSide k, v, ka, va;    // as in AppendParams
     const uint16_t* q;
     uint16_t* out;
     const int32_t* page_table;
@@ -47,7 +47,8 @@ struct AttnParams {
 };
 
 struct AppendParams {
-    KvSide k, v;
+    KvSide k, v;            // for a cache of codes: bytes, and strides in bytes
+    KvSide ka, va;          // of a cache of codes: scales and biases, strides in pairs of them
     const void* in[3];      // q, k, v
     int64_t in_stride[3];
     uint16_t* q_out;
@@ -62,6 +63,19 @@ struct AppendParams {
     int64_t num_pages;
     int32_t tokens, rows, q_heads, kv_heads, max_pages, page_shift, rot_dim, interleaved;
     float eps;
+};
+
+struct ReadParams {
+    KvSide side[2], affine[2];   // of keys and values, as in AppendParams
+    void* out[2];
+    int64_t seq_stride[2], row_stride[2];
+    const int32_t* lengths;
+    const int32_t* starts;
+    const int32_t* page_table;
+    uint32_t* err;
+    int64_t num_pages;
+    int32_t seqs, rows, kv_heads, max_pages, page_shift;
+    int32_t positions;           // that the page table holds for a sequence
 };
 
 struct AttnWorkspace {
@@ -80,7 +94,14 @@ constexpr AttnWorkspace attn_workspace(int head_dim, int rows) {
 }
 
 cudaError_t configure_attention();
-cudaError_t launch_attention(int head_dim, const AttnParams& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_append(int head_dim, bool in_f32, const AppendParams& p, cudaStream_t stream);
+// bits: of a cache of codes; 16 for one of bfloat16
+cudaError_t launch_attention(int head_dim, int bits, const AttnParams& p, int num_sms, cudaStream_t stream);
+cudaError_t configure_attention_codes8();
+cudaError_t configure_attention_codes4();
+cudaError_t launch_attention_codes8(int head_dim, const AttnParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_attention_codes4(int head_dim, const AttnParams& p, int num_sms, cudaStream_t stream);
+// bits: of a cache of codes; 16 for one of bfloat16
+cudaError_t launch_append(int head_dim, bool in_f32, int bits, const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_read(int head_dim, bool out_f32, int bits, const ReadParams& p, cudaStream_t stream);
 
 }  // namespace qmmk

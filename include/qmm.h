@@ -300,7 +300,8 @@ enum {
     QMM_KV_BAD_PAGE = 16,     /* a page table entry in use lies outside 0..num_pages-1: read as zeros, not written */
     QMM_KV_BAD_LENGTH = 32,   /* a length above max_pages * page_size: rows stand where it says, and what is past the page
                                  table was neither written nor seen */
-    QMM_KV_BAD_POSITION = 64  /* a rotation position outside the rope table: the row was not rotated */
+    QMM_KV_BAD_POSITION = 64, /* a rotation position outside the rope table: the row was not rotated */
+    QMM_KV_NOT_FINITE = 128   /* an infinity or NaN was appended to a cache of codes */
 };
 
 /* What a plan for the cache operators fixes. */
@@ -418,6 +419,144 @@ typedef struct qmm_attention_args {
 int qmm_check_attention_args(const qmm_kv_desc* d, const qmm_kv_cache* cache, const qmm_attention_args* a);
 int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_attention_args* a, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The same operators over a cache of codes: every 64 elements of a head
+ * (positions are quantised one by one) are held as 8- or 4-bit codes c with a
+ * binary16 scale s and bias b, and stand for s c + b, as a projection's weights
+ * do. Code j of a head lies in bits j * bits .. j * bits + bits - 1 of its bytes
+ * (4 bits: the even code in the low half).
+ *
+ * Values x are quantised in float32, after norm and rotation and without a
+ * rounding before:
+ *   lo, hi = least and largest of the 64,   b = f16(lo),   s = f16((hi - lo) / top),
+ *   c = round((x - b) * (1 / s)) brought to 0..top,   c = 0 where s = 0,
+ * with top = 255 or 15, and roundings to the nearest, ties to even. An element
+ * is held within s/2 + 2^-11 (|lo| + |hi|) + 2^-17, times 1 + 2^-10. Elements
+ * beyond +-QMM_KVQ_LARGEST are brought to it and NaN to 0, so that what is
+ * appended is always finite; an infinity or NaN among them sets
+ * QMM_KV_NOT_FINITE in the plan's error word.
+ */
+#define QMM_KVQ_GROUP 64
+#define QMM_KVQ_LARGEST 65280
+
+/* The cache: as qmm_kv_cache, with strides of the codes in bytes (multiples of 16) and of the scales and biases in
+   pairs (multiples of head_dim / 64). */
+typedef struct qmm_kvq_cache {
+    void* k;              /* codes, head_dim * bits / 8 bytes of a head, 16-byte aligned */
+    void* v;
+    void* k_affine;       /* (scale, bias) binary16 pairs, head_dim / 64 of a head, 16-byte aligned */
+    void* v_affine;
+    int64_t num_pages;
+    int64_t k_page_stride, k_head_stride, k_slot_stride;
+    int64_t v_page_stride, v_head_stride, v_slot_stride;
+    int64_t ka_page_stride, ka_head_stride, ka_slot_stride;
+    int64_t va_page_stride, va_head_stride, va_slot_stride;
+    int32_t bits;         /* 8 or 4 */
+} qmm_kvq_cache;
+
+/* qmm_qk_norm_rope with keys and values quantised as they are written. The same plan, arguments and checks. */
+int qmm_check_kvq_qk_norm_rope_args(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_append_args* a);
+int qmm_kvq_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, const qmm_append_args* a, void* stream);
+
+/*
+ * qmm_attention over a cache of codes. The same plan, arguments and checks.
+ * Scores are products of the queries with whole codes, scaled in float32. Values
+ * enter the second product as binary16 (s c + b within 2^-11 of its value and of
+ * 128 s, or 8 s for 4 bits) and the softmax's weights as binary16 too (within
+ * 2^-11); sums and maxima are float32. s c + b beyond binary16 is infinite.
+ */
+int qmm_check_kvq_attention_args(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_attention_args* a);
+int qmm_kvq_attention(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, const qmm_attention_args* a, void* stream);
+
+/* What qmm_kvq_read reads and writes. All pointers are device pointers. */
+typedef struct qmm_read_args {
+    void* k_out;               /* row j of sequence s at k_out + s * k_seq_stride + j * k_row_stride: kv_heads * head_dim */
+    void* v_out;               /* elements of out_dtype, 16-byte aligned rows */
+    int64_t k_seq_stride, k_row_stride;   /* elements (multiples of 16 bytes) */
+    int64_t v_seq_stride, v_row_stride;
+    const int32_t* lengths;    /* [seqs] */
+    const int32_t* starts;     /* [seqs] the position of row 0; NULL: 0 */
+    const int32_t* page_table; /* [seqs, max_pages] */
+    int32_t seqs;              /* <= max_seqs */
+    int32_t rows;              /* rows of k_out and v_out for a sequence */
+    int32_t out_dtype;         /* QMM_OUT_F32 or QMM_OUT_BF16 */
+} qmm_read_args;
+
+/*
+ * Reads a cache of codes back: row j of sequence s gets s c + b of position
+ * starts[s] + j, exact in float32 but for one rounding, for positions from 0 to
+ * lengths[s] - 1. Rows of other positions are left as they were. Pages and
+ * lengths that are out of range are treated as in qmm_attention (zeros, and a
+ * bit of the error word). k_out, v_out and the cache do not overlap. One launch.
+ */
+int qmm_check_kvq_read_args(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_read_args* a);
+int qmm_kvq_read(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, const qmm_read_args* a, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a projection that they share:
+ *   out[m, :] = y[m, :] + scale[i] * (x[m, :] . A[i]^T) . B[i]^T,   i = ids[m],
+ * with y the projection's result for x. A row with id -1 has none: out = y.
+ * Rows of an adapter may stand anywhere. Adapters of a smaller rank are filled
+ * up with zero rows of A (and zero columns of B).
+ */
+#define QMM_ADAPTER_MAX_RANK 128
+#define QMM_ADAPTER_MAX_ROWS (1 << 20)
+
+enum { QMM_ADAPTER_BAD_ID = 1 };   /* error bit: an id outside -1..adapters-1, treated as -1 */
+
+/* What a plan for adapters fixes. */
+typedef struct qmm_adapter_desc {
+    int64_t K;          /* width of x, a multiple of 64 */
+    int64_t N;          /* width of y and out */
+    int32_t rank;       /* a multiple of 8, at most QMM_ADAPTER_MAX_RANK */
+    int32_t adapters;   /* how many A and B hold */
+    int32_t max_rows;   /* largest rows of a call, at most QMM_ADAPTER_MAX_ROWS */
+    int32_t out_dtype;  /* of y and out: QMM_OUT_F32 or QMM_OUT_BF16 */
+} qmm_adapter_desc;
+
+typedef struct qmm_adapter_plan qmm_adapter_plan_t;
+
+/* Validate a descriptor on the host (no CUDA call): QMM_OK, QMM_ERR_INVALID_ARG or QMM_ERR_UNSUPPORTED. */
+int qmm_adapter_validate_desc(const qmm_adapter_desc* d);
+
+/* Device workspace of a plan for `d` (error word and x . A^T of max_rows rows); 0 if d is invalid. */
+size_t qmm_adapter_workspace_bytes(const qmm_adapter_desc* d);
+
+/* Create a plan on the current device; device, workspace, streams and threads as for qmm_kv_plan. */
+int qmm_adapter_plan(qmm_adapter_plan_t** plan, const qmm_adapter_desc* d, void* workspace, size_t ws_bytes);
+
+/* Wait for the device, then read and clear the plan's error word, as qmm_kv_error. */
+int qmm_adapter_error(const qmm_adapter_plan_t* p, uint32_t* flags);
+
+/* Free the plan and any workspace it allocated. NULL is accepted. */
+void qmm_adapter_destroy(qmm_adapter_plan_t* p);
+
+/* What qmm_add_adapters reads and writes. All pointers are device pointers. */
+typedef struct qmm_adapter_args {
+    const void* x;        /* [rows, K] bfloat16, 16-byte aligned rows */
+    const void* a;        /* [adapters, rank, K] bfloat16, 16-byte aligned */
+    const void* b;        /* [adapters, N, rank] bfloat16, 16-byte aligned */
+    const float* scale;   /* [adapters]; NULL: 1 */
+    const int32_t* ids;   /* [rows] */
+    const void* y;        /* [rows, N] of out_dtype; may be out */
+    void* out;            /* [rows, N] */
+    int64_t x_stride;     /* elements from row to row (a multiple of 8) */
+    int64_t y_stride, out_stride;
+    int32_t rows;
+} qmm_adapter_args;
+
+/*
+ * Adds the adapters' products. x . A^T is summed in float32 and enters the
+ * second product as two bfloat16 terms (within 2^-17); that is summed in
+ * float32 with y and rounded once. The order of the sums is fixed: a call gives
+ * the same bits for the same inputs. out may be y itself (rows at the same
+ * places) and otherwise overlaps nothing. Two launches. rows = 0 is a no-op.
+ */
+int qmm_check_adapter_args(const qmm_adapter_desc* d, const qmm_adapter_args* a);
+int qmm_add_adapters(const qmm_adapter_plan_t* p, const qmm_adapter_args* a, void* stream);
+
 /* Largest vocabulary of qmm_sample. */
 #define QMM_SAMPLE_MAX_VOCAB 393216
 
@@ -443,6 +582,30 @@ int qmm_attention(const qmm_kv_plan_t* p, const qmm_kv_cache* cache, const qmm_a
 int qmm_sample(const void* logits, int M, int vocab, int64_t stride, int in_dtype, const float* temperature,
                const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
                float* probs, void* stream);
+
+/* Most alternatives of qmm_logprobs. */
+#define QMM_LOGPROBS_MAX_TOP 32
+
+/*
+ * Log probabilities of M rows of logits [M, vocab] (as for qmm_sample, rows
+ * `stride` elements apart), in one pass over them: with
+ *   lse = log sum_i exp(l_i),
+ *   token_logprobs[m] = l_t - lse for the given token t = tokens[m],
+ *   entropy[m] = -sum_i p_i log p_i, p_i = exp(l_i - lse),
+ *   top_tokens[m, 0..top-1], top_logprobs[m, 0..top-1]: the tokens of the largest
+ *     logits by falling logit, equal ones by rising index, and their l_i - lse.
+ * NaN logits count as -infinity and +infinity as the largest float32. A token
+ * outside 0..vocab-1 has the log probability -infinity; so has every token of a
+ * row without any logit above -infinity, whose entropy is 0. Places past the
+ * vocabulary get token -1 and -infinity. tokens and token_logprobs may both be
+ * NULL, and so may entropy; top = 0 with both of its arrays NULL asks for no
+ * alternatives (0 <= top <= QMM_LOGPROBS_MAX_TOP). 1 <= vocab <=
+ * QMM_SAMPLE_MAX_VOCAB. M = 0 is a no-op. One launch, on the current device; no
+ * plan, no workspace. The same logits give the same bits, for one number of rows
+ * and one place of the row's first logit in its 16 bytes.
+ */
+int qmm_logprobs(const void* logits, int M, int vocab, int64_t stride, int in_dtype, const int32_t* tokens,
+                 float* token_logprobs, float* entropy, int top, int32_t* top_tokens, float* top_logprobs, void* stream);
 
 /* Static description of a status code; never NULL. */
 const char* qmm_status_string(int status);
