@@ -1,0 +1,697 @@
+// Attention over a paged cache of 8- or 4-bit codes for up to 16 query rows of a cache head.
+//
+// The products are transposed, so that codes are their left operands and tiles of 8 query rows their right ones:
+//   S^T = K Q^T,   O^T = V^T P^T.
+// Scores of a lane are those of a position and two rows; two of them packed to binary16 and transposed across the warp
+// (movmatrix) are the second product's operand. The codes of a step stay in registers between shared memory and product:
+//   - A key's codes c become binary16 numbers 1024 + c (by a byte permutation, two at a time; of 4-bit codes half become
+//     64 + c, by masks), the queries q f with a power of two f of their row. A group of 64 elements adds
+//       s (sum q f (1024 + c) - 1024 sum q f) + b sum q f
+//     to f times the score, in float32.
+//   - A value becomes s (1024 + c) + r, one fused multiply-add with r = f16(b - 1024 s). What that rounding left out,
+//     e = b - 1024 s - r, is the same for a whole group of a position: sum P e is one more row of the product. Where |s| is
+//     so large that 1024 s is no binary16 number the codes are centred first.
+//   - The weights P are binary16 numbers of up to 2^15: one product, where the kernel of bfloat16 caches has two.
+//
+// The bound of long sequences is instructions: about 2 for an element of the cache.
+#pragma once
+
+#include <type_traits>
+
+#include "qmm_attention_shared.cuh"
+#include "qmm_attention_tiles.cuh"
+#include "qmm_codes.cuh"
+
+namespace qmmk {
+
+namespace {
+
+// ROWS8: tiles of 8 query rows, 1 or 2. Warps take parts of a step's positions, so that each has all rows.
+template <int D, int ROWS8, int BITS>
+struct CodesCfg {
+    static constexpr int kD = D, kBits = BITS, kRows = 8 * ROWS8;
+    static constexpr bool kInlineJoin = true, kSplitRegs = true;
+    static constexpr int kCompute = D == 256 ? 8 : 4;              // computing warps
+    static constexpr int kTeamWarps = D == 256 ? 4 : 2;
+    static constexpr int kTeams = kCompute / kTeamWarps;
+    static constexpr int kTiles = 4 / kTeamWarps;                  // 16-position tiles of a warp
+    static constexpr int kThreads = 32 * (kCompute + 4);           // and a group of four that starts the copies
+    static constexpr int kLaunchRegs = D == 256 ? 168 : 128;
+    static constexpr int kComputeRegs = D == 256 ? (ROWS8 == 1 ? 200 : 216) : ROWS8 == 1 ? 152 : 176;
+    static constexpr int kCopyRegs = ROWS8 == 1 ? 104 : D == 256 ? 72 : 80;
+    static_assert(kCompute * kComputeRegs + 4 * kCopyRegs <= (kCompute + 4) * kLaunchRegs, "registers of a CTA");
+    static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+    static constexpr int kShortShare = D < 256 ? 4 : 2;            // steps of the shortest share
+    static constexpr int kRowBytes = D * BITS / 8;                 // a position's codes
+    static constexpr int kPairBytes = D / 64 * 4;                  // its scales and biases, after the step's codes
+    static constexpr int kSideBytes = kStep * (kRowBytes + kPairBytes);
+    static constexpr int kJoinCols = D == 256 && ROWS8 == 2 ? 32 : 64;   // columns of all rows that the warps join at once
+    static constexpr int kJoinBytes = kCompute * kRows * kJoinCols * 4;
+    static constexpr bool kQueryRegs = D < 256;                    // else the queries stay in shared memory
+    static constexpr int kQueryBytes = kQueryRegs ? 0 : D * kRows * 2;
+    static constexpr int kSumBytes = kRows * (D / 64 * 8 + 4);     // of the queries' groups, and their rows' units
+    static constexpr int kSums = kQueryRegs ? kCompute : 1;        // each warp has its own, or all the same
+    static constexpr int kRoom = D == 256 ? 227 * 1024 : 113 * 1024;   // of a CTA
+    static constexpr int kSlotBytes = 2 * kSideBytes;              // both sides of a step
+    static constexpr int kMostSlots = 8;                           // of all teams
+    static constexpr int kFixedBytes = kJoinBytes + kQueryBytes + kSums * kSumBytes + (kCompute + 1) * kRows * 8 + 2 * kMostSlots * 8 + 16;
+    static constexpr int kFit = (kRoom - kFixedBytes) / (kTeams * kSlotBytes);
+    static constexpr int kSlots = kFit < kMostSlots / kTeams ? kFit : kMostSlots / kTeams;
+    static constexpr int kRingBytes = kSlots * kSlotBytes;         // of a team
+    static constexpr int kJoinAt = kTeams * kRingBytes;
+    static constexpr int kQueryAt = kJoinAt + kJoinBytes;
+    static constexpr int kSumsAt = kQueryAt + kQueryBytes;
+    static constexpr int kMlAt = kSumsAt + kSums * kSumBytes;
+    static constexpr int kTotalAt = kMlAt + kCompute * kRows * 8;
+    static constexpr int kBarsAt = kTotalAt + kRows * 8;
+    static constexpr int kLastAt = kBarsAt + 2 * kTeams * kSlots * 8;
+    static constexpr int kSmem = kLastAt + 16;
+    static_assert((kJoin + 2) * kRows * 4 <= kJoinBytes, "the weights of a join fit its buffer");
+    static_assert(kSmem <= kRoom && kSlots >= 2, "shared memory of an SM");
+    static_assert(kSideBytes % 128 == 0 && kSumBytes % 16 == 0 && kMlAt % 16 == 0 && kBarsAt % 8 == 0, "alignment");
+
+    // Codes in a side: the 16-byte chunk c of the position r of a tile of 16, by rows of positions for keys and with the
+    // even and the odd positions of eight apart for values, so that the vectors that a warp reads at once lie in
+    // different banks.
+    static constexpr int kChunks = kRowBytes / 16;
+    static __device__ __forceinline__ int key_place(int r, int c) {
+        const int x = BITS == 8 ? (kChunks >= 8 ? (r & 1) << 2 : 0) : kChunks == 8 ? (r & 3) << 1 : kChunks == 4 ? r & 2 : 0;
+        return r * kRowBytes + ((c ^ x) << 4);
+    }
+    static __device__ __forceinline__ int value_place(int r, int c) {
+        const int slot = (r & 8) | ((r & 1) << 2) | ((r >> 1) & 3);
+        const int x = kChunks >= 8 ? (slot & 3) << 1 : kChunks == 4 ? slot & 2 : 0;
+        return slot * kRowBytes + ((c ^ x) << 4);
+    }
+};
+
+// Transposes an 8 x 8 matrix of 16-bit elements, two neighbours of a row in each lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+
+// The places among a lane's 16 neighbours of a group of the elements i = 0..3 of its fragment of the product w = 0..3: two
+// in the first half and two in the second. 4-bit codes come from a word's nibbles k and k + 4.
+template <int BITS>
+__device__ __forceinline__ constexpr int element_of(int w, int i) {
+    if (BITS == 8) return 4 * w + i;
+    return 8 * (w >> 1) + 2 * (w & 1) + (i & 1) * 4 + (i >> 1);
+}
+
+// The two halves of product w's fragment from a lane's codes of 16 neighbours: 1024 + c; of 4-bit codes 64 + c in the second.
+template <int BITS>
+__device__ __forceinline__ void key_fragment(const uint32_t (&codes)[BITS / 2], int w, uint32_t& first, uint32_t& second) {
+    if constexpr (BITS == 8) {
+        first = __byte_perm(codes[w], 0x64646464u, 0x4140);
+        second = __byte_perm(codes[w], 0x64646464u, 0x4342);
+    } else {
+        const uint32_t x = w & 1 ? codes[w >> 1] >> 8 : codes[w >> 1];
+        first = (x & 0x000F000Fu) | kHalf1024;
+        second = (x & 0x00F000F0u) | kHalf64;
+    }
+}
+
+// What the codes of a pair of positions become values by, for the even and the odd columns of a lane: (h + less) * scale +
+// add, and what the addend's rounding left out.
+template <int BITS>
+struct ValueTerms {
+    __half2 scale, add[2];
+    uint32_t left[2];
+    // first, second: (scale, bias) of the two positions
+    __device__ __forceinline__ ValueTerms(uint32_t first, uint32_t second, bool centred) {
+        scale = half2_of(__byte_perm(first, second, 0x5410));
+        const __half2 bias = half2_of(__byte_perm(first, second, 0x7632));
+        if (centred) {
+            add[0] = add[1] = __hfma2(half2_of(BITS == 8 ? kHalf128 : kHalf8), scale, bias);
+            left[0] = left[1] = 0u;
+            return;
+        }
+        auto set = [&](int i, uint32_t minus) {   // -1024 or -64
+            const __half2 m = half2_of(minus);
+            add[i] = __hfma2(m, scale, bias);
+            left[i] = bits_of(__hadd2(bias, __hfma2(m, scale, __hneg2(add[i]))));   // b - (b - 1024 s - add's error)
+        };
+        set(0, kHalf1024 | 0x80008000u);
+        if constexpr (BITS == 4) set(1, kHalf64 | 0x80008000u);
+        else add[1] = add[0], left[1] = left[0];
+    }
+};
+
+// The values of four neighbouring columns of two positions, from their codes' words: pairs over the positions. quarter: of a
+// word of 4-bit codes, its half.
+template <int BITS>
+__device__ __forceinline__ void value_pairs(uint32_t first, uint32_t second, int quarter, const ValueTerms<BITS>& t, bool centred,
+                                            uint32_t (&v)[4]) {
+    __half2 h[4];
+    if constexpr (BITS == 8) {
+        const uint32_t x = __byte_perm(first, second, 0x5140), y = __byte_perm(first, second, 0x7362);
+        h[0] = half2_of(__byte_perm(x, 0x64646464u, 0x4140));
+        h[1] = half2_of(__byte_perm(x, 0x64646464u, 0x4342));
+        h[2] = half2_of(__byte_perm(y, 0x64646464u, 0x4140));
+        h[3] = half2_of(__byte_perm(y, 0x64646464u, 0x4342));
+    } else {
+        const uint32_t x = __byte_perm(first, second, quarter == 0 ? 0x5410 : 0x7632), y = x >> 8;
+        h[0] = half2_of((x & 0x000F000Fu) | kHalf1024);
+        h[1] = half2_of((x & 0x00F000F0u) | kHalf64);
+        h[2] = half2_of((y & 0x000F000Fu) | kHalf1024);
+        h[3] = half2_of((y & 0x00F000F0u) | kHalf64);
+    }
+    if (centred) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __hsub2(h[i], half2_of(BITS == 8 ? kHalf1152 : i & 1 ? kHalf72 : kHalf1032));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = bits_of(__hfma2(h[i], t.scale, t.add[i & 1]));
+}
+
+template <int D, int ROWS8, int BITS>
+__global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D, ROWS8, BITS>::kCtasPerSm)
+    qmm_attention_codes_kernel(const __grid_constant__ AttnParams p) {
+    using Cfg = CodesCfg<D, ROWS8, BITS>;
+    constexpr int kRows = Cfg::kRows;              // query rows of a CTA
+    constexpr int kTiles = Cfg::kTiles;
+    constexpr int kPartRows = 16 * kTiles;         // positions of a warp's part of a step
+    constexpr int kThreads = 32 * Cfg::kCompute;   // computing threads
+    constexpr int kGroups = D / 64;
+    constexpr int kEach = D == 64 ? 8 : 16;        // neighbouring columns of a lane
+    constexpr int kSets = D / (8 * kEach);         // sets of them
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t* const full = reinterpret_cast<uint64_t*>(smem + Cfg::kBarsAt);
+    uint64_t* const empty = full + Cfg::kTeams * Cfg::kSlots;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = smem_u32(smem);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Cfg::kTeams * Cfg::kSlots; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], Cfg::kTeamWarps);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    griddep_launch_dependents();
+    griddep_wait();
+
+    Share share;
+    const bool any = share.init(p, Cfg::kShortShare, lane);
+    float* const s_join = reinterpret_cast<float*>(smem + Cfg::kJoinAt);
+    uint32_t* const s_last = reinterpret_cast<uint32_t*>(smem + Cfg::kLastAt);
+    if (!any) return;
+    if (warp >= Cfg::kCompute) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kCopyRegs));
+        copy_codes<Cfg>(p, share, ring, full, empty, s_join, reinterpret_cast<const float*>(smem), s_last, warp - Cfg::kCompute, lane);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kComputeRegs));
+
+    const int team = warp / Cfg::kTeamWarps;    // takes the steps team, team + kTeams, ... of every item
+    const int part = warp % Cfg::kTeamWarps;    // its part of the step's positions
+    const int quad = lane & 3, gid = lane >> 2;
+    const uint32_t q_smem = ring + Cfg::kQueryAt;
+    uint8_t* const sums = smem + Cfg::kSumsAt + (Cfg::kQueryRegs ? warp * Cfg::kSumBytes : 0);   // [group][row] two floats
+    float* const units = reinterpret_cast<float*>(sums + kRows * kGroups * 8);
+    float* const s_ml = reinterpret_cast<float*>(smem + Cfg::kMlAt);           // [warp][row][2]
+    float* const s_total = reinterpret_cast<float*>(smem + Cfg::kTotalAt);     // [row][2]
+
+    uint64_t* const my_full = full + team * Cfg::kSlots;
+    uint64_t* const my_empty = empty + team * Cfg::kSlots;
+    int slot = 0, round = 0;   // of the next step in the team's ring
+    bool alive = true;
+    auto slot_full = [&]() -> uint32_t {
+        if (alive) alive = wait_phase(&my_full[slot], round & 1, p.err, kErrFullWait);
+        return ring + (team * Cfg::kSlots + slot) * Cfg::kSlotBytes;
+    };
+    auto slot_done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&my_empty[slot]);
+        if (++slot == Cfg::kSlots) {
+            slot = 0;
+            ++round;
+        }
+    };
+
+    Item it;
+    while (it.next(p, share, kRows, lane)) {
+        const SeqSpan span = it.span;
+        const int seq = it.seq, head = it.head, row0 = it.row0;
+        const int rows_left = p.rows * p.group - row0;
+        const int rows = rows_left < kRows ? rows_left : kRows;
+        const int first_pos = span.first;
+        auto seq_end = [&]() -> int { return min(first_pos + p.rows, p.positions); };   // span.len again
+
+        // query row = (token, head of the group)
+        auto token_of = [&](int i) -> int { return ((row0 + i) * p.group_inverse) >> 20; };   // (row0 + i) / group
+        auto row_offset = [&](int i, int64_t stride) -> int64_t {
+            const int tok = token_of(i);
+            return (static_cast<int64_t>(seq) * p.rows + tok) * stride +
+                   static_cast<int64_t>(head * p.group + row0 + i - tok * p.group) * D;
+        };
+        // The queries' fragments: a lane has 16 neighbours of every group of 64 elements of the row gid of each tile.
+        uint32_t qf[Cfg::kQueryRegs ? D / 16 : 1][ROWS8][2];
+        if (Cfg::kQueryRegs || warp == 0) {   // all warps have the same rows
+            __syncwarp();   // the last item's sums have been read
+#pragma unroll
+            for (int n = 0; n < ROWS8; ++n) {
+                const int i = n * 8 + gid;
+                const bool in = i < rows;
+                const uint16_t* src = p.q + (in ? row_offset(i, p.q_stride) : 0) + quad * 16;
+                uint32_t w[kGroups][8];
+                uint32_t most = 0;
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (in) v = *reinterpret_cast<const uint4*>(src + k * 64 + j * 8);
+                        w[k][4 * j] = v.x, w[k][4 * j + 1] = v.y, w[k][4 * j + 2] = v.z, w[k][4 * j + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        w[k][j] ^= p.query_sign;
+                        most = max(most, magnitude(w[k][j]));
+                    }
+                }
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                const QuerySize size(most, p.scale_log2);
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    float sum = 0.0f, more = 0.0f;   // of q f, and of q f times 1024 or 64
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float e[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int at = element_of<BITS>(j, x);
+                            e[x] = __uint_as_float(at & 1 ? w[k][at >> 1] & 0xFFFF0000u : w[k][at >> 1] << 16) * size.factor;
+                        }
+                        const uint32_t a = pack_f16(e[0], e[1]), b = pack_f16(e[2], e[3]);
+                        const float2 fa = __half22float2(half2_of(a)), fb = __half22float2(half2_of(b));
+                        const float low = fa.x + fa.y, high = fb.x + fb.y;
+                        sum += low + high;
+                        more += 1024.0f * low + (BITS == 8 ? 1024.0f : 64.0f) * high;
+                        if constexpr (Cfg::kQueryRegs) {
+                            qf[k * 4 + j][n][0] = a;
+                            qf[k * 4 + j][n][1] = b;
+                        } else {
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_smem + ((n * (D / 16) + k * 4 + j) * 32 + lane) * 8),
+                                         "r"(a), "r"(b) : "memory");
+                        }
+                    }
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                        more += __shfl_xor_sync(0xFFFFFFFFu, more, o);
+                    }
+                    if (quad == 0) *reinterpret_cast<float2*>(sums + (k * kRows + i) * 8) = make_float2(sum, more);
+                }
+                if (quad == 0) units[i] = size.unit;
+            }
+            __syncwarp();
+        }
+        if constexpr (!Cfg::kQueryRegs) named_barrier(1, kThreads);
+        // of the lane's two rows 2 quad and 2 quad + 1 of each tile
+        float unit[ROWS8][2], m[ROWS8][2], l[ROWS8][2];
+        int row_pos[ROWS8][2];   // their positions; -1 for none
+#pragma unroll
+        for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = n * 8 + quad * 2 + j;
+                unit[n][j] = units[i];
+                row_pos[n][j] = i < rows ? first_pos + token_of(i) : -1;
+                m[n][j] = -INFINITY;
+                l[n][j] = 0.0f;
+            }
+
+        float o[D / 16][ROWS8][4], left[kSets][ROWS8][4];   // columns by rows; what the values' rounding left out
+#pragma unroll
+        for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) o[c][n][j] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kSets; ++c) left[c][n][j] = 0.0f;
+            }
+
+        for (int i = team; i < it.steps; i += Cfg::kTeams) {
+            const int pos0 = span.step_pos(it.t0 + i) + part * kPartRows;   // the warp's first position
+            float sc[kTiles][ROWS8][4];   // [tile][rows][position gid or gid + 8, row]
+#pragma unroll
+            for (int s = 0; s < kTiles; ++s)
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sc[s][n][j] = 0.0f;
+            const uint32_t side = slot_full();
+            const uint32_t kst = side + part * kPartRows * Cfg::kRowBytes, vst = kst + Cfg::kSideBytes;
+            const uint32_t k_pairs = side + kStep * Cfg::kRowBytes + part * kPartRows * Cfg::kPairBytes, v_pairs = k_pairs + Cfg::kSideBytes;
+            // positions that every row sees need no mask
+            const bool whole = pos0 + kPartRows <= min(first_pos + 1, p.positions) &&
+                               (p.window == 0 || first_pos + p.rows - 1 - pos0 < p.window || pos0 + kPartRows <= p.sinks);
+            // Scales whose multiples may leave binary16 take the values' codes centred. A position that only some rows see
+            // weighs nothing in the others, but 0 * inf is not 0: where the values of such a one may not be binary16 numbers,
+            // each token's rows get a product of their own without what they do not see. Both are rare, and one path.
+            bool slow = false;
+#pragma unroll
+            for (int c = 0; c < kPartRows * kGroups; c += 32) {
+                if (kPartRows * kGroups < 32 && lane >= kPartRows * kGroups) break;
+                const uint32_t pair = lds32(v_pairs + (c + lane) * 4);
+                slow |= (pair & 0x7FFFu) > 0x5380u;   // 60
+                if (!whole && p.rows > 1) {
+                    const float2 sb = __half22float2(half2_of(pair));
+                    slow |= !(fabsf(sb.y) + ((1 << BITS) - 1) * fabsf(sb.x) < 65504.0f);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                float part_sc[kTiles][ROWS8][4];
+#pragma unroll
+                for (int s = 0; s < kTiles; ++s) {
+                    uint32_t codes[2][BITS / 2];   // of positions gid and gid + 8
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t at = kst + s * 16 * Cfg::kRowBytes;
+                        if constexpr (BITS == 8) {
+                            const uint4 v = lds128(at + Cfg::key_place(gid + 8 * h, 4 * k + quad));
+                            codes[h][0] = v.x, codes[h][1] = v.y, codes[h][2] = v.z, codes[h][3] = v.w;
+                        } else {
+                            const uint2 v = lds64(at + Cfg::key_place(gid + 8 * h, 2 * k + (quad >> 1)) + (quad & 1) * 8);
+                            codes[h][0] = v.x, codes[h][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t a[4];
+                        key_fragment<BITS>(codes[0], w, a[0], a[2]);
+                        key_fragment<BITS>(codes[1], w, a[1], a[3]);
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n) {
+                            uint32_t b0, b1;
+                            if constexpr (Cfg::kQueryRegs) {
+                                b0 = qf[k * 4 + w][n][0], b1 = qf[k * 4 + w][n][1];
+                            } else {
+                                const uint2 v = lds64(q_smem + ((n * (D / 16) + k * 4 + w) * 32 + lane) * 8);
+                                b0 = v.x, b1 = v.y;
+                            }
+                            if (w == 0) mma_f16_zc(part_sc[s][n], a[0], a[1], a[2], a[3], b0, b1);
+                            else mma_f16(part_sc[s][n], a[0], a[1], a[2], a[3], b0, b1);
+                        }
+                    }
+                }
+                uint4 q_sums[ROWS8];   // sum and more of the two rows
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n) q_sums[n] = *reinterpret_cast<const uint4*>(sums + (k * kRows + n * 8 + quad * 2) * 8);
+#pragma unroll
+                for (int s = 0; s < kTiles; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 sb = __half22float2(half2_of(lds32(k_pairs + (s * 16 + h * 8 + gid) * Cfg::kPairBytes + k * 4)));
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n) {
+                            float(&x)[4] = sc[s][n];
+                            const float(&a)[4] = part_sc[s][n];
+                            x[2 * h] = fmaf(sb.x, a[2 * h] - __uint_as_float(q_sums[n].y), fmaf(sb.y, __uint_as_float(q_sums[n].x), x[2 * h]));
+                            x[2 * h + 1] = fmaf(sb.x, a[2 * h + 1] - __uint_as_float(q_sums[n].w),
+                                                fmaf(sb.y, __uint_as_float(q_sums[n].z), x[2 * h + 1]));
+                        }
+                    }
+            }
+            float alpha[ROWS8][2];
+            bool same = true;
+#pragma unroll
+            for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!whole) {
+                        // position s * 16 + h * 8 of the lane's lies after its row or the table's end, or before the window
+                        // and past the sinks
+                        const int own = row_pos[n][j] - pos0 - gid;
+                        const int last = min(own, seq_end() - 1 - pos0 - gid);
+                        // (in 32 bits without a sign: wraps for rows without a position, which see nothing anyway)
+                        const int out = p.window == 0 ? -1 : static_cast<int>(static_cast<uint32_t>(own) - p.window);
+                        const int sink = p.window == 0 ? -1 : p.sinks - pos0 - gid;
+#pragma unroll
+                        for (int s = 0; s < kTiles; ++s)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int at = s * 16 + h * 8;
+                                if (at > last || (at <= out && at >= sink)) sc[s][n][2 * h + j] = -INFINITY;
+                            }
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int s = 0; s < kTiles; ++s) top = fmaxf(top, fmaxf(sc[s][n][j], sc[s][n][2 + j]));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                    // a unit is above 0, so that it keeps the order
+                    const float m_new = fmaxf(m[n][j], top == -INFINITY ? top : top * unit[n][j]);
+                    const float ref = m_new == -INFINITY ? 0.0f : m_new;
+                    alpha[n][j] = m_new == m[n][j] ? 1.0f : exp2_approx(m[n][j] - ref);
+                    same &= m_new == m[n][j];
+                    m[n][j] = m_new;
+                    const float less = kWeightBits - ref;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < kTiles; ++s)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float& x = sc[s][n][2 * h + j];
+                            x = exp2_approx(fmaf(x, unit[n][j], less));
+                            sum += x;
+                        }
+                    l[n][j] = fmaf(l[n][j], alpha[n][j], sum);
+                }
+            slow = __any_sync(0xFFFFFFFFu, slow);
+            if (__any_sync(0xFFFFFFFFu, !same)) {
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) o[c][n][j] *= alpha[n][j & 1];
+#pragma unroll
+                        for (int c = 0; c < kSets; ++c) left[c][n][j] *= alpha[n][j & 1];
+                    }
+            }
+
+            // Products of a tile's values; kSlow: with codes centred, for the rows of the token at `rp` alone, with what `keep`
+            // leaves of the pairs of positions.
+            auto values = [&](int s, auto slowly, const uint32_t (&pb)[ROWS8][2], const uint32_t (&keep)[2], int rp) {
+                constexpr bool kSlow = decltype(slowly)::value;
+                constexpr int kWords = kEach * BITS / 32, kPerWord = 32 / BITS;   // of a lane's codes
+                auto product = [&](float(&to)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int n) {
+                    if constexpr (!kSlow) {
+                        mma_f16(to, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                    } else {
+                        float x[4];
+                        mma_f16_zc(x, a0 & keep[0], a1 & keep[0], a2 & keep[1], a3 & keep[1], pb[n][0], pb[n][1]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (row_pos[n][j & 1] == rp) to[j] += x[j];
+                    }
+                };
+#pragma unroll
+                for (int c = 0; c < kSets; ++c) {
+                    uint32_t codes[4][kWords];   // of positions 2 quad + {0, 1, 8, 9}
+                    const int byte = (c * 8 + gid) * kEach * BITS / 8;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 2 * quad + (j & 1) + (j >> 1) * 8;
+                        const uint32_t at = vst + s * 16 * Cfg::kRowBytes + Cfg::value_place(r, byte >> 4) + (byte & 15);
+                        if constexpr (kWords == 4) {
+                            const uint4 v = lds128(at);
+                            codes[j][0] = v.x, codes[j][1] = v.y, codes[j][2] = v.z, codes[j][3] = v.w;
+                        } else if constexpr (kWords == 2) {
+                            const uint2 v = lds64(at);
+                            codes[j][0] = v.x, codes[j][1] = v.y;
+                        } else {
+                            codes[j][0] = lds32(at);
+                        }
+                    }
+                    const uint32_t at = v_pairs + (s * 16 + 2 * quad) * Cfg::kPairBytes + (c * 8 + gid) * kEach / 64 * 4;
+                    const ValueTerms<BITS> t0(lds32(at), lds32(at + Cfg::kPairBytes), kSlow);
+                    const ValueTerms<BITS> t1(lds32(at + 8 * Cfg::kPairBytes), lds32(at + 9 * Cfg::kPairBytes), kSlow);
+                    if constexpr (!kSlow) {
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n) product(left[c][n], t0.left[0], t0.left[1], t1.left[0], t1.left[1], n);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kEach; e += 4) {
+                        uint32_t v0[4], v1[4];
+                        value_pairs<BITS>(codes[0][e / kPerWord], codes[1][e / kPerWord], e % kPerWord / 4, t0, kSlow, v0);
+                        value_pairs<BITS>(codes[2][e / kPerWord], codes[3][e / kPerWord], e % kPerWord / 4, t1, kSlow, v1);
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2)
+#pragma unroll
+                            for (int n = 0; n < ROWS8; ++n)
+                                product(o[(c * kEach + e + k) / 2][n], v0[k], v0[k + 1], v1[k], v1[k + 1], n);
+                    }
+                }
+            };
+#pragma unroll
+            for (int s = 0; s < kTiles; ++s) {
+                uint32_t pb[ROWS8][2], keep[2] = {};
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) pb[n][h] = transposed(pack_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1]));
+                if (!slow) {
+                    values(s, std::false_type(), pb, keep, 0);
+                } else {
+#pragma unroll 1
+                    for (int r = 0; r < p.rows; ++r) {
+                        const int rp = first_pos + r;
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {   // the halves of a fragment word whose position token r sees
+                            keep[w] = 0u;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int pos = pos0 + s * 16 + w * 8 + quad * 2 + j;
+                                const int back = rp - pos;
+                                if (back >= 0 && (p.window == 0 || back < p.window || pos < p.sinks)) keep[w] |= 0xFFFFu << (16 * j);
+                            }
+                        }
+                        values(s, std::true_type(), pb, keep, rp);
+                    }
+                }
+            }
+            slot_done();
+        }
+
+        // join the warps: their outputs are brought to the rows' common maxima, and then only add up
+        float scale[ROWS8][2];
+#pragma unroll
+        for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float sum = l[n][j];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+                if (gid == 0) *reinterpret_cast<float2*>(s_ml + (warp * kRows + n * 8 + quad * 2 + j) * 2) = make_float2(m[n][j], sum);
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) o[c][n][k + j] += left[c / (kEach / 2)][n][k + j];
+                }
+            }
+        named_barrier(1, kThreads);
+#pragma unroll
+        for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = n * 8 + quad * 2 + j;
+                float2 ml[Cfg::kCompute];
+                float top = -INFINITY, total = 0.0f;
+#pragma unroll
+                for (int w = 0; w < Cfg::kCompute; ++w) {
+                    ml[w] = *reinterpret_cast<const float2*>(s_ml + (w * kRows + row) * 2);
+                    top = fmaxf(top, ml[w].x);
+                }
+                const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int w = 0; w < Cfg::kCompute; ++w) total = fmaf(ml[w].y, exp2_approx(ml[w].x - ref), total);
+                scale[n][j] = exp2_approx(m[n][j] - ref);
+                if (warp == 0 && gid == 0) *reinterpret_cast<float2*>(s_total + row * 2) = make_float2(top, total);
+            }
+        const int cta = blockIdx.x;
+        const bool cut = it.ua != 0 || it.ub != it.units;
+        const int c0 = cut ? cta_of(it.g0, share.total, share.ctas) : cta;
+        const Parts parts{p.part, p.part_ml, kRows, c0};
+        // as many columns at a time as the rows leave room for; four of them at place c ^ (row / 2 % 4): no bank conflicts
+        int wide = Cfg::kJoinCols;   // a power of two
+        while (wide < D && 2 * wide * rows * Cfg::kCompute * 4 <= Cfg::kJoinBytes) wide *= 2;
+        const int per_row = wide / 4, row_shift = 31 - __clz(per_row);
+#pragma unroll 1
+        for (int col0 = 0; col0 < D; col0 += wide) {
+            if (col0 > 0) named_barrier(1, kThreads);
+#pragma unroll
+            for (int c = 0; c < kSets; ++c) {
+                const int col = (c * 8 + gid) * kEach - col0;   // the lane's first
+                if (col < 0 || col >= wide) continue;
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int row = n * 8 + quad * 2 + j;
+                        if (row >= rows) continue;
+                        float* const at = s_join + (warp * rows + row) * wide;
+#pragma unroll
+                        for (int k = 0; k < kEach / 4; ++k) {
+                            const float(&a)[4] = o[c * (kEach / 2) + 2 * k][n];
+                            const float(&b)[4] = o[c * (kEach / 2) + 2 * k + 1][n];
+                            const float by = scale[n][j];
+                            *reinterpret_cast<float4*>(at + ((col / 4 + k) ^ ((row >> 1) & 3)) * 4) =
+                                make_float4(a[j] * by, a[2 + j] * by, b[j] * by, b[2 + j] * by);
+                        }
+                    }
+            }
+            named_barrier(1, kThreads);
+            for (int e = threadIdx.x; e < rows * per_row; e += kThreads) {
+                const int row = e >> row_shift, c4 = e & (per_row - 1), d = col0 + c4 * 4;
+                const float* const from = s_join + row * wide + (c4 ^ ((row >> 1) & 3)) * 4;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < Cfg::kCompute; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(from + w * rows * wide);
+                    acc.x += v.x;
+                    acc.y += v.y;
+                    acc.z += v.z;
+                    acc.w += v.w;
+                }
+                const float2 total = *reinterpret_cast<const float2*>(s_total + row * 2);
+                if (!cut) {
+                    const float inv = total.y == 0.0f ? 0.0f : 1.0f / total.y;
+                    *reinterpret_cast<uint2*>(p.out + row_offset(row, p.out_stride) + d) =
+                        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                } else {
+                    const int64_t at = parts.row(cta - c0, row);
+                    *reinterpret_cast<float4*>(p.part + at * D + d) = acc;
+                    if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = total;
+                }
+            }
+        }
+        named_barrier(1, kThreads);   // the join's buffers are free for the next item
+    }
+
+    named_barrier(2, Cfg::kThreads);   // the copying warps see to the joins
+}
+
+template <int D, int BITS>
+cudaError_t configure_codes_dim() {
+    cudaError_t e = configure<CodesCfg<D, 1, BITS>>(qmm_attention_codes_kernel<D, 1, BITS>);
+    if (e == cudaSuccess) e = configure<CodesCfg<D, 2, BITS>>(qmm_attention_codes_kernel<D, 2, BITS>);
+    if (e == cudaSuccess) e = configure_tiles<D, 2, BITS>();
+    if (e == cudaSuccess) e = configure_tiles<D, 4, BITS>();
+    return e;
+}
+
+template <int D, int BITS>
+cudaError_t launch_codes_dim(const AttnParams& p, int num_sms, cudaStream_t stream) {
+    const int rows = p.rows * p.group;
+    if (rows <= 8) return launch<CodesCfg<D, 1, BITS>>(qmm_attention_codes_kernel<D, 1, BITS>, p, num_sms, stream);
+    if (rows <= 16) return launch<CodesCfg<D, 2, BITS>>(qmm_attention_codes_kernel<D, 2, BITS>, p, num_sms, stream);
+    return rows <= 32 ? launch_tiles<D, 2, BITS>(p, num_sms, stream) : launch_tiles<D, 4, BITS>(p, num_sms, stream);
+}
+
+template <int BITS>
+cudaError_t configure_codes() {
+    cudaError_t e = configure_codes_dim<64, BITS>();
+    if (e == cudaSuccess) e = configure_codes_dim<128, BITS>();
+    if (e == cudaSuccess) e = configure_codes_dim<256, BITS>();
+    return e;
+}
+
+template <int BITS>
+cudaError_t launch_codes(int head_dim, const AttnParams& p, int num_sms, cudaStream_t stream) {
+    if (head_dim == 64) return launch_codes_dim<64, BITS>(p, num_sms, stream);
+    if (head_dim == 128) return launch_codes_dim<128, BITS>(p, num_sms, stream);
+    return launch_codes_dim<256, BITS>(p, num_sms, stream);
+}
+
+}  // namespace
+
+}  // namespace qmmk

@@ -1,0 +1,38 @@
+// Codes of a quantized cache in the attention kernels: binary16 numbers from codes, and queries as binary16 numbers.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace qmmk {
+
+namespace {
+
+constexpr uint32_t kHalf1152 = 0x64806480u, kHalf1032 = 0x64086408u, kHalf1024 = 0x64006400u;   // pairs of binary16 numbers
+constexpr uint32_t kHalf128 = 0x58005800u, kHalf72 = 0x54805480u, kHalf64 = 0x54005400u, kHalf8 = 0x48004800u;
+constexpr float kWeightBits = 15.0f;   // weights are binary16 numbers of up to 2^15, so that those from 2^-29 on keep their bits
+
+__device__ __forceinline__ uint32_t bits_of(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return bits_of(__floats2half2_rn(a, b)); }
+
+// The larger magnitude of a pair of bfloat16 numbers, as an integer.
+__device__ __forceinline__ uint32_t magnitude(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
+
+// A query row's power of two, which brings its largest magnitude to 2^14..2^15 in binary16 (elements down to 2^-28 of that
+// keep all their bits), and what its scores then count in powers of two. That is not 0: masked scores of -infinity were NaN.
+struct QuerySize {
+    float factor, unit;
+    __device__ __forceinline__ QuerySize(uint32_t most, float scale_log2) {
+        const int power = min(141 - static_cast<int>(most >> 7), 126);
+        factor = __uint_as_float(static_cast<uint32_t>(127 + power) << 23);
+        unit = fmaxf(scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - power) << 23), 1e-45f);
+    }
+    __device__ __forceinline__ uint32_t f16(uint32_t w) const {
+        return pack_f16(__uint_as_float(w << 16) * factor, __uint_as_float(w & 0xFFFF0000u) * factor);
+    }
+};
+
+}  // namespace
+
+}  // namespace qmmk
