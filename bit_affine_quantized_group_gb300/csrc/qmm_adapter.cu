@@ -4,13 +4,17 @@
 // Both products are m16n8k16 tensor-core products of up to 16 rows of one
 // adapter: the rows of a block of 64 are put in the order of their adapters and
 // cut into such tiles, which every CTA does for itself. Their bound is bytes: A
-// and B of the adapters in use once, x, y and out.
-//   - low: the warps of a cluster's CTAs take a tile's 8 columns of rank each,
-//     the CTAs slices of K, and add their partial sums through distributed shared
-//     memory in the order of the slices.
-//   - out: warps take a tile's 32 columns each. low enters as two bfloat16 terms
-//     (high + low within 2^-17), which is below what float32 outputs of that many
-//     terms are off by; one term would round more than bfloat16 outputs do.
+// and B of the adapters in use once, x, y and out; of few rows latency, so that
+// every warp has all its loads on their way at once.
+//   - low: the warps of a cluster's CTAs take a tile's 16 columns of rank each,
+//     the CTAs slices of K. They write their sums into the shared memory of the
+//     CTA that a row belongs to, which adds them in the order of the slices.
+//   - out: each warp takes a run of a tile's columns, 32 at a time. low enters as
+//     two bfloat16 terms (high + low within 2^-17), for float32 outputs as three
+//     (2^-26): one would round more than bfloat16 outputs do. Tiles, y and B are
+//     read while the first kernel still runs.
+// In both a lane of a quad has 8 neighbouring elements of the 32 that two
+// products sum over, so that loads are whole 16-byte vectors of whole sectors.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,8 +50,11 @@ constexpr int kTile = 16;             // rows of a product
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlices = 16;           // of K at most: the CTAs of a cluster
-constexpr int kStepK = 64;            // elements of x that a lane group loads at once
+constexpr int kStep = 32;             // elements that two products sum over
+constexpr int kAhead = 5;             // steps of K that a warp loads at once
 constexpr size_t kErrBytes = 256;
+
+constexpr int terms_of(int out_dtype) { return out_dtype == QMM_OUT_F32 ? 3 : 2; }
 
 struct AdapterParams {
     const uint16_t* x;
@@ -57,8 +64,8 @@ struct AdapterParams {
     const int32_t* ids;
     const void* y;
     void* out;
-    uint16_t* high;          // [rows, rank] two bfloat16 terms of low
-    uint16_t* low;
+    uint16_t* low;           // [term][rows][rank] bfloat16
+    int64_t low_term;        // elements from term to term
     uint32_t* err;
     int64_t x_stride, y_stride, out_stride;
     int64_t K, N;
@@ -67,10 +74,11 @@ struct AdapterParams {
 
 // The rows of a block in the order of their adapters (-1 first), and the tiles of up to 16 of one adapter.
 struct Tiles {
-    int32_t id[kBlock];      // of the rows as they stand
+    int4 id[kBlock / 4];     // of the rows as they stand
     uint8_t row[kBlock];     // at each place of the order
     int32_t tile_id[kBlock];
     uint8_t first[kBlock], size[kBlock];   // places of a tile
+    uint8_t tile[kBlock];    // of a place
     uint32_t starts[2];
     int tiles;
 };
@@ -78,30 +86,30 @@ struct Tiles {
 // By the whole CTA; ids outside -1..adapters-1 count as -1.
 __device__ __forceinline__ void find_tiles(const AdapterParams& p, int row0, Tiles& t) {
     const int tid = threadIdx.x, rows = min(kBlock, p.rows - row0);
-    int id = -1;
-    if (tid < rows) {
-        id = p.ids[row0 + tid];
-        if (id < -1 || id >= p.adapters) {
-            atomicOr(p.err, static_cast<uint32_t>(QMM_ADAPTER_BAD_ID));
-            id = -1;
-        }
-        t.id[tid] = id;
-    }
-    __syncthreads();
     if (tid < kBlock) {
-        int before = 0, same = 0;   // rows of smaller ids, and earlier rows of this one
-        if (tid < rows)
-            for (int j = 0; j < rows; ++j) {
-                const int other = t.id[j];
-                before += other < id;
-                same += other == id && j < tid;
+        int id = 0x7FFFFFFF;   // behind all others
+        if (tid < rows) {
+            id = p.ids[row0 + tid];
+            if (id < -1 || id >= p.adapters) {
+                atomicOr(p.err, static_cast<uint32_t>(QMM_ADAPTER_BAD_ID));
+                id = -1;
             }
+        }
+        reinterpret_cast<int32_t*>(t.id)[tid] = id;
+        if (tid < 2) t.starts[tid] = 0;
+        named_barrier(1, kBlock);
+        int before = 0, same = 0;   // rows of smaller ids, and earlier rows of this one
+#pragma unroll
+        for (int j = 0; j < kBlock; j += 4) {
+            const int4 other = t.id[j / 4];
+            before += (other.x < id) + (other.y < id) + (other.z < id) + (other.w < id);
+            same += (other.x == id && j < tid) + (other.y == id && j + 1 < tid) + (other.z == id && j + 2 < tid) +
+                    (other.w == id && j + 3 < tid);
+        }
         const int place = before + same;
         if (tid < rows) t.row[place] = static_cast<uint8_t>(tid);
         // which places begin a tile
         const bool begins = tid < rows && same % kTile == 0;
-        if (tid < 2) t.starts[tid] = 0;
-        named_barrier(1, kBlock);
         if (begins) atomicOr(&t.starts[place >> 5], 1u << (place & 31));
         named_barrier(1, kBlock);
         const uint32_t s0 = t.starts[0], s1 = t.starts[1];
@@ -114,6 +122,7 @@ __device__ __forceinline__ void find_tiles(const AdapterParams& p, int row0, Til
             t.first[tile] = static_cast<uint8_t>(place);
             t.size[tile] = static_cast<uint8_t>(next - place);
         }
+        if (tid < rows) t.tile[place] = static_cast<uint8_t>(__popcll(starts & (0xFFFFFFFFFFFFFFFFull >> (63 - place))) - 1);
         if (tid == 0) t.tiles = __popc(s0) + __popc(s1);
     }
     __syncthreads();
@@ -131,203 +140,257 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// v as two bfloat16 terms; an infinity or NaN stands in the first alone.
-__device__ __forceinline__ void split(float v, uint16_t& high, uint16_t& low) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    const float f = __bfloat162float(h);
-    high = __bfloat16_as_ushort(h);
-    low = __bfloat16_as_ushort(__float2bfloat16_rn(fabsf(f) < INFINITY ? v - f : 0.0f));
+// v as bfloat16 terms of falling size; an infinity or NaN stands in the first alone.
+template <int TERMS>
+__device__ __forceinline__ void split(float v, uint32_t (&term)[TERMS]) {
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        const float f = __bfloat162float(h);
+        term[i] = __bfloat16_as_ushort(h);
+        v = fabsf(f) < INFINITY ? v - f : 0.0f;
+    }
 }
 
-// 16 elements of a lane: the products' four steps of 64 elements of K, of which a lane of a quad takes 16 neighbours.
-struct Sixteen {
-    uint4 v[2];
-    __device__ __forceinline__ void load(const uint16_t* p) {
-        v[0] = __ldg(reinterpret_cast<const uint4*>(p));
-        v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-    }
-    __device__ __forceinline__ void clear() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ uint32_t word(int i) const {
-        const uint4& w = v[i >> 2];
-        return (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w;
-    }
-};
+__device__ __forceinline__ uint4 load16(const uint16_t* p, bool in) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (in) v = __ldg(reinterpret_cast<const uint4*>(p));
+    return v;
+}
 
-// Grid: clusters of `slices` CTAs; block of rows, then one of `groups` that share its units (a tile's 8 columns of rank).
-__global__ void __launch_bounds__(kThreads) qmm_adapter_low_kernel(const __grid_constant__ AdapterParams p, int slices, int groups) {
-    extern __shared__ __align__(16) float s_part[];   // [place][rank] of this CTA's slice
-    __shared__ Tiles t;
+// Two products of fragments that hold 8 neighbouring elements a lane: rows a0 (gid) and a1 (gid + 8), column gid of b.
+__device__ __forceinline__ void mma_32(float (&d)[4], const uint4& a0, const uint4& a1, const uint4& b) {
+    const uint32_t first[4] = {a0.x, a1.x, a0.y, a1.y}, second[4] = {a0.z, a1.z, a0.w, a1.w};
+    mma_bf16(d, first, b.x, b.y);
+    mma_bf16(d, second, b.z, b.w);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Grid: clusters of `slices` CTAs; block of rows, then one of `groups` that share its units (a tile's 16 columns of rank).
+template <int TERMS>
+__global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __grid_constant__ AdapterParams p, int slices, int groups) {
+    // The sums of the places `slice`, `slice` + slices, ... from every CTA of the cluster: [place / slices][slice][rank].
+    // (slices is a power of two)
+    extern __shared__ __align__(16) float s_part[];
+    __shared__ __align__(16) Tiles t;
     cg::cluster_group cluster = cg::this_cluster();
     const int slice = static_cast<int>(blockIdx.x % slices), of = static_cast<int>(blockIdx.x / slices);
     const int group = of % groups, row0 = of / groups * kBlock;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, quad = lane & 3;
-    griddep_launch_dependents();
+    cluster_arrive();   // this CTA has started, and its memory may be written
     griddep_wait();
+    griddep_launch_dependents();   // not before: the second kernel reads what came before this one without waiting
     find_tiles(p, row0, t);
-    const int columns = p.rank / 8, units = t.tiles * columns;
-    const int64_t steps = p.K / kStepK;
-    const int64_t k0 = steps * slice / slices * kStepK, k1 = steps * (slice + 1) / slices * kStepK;
+    cluster_wait();
+    const int columns = (p.rank + 15) / 16, units = t.tiles * columns;
+    const int steps = static_cast<int>(p.K / kStep);
+    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * slice / slices);
+    const int count = static_cast<int>(static_cast<int64_t>(steps) * (slice + 1) / slices) - s0;
 
     for (int u = group + warp * groups; u < units; u += kWarps * groups) {
-        const int tile = u / columns, column = u - tile * columns, id = t.tile_id[tile];
+        const int tile = u / columns, column = (u - tile * columns) * 16, id = t.tile_id[tile];
         if (id < 0) continue;
         const int first = t.first[tile], size = t.size[tile];
-        const uint16_t* const a = p.a + (static_cast<int64_t>(id) * p.rank + column * 8 + gid) * p.K + quad * 16;
+        const bool two = column + 8 < p.rank;
+        const uint16_t* const a = p.a + (static_cast<int64_t>(id) * p.rank + column + gid) * p.K + s0 * kStep + quad * 8;
+        const int64_t a_next = 8 * p.K;
         const uint16_t* x[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int place = gid + 8 * h;
-            x[h] = p.x + static_cast<int64_t>(row0 + (place < size ? t.row[first + place] : 0)) * p.x_stride + quad * 16;
-        }
-        const bool in0 = gid < size, in1 = gid + 8 < size;
-        float acc[2][4] = {};   // of the even and the odd steps
-        for (int64_t k = k0; k < k1; k += kStepK) {
-            Sixteen wa, w0, w1;
-            wa.load(a + k);
-            if (in0) w0.load(x[0] + k);
-            else w0.clear();
-            if (in1) w1.load(x[1] + k);
-            else w1.clear();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t f[4] = {w0.word(2 * i), w1.word(2 * i), w0.word(2 * i + 1), w1.word(2 * i + 1)};
-                mma_bf16(acc[i & 1], f, wa.word(2 * i), wa.word(2 * i + 1));
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (gid + 8 * h < size)
-                *reinterpret_cast<float2*>(s_part + (first + gid + 8 * h) * p.rank + column * 8 + quad * 2) =
-                    make_float2(acc[0][2 * h] + acc[1][2 * h], acc[0][2 * h + 1] + acc[1][2 * h + 1]);
-    }
-    cluster.sync();
-    // each CTA adds up a share of the units: two elements of up to 4 rows a lane
-    int mine = 0;
-    for (int u = group; u < units; u += groups, ++mine) {
-        if (mine % slices != slice || (mine / slices) % kWarps != warp) continue;
-        const int tile = u / columns, column = u - tile * columns, id = t.tile_id[tile];
-        if (id < 0) continue;
-        const int first = t.first[tile], size = t.size[tile];
-        const float by = p.scale != nullptr ? p.scale[id] : 1.0f;
-        for (int place = gid; place < size; place += 8) {
-            float2 sum = make_float2(0.0f, 0.0f);
-            for (int i = 0; i < slices; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(s_part, i) +
-                                                                  (first + place) * p.rank + column * 8 + quad * 2);
-                sum.x += v.x;
-                sum.y += v.y;
-            }
-            uint16_t h[2], l[2];
-            split(sum.x * by, h[0], l[0]);
-            split(sum.y * by, h[1], l[1]);
-            const int64_t at = static_cast<int64_t>(row0 + t.row[first + place]) * p.rank + column * 8 + quad * 2;
-            *reinterpret_cast<uint32_t*>(p.high + at) = h[0] | static_cast<uint32_t>(h[1]) << 16;
-            *reinterpret_cast<uint32_t*>(p.low + at) = l[0] | static_cast<uint32_t>(l[1]) << 16;
-        }
-    }
-    cluster.sync();   // other CTAs have read this one's sums
-}
-
-// Warps take units of a tile's 32 columns: a lane has 8 neighbouring columns of two rows. WIDE: rows of y and out are read and written 16 bytes at a time.
-template <bool F32, bool WIDE>
-__global__ void __launch_bounds__(kThreads) qmm_adapter_out_kernel(const __grid_constant__ AdapterParams p, int groups) {
-    __shared__ Tiles t;
-    using T = std::conditional_t<F32, float, uint16_t>;
-    const int group = static_cast<int>(blockIdx.x % groups), row0 = static_cast<int>(blockIdx.x / groups) * kBlock;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, quad = lane & 3;
-    griddep_launch_dependents();
-    griddep_wait();
-    find_tiles(p, row0, t);
-    const int64_t columns = (p.N + 31) / 32, units = t.tiles * columns;
-    const int steps = (p.rank + 15) / 16;
-    for (int64_t u = static_cast<int64_t>(group) * kWarps + warp; u < units; u += static_cast<int64_t>(groups) * kWarps) {
-        const int tile = static_cast<int>(u / columns);
-        const int64_t n0 = (u - tile * columns) * 32;
-        const int id = t.tile_id[tile], first = t.first[tile], size = t.size[tile];
-        if (id < 0 && p.y == p.out) continue;
-        int64_t row[2];
         bool in[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             in[h] = gid + 8 * h < size;
-            row[h] = row0 + (in[h] ? t.row[first + gid + 8 * h] : 0);
+            x[h] = p.x + static_cast<int64_t>(row0 + (in[h] ? t.row[first + gid + 8 * h] : 0)) * p.x_stride + s0 * kStep + quad * 8;
         }
-        float acc[4][4] = {};   // products of 8 columns: n0 + 8 (their lane's quad) + 2 j + {0, 1}
-        if (id >= 0) {
-            const uint16_t* b[4];
-            bool in_b[4];
+        float acc[2][4] = {};
+        for (int k0 = 0; k0 < count; k0 += kAhead) {
+            uint4 wa[kAhead][2], wx[kAhead][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = n0 + 8 * (gid >> 1) + 2 * j + (gid & 1);
-                in_b[j] = n < p.N;
-                b[j] = p.b + (static_cast<int64_t>(id) * p.N + (in_b[j] ? n : 0)) * p.rank + quad * 4;
+            for (int k = 0; k < kAhead; ++k) {
+                const bool some = k0 + k < count;
+                const int at = (k0 + k) * kStep;
+                wa[k][0] = load16(a + at, some);
+                wa[k][1] = load16(a + a_next + at, some && two);
+                wx[k][0] = load16(x[0] + at, some && in[0]);
+                wx[k][1] = load16(x[1] + at, some && in[1]);
             }
-            for (int k = 0; k < steps; ++k) {
-                const bool in_k = k * 16 + quad * 4 < p.rank;
-                uint32_t f[2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint2 hi = make_uint2(0u, 0u), lo = make_uint2(0u, 0u);
-                    if (in[h] && in_k) {
-                        hi = *reinterpret_cast<const uint2*>(p.high + row[h] * p.rank + k * 16 + quad * 4);
-                        lo = *reinterpret_cast<const uint2*>(p.low + row[h] * p.rank + k * 16 + quad * 4);
-                    }
-                    f[0][h] = hi.x, f[0][h + 2] = hi.y, f[1][h] = lo.x, f[1][h + 2] = lo.y;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint2 w = make_uint2(0u, 0u);
-                    if (in_b[j] && in_k) w = __ldg(reinterpret_cast<const uint2*>(b[j] + k * 16));
-                    mma_bf16(acc[j], f[0], w.x, w.y);
-                    mma_bf16(acc[j], f[1], w.x, w.y);
-                }
+            for (int k = 0; k < kAhead; ++k) {
+                mma_32(acc[0], wx[k][0], wx[k][1], wa[k][0]);
+                mma_32(acc[1], wx[k][0], wx[k][1], wa[k][1]);
             }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (!in[h]) continue;
-            const int64_t n = n0 + quad * 8;
-            const T* const y = static_cast<const T*>(p.y) + row[h] * p.y_stride + n;
-            T* const out = static_cast<T*>(p.out) + row[h] * p.out_stride + n;
-            if (WIDE && n + 8 <= p.N) {
-                if constexpr (F32) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float4 v = *reinterpret_cast<const float4*>(y + 4 * k);
-                        v.x += acc[2 * k][2 * h], v.y += acc[2 * k][2 * h + 1];
-                        v.z += acc[2 * k + 1][2 * h], v.w += acc[2 * k + 1][2 * h + 1];
-                        *reinterpret_cast<float4*>(out + 4 * k) = v;
-                    }
-                } else {
-                    const uint4 v = *reinterpret_cast<const uint4*>(y);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t r[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        r[j] = pack_bf16(__uint_as_float(w[j] << 16) + acc[j][2 * h],
-                                         __uint_as_float(w[j] & 0xFFFF0000u) + acc[j][2 * h + 1]);
-                    *reinterpret_cast<uint4*>(out) = make_uint4(r[0], r[1], r[2], r[3]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (n + j >= p.N) break;
-                    const float add = acc[j >> 1][2 * h + (j & 1)];
-                    if constexpr (F32) out[j] = y[j] + add;
-                    else out[j] = static_cast<uint16_t>(pack_bf16(__uint_as_float(static_cast<uint32_t>(y[j]) << 16) + add, 0.0f));
-                }
+            const int place = first + gid + 8 * h, owner = place & (slices - 1);
+            float* const to = cluster.map_shared_rank(s_part, owner) + (place - owner + slice) * p.rank + column + quad * 2;
+            *reinterpret_cast<float2*>(to) = make_float2(acc[0][2 * h], acc[0][2 * h + 1]);
+            if (two) *reinterpret_cast<float2*>(to + 8) = make_float2(acc[1][2 * h], acc[1][2 * h + 1]);
+        }
+    }
+    cluster_arrive();
+    cluster_wait();
+    // a place for each warp, two columns for each lane, of the units of this group
+    const int rows = min(kBlock, p.rows - row0);
+    for (int place = slice + warp * slices; place < rows; place += kWarps * slices) {
+        const int tile = t.tile[place], id = t.tile_id[tile];
+        if (id < 0) continue;
+        const float by = p.scale != nullptr ? p.scale[id] : 1.0f;
+        const int64_t at = static_cast<int64_t>(row0 + t.row[place]) * p.rank;
+        for (int c = 2 * lane; c < p.rank; c += 64) {
+            if ((tile * columns + c / 16) % groups != group) continue;
+            const float* from = s_part + (place - slice) * p.rank + c;
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+            for (int i = 0; i < slices; ++i, from += p.rank) {
+                const float2 v = *reinterpret_cast<const float2*>(from);
+                sum.x += v.x;
+                sum.y += v.y;
             }
+            uint32_t x[TERMS], y[TERMS];
+            split(sum.x * by, x);
+            split(sum.y * by, y);
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i) *reinterpret_cast<uint32_t*>(p.low + i * p.low_term + at + c) = x[i] | y[i] << 16;
         }
     }
 }
 
+// A run of units of a tile's 32 columns for each warp; a lane has 8 neighbouring columns of two rows. STEPS: 32 elements of
+// rank each. WIDE: rows of y and out are read and written 16 bytes at a time.
+template <bool F32, int STEPS, bool WIDE>
+__global__ void __launch_bounds__(kThreads, STEPS == 1 ? 3 : 2) qmm_adapter_out_kernel(const __grid_constant__ AdapterParams p, int groups) {
+    constexpr int kTerms = F32 ? 3 : 2;
+    constexpr bool kKeep = STEPS <= 2;   // low stays in registers over a tile's units
+    __shared__ __align__(16) Tiles t;
+    using T = std::conditional_t<F32, float, uint16_t>;
+    const int group = static_cast<int>(blockIdx.x % groups), row0 = static_cast<int>(blockIdx.x / groups) * kBlock;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, quad = lane & 3;
+    griddep_launch_dependents();
+    find_tiles(p, row0, t);
+    const uint32_t columns = static_cast<uint32_t>((p.N + 31) / 32);
+    const uint64_t units = static_cast<uint64_t>(t.tiles) * columns;
+    const uint32_t all = groups * kWarps, mine = group * kWarps + warp;
+    uint64_t u = units * mine / all;
+    const uint64_t u1 = units * (mine + 1) / all;
+    bool waited = false;   // for the first kernel
+    while (u < u1) {
+        const int tile = static_cast<int>(u / columns);
+        uint32_t column = static_cast<uint32_t>(u - static_cast<uint64_t>(tile) * columns);
+        const uint32_t end = u1 - u < columns - column ? column + static_cast<uint32_t>(u1 - u) : columns;
+        u += end - column;
+        const int id = t.tile_id[tile], first = t.first[tile], size = t.size[tile];
+        if (id < 0 && p.y == p.out) continue;
+        bool in[2];
+        const T* y[2];
+        T* out[2];
+        const uint16_t* low[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            in[h] = gid + 8 * h < size;
+            const int64_t row = row0 + (in[h] ? t.row[first + gid + 8 * h] : 0);
+            y[h] = static_cast<const T*>(p.y) + row * p.y_stride;
+            out[h] = static_cast<T*>(p.out) + row * p.out_stride;
+            low[h] = p.low + row * p.rank + quad * 8;
+        }
+        // the columns of a unit: 8 (gid / 2) + 2 j + gid % 2 for the product j, so that a lane gets the 8 from 8 quad on
+        const int own = 8 * (gid >> 1) + (gid & 1);
+        const uint16_t* b = p.b + (static_cast<int64_t>(id < 0 ? 0 : id) * p.N + static_cast<int64_t>(column) * 32 + own) * p.rank + quad * 8;
+        const int b_next = 2 * p.rank;
+        bool in_rank[STEPS];   // this lane's elements are there
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) in_rank[k] = id >= 0 && k * 32 + quad * 8 < p.rank;
+        uint4 l[kKeep ? STEPS : 1][kTerms][2];
+        bool loaded = false;
+#pragma unroll 1
+        for (; column < end; ++column, b += 16 * b_next) {
+            const int64_t n0 = static_cast<int64_t>(column) * 32, n = n0 + quad * 8;
+            const bool full = n0 + 32 <= p.N, whole = WIDE && n + 8 <= p.N;
+            // y and B of the unit
+            uint4 wy[2][F32 ? 2 : 1], wb[STEPS][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < (F32 ? 2 : 1); ++k)
+                    if (in[h] && whole) wy[h][k] = *reinterpret_cast<const uint4*>(y[h] + n + 4 * k);
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    wb[k][j] = load16(b + j * b_next + k * 32, in_rank[k] && (full || n0 + own + 2 * j < p.N));
+            if (!waited) {
+                griddep_wait();
+                waited = true;
+            }
+            auto load_low = [&](int k, uint4(&to)[kTerms][2]) {
+#pragma unroll
+                for (int i = 0; i < kTerms; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        to[i][h] = make_uint4(0u, 0u, 0u, 0u);
+                        if (in[h] && in_rank[k])
+                            to[i][h] = __ldcg(reinterpret_cast<const uint4*>(low[h] + i * p.low_term + k * 32));
+                    }
+            };
+            float acc[4][4] = {};
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                uint4(&lk)[kTerms][2] = l[kKeep ? k : 0];
+                if (!kKeep || !loaded) load_low(k, lk);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < kTerms; ++i) mma_32(acc[j], lk[i][0], lk[i][1], wb[k][j]);
+            }
+            loaded = true;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!in[h]) continue;
+                if (whole) {
+                    if constexpr (F32) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4& v = wy[h][k];
+                            *reinterpret_cast<float4*>(out[h] + n + 4 * k) = make_float4(
+                                __uint_as_float(v.x) + acc[2 * k][2 * h], __uint_as_float(v.y) + acc[2 * k][2 * h + 1],
+                                __uint_as_float(v.z) + acc[2 * k + 1][2 * h], __uint_as_float(v.w) + acc[2 * k + 1][2 * h + 1]);
+                        }
+                    } else {
+                        const uint32_t w[4] = {wy[h][0].x, wy[h][0].y, wy[h][0].z, wy[h][0].w};
+                        uint32_t r[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            r[j] = pack_bf16(__uint_as_float(w[j] << 16) + acc[j][2 * h],
+                                             __uint_as_float(w[j] & 0xFFFF0000u) + acc[j][2 * h + 1]);
+                        *reinterpret_cast<uint4*>(out[h] + n) = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (n + j >= p.N) break;
+                        const float add = acc[j >> 1][2 * h + (j & 1)];
+                        if constexpr (F32) out[h][n + j] = y[h][n + j] + add;
+                        else
+                            out[h][n + j] = static_cast<uint16_t>(
+                                pack_bf16(__uint_as_float(static_cast<uint32_t>(y[h][n + j]) << 16) + add, 0.0f));
+                    }
+                }
+            }
+        }
+    }
+    if (!waited) griddep_wait();   // (the next kernel must not start behind a first kernel that still runs)
+}
+
+template <int TERMS>
 cudaError_t launch_low(const AdapterParams& p, int num_sms, cudaStream_t stream) {
     const int64_t blocks = (p.rows + kBlock - 1) / kBlock;
-    const int64_t steps = p.K / kStepK;
+    const int64_t steps = p.K / kStep;
+    // two CTAs an SM; units of a block: one for each 16 columns of rank of up to as many tiles as it has rows
     int slices = kSlices;
-    while (slices > steps) slices /= 2;
-    // units of a block: one for each 8 columns of rank of up to as many tiles as it has rows
-    const int64_t units = static_cast<int64_t>(p.rows < kBlock ? p.rows : kBlock) * (p.rank / 8);
+    while (slices > 1 && (slices > steps || slices * blocks > 2 * num_sms)) slices /= 2;
+    const int64_t units = static_cast<int64_t>(p.rows < kBlock ? p.rows : kBlock) * ((p.rank + 15) / 16);
     int64_t groups = 2 * num_sms / (blocks * slices);
     const int64_t most = (units + kWarps - 1) / kWarps;
     groups = groups < 1 ? 1 : groups > most ? most : groups;
@@ -340,18 +403,18 @@ cudaError_t launch_low(const AdapterParams& p, int num_sms, cudaStream_t stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * groups * slices));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(kBlock) * p.rank * 4;
+    cfg.dynamicSmemBytes = static_cast<size_t>((kBlock + slices - 1) / slices * slices) * p.rank * 4;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, qmm_adapter_low_kernel, p, slices, static_cast<int>(groups));
+    return cudaLaunchKernelEx(&cfg, qmm_adapter_low_kernel<TERMS>, p, slices, static_cast<int>(groups));
 }
 
-template <bool F32, bool WIDE>
-cudaError_t launch_out(const AdapterParams& p, int num_sms, cudaStream_t stream) {
+template <bool F32, int STEPS, bool WIDE>
+cudaError_t launch_out_steps(const AdapterParams& p, int num_sms, cudaStream_t stream) {
     const int64_t blocks = (p.rows + kBlock - 1) / kBlock;
     const int64_t units = (p.rows < kBlock ? p.rows : kBlock) * ((p.N + 31) / 32);
-    int64_t groups = (4 * num_sms + blocks - 1) / blocks;
+    int64_t groups = ((STEPS == 1 ? 3 : 2) * num_sms + blocks - 1) / blocks;   // as many CTAs as run at once
     const int64_t most = (units + kWarps - 1) / kWarps;
     groups = groups > most ? most : groups;
     cudaLaunchAttribute attr[1];
@@ -363,7 +426,18 @@ cudaError_t launch_out(const AdapterParams& p, int num_sms, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qmm_adapter_out_kernel<F32, WIDE>, p, static_cast<int>(groups));
+    return cudaLaunchKernelEx(&cfg, qmm_adapter_out_kernel<F32, STEPS, WIDE>, p, static_cast<int>(groups));
+}
+
+template <bool F32>
+cudaError_t launch_out(const AdapterParams& p, bool wide, int num_sms, cudaStream_t stream) {
+    auto with = [&](auto steps) -> cudaError_t {
+        constexpr int STEPS = decltype(steps)::value;
+        return wide ? launch_out_steps<F32, STEPS, true>(p, num_sms, stream) : launch_out_steps<F32, STEPS, false>(p, num_sms, stream);
+    };
+    if (p.rank <= 32) return with(std::integral_constant<int, 1>());
+    if (p.rank <= 64) return with(std::integral_constant<int, 2>());
+    return with(std::integral_constant<int, 4>());
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -422,13 +496,13 @@ int qmm_adapter_validate_desc(const qmm_adapter_desc* d) {
     if (d->K < 1 || d->N < 1 || d->rank < 1 || d->adapters < 1 || d->max_rows < 1) return QMM_ERR_INVALID_ARG;
     if (d->K > (1LL << 30) || d->N > (1LL << 30) || d->max_rows > QMM_ADAPTER_MAX_ROWS) return QMM_ERR_INVALID_ARG;
     if (d->out_dtype != QMM_OUT_F32 && d->out_dtype != QMM_OUT_BF16) return QMM_ERR_INVALID_ARG;
-    if (d->K % kStepK != 0 || d->rank % 8 != 0 || d->rank > QMM_ADAPTER_MAX_RANK) return QMM_ERR_UNSUPPORTED;
+    if (d->K % 64 != 0 || d->rank % 8 != 0 || d->rank > QMM_ADAPTER_MAX_RANK) return QMM_ERR_UNSUPPORTED;
     return QMM_OK;
 }
 
 size_t qmm_adapter_workspace_bytes(const qmm_adapter_desc* d) {
     if (qmm_adapter_validate_desc(d) != QMM_OK) return 0;
-    return kErrBytes + static_cast<size_t>(d->max_rows) * d->rank * 2 * sizeof(uint16_t);
+    return kErrBytes + static_cast<size_t>(d->max_rows) * d->rank * terms_of(d->out_dtype) * sizeof(uint16_t);
 }
 
 int qmm_adapter_plan(qmm_adapter_plan_t** plan, const qmm_adapter_desc* d, void* workspace, size_t ws_bytes) {
@@ -441,7 +515,8 @@ int qmm_adapter_plan(qmm_adapter_plan_t** plan, const qmm_adapter_desc* d, void*
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return QMM_ERR_CUDA;
-    if (cudaFuncSetAttribute(qmm_adapter_low_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    if (cudaFuncSetAttribute(qmm_adapter_low_kernel<2>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(qmm_adapter_low_kernel<3>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return QMM_ERR_CUDA;
     struct qmm_adapter_plan* p = new (std::nothrow) struct qmm_adapter_plan();
     if (p == nullptr) return QMM_ERR_ALLOC;
@@ -504,8 +579,8 @@ int qmm_add_adapters(const qmm_adapter_plan_t* p, const qmm_adapter_args* a, voi
     ap.y = a->y;
     ap.out = a->out;
     ap.err = reinterpret_cast<uint32_t*>(p->ws);
-    ap.high = reinterpret_cast<uint16_t*>(p->ws + kErrBytes);
-    ap.low = ap.high + static_cast<size_t>(p->d.max_rows) * p->d.rank;
+    ap.low = reinterpret_cast<uint16_t*>(p->ws + kErrBytes);
+    ap.low_term = static_cast<int64_t>(p->d.max_rows) * p->d.rank;
     ap.x_stride = a->x_stride;
     ap.y_stride = a->y_stride;
     ap.out_stride = a->out_stride;
@@ -520,11 +595,8 @@ int qmm_add_adapters(const qmm_adapter_plan_t* p, const qmm_adapter_args* a, voi
     const bool wide = aligned(a->y, 16) && aligned(a->out, 16) &&
                       (a->rows == 1 || (a->y_stride % vec == 0 && a->out_stride % vec == 0));
     pthread_mutex_lock(&p->launches);
-    cudaError_t e = launch_low(ap, p->num_sms, st);
-    if (e == cudaSuccess) {
-        if (f32) e = wide ? launch_out<true, true>(ap, p->num_sms, st) : launch_out<true, false>(ap, p->num_sms, st);
-        else e = wide ? launch_out<false, true>(ap, p->num_sms, st) : launch_out<false, false>(ap, p->num_sms, st);
-    }
+    cudaError_t e = f32 ? launch_low<3>(ap, p->num_sms, st) : launch_low<2>(ap, p->num_sms, st);
+    if (e == cudaSuccess) e = f32 ? launch_out<true>(ap, wide, p->num_sms, st) : launch_out<false>(ap, wide, p->num_sms, st);
     pthread_mutex_unlock(&p->launches);
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }

@@ -123,24 +123,46 @@ __device__ __forceinline__ void store_pairs(uint16_t* dst, int second, const Pai
     }
 }
 
-// Eight neighbouring values of a head as codes, of 8 or 4 bits in 8 or 4 bytes. The lanes of a group of 64 call it together;
-// `affine` gets their scale and bias. False: a value was not finite.
+// (a or b is NaN: so is the result)
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Eight neighbouring values of a head as codes, of 8 or 4 bits in 8 or 4 bytes. Whole warps call it, the lanes of a group of
+// 64 together; `affine` gets their scale and bias. False: a value was not finite.
 template <int BITS>
 __device__ __forceinline__ bool quantise(float (&x)[8], uint32_t (&codes)[BITS / 4], uint32_t& affine) {
     constexpr float kTop = (1 << BITS) - 1, kLargest = QMM_KVQ_LARGEST;
+    auto limits = [&](float& lo, float& hi) {
+        lo = hi = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            lo = min_nan(lo, x[i]);
+            hi = max_nan(hi, x[i]);
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        }
+    };
+    float lo, hi;
+    limits(lo, hi);
     bool finite = true;
-    float lo = kLargest, hi = -kLargest;
+    if (__any_sync(0xFFFFFFFFu, !(lo >= -kLargest && hi <= kLargest))) {   // (NaN among them)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        finite &= fabsf(x[i]) < INFINITY;
-        x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kLargest), kLargest) : 0.0f;
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        for (int i = 0; i < 8; ++i) {
+            finite &= fabsf(x[i]) < INFINITY;
+            x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kLargest), kLargest) : 0.0f;
+        }
+        limits(lo, hi);
     }
     const __half scale = __float2half_rn(__fdiv_rn(hi - lo, kTop)), bias = __float2half_rn(lo);
     const float s = __half2float(scale), b = __half2float(bias);
@@ -148,17 +170,25 @@ __device__ __forceinline__ bool quantise(float (&x)[8], uint32_t (&codes)[BITS /
     affine = static_cast<uint32_t>(__half_as_ushort(scale)) | static_cast<uint32_t>(__half_as_ushort(bias)) << 16;
     uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)   // the sum's last bits are the whole number, rounded to the nearest, ties to even
-        c[i] = __float_as_uint(fminf(fmaxf(__fmul_rn(x[i] - b, inverse), 0.0f), kTop) + 0x1p23f);
+    for (int i = 0; i < 8; i += 2) {
+        float f[2];
+        add_x2(f[0], f[1], x[i], x[i + 1], -b, -b);
+        mul_x2(f[0], f[1], f[0], f[1], inverse, inverse);
+        f[0] = fminf(fmaxf(f[0], 0.0f), kTop), f[1] = fminf(fmaxf(f[1], 0.0f), kTop);
+        // the sums' last bits are the whole numbers, rounded to the nearest, ties to even
+        add_x2(f[0], f[1], f[0], f[1], 0x1p23f, 0x1p23f);
+        c[i] = __float_as_uint(f[0]), c[i + 1] = __float_as_uint(f[1]);
+    }
     if constexpr (BITS == 8) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             codes[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040), __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040),
                                    0x5410);
     } else {
-        codes[0] = 0;
+        uint32_t two[4];   // (the sums' upper bits are shifted out, or masked)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) codes[0] |= (c[i] & 15u) << (4 * i);
+        for (int k = 0; k < 4; ++k) two[k] = (c[2 * k] & 15u) | ((c[2 * k + 1] & 15u) << 4);
+        codes[0] = __byte_perm(__byte_perm(two[0], two[1], 0x0040), __byte_perm(two[2], two[3], 0x0040), 0x5410);
     }
     return finite;
 }

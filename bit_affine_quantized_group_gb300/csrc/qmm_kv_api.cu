@@ -121,10 +121,11 @@ int check_read(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_read_
     const int64_t seqs = a->seqs, rows = a->rows;
     if (seqs < 0 || seqs > d->max_seqs || rows < 0) return QMM_ERR_INVALID_ARG;
     if (seqs == 0 || rows == 0) return QMM_OK;
-    // outputs of 16 bytes of a sequence, and blocks of 1024 of them, are counted in 32 bits
+    // outputs of 16 bytes of a sequence, and blocks of 256 threads with four rows each, are counted in 32 bits
     const int size = a->out_dtype == QMM_OUT_F32 ? 4 : 2;
     const int64_t width = static_cast<int64_t>(d->kv_heads) * d->head_dim, units = rows * (width * size / 16);
-    if (units > (1LL << 31) || 2 * seqs * ((units + 1023) / 1024) > 0x7FFFFFFF) return QMM_ERR_UNSUPPORTED;
+    const int64_t blocks = ((rows + 6) / 4 * (width * size / 16) + 255) / 256;
+    if (units > (1LL << 31) || 2 * seqs * blocks > 0x7FFFFFFF) return QMM_ERR_UNSUPPORTED;
     const int64_t strides[4] = {a->k_seq_stride, a->k_row_stride, a->v_seq_stride, a->v_row_stride};
     const int64_t least[4] = {seqs > 1 ? width : 0, rows > 1 ? width : 0, seqs > 1 ? width : 0, rows > 1 ? width : 0};
     for (int i = 0; i < 4; ++i)

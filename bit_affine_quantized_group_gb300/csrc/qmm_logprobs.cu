@@ -23,12 +23,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kTop = QMM_LOGPROBS_MAX_TOP;
 constexpr int kList = 1024;            // candidates that are ranked by counting
 constexpr int kRanks = 16;             // CTAs of a row at most
 constexpr int kAhead = 4;              // chunks that a thread loads before it works on the last
+constexpr int kSome = 16;              // threads that may be looked at beyond the needed ones
+constexpr float kRise = 16.0f;         // that logits may lie above a thread's reference before its sums are brought to a new one
 constexpr float kLeast = -1000.0f;     // differences are brought to it: e^-1000 is 0, and no infinity meets a 0
 constexpr float kLog2E = 1.4426950408889634f;
 
@@ -45,16 +45,16 @@ struct LogprobsParams {
     int32_t vocab, top;
 };
 
+template <int THREADS>
 struct Shared {
     u64 best[kTop];                    // of this CTA, by rank; 0 for none
-    float max, sum, weighted;          // m, s and t of this CTA
-    u64 all[kRanks * kTop];            // the first CTA's copy of all lists
-    float stats[kRanks][3];
+    u64 all[kRanks * kTop];            // in the first CTA: the lists of all of them
+    float stats[kRanks][4];            // and their m, s and t
     u64 list[kList];
-    float warp_max[kWarps], warp_sum[kWarps], warp_weighted[kWarps];
-    u64 warp_best[kWarps];
-    uint32_t selected[kThreads];
-    uint32_t selected_size, list_size;
+    float warp_max[THREADS / 32], warp_sum[THREADS / 32], warp_weighted[THREADS / 32];
+    u64 warp_best[THREADS / 32];
+    uint32_t selected[THREADS];
+    uint32_t selected_size, list_size, key_low, key_high;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -121,14 +121,29 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (sizeof(T) == 4) {
-                v[i] = clean(__uint_as_float(u[i]));
+                v[i] = __uint_as_float(u[i]);
             } else {
-                v[2 * i] = clean(__uint_as_float(u[i] << 16));
-                v[2 * i + 1] = clean(__uint_as_float(u[i] & 0xFFFF0000u));
+                v[2 * i] = __uint_as_float(u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
             }
         }
     }
+    // the largest element; NaN only where all are
+    static __device__ __forceinline__ float largest(const uint4& w) {
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+        } else {
+            auto pair = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+            const __nv_bfloat162 m = __hmax2(__hmax2(pair(w.x), pair(w.y)), __hmax2(pair(w.z), pair(w.w)));
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+            return fmaxf(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+        }
+    }
 };
+
+// The cluster's barrier in halves: what a thread did before its arrival is seen behind the others' waits.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 __device__ __forceinline__ u64 warp_max64(u64 v) {
 #pragma unroll
@@ -139,68 +154,93 @@ __device__ __forceinline__ u64 warp_max64(u64 v) {
     return v;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads, 2) qmm_logprobs_kernel(const __grid_constant__ LogprobsParams p, int ranks) {
+template <class T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(const __grid_constant__ LogprobsParams p, int ranks) {
     using R = Row<T>;
-    __shared__ Shared s;
+    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+    __shared__ __align__(16) Shared<THREADS> s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / ranks;
     const int rank = static_cast<int>(blockIdx.x - row * ranks);
+    if (ranks > 1) cluster_arrive();   // this CTA has started, and its memory may be written
     griddep_launch_dependents();
     griddep_wait();
     const R r(static_cast<const T*>(p.logits) + row * p.stride, p.vocab);
     const int per = (r.chunks + ranks - 1) / ranks;
     const int c0 = rank * per, c1 = min(r.chunks, c0 + per);
 
-    // the pass over the share
-    float m = -INFINITY, sum = 0.0f, weighted = 0.0f;
+    // The pass over the share. Sums are held to a reference that few chunks change: the first one's largest logit, until one
+    // lies kRise above it.
+    float m = -INFINITY, ref = -INFINITY;
+    float sums[2] = {}, weights[2] = {};   // s and t, of the even and the odd elements
     int at = -1;   // the chunk that m came from first
     auto take = [&](int c, const uint4& w) {
         float v[R::kVec];
         R::values(w, v);
-        float most = v[0];
+        float most = fmaxf(R::largest(w), -INFINITY);
+        if (most == INFINITY) {
+            most = FLT_MAX;
 #pragma unroll
-        for (int i = 1; i < R::kVec; ++i) most = fmaxf(most, v[i]);
-        if (at < 0 || most > m) at = c;
-        const float now = fmaxf(m, most), d = fmaxf(m - now, kLeast), shrink = exp2_approx(d * kLog2E);
-        m = now;
-        weighted = fmaf(sum, d, weighted) * shrink;
-        sum *= shrink;
+            for (int i = 0; i < R::kVec; ++i) v[i] = clean(v[i]);
+        }
+        if (most > m || at < 0) at = c;
+        m = fmaxf(m, most);
+        if (most > ref + kRise) {   // (also where ref is still -infinity)
+            const float d = fmaxf(ref - most, kLeast), shrink = exp2_approx(d * kLog2E);
+            ref = most;
 #pragma unroll
-        for (int i = 0; i < R::kVec; ++i) {
-            const float below = fmaxf(v[i] - now, kLeast), e = exp2_approx(below * kLog2E);
-            sum += e;
-            weighted = fmaf(e, below, weighted);
+            for (int i = 0; i < 2; ++i) {
+                weights[i] = fmaf(sums[i], d, weights[i]) * shrink;
+                sums[i] *= shrink;
+            }
+        }
+        const float less = -ref;
+#pragma unroll
+        for (int i = 0; i < R::kVec; i += 2) {   // (NaN - ref and -infinity - -infinity come to kLeast too)
+            float x[2], e[2];
+            add_x2(x[0], x[1], v[i], v[i + 1], less, less);
+            x[0] = fmaxf(x[0], kLeast), x[1] = fmaxf(x[1], kLeast);
+            mul_x2(e[0], e[1], x[0], x[1], kLog2E, kLog2E);
+            e[0] = exp2_approx(e[0]), e[1] = exp2_approx(e[1]);
+            add_x2(sums[0], sums[1], sums[0], sums[1], e[0], e[1]);
+            fma_x2(weights[0], weights[1], e[0], e[1], x[0], x[1], weights[0], weights[1]);
         }
     };
+    // the row's first and last chunk may be cut short
+    const int w0 = max(c0, r.whole(0) ? 0 : 1), w1 = min(c1, r.whole(r.chunks - 1) ? r.chunks : r.chunks - 1);
+    const uint4* const chunks = reinterpret_cast<const uint4*>(r.base - r.head);
     uint4 next[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-        if (c0 + tid + k * kThreads < c1) next[k] = r.load(c0 + tid + k * kThreads);
+        if (w0 + tid + k * kThreads < w1) next[k] = __ldg(chunks + w0 + tid + k * kThreads);
+    if (tid == 0 && c0 < w0 && c0 < c1) take(c0, r.load(c0));
 #pragma unroll 1
-    for (int c = c0 + tid; c < c1; c += kAhead * kThreads) {
+    for (int c = w0 + tid; c < w1; c += kAhead * kThreads) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int mine = c + k * kThreads, later = mine + kAhead * kThreads;
-            if (mine >= c1) break;
+            if (mine >= w1) break;
             const uint4 w = next[k];
-            if (later < c1) next[k] = r.load(later);
+            if (later < w1) next[k] = __ldg(chunks + later);
             take(mine, w);
         }
     }
+    if (tid == 1 && w1 < c1 && w1 >= w0) take(w1, r.load(w1));   // (after the others: `at` is the first of equal ones)
+    m += 0.0f;
+    const float sum = sums[0] + sums[1], weighted = weights[0] + weights[1];
 
     // of the CTA
     float most = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     if (lane == 0) s.warp_max[warp] = most;
-    if (tid == 0) s.selected_size = s.list_size = 0;
+    if (tid == 0) s.selected_size = s.list_size = s.key_high = 0, s.key_low = 0xFFFFFFFFu;
     if (tid < kTop) s.best[tid] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) most = fmaxf(most, s.warp_max[i]);
     {
-        const float d = fmaxf(m - most, kLeast), shrink = exp2_approx(d * kLog2E);
+        const float d = fmaxf(ref - most, kLeast), shrink = exp2_approx(d * kLog2E);
         float b = fmaf(sum, d, weighted) * shrink, a = sum * shrink;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -211,20 +251,25 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_logprobs_kernel(const __grid_
     }
 
     if (p.top > 0) {
-        // the p.top best of the threads' largest logits: the last of them is (bound, last)
+        // a bound that the largest logits of p.top threads reach, and of few more: (bound, last)
         const bool some = at >= 0;
         const uint32_t key = some ? key_of(m) : 0u;
+        const uint32_t low_key = __reduce_min_sync(0xFFFFFFFFu, some ? key : 0xFFFFFFFFu), high_key = __reduce_max_sync(0xFFFFFFFFu, key);
+        if (lane == 0) atomicMin(&s.key_low, low_key), atomicMax(&s.key_high, high_key);
         uint32_t bound = 0;
         int last = 0x7FFFFFFF;
-        if (__syncthreads_count(some) > p.top) {
-            int above = 0;   // threads with key >= bound
+        int reach = __syncthreads_count(some);   // threads with key >= bound
+        if (reach > p.top + kSome) {
+            // bit by bit below the first that the keys differ in
+            const uint32_t differ = s.key_low ^ s.key_high;
+            bound = s.key_low & ~(differ == 0 ? 0u : 0xFFFFFFFFu >> __clz(differ));
 #pragma unroll 1
-            for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+            for (uint32_t bit = differ == 0 ? 0u : 0x80000000u >> __clz(differ); bit != 0 && reach > p.top + kSome; bit >>= 1) {
                 const int n = __syncthreads_count(key >= (bound | bit));
-                if (n >= p.top) bound |= bit, above = n;
+                if (n >= p.top) bound |= bit, reach = n;
             }
-            if (above > p.top) {   // equal logits: those of the first chunks
-                int low = -1;      // too few up to here
+            if (reach > p.top + kSome) {   // equal logits: those of the first chunks
+                int low = -1;              // too few up to here
                 last = r.chunks - 1;
 #pragma unroll 1
                 while (last - low > 1) {
@@ -237,19 +282,24 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_logprobs_kernel(const __grid_
         if (some && (key > bound || (key == bound && at <= last))) s.selected[atomicAdd(&s.selected_size, 1u)] = tid;
         __syncthreads();
         const int selected = static_cast<int>(s.selected_size);
-        // every element of those threads that is no worse
+        // every element of those threads' chunks that is no worse; the row's first and last chunk are looked at in any case
+        const float bound_value = bound <= key_of(-INFINITY) ? -INFINITY : value_of(bound);
+        auto look = [&](int c, const uint4& w, auto&& f) {
+            if (!(fmaxf(R::largest(w), -INFINITY) >= bound_value)) return;
+            float v[R::kVec];
+            R::values(w, v);
+#pragma unroll
+            for (int k = 0; k < R::kVec; ++k) {
+                const uint32_t q = key_of(clean(v[k]));
+                const int e = r.first(c) + k;
+                if ((q > bound || (q == bound && c <= last)) && e >= 0 && e < p.vocab) f(entry_of(q, e));
+            }
+        };
         auto each = [&](auto&& f) {
             for (int i = warp; i < selected; i += kWarps)
-                for (int c = c0 + static_cast<int>(s.selected[i]) + lane * kThreads; c < c1; c += 32 * kThreads) {
-                    float v[R::kVec];
-                    R::values(r.load(c), v);
-#pragma unroll
-                    for (int k = 0; k < R::kVec; ++k) {
-                        const uint32_t q = key_of(v[k]);
-                        const int e = r.first(c) + k;
-                        if ((q > bound || (q == bound && c <= last)) && e >= 0 && e < p.vocab) f(entry_of(q, e));
-                    }
-                }
+                for (int c = w0 + static_cast<int>(s.selected[i]) + lane * kThreads; c < w1; c += 32 * kThreads) look(c, __ldg(chunks + c), f);
+            if (tid == 0 && c0 < w0 && c0 < c1) look(c0, r.load(c0), f);
+            if (tid == 32 && w1 < c1 && w1 >= w0) look(w1, r.load(w1), f);
         };
         each([&](u64 entry) {
             const uint32_t slot = atomicAdd(&s.list_size, 1u);
@@ -282,28 +332,20 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_logprobs_kernel(const __grid_
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        float a = 0.0f, b = 0.0f;
+    float total = 0.0f, total_weighted = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) a += s.warp_sum[i], b += s.warp_weighted[i];
-        s.max = most, s.sum = a, s.weighted = b;
-    }
+    for (int i = 0; i < kWarps; ++i) total += s.warp_sum[i], total_weighted += s.warp_weighted[i];
 
     // of the row, by its first CTA
     const u64* best = s.best;
-    float total, total_weighted;
     if (ranks > 1) {
         cg::cluster_group cluster = cg::this_cluster();
-        cluster.sync();
-        if (rank == 0) {
-            if (tid < ranks * kTop) s.all[tid] = cluster.map_shared_rank(s.best, tid / kTop)[tid % kTop];
-            if (tid < ranks) {
-                const Shared* of = cluster.map_shared_rank(&s, tid);
-                s.stats[tid][0] = of->max, s.stats[tid][1] = of->sum, s.stats[tid][2] = of->weighted;
-            }
-        }
-        cluster.sync();   // the other CTAs' memory has been read
+        cluster_wait();   // the first CTA has started
+        if (tid < kTop) *cluster.map_shared_rank(&s.all[rank * kTop + tid], 0) = s.best[tid];
+        if (tid == 0) *cluster.map_shared_rank(reinterpret_cast<float4*>(s.stats[rank]), 0) = make_float4(most, total, total_weighted, 0.0f);
+        cluster_arrive();
         if (rank != 0) return;
+        cluster_wait();
         for (int i = 0; i < ranks; ++i) most = fmaxf(most, s.stats[i][0]);
         total = total_weighted = 0.0f;
         for (int i = 0; i < ranks; ++i) {
@@ -311,19 +353,17 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_logprobs_kernel(const __grid_
             total = fmaf(s.stats[i][1], shrink, total);
             total_weighted = fmaf(fmaf(s.stats[i][1], d, s.stats[i][2]), shrink, total_weighted);
         }
-        if (tid < ranks * kTop) {
-            const u64 mine = s.all[tid];
+        // (this CTA's own list of candidates is no longer in use)
+        for (int j = tid; j < ranks * kTop; j += kThreads) {
+            const u64 mine = s.all[j];
+            if (mine == 0) continue;
             int before = 0;
             for (int i = 0; i < ranks; ++i)
-                for (int j = 0; j < p.top; ++j) before += s.all[i * kTop + j] > mine;
-            if (mine != 0 && before < p.top) s.list[before] = mine;
+                for (int k = 0; k < p.top; ++k) before += s.all[i * kTop + k] > mine;
+            if (before < p.top) s.list[before] = mine;
         }
-        // (this CTA's own list of candidates is no longer in use)
         __syncthreads();
         best = s.list;
-    } else {
-        __syncthreads();
-        total = s.sum, total_weighted = s.weighted;
     }
     const float log_total = logf(total);
     if (tid == 0) {
@@ -343,17 +383,14 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_logprobs_kernel(const __grid_
     }
 }
 
-template <class T>
-int launch_rows(const LogprobsParams& p, int M, cudaStream_t stream) {
-    // as many CTAs for a row as fill the GPU, of 2048 logits at least
-    int ranks = kRanks;
-    while (ranks > 1 && (static_cast<int64_t>(M) * ranks > 2 * 152 || p.vocab / ranks < 2048)) ranks /= 2;
+template <class T, int THREADS>
+int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
     if (ranks > 8) {
         static std::atomic<u64> configured{0};   // one bit for each device
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
         if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
-            const void* kernel = reinterpret_cast<const void*>(&qmm_logprobs_kernel<T>);
+            const void* kernel = reinterpret_cast<const void*>(&qmm_logprobs_kernel<T, THREADS>);
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
                 return QMM_ERR_CUDA;
             if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
@@ -367,11 +404,24 @@ int launch_rows(const LogprobsParams& p, int M, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M) * ranks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, qmm_logprobs_kernel<T>, p, ranks) == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, qmm_logprobs_kernel<T, THREADS>, p, ranks) == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+template <class T>
+int launch_rows(const LogprobsParams& p, int M, cudaStream_t stream) {
+    // Few rows: as many CTAs of 512 threads for each as fill the GPU, of 2048 logits at least. Many: CTAs of 256 threads, 6 an
+    // SM or more, so that one's steps behind the pass and the last rows' overhang cost little.
+    int ranks = kRanks;
+    if (static_cast<int64_t>(M) * 2 <= 2 * 152) {
+        while (ranks > 1 && (M * ranks > 2 * 152 || p.vocab / ranks < 2048)) ranks /= 2;
+        return launch<T, 512>(p, M, ranks, stream);
+    }
+    while (ranks > 1 && (static_cast<int64_t>(M) * ranks > 12 * 152 || p.vocab / ranks < 8192)) ranks /= 2;
+    return launch<T, 256>(p, M, ranks, stream);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -549,8 +549,8 @@ typedef struct qmm_adapter_args {
 
 /*
  * Adds the adapters' products. x . A^T is summed in float32 and enters the
- * second product as two bfloat16 terms (within 2^-17); that is summed in
- * float32 with y and rounded once. The order of the sums is fixed: a call gives
+ * second product as bfloat16 terms (two within 2^-17, for float32 outputs three
+ * within 2^-26); that is summed in float32 with y and rounded once. The order of the sums is fixed: a call gives
  * the same bits for the same inputs. out may be y itself (rows at the same
  * places) and otherwise overlaps nothing. Two launches. rows = 0 is a no-op.
  */
