@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
 // A run of units of a tile's 32 columns for each warp; a lane has 8 neighbouring columns of two rows. STEPS: 32 elements of
 // rank each. WIDE: rows of y and out are read and written 16 bytes at a time.
 template <bool F32, int STEPS, bool WIDE>
-__global__ void __launch_bounds__(kThreads, STEPS == 1 ? 3 : 2) qmm_adapter_out_kernel(const __grid_constant__ AdapterParams p, int groups) {
+__global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adapter_out_kernel(const __grid_constant__ AdapterParams p, int groups) {
     constexpr int kTerms = F32 ? 3 : 2;
     constexpr bool kKeep = STEPS <= 2;   // low stays in registers over a tile's units
     __shared__ __align__(16) Tiles t;
@@ -271,15 +271,15 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 ? 3 : 2) qmm_adapter_out_
     griddep_launch_dependents();
     find_tiles(p, row0, t);
     const uint32_t columns = static_cast<uint32_t>((p.N + 31) / 32);
-    const uint64_t units = static_cast<uint64_t>(t.tiles) * columns;
-    const uint32_t all = groups * kWarps, mine = group * kWarps + warp;
-    uint64_t u = units * mine / all;
-    const uint64_t u1 = units * (mine + 1) / all;
+    const uint32_t units = t.tiles * columns;   // (2^31 at most)
+    const uint32_t all = groups * kWarps, mine = group * kWarps + warp, each = units / all, rest = units - each * all;
+    uint32_t u = mine * each + min(mine, rest);
+    const uint32_t u1 = u + each + (mine < rest ? 1 : 0);
     bool waited = false;   // for the first kernel
     while (u < u1) {
         const int tile = static_cast<int>(u / columns);
-        uint32_t column = static_cast<uint32_t>(u - static_cast<uint64_t>(tile) * columns);
-        const uint32_t end = u1 - u < columns - column ? column + static_cast<uint32_t>(u1 - u) : columns;
+        uint32_t column = u - tile * columns;
+        const uint32_t end = min(column + (u1 - u), columns);
         u += end - column;
         const int id = t.tile_id[tile], first = t.first[tile], size = t.size[tile];
         if (id < 0 && p.y == p.out) continue;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 ? 3 : 2) qmm_adapter_out_
         for (; column < end; ++column, b += 16 * b_next) {
             const int64_t n0 = static_cast<int64_t>(column) * 32, n = n0 + quad * 8;
             const bool full = n0 + 32 <= p.N, whole = WIDE && n + 8 <= p.N;
-            // y and B of the unit
+            // y and B of the unit (with the next one's on their way too, and so one CTA less an SM, 2048 rows took a fifth longer)
             uint4 wy[2][F32 ? 2 : 1], wb[STEPS][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -388,11 +388,12 @@ cudaError_t launch_low(const AdapterParams& p, int num_sms, cudaStream_t stream)
     const int64_t blocks = (p.rows + kBlock - 1) / kBlock;
     const int64_t steps = p.K / kStep;
     // two CTAs an SM; units of a block: one for each 16 columns of rank of up to as many tiles as it has rows
-    int slices = kSlices;
-    while (slices > 1 && (slices > steps || slices * blocks > 2 * num_sms)) slices /= 2;
     const int64_t units = static_cast<int64_t>(p.rows < kBlock ? p.rows : kBlock) * ((p.rank + 15) / 16);
-    int64_t groups = 2 * num_sms / (blocks * slices);
     const int64_t most = (units + kWarps - 1) / kWarps;
+    // (clusters of 16 leave SMs of their part of the GPU without work where there are many: 64 rows of rank 64 took 8.7 us)
+    int slices = blocks * most * kSlices <= num_sms ? kSlices : kSlices / 2;
+    while (slices > 1 && (slices > steps || slices * blocks > 2 * num_sms)) slices /= 2;
+    int64_t groups = 2 * num_sms / (blocks * slices);
     groups = groups < 1 ? 1 : groups > most ? most : groups;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -414,7 +415,7 @@ template <bool F32, int STEPS, bool WIDE>
 cudaError_t launch_out_steps(const AdapterParams& p, int num_sms, cudaStream_t stream) {
     const int64_t blocks = (p.rows + kBlock - 1) / kBlock;
     const int64_t units = (p.rows < kBlock ? p.rows : kBlock) * ((p.N + 31) / 32);
-    int64_t groups = ((STEPS == 1 ? 3 : 2) * num_sms + blocks - 1) / blocks;   // as many CTAs as run at once
+    int64_t groups = ((STEPS == 1 && !F32 ? 3 : 2) * num_sms + blocks - 1) / blocks;   // as many CTAs as run at once
     const int64_t most = (units + kWarps - 1) / kWarps;
     groups = groups > most ? most : groups;
     cudaLaunchAttribute attr[1];

@@ -3,11 +3,12 @@
 //   m' = max(m, l),  d = m - m',  t = (t + s d) e^d + sum e^(l - m') (l - m'),  s = s e^d + sum e^(l - m'),
 //   lse = m + log s,   entropy = log s - t / s   (every term of -t is positive, so that nothing cancels).
 //
-// A thread keeps m, s, t and the chunk that its largest logit came from. The
-// `top` best (logit, index) of a CTA's share are no worse than the `top` best of
-// the threads' largest logits, and so lie with those `top` threads: their chunks
-// alone, a sixteenth of the share, are read again. Each CTA of a row ranks what it
-// finds by counting, the first one of the cluster ranks the CTAs' lists.
+// A thread keeps m, s, t, the chunk of 16 bytes that its largest logit came from
+// and the largest logit of its other chunks. The `top` best (logit, index) of a
+// CTA's share are no worse than the `top` best of the threads' largest logits, and
+// so lie with those threads: that one chunk of theirs is read again, and all of
+// them where a second one reaches as far. Each CTA of a row ranks what it finds by
+// counting, the first one of the cluster ranks the CTAs' lists.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -26,8 +27,11 @@ namespace cg = cooperative_groups;
 constexpr int kTop = QMM_LOGPROBS_MAX_TOP;
 constexpr int kList = 1024;            // candidates that are ranked by counting
 constexpr int kRanks = 16;             // CTAs of a row at most
-constexpr int kAhead = 4;              // chunks that a thread loads before it works on the last
+// Chunks that a thread has on their way. Of 512 rows at once the pass is bound by how many bytes are: four in registers came to
+// 3.4 TB/s, and more left no room for the CTAs.
+constexpr int kAhead = 5;
 constexpr int kSome = 16;              // threads that may be looked at beyond the needed ones
+constexpr int kManyThreads = 256, kManyCtas = 4 * 152;   // of a CTA and at once, where rows are many
 constexpr float kRise = 16.0f;         // that logits may lie above a thread's reference before its sums are brought to a new one
 constexpr float kLeast = -1000.0f;     // differences are brought to it: e^-1000 is 0, and no infinity meets a 0
 constexpr float kLog2E = 1.4426950408889634f;
@@ -53,8 +57,11 @@ struct Shared {
     u64 list[kList];
     float warp_max[THREADS / 32], warp_sum[THREADS / 32], warp_weighted[THREADS / 32];
     u64 warp_best[THREADS / 32];
-    uint32_t selected[THREADS];
-    uint32_t selected_size, list_size, key_low, key_high;
+    uint32_t keys[THREADS];            // of the threads' largest logits; 0 for none
+    int at[THREADS];                   // their chunks
+    uint32_t again[THREADS];           // threads with more than that chunk to look at
+    uint32_t again_size, list_size, bound;
+    int last;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -141,6 +148,14 @@ struct Row {
     }
 };
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until no more than the last N groups of this thread are on their way
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // The cluster's barrier in halves: what a thread did before its arrival is seen behind the others' waits.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
@@ -159,6 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
     using R = Row<T>;
     constexpr int kThreads = THREADS, kWarps = THREADS / 32;
     __shared__ __align__(16) Shared<THREADS> s;
+    extern __shared__ __align__(16) uint4 s_ring[];   // [kAhead][thread]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / ranks;
     const int rank = static_cast<int>(blockIdx.x - row * ranks);
@@ -174,18 +190,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
     float m = -INFINITY, ref = -INFINITY;
     float sums[2] = {}, weights[2] = {};   // s and t, of the even and the odd elements
     int at = -1;   // the chunk that m came from first
+    float other = -INFINITY;   // the largest logit of the other chunks
     auto take = [&](int c, const uint4& w) {
         float v[R::kVec];
         R::values(w, v);
-        float most = fmaxf(R::largest(w), -INFINITY);
-        if (most == INFINITY) {
-            most = FLT_MAX;
+        float most = R::largest(w);   // (NaN for nothing but NaN, which changes nothing below)
+        if (most > ref + kRise) {     // (also where ref is still -infinity, and for an infinity, which becomes the largest number)
+            if (most == INFINITY) {
+                most = FLT_MAX;
 #pragma unroll
-            for (int i = 0; i < R::kVec; ++i) v[i] = clean(v[i]);
-        }
-        if (most > m || at < 0) at = c;
-        m = fmaxf(m, most);
-        if (most > ref + kRise) {   // (also where ref is still -infinity)
+                for (int i = 0; i < R::kVec; ++i) v[i] = clean(v[i]);
+            }
             const float d = fmaxf(ref - most, kLeast), shrink = exp2_approx(d * kLog2E);
             ref = most;
 #pragma unroll
@@ -194,6 +209,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
                 sums[i] *= shrink;
             }
         }
+        if (most > m) at = c;
+        other = fmaxf(other, fminf(m, most));
+        m = fmaxf(m, most);
         const float less = -ref;
 #pragma unroll
         for (int i = 0; i < R::kVec; i += 2) {   // (NaN - ref and -infinity - -infinity come to kLeast too)
@@ -209,23 +227,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
     // the row's first and last chunk may be cut short
     const int w0 = max(c0, r.whole(0) ? 0 : 1), w1 = min(c1, r.whole(r.chunks - 1) ? r.chunks : r.chunks - 1);
     const uint4* const chunks = reinterpret_cast<const uint4*>(r.base - r.head);
-    uint4 next[kAhead];
+    // every thread reads what it has copied itself, and refills a place when what it held has been used
+    const uint32_t ring = smem_u32(s_ring + tid);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-        if (w0 + tid + k * kThreads < w1) next[k] = __ldg(chunks + w0 + tid + k * kThreads);
-    if (tid == 0 && c0 < w0 && c0 < c1) take(c0, r.load(c0));
+    for (int k = 0; k < kAhead - 1; ++k) {
+        const int c = w0 + tid + k * kThreads;
+        if (c < w1) cp_async_16(ring + k * (kThreads * 16), chunks + c);
+        cp_async_commit();
+    }
+    const bool with_first = tid == 0 && c0 < w0 && c0 < c1, with_last = tid == 1 && w1 < c1 && w1 >= w0;
+    // (the first of its chunks, where none has a logit above -infinity)
+    at = with_first ? c0 : w0 + tid < w1 ? w0 + tid : with_last ? w1 : -1;
+    if (with_first) take(c0, r.load(c0));
+    const uint4* ahead = chunks + w0 + tid + (kAhead - 1) * kThreads;
 #pragma unroll 1
     for (int c = w0 + tid; c < w1; c += kAhead * kThreads) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int mine = c + k * kThreads, later = mine + kAhead * kThreads;
+            const int mine = c + k * kThreads;
             if (mine >= w1) break;
-            const uint4 w = next[k];
-            if (later < w1) next[k] = __ldg(chunks + later);
-            take(mine, w);
+            if (mine + (kAhead - 1) * kThreads < w1) cp_async_16(ring + (k + kAhead - 1) % kAhead * (kThreads * 16), ahead);
+            cp_async_commit();
+            ahead += kThreads;
+            cp_async_wait<kAhead - 1>();
+            take(mine, s_ring[k * kThreads + tid]);
         }
     }
-    if (tid == 1 && w1 < c1 && w1 >= w0) take(w1, r.load(w1));   // (after the others: `at` is the first of equal ones)
+    if (with_last) take(w1, r.load(w1));   // (after the others: `at` is the first of equal ones)
     m += 0.0f;
     const float sum = sums[0] + sums[1], weighted = weights[0] + weights[1];
 
@@ -234,7 +262,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     if (lane == 0) s.warp_max[warp] = most;
-    if (tid == 0) s.selected_size = s.list_size = s.key_high = 0, s.key_low = 0xFFFFFFFFu;
+    if (tid == 0) s.again_size = s.list_size = 0;
+    const uint32_t key = at >= 0 ? key_of(m) : 0u;
+    s.keys[tid] = key;
+    s.at[tid] = at;
     if (tid < kTop) s.best[tid] = 0;
     __syncthreads();
 #pragma unroll
@@ -251,39 +282,58 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
     }
 
     if (p.top > 0) {
-        // a bound that the largest logits of p.top threads reach, and of few more: (bound, last)
-        const bool some = at >= 0;
-        const uint32_t key = some ? key_of(m) : 0u;
-        const uint32_t low_key = __reduce_min_sync(0xFFFFFFFFu, some ? key : 0xFFFFFFFFu), high_key = __reduce_max_sync(0xFFFFFFFFu, key);
-        if (lane == 0) atomicMin(&s.key_low, low_key), atomicMax(&s.key_high, high_key);
-        uint32_t bound = 0;
-        int last = 0x7FFFFFFF;
-        int reach = __syncthreads_count(some);   // threads with key >= bound
-        if (reach > p.top + kSome) {
-            // bit by bit below the first that the keys differ in
-            const uint32_t differ = s.key_low ^ s.key_high;
-            bound = s.key_low & ~(differ == 0 ? 0u : 0xFFFFFFFFu >> __clz(differ));
-#pragma unroll 1
-            for (uint32_t bit = differ == 0 ? 0u : 0x80000000u >> __clz(differ); bit != 0 && reach > p.top + kSome; bit >>= 1) {
-                const int n = __syncthreads_count(key >= (bound | bit));
-                if (n >= p.top) bound |= bit, reach = n;
+        // a bound that the largest logits of p.top threads reach, and of few more: (bound, last). By one warp, for it costs the
+        // same time and less of the other rows'.
+        if (warp == 0) {
+            uint32_t keys[kWarps], low_key = 0xFFFFFFFFu, high_key = 0;
+            int count = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                keys[i] = s.keys[i * 32 + lane];
+                if (keys[i] != 0) low_key = min(low_key, keys[i]);
+                high_key = max(high_key, keys[i]);
+                count += keys[i] != 0;
             }
-            if (reach > p.top + kSome) {   // equal logits: those of the first chunks
-                int low = -1;              // too few up to here
-                last = r.chunks - 1;
+            low_key = __reduce_min_sync(0xFFFFFFFFu, low_key);
+            high_key = __reduce_max_sync(0xFFFFFFFFu, high_key);
+            int reach = __reduce_add_sync(0xFFFFFFFFu, count);   // threads with key >= bound
+            uint32_t bound = 0;
+            int last = 0x7FFFFFFF;
+            if (reach > p.top + kSome) {
+                // bit by bit below the first that the keys differ in
+                const uint32_t differ = low_key ^ high_key;
+                bound = low_key & ~(differ == 0 ? 0u : 0xFFFFFFFFu >> __clz(differ));
 #pragma unroll 1
-                while (last - low > 1) {
-                    const int mid = low + (last - low) / 2;
-                    if (__syncthreads_count(key > bound || (key == bound && at <= mid)) >= p.top) last = mid;
-                    else low = mid;
+                for (uint32_t bit = differ == 0 ? 0u : 0x80000000u >> __clz(differ); bit != 0 && reach > p.top + kSome; bit >>= 1) {
+                    int n = 0;
+#pragma unroll
+                    for (int i = 0; i < kWarps; ++i) n += keys[i] >= (bound | bit);
+                    n = __reduce_add_sync(0xFFFFFFFFu, n);
+                    if (n >= p.top) bound |= bit, reach = n;
+                }
+                if (reach > p.top + kSome) {   // equal logits: those of the first chunks
+                    int low = -1;              // too few up to here
+                    last = r.chunks - 1;
+#pragma unroll 1
+                    while (last - low > 1) {
+                        const int mid = low + (last - low) / 2;
+                        int n = 0;
+#pragma unroll 1
+                        for (int i = 0; i < kWarps; ++i)
+                            n += s.keys[i * 32 + lane] > bound || (s.keys[i * 32 + lane] == bound && s.at[i * 32 + lane] <= mid);
+                        n = __reduce_add_sync(0xFFFFFFFFu, n);
+                        if (n >= p.top) last = mid;
+                        else low = mid;
+                    }
                 }
             }
+            if (lane == 0) s.bound = bound, s.last = last;
         }
-        if (some && (key > bound || (key == bound && at <= last))) s.selected[atomicAdd(&s.selected_size, 1u)] = tid;
         __syncthreads();
-        const int selected = static_cast<int>(s.selected_size);
-        // every element of those threads' chunks that is no worse; the row's first and last chunk are looked at in any case
+        const uint32_t bound = s.bound;
+        const int last = s.last;
         const float bound_value = bound <= key_of(-INFINITY) ? -INFINITY : value_of(bound);
+        // every element of a chunk that is no worse
         auto look = [&](int c, const uint4& w, auto&& f) {
             if (!(fmaxf(R::largest(w), -INFINITY) >= bound_value)) return;
             float v[R::kVec];
@@ -295,16 +345,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
                 if ((q > bound || (q == bound && c <= last)) && e >= 0 && e < p.vocab) f(entry_of(q, e));
             }
         };
-        auto each = [&](auto&& f) {
-            for (int i = warp; i < selected; i += kWarps)
-                for (int c = w0 + static_cast<int>(s.selected[i]) + lane * kThreads; c < w1; c += 32 * kThreads) look(c, __ldg(chunks + c), f);
-            if (tid == 0 && c0 < w0 && c0 < c1) look(c0, r.load(c0), f);
-            if (tid == 32 && w1 < c1 && w1 >= w0) look(w1, r.load(w1), f);
+        // the chunks of the threads `again`, and with `all` those of their largest logits too
+        auto each = [&](bool all, auto&& f) {
+            const int count = static_cast<int>(s.again_size);
+            for (int i = warp; i < count; i += kWarps) {
+                const int of = static_cast<int>(s.again[i]), seen = all ? -1 : s.at[of];
+                for (int c = w0 + of + lane * kThreads; c < w1; c += 32 * kThreads)
+                    if (c != seen) look(c, __ldg(chunks + c), f);
+                if (lane == 0 && of == 0 && c0 < w0 && c0 < c1 && c0 != seen) look(c0, r.load(c0), f);
+                if (lane == 0 && of == 1 && w1 < c1 && w1 >= w0 && w1 != seen) look(w1, r.load(w1), f);
+            }
         };
-        each([&](u64 entry) {
+        auto note = [&](u64 entry) {
             const uint32_t slot = atomicAdd(&s.list_size, 1u);
             if (slot < kList) s.list[slot] = entry;
-        });
+        };
+        const bool mine = key > bound || (key == bound && at <= last && at >= 0);
+        if (mine) {
+            if (other >= bound_value) s.again[atomicAdd(&s.again_size, 1u)] = tid;
+            look(at, r.load(at), note);
+        }
+        __syncthreads();
+        each(false, note);
         __syncthreads();
         const int found = static_cast<int>(s.list_size);
         if (found <= kList) {
@@ -315,11 +377,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
                 if (before < p.top) s.best[before] = mine;
             }
         } else {   // rising logits, and the like: one after the other
+            if (mine && !(other >= bound_value)) s.again[atomicAdd(&s.again_size, 1u)] = tid;
+            __syncthreads();
             u64 previous = ~0ull;
 #pragma unroll 1
             for (int k = 0; k < p.top; ++k) {
                 u64 best = 0;
-                each([&](u64 entry) { best = entry < previous && entry > best ? entry : best; });
+                each(true, [&](u64 entry) { best = entry < previous && entry > best ? entry : best; });
                 best = warp_max64(best);
                 if (lane == 0) s.warp_best[warp] = best;
                 __syncthreads();
@@ -385,16 +449,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
 
 template <class T, int THREADS>
 int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
-    if (ranks > 8) {
-        static std::atomic<u64> configured{0};   // one bit for each device
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
-        if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
-            const void* kernel = reinterpret_cast<const void*>(&qmm_logprobs_kernel<T, THREADS>);
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-                return QMM_ERR_CUDA;
-            if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
-        }
+    static std::atomic<u64> configured{0};   // one bit for each device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
+    if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
+        const void* kernel = reinterpret_cast<const void*>(&qmm_logprobs_kernel<T, THREADS>);
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, THREADS * kAhead * 16) != cudaSuccess)
+            return QMM_ERR_CUDA;
+        if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -405,6 +468,7 @@ int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M) * ranks);
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = THREADS * kAhead * 16;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -413,15 +477,15 @@ int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
 
 template <class T>
 int launch_rows(const LogprobsParams& p, int M, cudaStream_t stream) {
-    // Few rows: as many CTAs of 512 threads for each as fill the GPU, of 2048 logits at least. Many: CTAs of 256 threads, 6 an
-    // SM or more, so that one's steps behind the pass and the last rows' overhang cost little.
+    // Few rows: as many CTAs of 512 threads for each as fill the GPU, of 2048 logits at least. Many: smaller CTAs, so that one's
+    // steps behind the pass and the last rows' overhang cost little.
     int ranks = kRanks;
     if (static_cast<int64_t>(M) * 2 <= 2 * 152) {
         while (ranks > 1 && (M * ranks > 2 * 152 || p.vocab / ranks < 2048)) ranks /= 2;
         return launch<T, 512>(p, M, ranks, stream);
     }
-    while (ranks > 1 && (static_cast<int64_t>(M) * ranks > 12 * 152 || p.vocab / ranks < 8192)) ranks /= 2;
-    return launch<T, 256>(p, M, ranks, stream);
+    while (ranks > 1 && (static_cast<int64_t>(M) * ranks > kManyCtas || p.vocab / ranks < 8192)) ranks /= 2;
+    return launch<T, kManyThreads>(p, M, ranks, stream);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
