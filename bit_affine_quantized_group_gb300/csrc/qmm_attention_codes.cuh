@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
     constexpr int kGroups = D / 64;
     constexpr int kEach = D == 64 ? 8 : 16;        // neighbouring columns of a lane
     constexpr int kSets = D / (8 * kEach);         // sets of them
+    constexpr int kPairsAt = kStep * Cfg::kRowBytes;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* const full = reinterpret_cast<uint64_t*>(smem + Cfg::kBarsAt);
     uint64_t* const empty = full + Cfg::kTeams * Cfg::kSlots;
@@ -214,6 +215,22 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
     float* const units = reinterpret_cast<float*>(sums + kRows * kGroups * 8);
     float* const s_ml = reinterpret_cast<float*>(smem + Cfg::kMlAt);           // [warp][row][2]
     float* const s_total = reinterpret_cast<float*>(smem + Cfg::kTotalAt);     // [row][2]
+
+    // What a lane reads of a slot, of which all else lies at fixed distances: its chunks of the position gid of each group of
+    // keys, its columns of the position 2 quad of values, and their positions' scales and biases.
+    uint32_t key_at[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k)
+        key_at[k] = part * kPartRows * Cfg::kRowBytes +
+                    (BITS == 8 ? Cfg::key_place(gid, 4 * k + quad) : Cfg::key_place(gid, 2 * k + (quad >> 1)) + (quad & 1) * 8);
+    uint32_t value_at[kSets];
+#pragma unroll
+    for (int c = 0; c < kSets; ++c) {
+        const int byte = (c * 8 + gid) * kEach * BITS / 8;
+        value_at[c] = Cfg::kSideBytes + part * kPartRows * Cfg::kRowBytes + Cfg::value_place(2 * quad, byte >> 4) + (byte & 15);
+    }
+    const uint32_t key_pair_at = kPairsAt + (part * kPartRows + gid) * Cfg::kPairBytes;
+    const uint32_t value_pair_at = Cfg::kSideBytes + kPairsAt + (part * kPartRows + 2 * quad) * Cfg::kPairBytes + gid * kEach / 64 * 4;
 
     uint64_t* const my_full = full + team * Cfg::kSlots;
     uint64_t* const my_empty = empty + team * Cfg::kSlots;
@@ -347,8 +364,6 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sc[s][n][j] = 0.0f;
             const uint32_t side = slot_full();
-            const uint32_t kst = side + part * kPartRows * Cfg::kRowBytes, vst = kst + Cfg::kSideBytes;
-            const uint32_t k_pairs = side + kStep * Cfg::kRowBytes + part * kPartRows * Cfg::kPairBytes, v_pairs = k_pairs + Cfg::kSideBytes;
             // positions that every row sees need no mask
             const bool whole = pos0 + kPartRows <= min(first_pos + 1, p.positions) &&
                                (p.window == 0 || first_pos + p.rows - 1 - pos0 < p.window || pos0 + kPartRows <= p.sinks);
@@ -359,7 +374,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
             for (int c = 0; c < kPartRows * kGroups; c += 32) {
                 if (kPartRows * kGroups < 32 && lane >= kPartRows * kGroups) break;
-                const uint32_t pair = lds32(v_pairs + (c + lane) * 4);
+                const uint32_t pair = lds32(side + (Cfg::kSideBytes + kPairsAt + part * kPartRows * Cfg::kPairBytes) + (c + lane) * 4);
                 slow |= (pair & 0x7FFFu) > 0x5380u;   // 60
                 if (!whole && p.rows > 1) {
                     const float2 sb = __half22float2(half2_of(pair));
@@ -374,12 +389,12 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     uint32_t codes[2][BITS / 2];   // of positions gid and gid + 8
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t at = kst + s * 16 * Cfg::kRowBytes;
+                        const uint32_t at = side + key_at[k] + (s * 16 + h * 8) * Cfg::kRowBytes;
                         if constexpr (BITS == 8) {
-                            const uint4 v = lds128(at + Cfg::key_place(gid + 8 * h, 4 * k + quad));
+                            const uint4 v = lds128(at);
                             codes[h][0] = v.x, codes[h][1] = v.y, codes[h][2] = v.z, codes[h][3] = v.w;
                         } else {
-                            const uint2 v = lds64(at + Cfg::key_place(gid + 8 * h, 2 * k + (quad >> 1)) + (quad & 1) * 8);
+                            const uint2 v = lds64(at);
                             codes[h][0] = v.x, codes[h][1] = v.y;
                         }
                     }
@@ -409,7 +424,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                 for (int s = 0; s < kTiles; ++s)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float2 sb = __half22float2(half2_of(lds32(k_pairs + (s * 16 + h * 8 + gid) * Cfg::kPairBytes + k * 4)));
+                        const float2 sb = __half22float2(half2_of(lds32(side + key_pair_at + (s * 16 + h * 8) * Cfg::kPairBytes + k * 4)));
 #pragma unroll
                         for (int n = 0; n < ROWS8; ++n) {
                             float(&x)[4] = sc[s][n];
@@ -497,11 +512,10 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                 for (int c = 0; c < kSets; ++c) {
                     uint32_t codes[4][kWords];   // of positions 2 quad + {0, 1, 8, 9}
-                    const int byte = (c * 8 + gid) * kEach * BITS / 8;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int r = 2 * quad + (j & 1) + (j >> 1) * 8;
-                        const uint32_t at = vst + s * 16 * Cfg::kRowBytes + Cfg::value_place(r, byte >> 4) + (byte & 15);
+                        // (the odd positions of eight lie four rows behind the even ones)
+                        const uint32_t at = side + value_at[c] + (s * 16 + (j & 1) * 4 + (j >> 1) * 8) * Cfg::kRowBytes;
                         if constexpr (kWords == 4) {
                             const uint4 v = lds128(at);
                             codes[j][0] = v.x, codes[j][1] = v.y, codes[j][2] = v.z, codes[j][3] = v.w;
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                             codes[j][0] = lds32(at);
                         }
                     }
-                    const uint32_t at = v_pairs + (s * 16 + 2 * quad) * Cfg::kPairBytes + (c * 8 + gid) * kEach / 64 * 4;
+                    const uint32_t at = side + value_pair_at + s * 16 * Cfg::kPairBytes + c * kEach / 8 * 4;
                     const ValueTerms<BITS> t0(lds32(at), lds32(at + Cfg::kPairBytes), kSlow);
                     const ValueTerms<BITS> t1(lds32(at + 8 * Cfg::kPairBytes), lds32(at + 9 * Cfg::kPairBytes), kSlow);
                     if constexpr (!kSlow) {
