@@ -4,7 +4,10 @@
                    -> norm -> gate/up projection with SwiGLU -> down projection ] x layers
               -> norm -> output head -> sampling
 
-    python examples/decode_step.py [--sequences 8] [--steps 64]
+    python examples/decode_step.py [--sequences 8] [--steps 64] [--cache-bits 16|8|4] [--adapters N] [--top N]
+
+With --cache-bits 8 or 4 keys and values are held as codes; with --adapters each sequence has one of N low-rank adapters beside the
+q/k/v projections; with --top the log probabilities of the drawn tokens and of the N likeliest ones are computed too.
 
 A step has no host work that depends on its data (lengths, tokens and random numbers live on the device), so it is
 captured once in a CUDA graph and replayed. The cache pages of a sequence are handed out in advance.
@@ -55,7 +58,7 @@ def rms_norm(x):
 
 class Decoder:
     def __init__(self, sequences=8, layers=2, hidden=2048, q_heads=16, kv_heads=8, head_dim=128, ffn=4096, vocab=32000,
-                 max_len=512, page=16, window=0, sinks=0, seed=0):
+                 max_len=512, page=16, window=0, sinks=0, seed=0, cache_bits=16, adapters=0, rank=16, top=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         S, D = sequences, head_dim
         self.cut = (q_heads * D, kv_heads * D, kv_heads * D)
@@ -72,7 +75,12 @@ class Decoder:
         pages = -(-max_len // page)
         self.kv = qmm.KVPlan(q_heads, kv_heads, D, page, max_seqs=S, max_rows=1, max_pages=pages, window=window, sinks=sinks)
         pool = lambda: torch.zeros((S * pages, kv_heads, page, D), dtype=torch.bfloat16, device="cuda")  # noqa: E731
-        self.caches = [qmm.KVCache(pool(), pool()) for _ in range(layers)]
+        if cache_bits == 16:
+            self.caches = [qmm.KVCache(pool(), pool()) for _ in range(layers)]
+        else:
+            codes = lambda: torch.zeros((S * pages, kv_heads, page, D * cache_bits // 8), dtype=torch.uint8, device="cuda")  # noqa: E731
+            pairs = lambda: torch.zeros((S * pages, kv_heads, page, D // 64, 2), dtype=torch.float16, device="cuda")  # noqa: E731
+            self.caches = [qmm.QuantKVCache(codes(), codes(), pairs(), pairs(), cache_bits) for _ in range(layers)]
         self.page_table = torch.randperm(S * pages, generator=gen, device="cuda").int().view(S, pages)
         self.queries = torch.empty((S, q_heads * D), dtype=torch.bfloat16, device="cuda")
         self.attended = torch.empty_like(self.queries)
@@ -82,13 +90,30 @@ class Decoder:
         self.uniform = torch.rand((max_len, S), generator=gen, device="cuda")
         self.tokens, self.probs, self.lengths = f(1, torch.int32), f(0.0), f(0, torch.int32)
 
+        self.adapters = []   # (plan, A, B) of each layer's q/k/v projection
+        if adapters:
+            normal = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+            for _ in range(layers):
+                a, b = normal(adapters, rank, hidden) * hidden ** -0.5, normal(adapters, sum(self.cut), rank) * rank ** -0.5
+                self.adapters.append((qmm.AdapterPlan(hidden, sum(self.cut), rank, adapters, S), a.to(torch.bfloat16), b.to(torch.bfloat16)))
+            self.adapter_scale = torch.full((adapters,), 0.5, device="cuda")
+            self.adapter_ids = torch.arange(S, device="cuda").int() % (adapters + 1) - 1   # -1: a sequence without one
+        self.scores = None   # log probabilities of the drawn tokens, entropy, likeliest tokens and their log probabilities
+        if top:
+            self.scores = f(0.0), f(0.0), torch.zeros((S, top), dtype=torch.int32, device="cuda"), torch.zeros((S, top), device="cuda")
+
     def step(self):
         """Appends every sequence's last token to its cache and draws its next."""
         u = self.uniform.index_select(0, self.lengths[:1].long()).view(-1)
         self.lengths += 1
         x = self.embedding[self.tokens.long()].float()
-        for qkv, out, up, down, cache in zip(self.qkv, self.out, self.up, self.down, self.caches):
-            q, k, v = qkv(rms_norm(x)).split(self.cut, 1)
+        for i, (qkv, out, up, down, cache) in enumerate(zip(self.qkv, self.out, self.up, self.down, self.caches)):
+            h = rms_norm(x)
+            qkv_out = qkv(h)
+            if self.adapters:
+                plan, a, b = self.adapters[i]
+                qmm.add_adapters(plan, h, a, b, self.adapter_scale, self.adapter_ids, qkv_out, qkv_out)
+            q, k, v = qkv_out.split(self.cut, 1)
             qmm.qk_norm_rope(self.kv, q, k, v, self.q_weight, self.k_weight, self.rope, self.lengths, self.page_table,
                              cache, self.queries)
             qmm.attention(self.kv, self.queries, cache, self.page_table, self.lengths, self.attended)
@@ -96,6 +121,8 @@ class Decoder:
             x = x + down(up.swiglu(rms_norm(x))).float()
         logits = self.head(rms_norm(x))
         qmm.sample(logits, self.temperature, self.top_k, self.top_p, self.min_p, u, self.tokens, self.probs)
+        if self.scores is not None:
+            qmm.logprobs(logits, self.tokens, *self.scores)
 
     def restart(self):
         self.lengths.zero_()
@@ -123,7 +150,9 @@ class Decoder:
             stream.synchronize()
             seconds = time.perf_counter() - t
         if self.kv.error_flags() != 0:
-            raise RuntimeError("a cache operator met a bad page, length or position")
+            raise RuntimeError("a cache operator met a bad page, length or position, or a value that is not finite")
+        if any(plan.error_flags() for plan, _, _ in self.adapters):
+            raise RuntimeError("a row names an adapter that is not there")
         return drawn, seconds
 
 
@@ -131,11 +160,17 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--sequences", type=int, default=8)
     ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--cache-bits", type=int, default=16, choices=(16, 8, 4))
+    ap.add_argument("--adapters", type=int, default=0)
+    ap.add_argument("--top", type=int, default=0)
     a = ap.parse_args()
-    decoder = Decoder(sequences=a.sequences, max_len=max(512, a.steps + 1))
+    decoder = Decoder(sequences=a.sequences, max_len=max(512, a.steps + 1), cache_bits=a.cache_bits, adapters=a.adapters, top=a.top)
     tokens, seconds = decoder.generate(a.steps)
     print(f"{a.sequences} sequences, {a.steps} steps: {seconds / a.steps * 1e6:.1f} us a step")
     print("first sequence:", tokens[:16, 0].tolist())
+    if decoder.scores is not None:
+        print("its last token: log probability %.3f, entropy %.3f, likeliest %s" % (
+            float(decoder.scores[0][0]), float(decoder.scores[1][0]), decoder.scores[2][0].tolist()))
 
 
 if __name__ == "__main__":
