@@ -50,6 +50,9 @@ constexpr int kTile = 16;             // rows of a product
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlices = 16;           // of K at most: the CTAs of a cluster
+// Clusters of 16 CTAs that run at once; more of them wait. (64 rows of rank 64: 5.5 us with clusters of 8, 8.5 with 16 of 16;
+// 16 rows of rank 16, which need two: 5.2 and 4.2.)
+constexpr int kWideClusters = 8;
 constexpr int kStep = 32;             // elements that two products sum over
 constexpr int kAhead = 5;             // steps of K that a warp loads at once
 constexpr size_t kErrBytes = 256;
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
     // (slices is a power of two)
     extern __shared__ __align__(16) float s_part[];
     __shared__ __align__(16) Tiles t;
+    __shared__ float s_scale[kBlock];   // of the tiles
     cg::cluster_group cluster = cg::this_cluster();
     const int slice = static_cast<int>(blockIdx.x % slices), of = static_cast<int>(blockIdx.x / slices);
     const int group = of % groups, row0 = of / groups * kBlock;
@@ -183,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
     griddep_wait();
     griddep_launch_dependents();   // not before: the second kernel reads what came before this one without waiting
     find_tiles(p, row0, t);
+    float scale = 1.0f;   // (on its way while the products run)
+    if (p.scale != nullptr && threadIdx.x < t.tiles && t.tile_id[threadIdx.x] >= 0) scale = __ldg(p.scale + t.tile_id[threadIdx.x]);
     cluster_wait();
     const int columns = (p.rank + 15) / 16, units = t.tiles * columns;
     const int steps = static_cast<int>(p.K / kStep);
@@ -230,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
             if (two) *reinterpret_cast<float2*>(to + 8) = make_float2(acc[1][2 * h], acc[1][2 * h + 1]);
         }
     }
+    if (threadIdx.x < kBlock) s_scale[threadIdx.x] = scale;
     cluster_arrive();
     cluster_wait();
     // a place for each warp, two columns for each lane, of the units of this group
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
     for (int place = slice + warp * slices; place < rows; place += kWarps * slices) {
         const int tile = t.tile[place], id = t.tile_id[tile];
         if (id < 0) continue;
-        const float by = p.scale != nullptr ? p.scale[id] : 1.0f;
+        const float by = s_scale[tile];
         const int64_t at = static_cast<int64_t>(row0 + t.row[place]) * p.rank;
         for (int c = 2 * lane; c < p.rank; c += 64) {
             if ((tile * columns + c / 16) % groups != group) continue;
@@ -390,8 +397,7 @@ cudaError_t launch_low(const AdapterParams& p, int num_sms, cudaStream_t stream)
     // two CTAs an SM; units of a block: one for each 16 columns of rank of up to as many tiles as it has rows
     const int64_t units = static_cast<int64_t>(p.rows < kBlock ? p.rows : kBlock) * ((p.rank + 15) / 16);
     const int64_t most = (units + kWarps - 1) / kWarps;
-    // (clusters of 16 leave SMs of their part of the GPU without work where there are many: 64 rows of rank 64 took 8.7 us)
-    int slices = blocks * most * kSlices <= num_sms ? kSlices : kSlices / 2;
+    int slices = blocks * most <= kWideClusters ? kSlices : kSlices / 2;
     while (slices > 1 && (slices > steps || slices * blocks > 2 * num_sms)) slices /= 2;
     int64_t groups = 2 * num_sms / (blocks * slices);
     groups = groups < 1 ? 1 : groups > most ? most : groups;

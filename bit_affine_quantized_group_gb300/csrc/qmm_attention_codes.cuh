@@ -108,8 +108,8 @@ __device__ __forceinline__ void key_fragment(const uint32_t (&codes)[BITS / 2], 
         second = __byte_perm(codes[w], 0x64646464u, 0x4342);
     } else {
         const uint32_t x = w & 1 ? codes[w >> 1] >> 8 : codes[w >> 1];
-        first = (x & 0x000F000Fu) | kHalf1024;
-        second = (x & 0x00F000F0u) | kHalf64;
+        first = and_or(x, 0x000F000Fu, kHalf1024);
+        second = and_or(x, 0x00F000F0u, kHalf64);
     }
 }
 
@@ -153,10 +153,10 @@ __device__ __forceinline__ void value_pairs(uint32_t first, uint32_t second, int
         h[3] = half2_of(__byte_perm(y, 0x64646464u, 0x4342));
     } else {
         const uint32_t x = __byte_perm(first, second, quarter == 0 ? 0x5410 : 0x7632), y = x >> 8;
-        h[0] = half2_of((x & 0x000F000Fu) | kHalf1024);
-        h[1] = half2_of((x & 0x00F000F0u) | kHalf64);
-        h[2] = half2_of((y & 0x000F000Fu) | kHalf1024);
-        h[3] = half2_of((y & 0x00F000F0u) | kHalf64);
+        h[0] = half2_of(and_or(x, 0x000F000Fu, kHalf1024));
+        h[1] = half2_of(and_or(x, 0x00F000F0u, kHalf64));
+        h[2] = half2_of(and_or(y, 0x000F000Fu, kHalf1024));
+        h[3] = half2_of(and_or(y, 0x00F000F0u, kHalf64));
     }
     if (centred) {
 #pragma unroll

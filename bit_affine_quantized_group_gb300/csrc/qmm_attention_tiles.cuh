@@ -137,10 +137,10 @@ __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
             } else {
                 const uint32_t x = w[u], y = x >> 8;
                 const __half2 low = half2_of(kHalf1032), high = half2_of(kHalf72);
-                const uint32_t e0 = bits_of(__hsub2(half2_of((x & 0x000F000Fu) | 0x64006400u), low));    // 0, 4
-                const uint32_t e1 = bits_of(__hsub2(half2_of((x & 0x00F000F0u) | 0x54005400u), high));   // 1, 5
-                const uint32_t e2 = bits_of(__hsub2(half2_of((y & 0x000F000Fu) | 0x64006400u), low));    // 2, 6
-                const uint32_t e3 = bits_of(__hsub2(half2_of((y & 0x00F000F0u) | 0x54005400u), high));   // 3, 7
+                const uint32_t e0 = bits_of(__hsub2(half2_of(and_or(x, 0x000F000Fu, 0x64006400u)), low));    // 0, 4
+                const uint32_t e1 = bits_of(__hsub2(half2_of(and_or(x, 0x00F000F0u, 0x54005400u)), high));   // 1, 5
+                const uint32_t e2 = bits_of(__hsub2(half2_of(and_or(y, 0x000F000Fu, 0x64006400u)), low));    // 2, 6
+                const uint32_t e3 = bits_of(__hsub2(half2_of(and_or(y, 0x00F000F0u, 0x54005400u)), high));   // 3, 7
                 h[0] = half2_of(__byte_perm(e0, e1, 0x5410)), h[1] = half2_of(__byte_perm(e2, e3, 0x5410));
                 h[2] = half2_of(__byte_perm(e0, e1, 0x7632)), h[3] = half2_of(__byte_perm(e2, e3, 0x7632));
             }

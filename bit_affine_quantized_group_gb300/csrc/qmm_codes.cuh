@@ -16,6 +16,13 @@ __device__ __forceinline__ uint32_t bits_of(__half2 v) { return *reinterpret_cas
 __device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return bits_of(__floats2half2_rn(a, b)); }
 
+// (x & mask) | bits in one instruction (of two constants the compiler makes two).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
+}
+
 // The larger magnitude of a pair of bfloat16 numbers, as an integer.
 __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
 
