@@ -30,7 +30,7 @@ constexpr int kRanks = 16;             // CTAs of a row at most
 // Chunks that a thread has on their way. Of 512 rows at once the pass is bound by how many bytes are: four in registers came to
 // 3.4 TB/s, and more left no room for the CTAs.
 constexpr int kAhead = 5;
-constexpr int kSome = 16;              // threads that may be looked at beyond the needed ones
+constexpr int kSome = 8;               // threads that may be looked at beyond the needed ones
 constexpr int kManyThreads = 256, kManyCtas = 4 * 152;   // of a CTA and at once, where rows are many
 constexpr float kRise = 16.0f;         // that logits may lie above a thread's reference before its sums are brought to a new one
 constexpr float kLeast = -1000.0f;     // differences are brought to it: e^-1000 is 0, and no infinity meets a 0
@@ -285,18 +285,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
         // a bound that the largest logits of p.top threads reach, and of few more: (bound, last). By one warp, for it costs the
         // same time and less of the other rows'.
         if (warp == 0) {
-            uint32_t keys[kWarps], low_key = 0xFFFFFFFFu, high_key = 0;
+            // (the largest of every few threads do: p.top of them are p.top threads)
+            constexpr int kKeys = 4, kOf = kWarps / kKeys;
+            uint32_t keys[kKeys], low_key = 0xFFFFFFFFu, high_key = 0;
             int count = 0;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                keys[i] = s.keys[i * 32 + lane];
+            for (int i = 0; i < kKeys; ++i) {
+                keys[i] = 0;
+#pragma unroll
+                for (int j = 0; j < kOf; ++j) keys[i] = max(keys[i], s.keys[(i * kOf + j) * 32 + lane]);
                 if (keys[i] != 0) low_key = min(low_key, keys[i]);
                 high_key = max(high_key, keys[i]);
                 count += keys[i] != 0;
             }
             low_key = __reduce_min_sync(0xFFFFFFFFu, low_key);
             high_key = __reduce_max_sync(0xFFFFFFFFu, high_key);
-            int reach = __reduce_add_sync(0xFFFFFFFFu, count);   // threads with key >= bound
+            int reach = __reduce_add_sync(0xFFFFFFFFu, count);   // of them with key >= bound
             uint32_t bound = 0;
             int last = 0x7FFFFFFF;
             if (reach > p.top + kSome) {
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
                 for (uint32_t bit = differ == 0 ? 0u : 0x80000000u >> __clz(differ); bit != 0 && reach > p.top + kSome; bit >>= 1) {
                     int n = 0;
 #pragma unroll
-                    for (int i = 0; i < kWarps; ++i) n += keys[i] >= (bound | bit);
+                    for (int i = 0; i < kKeys; ++i) n += keys[i] >= (bound | bit);
                     n = __reduce_add_sync(0xFFFFFFFFu, n);
                     if (n >= p.top) bound |= bit, reach = n;
                 }
@@ -363,11 +367,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
         const bool mine = key > bound || (key == bound && at <= last && at >= 0);
         if (mine) {
             if (other >= bound_value) s.again[atomicAdd(&s.again_size, 1u)] = tid;
-            look(at, r.load(at), note);
+            // (of short shares it is still where it was copied to)
+            const bool held = w1 - w0 <= kAhead * kThreads && at >= w0 && at < w1;
+            look(at, held ? s_ring[at - w0] : r.load(at), note);
         }
         __syncthreads();
-        each(false, note);
-        __syncthreads();
+        if (s.again_size != 0) {
+            each(false, note);
+            __syncthreads();
+        }
         const int found = static_cast<int>(s.list_size);
         if (found <= kList) {
             for (int i = tid; i < found; i += kThreads) {
@@ -377,6 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
                 if (before < p.top) s.best[before] = mine;
             }
         } else {   // rising logits, and the like: one after the other
+            __syncthreads();   // every thread has seen how many are to be looked at again
             if (mine && !(other >= bound_value)) s.again[atomicAdd(&s.again_size, 1u)] = tid;
             __syncthreads();
             u64 previous = ~0ull;
