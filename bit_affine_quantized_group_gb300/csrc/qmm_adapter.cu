@@ -298,8 +298,9 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
         for (int h = 0; h < 2; ++h) {
             in[h] = gid + 8 * h < size;
             const int64_t row = row0 + (in[h] ? t.row[first + gid + 8 * h] : 0);
-            y[h] = static_cast<const T*>(p.y) + row * p.y_stride;
-            out[h] = static_cast<T*>(p.out) + row * p.out_stride;
+            // of the lane's first column of the unit
+            y[h] = static_cast<const T*>(p.y) + row * p.y_stride + static_cast<int64_t>(column) * 32 + quad * 8;
+            out[h] = static_cast<T*>(p.out) + row * p.out_stride + static_cast<int64_t>(column) * 32 + quad * 8;
             low[h] = p.low + row * p.rank + quad * 8;
         }
         // the columns of a unit: 8 (gid / 2) + 2 j + gid % 2 for the product j, so that a lane gets the 8 from 8 quad on
@@ -309,24 +310,31 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
         bool in_rank[STEPS];   // this lane's elements are there
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) in_rank[k] = id >= 0 && k * 32 + quad * 8 < p.rank;
+        const bool all_rank = id >= 0 && p.rank == 32 * STEPS;
         uint4 l[kKeep ? STEPS : 1][kTerms][2];
         bool loaded = false;
 #pragma unroll 1
-        for (; column < end; ++column, b += 16 * b_next) {
-            const int64_t n0 = static_cast<int64_t>(column) * 32, n = n0 + quad * 8;
-            const bool full = n0 + 32 <= p.N, whole = WIDE && n + 8 <= p.N;
+        for (; column < end; ++column, b += 16 * b_next, y[0] += 32, y[1] += 32, out[0] += 32, out[1] += 32) {
+            const int left = static_cast<int>(min(p.N - static_cast<int64_t>(column) * 32, static_cast<int64_t>(32)));   // columns
+            const bool whole = WIDE && quad * 8 + 8 <= left;
             // y and B of the unit (with the next one's on their way too, and so one CTA less an SM, 2048 rows took a fifth longer)
             uint4 wy[2][F32 ? 2 : 1], wb[STEPS][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int k = 0; k < (F32 ? 2 : 1); ++k)
-                    if (in[h] && whole) wy[h][k] = *reinterpret_cast<const uint4*>(y[h] + n + 4 * k);
+                    if (in[h] && whole) wy[h][k] = *reinterpret_cast<const uint4*>(y[h] + 4 * k);
+            if (all_rank && left == 32) {
 #pragma unroll
-            for (int k = 0; k < STEPS; ++k)
+                for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    wb[k][j] = load16(b + j * b_next + k * 32, in_rank[k] && (full || n0 + own + 2 * j < p.N));
+                    for (int j = 0; j < 4; ++j) wb[k][j] = __ldg(reinterpret_cast<const uint4*>(b + j * b_next + k * 32));
+            } else {
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) wb[k][j] = load16(b + j * b_next + k * 32, in_rank[k] && own + 2 * j < left);
+            }
             if (!waited) {
                 griddep_wait();
                 waited = true;
@@ -337,8 +345,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         to[i][h] = make_uint4(0u, 0u, 0u, 0u);
-                        if (in[h] && in_rank[k])
-                            to[i][h] = __ldcg(reinterpret_cast<const uint4*>(low[h] + i * p.low_term + k * 32));
+                        if (in[h] && in_rank[k]) to[i][h] = __ldcg(reinterpret_cast<const uint4*>(low[h] + i * p.low_term + k * 32));
                     }
             };
             float acc[4][4] = {};
@@ -360,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const uint4& v = wy[h][k];
-                            *reinterpret_cast<float4*>(out[h] + n + 4 * k) = make_float4(
+                            *reinterpret_cast<float4*>(out[h] + 4 * k) = make_float4(
                                 __uint_as_float(v.x) + acc[2 * k][2 * h], __uint_as_float(v.y) + acc[2 * k][2 * h + 1],
                                 __uint_as_float(v.z) + acc[2 * k + 1][2 * h], __uint_as_float(v.w) + acc[2 * k + 1][2 * h + 1]);
                         }
@@ -371,17 +378,17 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
                         for (int j = 0; j < 4; ++j)
                             r[j] = pack_bf16(__uint_as_float(w[j] << 16) + acc[j][2 * h],
                                              __uint_as_float(w[j] & 0xFFFF0000u) + acc[j][2 * h + 1]);
-                        *reinterpret_cast<uint4*>(out[h] + n) = make_uint4(r[0], r[1], r[2], r[3]);
+                        *reinterpret_cast<uint4*>(out[h]) = make_uint4(r[0], r[1], r[2], r[3]);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        if (n + j >= p.N) break;
+                        if (quad * 8 + j >= left) break;
                         const float add = acc[j >> 1][2 * h + (j & 1)];
-                        if constexpr (F32) out[h][n + j] = y[h][n + j] + add;
+                        if constexpr (F32) out[h][j] = y[h][j] + add;
                         else
-                            out[h][n + j] = static_cast<uint16_t>(
-                                pack_bf16(__uint_as_float(static_cast<uint32_t>(y[h][n + j]) << 16) + add, 0.0f));
+                            out[h][j] = static_cast<uint16_t>(
+                                pack_bf16(__uint_as_float(static_cast<uint32_t>(y[h][j]) << 16) + add, 0.0f));
                     }
                 }
             }
