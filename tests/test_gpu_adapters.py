@@ -206,6 +206,51 @@ def test_beside_a_projection_in_a_graph(q):
                 now.check(out)
 
 
+def test_two_threads_share_a_plan(q):
+    """Host threads that launch on one stream: no call's two kernels have another's between them."""
+    import threading
+
+    import torch
+    a = Case(q, 40, 256, 128, 16, 6, "bfloat16", seed=1)
+    b = Case(q, 33, 256, 128, 16, 6, "bfloat16", seed=2, plan=a.plan)
+    want = [c.run() for c in (a, b)]
+    stream = torch.cuda.Stream()
+    work = [(c.tensors(), c.y.to(DEV), [torch.empty_like(w) for _ in range(50)]) for c, w in zip((a, b), want)]
+    torch.cuda.synchronize()
+
+    def launch(t, y, outs):
+        for out in outs:
+            q.add_adapters(a.plan, *t, y, out, stream=stream)
+
+    threads = [threading.Thread(target=launch, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w, (_, _, outs) in zip(want, work):
+        assert all(torch.equal(out, w) for out in outs)
+
+
+def test_y_is_the_kernel_before_and_out_the_one_after(q):
+    """y, x and ids written just before the call on the stream, out read just after, many times in a row."""
+    import torch
+    c = Case(q, 50, 512, 300, 32, 5, "bfloat16")
+    x, a, b, scale, ids = c.tensors()
+    want = c.run()
+    xs, ys, idss, out, seen = torch.zeros_like(x), torch.zeros_like(c.y.to(DEV)), torch.full_like(ids, -1), c.y.to(DEV), []
+    y = c.y.to(DEV)
+    for i in range(30):
+        for t in (xs, ys, idss):
+            t.fill_(0)
+        xs.copy_(x)
+        idss.copy_(ids)
+        ys.copy_(y)
+        q.add_adapters(c.plan, xs, a, b, scale, idss, ys, ys if i % 2 else out)
+        seen.append((ys if i % 2 else out).clone())
+    assert all(torch.equal(s, want) for s in seen)
+
+
 def test_far_into_large_tensors(q):
     """Adapters that lie past 2^32 bytes."""
     import torch

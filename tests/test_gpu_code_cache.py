@@ -317,11 +317,11 @@ def _reference(qs, pool, lengths, rows, window, sinks, scale):
 
 
 def _attend(q, lengths, hq, hkv, d, bits, rows=1, page=16, window=0, sinks=0, seed=0, layout="hnd", scale=None, q_size=1.5,
-            max_rows=None, change=None, told=None):
+            max_rows=None, change=None, told=None, size=1.0, extra=1):
     import torch
     from tests._codes import Pool
     gen = torch.Generator().manual_seed(seed)
-    pool = Pool(lengths, hkv, page, d, bits, gen, layout)
+    pool = Pool(lengths, hkv, page, d, bits, gen, layout, size=size, extra=extra)
     if change:
         change(pool)
     cache, table = pool.device(q)
@@ -369,7 +369,8 @@ def test_heads_and_rows(q, bits, hq, hkv, rows, d, lengths):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 4), (17, 1), (100, 33), (500, 16), (10000, 4), (128, 10000)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 4), (17, 1), (100, 33), (500, 16), (10000, 4), (128, 10000),
+                                          (2 ** 31 - 1, 2 ** 31 - 1)])
 @pytest.mark.parametrize("rows,d", [(1, 128), (5, 64), (16, 128), (3, 256)])
 def test_window_and_sinks(q, bits, window, sinks, rows, d):
     _fits(*_attend(q, [700, 5, 101, 0, 116], 4, 2, d, bits, rows=rows, window=window, sinks=sinks, seed=window % 1000 + sinks)[:4])
@@ -400,6 +401,74 @@ def test_many_sequences(q, bits):
 @pytest.mark.parametrize("scale,q_size", [(-0.1, 1.0), (0.0, 1.0), (0.5, 1e-3), (1e-6, 1e6), (1e-33, 1e33), (1e30, 1e-31), (0.09, 0.0)])
 def test_scales_and_sizes_of_queries(q, bits, scale, q_size):
     _fits(*_attend(q, [130, 30], 4, 1, 128, bits, rows=2, scale=scale, q_size=q_size, seed=4)[:4])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,rows", [(64, 1), (128, 1), (128, 3), (256, 2), (128, 9)])
+@pytest.mark.parametrize("size", [1e-6, 1e-3, 300.0, 15000.0])
+def test_sizes_of_keys_and_values(q, bits, d, rows, size):
+    """Scales that are no normal binary16 numbers, and scales whose multiples leave binary16. The scores stay small: their
+    tolerance grows with what is summed."""
+    got, want, tol, flags, (pool, *_) = _attend(q, [150, 70], 4, 1, d, bits, rows=rows, q_size=1.0 / size, size=size, seed=d + rows)
+    if size < 1e-3:   # values are multiples of 2^-24, and so held in binary16, but the weights' products round as ever
+        tol = tol + 2.0 ** -24
+        assert flags == 0 and (np.abs(got - want) <= tol).all()
+    else:
+        _fits(got, want, tol, flags)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("rows,window,told", [(1, 0, 100), (3, 0, 98), (3, 20, 100), (2, 0, 5000)])
+def test_lengths_past_the_page_table(q, bits, rows, window, told):
+    """Rows stand where the length says; what is past the table is not seen."""
+    from tests._codes import values
+    n, d, hq = 96, 128, 4
+    got, _, _, flags, (pool, qt, *_) = _attend(q, [n], hq, 1, d, bits, rows=rows, window=window, told=[told], extra=0)
+    assert flags == q.KV_BAD_LENGTH
+    k, v = (values(c, a).numpy()[:, 0] for c, a in pool.parts[0])
+    x = qt.double().numpy()
+    for r in range(rows):
+        pos = told - rows + r
+        j = np.arange(n)
+        j = j[(j <= pos) & ((pos - j < window) if window else True)]
+        for h in range(hq):
+            if not len(j):
+                assert (got[r, h] == 0).all()
+                continue
+            a = k[j] @ x[r, h] * d ** -0.5
+            e = np.exp(a - a.max())
+            want = e / e.sum() @ v[j]
+            size = np.abs(x[r, h]).sum() * 1279 * d ** -0.5 * float(pool.parts[0][0][1][..., 0].max())
+            assert (np.abs(got[r, h] - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + 2.0 ** -17 * size) * np.abs(v).max()).all()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_two_threads_share_a_plan(q, bits):
+    """Host threads that launch attention of many rows, whose joins are launches of their own, on one stream."""
+    import threading
+
+    import torch
+    runs = [_attend(q, [9000], 8, 1, 128, bits, rows=4, seed=s)[4] for s in (1, 2)]
+    want = [out.clone() for *_, out in runs]
+    plan = q.KVPlan(8, 1, 128, 16, max_seqs=1, max_rows=4, max_pages=runs[0][0].max_pages)
+    stream = torch.cuda.Stream()
+    outs = [[torch.empty_like(want[i]) for _ in range(20)] for i in range(2)]
+    args = [(qt.to(DEV), pool.cache, pool.table.cuda(), _int32([9000])) for pool, qt, *_ in runs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        x, cache, table, lens = args[i]
+        for out in outs[i]:
+            q.attention(plan, x, cache, table, lens, out, stream=stream)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(out, want[i]) for out in outs[i])
 
 
 @pytest.mark.parametrize("bits", [8, 4])
