@@ -462,22 +462,24 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     for (int s = 0; s < kTiles; ++s) top = fmaxf(top, fmaxf(sc[s][n][j], sc[s][n][2 + j]));
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    // a unit is above 0, so that it keeps the order
-                    const float m_new = fmaxf(m[n][j], top == -INFINITY ? top : top * unit[n][j]);
+                    // The maximum is one of scores before their unit, which is above 0 and keeps the order: a difference to it
+                    // is exact to a rounding of its own, so that no weight passes 2^15, and becomes an infinity, however large
+                    // the scores.
+                    const float m_new = fmaxf(m[n][j], top);
                     const float ref = m_new == -INFINITY ? 0.0f : m_new;
-                    alpha[n][j] = m_new == m[n][j] ? 1.0f : exp2_approx(m[n][j] - ref);
+                    alpha[n][j] = m_new == m[n][j] ? 1.0f : exp2_approx((m[n][j] - ref) * unit[n][j]);
                     same &= m_new == m[n][j];
                     m[n][j] = m_new;
-                    const float less = kWeightBits - ref;
                     float sum = 0.0f;
 #pragma unroll
-                    for (int s = 0; s < kTiles; ++s)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float& x = sc[s][n][2 * h + j];
-                            x = exp2_approx(fmaf(x, unit[n][j], less));
-                            sum += x;
-                        }
+                    for (int s = 0; s < kTiles; ++s) {
+                        float &x = sc[s][n][j], &y = sc[s][n][2 + j];
+                        add_x2(x, y, x, y, -ref, -ref);
+                        fma_x2(x, y, x, y, unit[n][j], unit[n][j], kWeightBits, kWeightBits);
+                        x = exp2_approx(x), y = exp2_approx(y);
+                        sum += x;
+                        sum += y;
+                    }
                     l[n][j] = fmaf(l[n][j], alpha[n][j], sum);
                 }
             slow = __any_sync(0xFFFFFFFFu, slow);
@@ -583,6 +585,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float sum = l[n][j];
+                m[n][j] *= unit[n][j];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
                 if (gid == 0) *reinterpret_cast<float2*>(s_ml + (warp * kRows + n * 8 + quad * 2 + j) * 2) = make_float2(m[n][j], sum);

@@ -425,18 +425,19 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                // scale_log2 is not negative (the queries take its sign), so that it keeps the order
-                const float m_new = fmaxf(m[h], top == -INFINITY ? top : top * unit[h]);
+                // scale_log2 is not negative (the queries take its sign), so that it keeps the order. Of codes the maximum is one
+                // of scores before their unit: no weight passes 2^15 then, however large the scores.
+                const float m_new = fmaxf(m[h], BITS != 16 || top == -INFINITY ? top : top * unit[h]);
                 const float ref = m_new == -INFINITY ? 0.0f : m_new;
-                alpha[h] = m_new == m[h] ? 1.0f : exp2_approx(m[h] - ref);
+                alpha[h] = m_new == m[h] ? 1.0f : exp2_approx(BITS == 16 ? m[h] - ref : (m[h] - ref) * unit[h]);
                 m[h] = m_new;
-                const float less = BITS == 16 ? -ref : kWeightBits - ref;
                 float sum = 0.0f;
 #pragma unroll
                 for (int s = 0; s < kTiles; ++s) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        pr[s][h][j] = exp2_approx(fmaf(pr[s][h][j], unit[h], less));
+                        const float x = pr[s][h][j];
+                        pr[s][h][j] = exp2_approx(BITS == 16 ? fmaf(x, unit[h], -ref) : fmaf(x - ref, unit[h], kWeightBits));
                         sum += pr[s][h][j];
                     }
                 }
@@ -566,6 +567,7 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             sum[h] = l[h];
+            if constexpr (BITS != 16) m[h] *= unit[h];
             sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 1);
             sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 2);
             if (kGroups > 1 && quad == 0)

@@ -404,6 +404,31 @@ def test_scales_and_sizes_of_queries(q, bits, scale, q_size):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,rows", [(64, 1), (128, 3), (256, 2), (128, 9)])
+@pytest.mark.parametrize("q_size", [1e7, 3e7, 1e8, 1e10])
+def test_scores_whose_steps_are_larger_than_one(q, bits, d, rows, q_size):
+    """Scores of 1e7 to 1e11, whose roundings are larger than the exponents of weights. No output leaves the values' range, and a
+    row takes the value of its best key where that leads the others by more than the scores' error."""
+    from tests._codes import values
+    got, want, tol, flags, (pool, qt, *_) = _attend(q, [200, 70], 4, 1, d, bits, rows=rows, q_size=q_size, seed=d + rows)
+    assert flags == 0 and np.isfinite(got).all()
+    x, led = qt.double().numpy(), 0
+    for s, n in enumerate((200, 70)):
+        k, v = (values(c, a).numpy()[:, 0] for c, a in pool.parts[s])
+        step = float(pool.parts[s][0][1][..., 0].max())
+        most = np.abs(v).max()
+        assert (np.abs(got[s * rows:(s + 1) * rows]) <= most * (1 + 2.0 ** -7)).all()
+        for r in range(s * rows, (s + 1) * rows):
+            for h in range(4):
+                scores = np.sort((k[:n - rows + 1 + r - s * rows] @ x[r, h]) * d ** -0.5)
+                error = 2.0 ** -17 * 1279 * step * np.abs(x[r, h]).sum() * d ** -0.5   # of a score
+                if scores[-1] - scores[-2] > 2 * error + 40:   # e^-40 of 200 keys is nothing
+                    led += 1
+                    assert (np.abs(got[r, h] - want[r, h]) <= 2.0 ** -8 * np.abs(want[r, h]) + 2.0 ** -10 * most).all()
+    assert led >= 1
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("d,rows", [(64, 1), (128, 1), (128, 3), (256, 2), (128, 9)])
 @pytest.mark.parametrize("size", [1e-6, 1e-3, 300.0, 15000.0])
 def test_sizes_of_keys_and_values(q, bits, d, rows, size):
