@@ -579,9 +579,9 @@ def _check_step(plan, cache, page_table, lengths, tokens, *others):
 def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_table, cache, out, positions=None,
                  stream=None) -> None:
     """Norms of q and k for each head, rotation, and the append of k and v to the cache (qmm_qk_norm_rope, or
-    qmm_kvq_qk_norm_rope for a QuantKVCache, which quantises them). q, k, v:
-    [tokens, heads * head_dim] of float32 or bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and
-    k_weight: float32 [head_dim] or None; rope: float32 [positions, rot_dim], cosines then sines."""
+    qmm_kvq_qk_norm_rope for a QuantKVCache, which quantises them). q, k, v: [tokens, heads * head_dim] of float32 or
+    bfloat16, rows of any stride; out: the queries, bfloat16. q_weight and k_weight: float32 [head_dim] or None; rope:
+    float32 [positions, rot_dim], cosines then sines."""
     dtype, tokens = q.dtype, q.shape[0]
     seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, q, k, v, out, q_weight, k_weight, rope, positions)
     if dtype is not _F32 and dtype is not _BF16:
@@ -609,8 +609,9 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
 
 
 def attention(plan: KVPlan, q, cache, page_table, lengths, out, stream=None) -> None:
-    """Attention of the new tokens over the cache (qmm_attention, or qmm_kvq_attention for a QuantKVCache): q and out [tokens, q_heads, head_dim] bfloat16 (or
-    [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows for each sequence."""
+    """Attention of the new tokens over the cache (qmm_attention, or qmm_kvq_attention for a QuantKVCache): q and out
+    [tokens, q_heads, head_dim] bfloat16 (or [tokens, q_heads * head_dim]), tokens = seqs * rows with 1 to max_rows rows
+    for each sequence."""
     tokens = q.shape[0]
     seqs, rows = _check_step(plan, cache, page_table, lengths, tokens, q, out)
     args = _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),

@@ -15,6 +15,14 @@
 //     read while the first kernel still runs.
 // In both a lane of a quad has 8 neighbouring elements of the 32 that two
 // products sum over, so that loads are whole 16-byte vectors of whole sectors.
+// K 4096, N 6144, a row for each of 16 adapters of rank 16: 7.0 us, of which 4.2
+// are the first kernel and 2.2 a launch. 64 rows of 16 adapters of rank 64, K
+// 5120, N 17408, float32: 19.1 us. 2048 rows, rank 32, K 5120, N 6144: 22.9 us
+// (3.2 TB/s), 11.3 of them the first kernel: both wait for loads, of which a
+// lane's registers hold no more. (Tried there: loads of the step five on as soon
+// as a step's products run, y through a ring of asynchronous copies, no gain;
+// 32 columns of rank a unit, with two warps on a unit's K: 1 us more, 5 % less
+// for 16,000 rows of rank 64.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -428,9 +436,18 @@ template <bool F32, int STEPS, bool WIDE>
 cudaError_t launch_out_steps(const AdapterParams& p, int num_sms, cudaStream_t stream) {
     const int64_t blocks = (p.rows + kBlock - 1) / kBlock;
     const int64_t units = (p.rows < kBlock ? p.rows : kBlock) * ((p.N + 31) / 32);
-    int64_t groups = ((STEPS == 1 && !F32 ? 3 : 2) * num_sms + blocks - 1) / blocks;   // as many CTAs as run at once
-    const int64_t most = (units + kWarps - 1) / kWarps;
-    groups = groups > most ? most : groups;
+    // As many CTAs as run at once, or up to four times as many: what takes least where a warp's unit and a CTA's start take one
+    // each. (2048 rows: 22.9 us, with 24 CTAs more than run at once 27.4; 19,456 rows, 304 blocks: 123 with three rounds of
+    // CTAs, 140 with one.)
+    const int64_t most = (units + kWarps - 1) / kWarps, slots = (STEPS == 1 && !F32 ? 3 : 2) * num_sms;
+    const int64_t work = ((p.rows < kBlock ? 1 : kBlock / kTile) * ((p.N + 31) / 32) + kWarps - 1) / kWarps;   // of a warp, at least
+    int64_t groups = 1, least = INT64_MAX;
+    for (int rounds = 1; rounds <= 4; ++rounds) {
+        int64_t g = rounds * slots / blocks;
+        g = g < 1 ? 1 : g > most ? most : g;
+        const int64_t cost = (blocks * g + slots - 1) / slots * ((work + g - 1) / g + 1);
+        if (cost < least) least = cost, groups = g;
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -17,6 +17,9 @@
 // which a lane has eight neighbours and eight lanes a group of 64, whose least
 // and largest they find by shuffles:
 //   b = f16(lo),  s = f16((hi - lo) / top),  c = round((x - b) (1 / s)).
+// The same 4 x 2048 tokens: 40 us, bound by instructions (35.0 M of warps, 28.5 M
+// for the bfloat16 cache) with seven CTAs on an SM, as many as their registers
+// leave room for.
 #include <cuda_bf16.h>
 
 #include <type_traits>

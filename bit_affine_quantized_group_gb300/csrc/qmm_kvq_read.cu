@@ -5,6 +5,8 @@
 // instructions are few enough: with indexes and pages looked up for every 16
 // bytes they were 174 for those, 81 % of the issue slots at 4.5 TB/s. A thread
 // has the same 16 bytes of four positions of a page; neighbours write neighbours.
+// 16 sequences of up to 8191 positions of 8 heads of 128, 8 bits to bfloat16: 66.6
+// us, 6.3 TB/s; two of 100 positions: 2.2 us, a launch.
 #include <cuda_bf16.h>
 
 #include <type_traits>

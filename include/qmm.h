@@ -460,11 +460,14 @@ int qmm_check_kvq_qk_norm_rope_args(const qmm_kv_desc* d, const qmm_kvq_cache* c
 int qmm_kvq_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, const qmm_append_args* a, void* stream);
 
 /*
- * qmm_attention over a cache of codes. The same plan, arguments and checks.
- * Scores are products of the queries with whole codes, scaled in float32. Values
- * enter the second product as binary16 (s c + b within 2^-11 of its value and of
- * 128 s, or 8 s for 4 bits) and the softmax's weights as binary16 too (within
- * 2^-11); sums and maxima are float32. s c + b beyond binary16 is infinite.
+ * qmm_attention over a cache of codes. The same plan, arguments and checks. Each
+ * query row enters as binary16 numbers of a power of two that brings its largest
+ * element to 2^14..2^15 (elements down to 2^-28 of that keep all bits). Values
+ * enter as binary16, s c + b within 2^-11 of its value and of |b| + 128 |s| (8 |s|
+ * for 4 bits), and so do keys where rows * q_heads / kv_heads is more than 16; of
+ * fewer, scores are products with the codes themselves, scaled in float32. The
+ * softmax's weights are binary16 (within 2^-11); sums and maxima are float32.
+ * s c + b beyond binary16 is infinite.
  */
 int qmm_check_kvq_attention_args(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_attention_args* a);
 int qmm_kvq_attention(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, const qmm_attention_args* a, void* stream);
@@ -550,9 +553,11 @@ typedef struct qmm_adapter_args {
 /*
  * Adds the adapters' products. x . A^T is summed in float32 and enters the
  * second product as bfloat16 terms (two within 2^-17, for float32 outputs three
- * within 2^-26); that is summed in float32 with y and rounded once. The order of the sums is fixed: a call gives
- * the same bits for the same inputs. out may be y itself (rows at the same
- * places) and otherwise overlaps nothing. Two launches. rows = 0 is a no-op.
+ * within 2^-26); that is summed in float32 with y and rounded once. A lower term
+ * may be 0, and 0 times an infinity of B is NaN, so that an infinite element of B
+ * makes its column of the adapter's rows NaN. The order of the sums is fixed: a
+ * call gives the same bits for the same inputs. out may be y itself (rows at the
+ * same places) and otherwise overlaps nothing. Two launches. rows = 0 is a no-op.
  */
 int qmm_check_adapter_args(const qmm_adapter_desc* d, const qmm_adapter_args* a);
 int qmm_add_adapters(const qmm_adapter_plan_t* p, const qmm_adapter_args* a, void* stream);
