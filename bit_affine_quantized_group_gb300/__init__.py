@@ -589,9 +589,12 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype is not _F32 or w.numel() != plan.head_dim or not w.is_contiguous()):
             raise ValueError("q_weight and k_weight are float32 [head_dim] or None")
-    if plan.rot_dim and (rope is None or rope.dtype is not _F32 or not rope.is_contiguous() or rope.dim() != 2 or
-                         rope.shape[1] != plan.rot_dim):
-        raise ValueError("rope is a float32 tensor [positions, rot_dim]")
+    rope_len = 0
+    if plan.rot_dim:
+        shape = () if rope is None else rope.shape
+        if len(shape) != 2 or shape[1] != plan.rot_dim or rope.dtype is not _F32 or not rope.is_contiguous():
+            raise ValueError("rope is a float32 tensor [positions, rot_dim]")
+        rope_len = shape[0]
     if positions is not None and (positions.dtype is not _I32 or positions.numel() != tokens or
                                   not positions.is_contiguous()):
         raise ValueError("positions is an int32 tensor [tokens]")
@@ -599,7 +602,7 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, tokens, plan.q_width, dtype, "q"),
         _rows(k, tokens, plan.kv_width, dtype, "k"), _rows(v, tokens, plan.kv_width, dtype, "v"),
         0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
-        rope.data_ptr() if plan.rot_dim else 0, rope.shape[0] if plan.rot_dim else 0, lengths.data_ptr(),
+        rope.data_ptr() if plan.rot_dim else 0, rope_len, lengths.data_ptr(),
         0 if positions is None else positions.data_ptr(), page_table.data_ptr(), out.data_ptr(),
         _rows(out, tokens, plan.q_width, _BF16, "out"), seqs, rows, QMM_IN_F32 if dtype is _F32 else QMM_IN_BF16)
     call = _LIB.qmm_kvq_qk_norm_rope if isinstance(cache, QuantKVCache) else _LIB.qmm_qk_norm_rope
@@ -624,12 +627,12 @@ def attention(plan: KVPlan, q, cache, page_table, lengths, out, stream=None) -> 
 
 
 def _dense(t, seqs, plan, dtype, what):
-    """Strides from sequence to sequence and from row to row of a tensor [seqs, rows, kv_heads, head_dim]."""
+    """Rows, and the strides from sequence to sequence and from row to row, of a tensor [seqs, rows, kv_heads, head_dim]."""
     shape, st, heads, d = t.shape, t.stride(), plan.page_shape[0], plan.head_dim
     if t.dtype is not dtype or len(shape) != 4 or shape[0] != seqs or shape[2] != heads or shape[3] != d or st[3] != 1 or \
             (st[2] != d and heads > 1):
         raise ValueError(f"{what} is a {dtype} tensor [seqs, rows, kv_heads, head_dim] of adjacent heads")
-    return st[0], st[1]
+    return shape[1], st[0], st[1]
 
 
 def kv_read(plan: KVPlan, cache: QuantKVCache, page_table, lengths, k_out, v_out, starts=None, stream=None) -> None:
@@ -644,11 +647,12 @@ def kv_read(plan: KVPlan, cache: QuantKVCache, page_table, lengths, k_out, v_out
         raise ValueError("k_out and v_out are float32 or bfloat16")
     if starts is not None and (starts.dtype is not _I32 or starts.numel() != seqs or not starts.is_contiguous()):
         raise ValueError("starts is an int32 tensor [seqs]")
-    k_strides, v_strides = _dense(k_out, seqs, plan, dtype, "k_out"), _dense(v_out, seqs, plan, dtype, "v_out")
-    if k_out.shape[1] != v_out.shape[1]:
+    rows, k_seq, k_row = _dense(k_out, seqs, plan, dtype, "k_out")
+    v_rows, v_seq, v_row = _dense(v_out, seqs, plan, dtype, "v_out")
+    if rows != v_rows:
         raise ValueError("k_out and v_out have the same number of rows")
-    args = _READ_ARGS.pack(k_out.data_ptr(), v_out.data_ptr(), *k_strides, *v_strides, lengths.data_ptr(),
-                           0 if starts is None else starts.data_ptr(), page_table.data_ptr(), seqs, k_out.shape[1],
+    args = _READ_ARGS.pack(k_out.data_ptr(), v_out.data_ptr(), k_seq, k_row, v_seq, v_row, lengths.data_ptr(),
+                           0 if starts is None else starts.data_ptr(), page_table.data_ptr(), seqs, rows,
                            QMM_OUT_F32 if dtype is _F32 else QMM_OUT_BF16)
     st = _LIB.qmm_kvq_read(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
@@ -730,9 +734,12 @@ def add_adapters(plan: AdapterPlan, x, a, b, scale, ids, y, out, stream=None) ->
     for t in (x, a, b, scale, ids, y, out):
         if t is not None and t.get_device() != device:
             raise ValueError(f"all tensors are on the plan's device {plan.device}")
-    if x.dim() != 2 or y.dim() != 2 or out.dim() != 2:
+    K, N, shape, dtype = plan.K, plan.N, x.shape, plan.out_dtype
+    if len(shape) != 2 or y.dim() != 2 or (out is not y and out.dim() != 2):
         raise ValueError("x, y and out are [rows, width]")
-    rows, K, N = x.shape[0], plan.K, plan.N
+    rows = shape[0]
+    y_stride = _rows(y, rows, N, dtype, "y")
+    out_stride = y_stride if out is y else _rows(out, rows, N, dtype, "out")
     if a.dtype is not _BF16 or b.dtype is not _BF16 or a.shape != (plan.adapters, plan.rank, K) or \
             b.shape != (plan.adapters, N, plan.rank) or not a.is_contiguous() or not b.is_contiguous():
         raise ValueError("a [adapters, rank, K] and b [adapters, N, rank] are contiguous bfloat16 tensors")
@@ -741,8 +748,8 @@ def add_adapters(plan: AdapterPlan, x, a, b, scale, ids, y, out, stream=None) ->
     if ids.dtype is not _I32 or ids.numel() != rows or not ids.is_contiguous():
         raise ValueError("ids is an int32 tensor [rows]")
     args = _ADAPTER_ARGS.pack(x.data_ptr(), a.data_ptr(), b.data_ptr(), 0 if scale is None else scale.data_ptr(),
-                              ids.data_ptr(), y.data_ptr(), out.data_ptr(), _rows(x, rows, K, _BF16, "x"),
-                              _rows(y, rows, N, plan.out_dtype, "y"), _rows(out, rows, N, plan.out_dtype, "out"), rows)
+                              ids.data_ptr(), y.data_ptr(), out.data_ptr(), _rows(x, rows, K, _BF16, "x"), y_stride,
+                              out_stride, rows)
     st = _LIB.qmm_add_adapters(plan._handle, args, _stream_on(stream, device))
     if st != QMM_OK:
         raise QmmError(st, "qmm_add_adapters")
