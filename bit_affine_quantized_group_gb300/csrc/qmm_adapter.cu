@@ -17,7 +17,7 @@
 // products sum over, so that loads are whole 16-byte vectors of whole sectors.
 // K 4096, N 6144, a row for each of 16 adapters of rank 16: 7.0 us, of which 4.2
 // are the first kernel and 2.2 a launch. 64 rows of 16 adapters of rank 64, K
-// 5120, N 17408, float32: 19.1 us. 2048 rows, rank 32, K 5120, N 6144: 22.9 us
+// 5120, N 17408, float32: 18.8 us. 2048 rows, rank 32, K 5120, N 6144: 22.9 us
 // (3.2 TB/s), 11.3 of them the first kernel: both wait for loads, of which a
 // lane's registers hold no more. (Tried there: loads of the step five on as soon
 // as a step's products run, y through a ring of asynchronous copies, no gain;
@@ -273,12 +273,21 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
     }
 }
 
+template <bool F32, int STEPS>
+constexpr bool staged = F32 || STEPS == 4;
+template <bool F32, int STEPS>
+constexpr int low_bytes = staged<F32, STEPS> ? STEPS * (F32 ? 3 : 2) * 2 * kThreads * 16 : 0;
+
 // A run of units of a tile's 32 columns for each warp; a lane has 8 neighbouring columns of two rows. STEPS: 32 elements of
 // rank each. WIDE: rows of y and out are read and written 16 bytes at a time.
 template <bool F32, int STEPS, bool WIDE>
 __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adapter_out_kernel(const __grid_constant__ AdapterParams p, int groups) {
     constexpr int kTerms = F32 ? 3 : 2;
-    constexpr bool kKeep = STEPS <= 2;   // low stays in registers over a tile's units
+    // low stays over a tile's units, in registers or in shared memory: that leaves registers for the next unit's B and y to be
+    // loaded as soon as this one's have been used. (64 rows of rank 64 in float32: 18.8 us, 19.1 without; 2048 of rank 128: 79
+    // and 113. 2048 rows of rank 32 in bfloat16, whose terms are fewer: 24.0 and 22.8.)
+    constexpr bool kStage = staged<F32, STEPS>;
+    extern __shared__ __align__(16) uint4 s_low[];   // [warp][step][term][row][lane]
     __shared__ __align__(16) Tiles t;
     using T = std::conditional_t<F32, float, uint16_t>;
     const int group = static_cast<int>(blockIdx.x % groups), row0 = static_cast<int>(blockIdx.x / groups) * kBlock;
@@ -319,54 +328,77 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) in_rank[k] = id >= 0 && k * 32 + quad * 8 < p.rank;
         const bool all_rank = id >= 0 && p.rank == 32 * STEPS;
-        uint4 l[kKeep ? STEPS : 1][kTerms][2];
+        uint4 l[kStage ? 1 : STEPS][kTerms][2];
         bool loaded = false;
-#pragma unroll 1
-        for (; column < end; ++column, b += 16 * b_next, y[0] += 32, y[1] += 32, out[0] += 32, out[1] += 32) {
-            const int left = static_cast<int>(min(p.N - static_cast<int64_t>(column) * 32, static_cast<int64_t>(32)));   // columns
-            const bool whole = WIDE && quad * 8 + 8 <= left;
-            // y and B of the unit (with the next one's on their way too, and so one CTA less an SM, 2048 rows took a fifth longer)
-            uint4 wy[2][F32 ? 2 : 1], wb[STEPS][4];
+        uint4 wy[2][F32 ? 2 : 1], wb[STEPS][4];   // y and B of a unit
+        auto load_y = [&](int ahead, int left) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int k = 0; k < (F32 ? 2 : 1); ++k)
-                    if (in[h] && whole) wy[h][k] = *reinterpret_cast<const uint4*>(y[h] + 4 * k);
+                    if (WIDE && in[h] && quad * 8 + 8 <= left) wy[h][k] = *reinterpret_cast<const uint4*>(y[h] + ahead + 4 * k);
+        };
+        auto load_b = [&](const uint16_t* from, int left) {
             if (all_rank && left == 32) {
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wb[k][j] = __ldg(reinterpret_cast<const uint4*>(b + j * b_next + k * 32));
+                    for (int j = 0; j < 4; ++j) wb[k][j] = __ldg(reinterpret_cast<const uint4*>(from + j * b_next + k * 32));
             } else {
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wb[k][j] = load16(b + j * b_next + k * 32, in_rank[k] && own + 2 * j < left);
+                    for (int j = 0; j < 4; ++j) wb[k][j] = load16(from + j * b_next + k * 32, in_rank[k] && own + 2 * j < left);
             }
+        };
+        auto columns_of = [&](uint32_t c) { return static_cast<int>(min(p.N - static_cast<int64_t>(c) * 32, static_cast<int64_t>(32))); };
+        int left = columns_of(column);
+        if constexpr (kStage) load_y(0, left), load_b(b, left);
+#pragma unroll 1
+        for (; column < end; ++column, b += 16 * b_next, y[0] += 32, y[1] += 32, out[0] += 32, out[1] += 32) {
+            const bool whole = WIDE && quad * 8 + 8 <= left;
+            const bool more = column + 1 < end;
+            const int left_next = more ? columns_of(column + 1) : 0;
+            const bool roll = kStage && more && all_rank && left_next == 32;
+            if constexpr (!kStage) load_y(0, left), load_b(b, left);
             if (!waited) {
                 griddep_wait();
                 waited = true;
             }
-            auto load_low = [&](int k, uint4(&to)[kTerms][2]) {
+            if (!loaded) {
+                loaded = true;
 #pragma unroll
-                for (int i = 0; i < kTerms; ++i)
+                for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        to[i][h] = make_uint4(0u, 0u, 0u, 0u);
-                        if (in[h] && in_rank[k]) to[i][h] = __ldcg(reinterpret_cast<const uint4*>(low[h] + i * p.low_term + k * 32));
-                    }
-            };
+                    for (int i = 0; i < kTerms; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (in[h] && in_rank[k]) v = __ldcg(reinterpret_cast<const uint4*>(low[h] + i * p.low_term + k * 32));
+                            if constexpr (kStage) s_low[(((warp * STEPS + k) * kTerms + i) * 2 + h) * 32 + lane] = v;
+                            else l[k][i][h] = v;
+                        }
+            }
             float acc[4][4] = {};
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
-                uint4(&lk)[kTerms][2] = l[kKeep ? k : 0];
-                if (!kKeep || !loaded) load_low(k, lk);
+                uint4(&lk)[kTerms][2] = l[kStage ? 0 : k];
+                if constexpr (kStage) {   // (each lane what it has written itself)
+#pragma unroll
+                    for (int i = 0; i < kTerms; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) lk[i][h] = s_low[(((warp * STEPS + k) * kTerms + i) * 2 + h) * 32 + lane];
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < kTerms; ++i) mma_32(acc[j], lk[i][0], lk[i][1], wb[k][j]);
+                if (roll) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) wb[k][j] = __ldg(reinterpret_cast<const uint4*>(b + 16 * b_next + j * b_next + k * 32));
+                }
             }
-            loaded = true;
+            if (kStage && more && !roll) load_b(b + 16 * b_next, left_next);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (!in[h]) continue;
@@ -400,6 +432,8 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
                     }
                 }
             }
+            if (kStage && more) load_y(32, left_next);
+            left = left_next;
         }
     }
     if (!waited) griddep_wait();   // (the next kernel must not start behind a first kernel that still runs)
@@ -454,6 +488,7 @@ cudaError_t launch_out_steps(const AdapterParams& p, int num_sms, cudaStream_t s
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * groups));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = low_bytes<F32, STEPS>;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -469,6 +504,14 @@ cudaError_t launch_out(const AdapterParams& p, bool wide, int num_sms, cudaStrea
     if (p.rank <= 32) return with(std::integral_constant<int, 1>());
     if (p.rank <= 64) return with(std::integral_constant<int, 2>());
     return with(std::integral_constant<int, 4>());
+}
+
+template <bool F32, int STEPS>
+cudaError_t configure_out() {
+    if (low_bytes<F32, STEPS> <= 32 * 1024) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(qmm_adapter_out_kernel<F32, STEPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, low_bytes<F32, STEPS>);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(qmm_adapter_out_kernel<F32, STEPS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, low_bytes<F32, STEPS>);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -548,6 +591,9 @@ int qmm_adapter_plan(qmm_adapter_plan_t** plan, const qmm_adapter_desc* d, void*
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return QMM_ERR_CUDA;
     if (cudaFuncSetAttribute(qmm_adapter_low_kernel<2>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(qmm_adapter_low_kernel<3>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return QMM_ERR_CUDA;
+    if (configure_out<true, 1>() != cudaSuccess || configure_out<true, 2>() != cudaSuccess || configure_out<true, 4>() != cudaSuccess ||
+        configure_out<false, 4>() != cudaSuccess)
         return QMM_ERR_CUDA;
     struct qmm_adapter_plan* p = new (std::nothrow) struct qmm_adapter_plan();
     if (p == nullptr) return QMM_ERR_ALLOC;

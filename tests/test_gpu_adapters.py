@@ -79,6 +79,16 @@ def test_shapes(q, dtype, rows, K, N, rank, adapters):
     assert c.plan.error_flags() == 0
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("N,rank", [(1728, 32), (1704, 32), (1701, 64), (1728, 64), (1728, 128), (1704, 128), (1703, 104), (1696, 40)])
+def test_many_columns_of_a_warp(q, dtype, N, rank):
+    """So many rows that each warp has several units of 32 columns, whole and cut short, of one tile and of two."""
+    gen = np.random.default_rng(N + rank)
+    ids = np.repeat(gen.integers(-1, 9, 64), gen.integers(1, 80, 64))[:2100].tolist()
+    c = Case(q, len(ids), 64, N, rank, 9, dtype, ids=ids, seed=N)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("ids", [[-1] * 70, [2] * 70, [0, 1] * 35, list(range(35)) * 2, [34] * 16 + [-1] * 16 + [3] * 38,
                                  [3] * 17 + [5] * 15 + [3] * 38, [-1] * 69 + [0]])
 def test_orders_of_adapters(q, ids):
