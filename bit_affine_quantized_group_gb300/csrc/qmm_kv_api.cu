@@ -137,6 +137,7 @@ int check_read(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_read_
             strides[i + 1] < (seqs - 1) * strides[i] + width)
             return QMM_ERR_INVALID_ARG;
     if (a->k_out == nullptr || a->v_out == nullptr || !aligned(a->k_out, 16) || !aligned(a->v_out, 16)) return QMM_ERR_INVALID_ARG;
+    if (a->k_out == a->v_out) return QMM_ERR_INVALID_ARG;
     if (a->lengths == nullptr || !aligned(a->lengths, 4) || a->page_table == nullptr || !aligned(a->page_table, 4) ||
         !aligned(a->starts, 4))
         return QMM_ERR_INVALID_ARG;

@@ -104,6 +104,12 @@ def test_read_args(q, kw, expect):
     assert q.lib.qmm_check_kvq_read_args(ctypes.byref(d), ctypes.byref(c), ctypes.byref(a)) == expect
 
 
+@pytest.mark.parametrize("kw", [{}, {"out_dtype": 0}, {"rows": 1}])
+def test_keys_and_values_are_not_read_to_one_place(q, kw):
+    d, c, a = q.make_kv_desc(**GOOD), _cache(q), q.QmmReadArgs(**{**READ, "v_out": READ["k_out"], **kw})
+    assert q.lib.qmm_check_kvq_read_args(ctypes.byref(d), ctypes.byref(c), ctypes.byref(a)) == q.QMM_ERR_INVALID_ARG
+
+
 ADAPTER = dict(K=4096, N=1000, rank=16, adapters=8, max_rows=64, out_dtype="bf16")
 
 
