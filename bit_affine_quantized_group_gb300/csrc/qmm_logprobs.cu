@@ -12,8 +12,8 @@
 //
 // One row of 151,936 float32 logits with 5 alternatives: 8.2 us, latency of the
 // launch (2.2), of 5 chunks a thread, of bound, list and cluster. 512 rows of
-// 100,277 bfloat16 logits with 20: 25.5 us, 4.0 TB/s, bound by the bytes on their
-// way and a row's steps behind the pass.
+// 100,277 bfloat16 logits with 20: 25.3 us, 4.1 TB/s, bound by the bytes on their
+// way and by the 4 us of a row's steps behind the pass (21.5 without alternatives).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -36,7 +36,6 @@ constexpr int kRanks = 16;             // CTAs of a row at most
 // 3.4 TB/s, and more left no room for the CTAs.
 constexpr int kAhead = 5;
 constexpr int kSome = 8;               // threads that may be looked at beyond the needed ones
-constexpr int kManyThreads = 256, kManyCtas = 4 * 152;   // of a CTA and at once, where rows are many
 constexpr float kRise = 16.0f;         // that logits may lie above a thread's reference before its sums are brought to a new one
 constexpr float kLeast = -1000.0f;     // differences are brought to it: e^-1000 is 0, and no infinity meets a 0
 constexpr float kLog2E = 1.4426950408889634f;
@@ -370,17 +369,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
             if (slot < kList) s.list[slot] = entry;
         };
         const bool mine = key > bound || (key == bound && at <= last && at >= 0);
+        // (the threads' own chunks are on their way while it is settled which others are to be looked at)
+        uint4 own = make_uint4(0u, 0u, 0u, 0u);
         if (mine) {
-            if (other >= bound_value) s.again[atomicAdd(&s.again_size, 1u)] = tid;
             // (of short shares it is still where it was copied to)
             const bool held = w1 - w0 <= kAhead * kThreads && at >= w0 && at < w1;
-            look(at, held ? s_ring[at - w0] : r.load(at), note);
+            own = held ? s_ring[at - w0] : r.load(at);
+            if (other >= bound_value) s.again[atomicAdd(&s.again_size, 1u)] = tid;
         }
         __syncthreads();
-        if (s.again_size != 0) {
-            each(false, note);
-            __syncthreads();
-        }
+        if (s.again_size != 0) each(false, note);
+        if (mine) look(at, own, note);
+        __syncthreads();
         const int found = static_cast<int>(s.list_size);
         if (found <= kList) {
             for (int i = tid; i < found; i += kThreads) {
@@ -491,15 +491,14 @@ int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
 
 template <class T>
 int launch_rows(const LogprobsParams& p, int M, cudaStream_t stream) {
-    // Few rows: as many CTAs of 512 threads for each as fill the GPU, of 2048 logits at least. Many: smaller CTAs, so that one's
-    // steps behind the pass and the last rows' overhang cost little.
+    // CTAs of 512 threads while two an SM hold all rows: as many for each row as fill the GPU, of 2048 logits at least. More
+    // rows: CTAs of 256, so that one's steps behind the pass and the last rows' overhang cost little. (256 rows of 151,936
+    // bfloat16 logits: 20.6 us, as two CTAs of 256 each 23.6, as one 31. 400 of 100,277: 24.1 as one CTA of 256 each.)
+    constexpr int kCtas = 2 * 152;
+    if (M > kCtas) return launch<T, 256>(p, M, 1, stream);
     int ranks = kRanks;
-    if (static_cast<int64_t>(M) * 2 <= 2 * 152) {
-        while (ranks > 1 && (M * ranks > 2 * 152 || p.vocab / ranks < 2048)) ranks /= 2;
-        return launch<T, 512>(p, M, ranks, stream);
-    }
-    while (ranks > 1 && (static_cast<int64_t>(M) * ranks > kManyCtas || p.vocab / ranks < 8192)) ranks /= 2;
-    return launch<T, kManyThreads>(p, M, ranks, stream);
+    while (ranks > 1 && (M * ranks > kCtas || p.vocab / ranks < 2048)) ranks /= 2;
+    return launch<T, 512>(p, M, ranks, stream);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
