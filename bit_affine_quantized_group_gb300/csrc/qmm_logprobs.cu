@@ -10,8 +10,8 @@
 // them where a second one reaches as far. Each CTA of a row ranks what it finds by
 // counting, the first one of the cluster ranks the CTAs' lists.
 //
-// One row of 151,936 float32 logits with 5 alternatives: 8.2 us, latency of the
-// launch (2.2), of 5 chunks a thread, of bound, list and cluster. 512 rows of
+// One row of 151,936 float32 logits with 5 alternatives: 7.3 us, latency of the
+// launch (2.2), of 10 chunks a thread, of bound, list and cluster. 512 rows of
 // 100,277 bfloat16 logits with 20: 25.3 us, 4.1 TB/s, bound by the bytes on their
 // way and by the 4 us of a row's steps behind the pass (21.5 without alternatives).
 #include <cooperative_groups.h>
@@ -31,7 +31,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kTop = QMM_LOGPROBS_MAX_TOP;
 constexpr int kList = 1024;            // candidates that are ranked by counting
-constexpr int kRanks = 16;             // CTAs of a row at most
+constexpr int kRanks = 8;              // CTAs of a row at most
 // Chunks that a thread has on their way. Of 512 rows at once the pass is bound by how many bytes are: four in registers came to
 // 3.4 TB/s, and more left no room for the CTAs.
 constexpr int kAhead = 5;
@@ -468,8 +468,7 @@ int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ERR_CUDA;
     if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
         const void* kernel = reinterpret_cast<const void*>(&qmm_logprobs_kernel<T, THREADS>);
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, THREADS * kAhead * 16) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, THREADS * kAhead * 16) != cudaSuccess)
             return QMM_ERR_CUDA;
         if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
@@ -491,13 +490,16 @@ int launch(const LogprobsParams& p, int M, int ranks, cudaStream_t stream) {
 
 template <class T>
 int launch_rows(const LogprobsParams& p, int M, cudaStream_t stream) {
-    // CTAs of 512 threads while two an SM hold all rows: as many for each row as fill the GPU, of 2048 logits at least. More
-    // rows: CTAs of 256, so that one's steps behind the pass and the last rows' overhang cost little. (256 rows of 151,936
-    // bfloat16 logits: 20.6 us, as two CTAs of 256 each 23.6, as one 31. 400 of 100,277: 24.1 as one CTA of 256 each.)
+    // CTAs of 512 threads while two an SM hold all rows, as clusters of them where that leaves each 16,384 logits and not much
+    // more than seven eighths of the places taken: of clusters that fill the GPU some wait. (151,936 bfloat16 logits, 20
+    // alternatives, 1, 2, 4 and 8 CTAs a row: 1 row 11.4, 9.4, 8.3 and 8.3 us, 8 rows 9.8, 8.6 and 9.3 for the last three, 64
+    // rows 15.6, 13.9 and 11.7, 76 rows 12.3, 10.3 and 16.8; 16 CTAs a row 11.1 for one. 32,000 logits: 5.5 to 6 us as one.)
+    // More rows: CTAs of 256, so that one's steps behind the pass and the last rows' overhang cost little. (256 rows: 20.3 us,
+    // as two CTAs of 256 each 23.6, as one 31. 400 of 100,277: 24.1 as one CTA of 256 each.)
     constexpr int kCtas = 2 * 152;
     if (M > kCtas) return launch<T, 256>(p, M, 1, stream);
-    int ranks = kRanks;
-    while (ranks > 1 && (M * ranks > kCtas || p.vocab / ranks < 2048)) ranks /= 2;
+    int ranks = M <= 6 ? kRanks : kRanks / 2;
+    while (ranks > 1 && (M * ranks > kCtas * 7 / 8 || p.vocab / ranks < 16384)) ranks /= 2;
     return launch<T, 512>(p, M, ranks, stream);
 }
 
