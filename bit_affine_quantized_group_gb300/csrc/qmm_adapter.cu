@@ -447,8 +447,10 @@ cudaError_t launch_low(const AdapterParams& p, int num_sms, cudaStream_t stream)
     const int64_t units = static_cast<int64_t>(p.rows < kBlock ? p.rows : kBlock) * ((p.rank + 15) / 16);
     const int64_t most = (units + kWarps - 1) / kWarps;
     int slices = blocks * most <= kWideClusters ? kSlices : kSlices / 2;
-    while (slices > 1 && (slices > steps || slices * blocks > 2 * num_sms)) slices /= 2;
-    int64_t groups = 2 * num_sms / (blocks * slices);
+    // of clusters that fill the GPU some wait: 1216 rows of one adapter of rank 32 took 22.7 us with 304 CTAs, 17.2 with 152
+    const int64_t places = 2 * num_sms * 7 / 8;
+    while (slices > 1 && (slices > steps || slices * blocks > places)) slices /= 2;
+    int64_t groups = (slices > 1 ? places : 2 * num_sms) / (blocks * slices);
     groups = groups < 1 ? 1 : groups > most ? most : groups;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
