@@ -52,6 +52,11 @@ struct CodesCfg {
     static constexpr int kSideBytes = kStep * (kRowBytes + kPairBytes);
     static constexpr int kJoinCols = D == 256 && ROWS8 == 2 ? 32 : 64;   // columns of all rows that the warps join at once
     static constexpr int kJoinBytes = kCompute * kRows * kJoinCols * 4;
+    // Weights are binary16 numbers of up to 2^kWeightBits. Times a scale of up to kMostScale (2 or 8, as a binary16 number) they
+    // still are.
+    static constexpr float kWeightBits = BITS == 8 ? 15.0f : 13.0f;
+    static constexpr uint32_t kMostScale = BITS == 8 ? 0x3FFFu : 0x47FFu;
+    static constexpr float kEven = 0x1p24f, kOdd = BITS == 8 ? 0x1p24f : 0x1p20f;   // what outputs of codes count by, by columns
     static constexpr bool kQueryRegs = D < 256;                    // else the queries stay in shared memory
     static constexpr int kQueryBytes = kQueryRegs ? 0 : D * kRows * 2;
     static constexpr int kSumBytes = kRows * (D / 64 * 8 + 4);     // of the queries' groups, and their rows' units
@@ -97,6 +102,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     return d;
 }
 
+// d = a b + c, with c the same for both rows of a lane
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
 // The places among a lane's 16 neighbours of a group of the elements i = 0..3 of its fragment of the product w = 0..3: two
 // in the first half and two in the second. 4-bit codes come from a word's nibbles k and k + 4.
 template <int BITS>
@@ -118,57 +130,36 @@ __device__ __forceinline__ void key_fragment(const uint32_t (&codes)[BITS / 2], 
     }
 }
 
-// What the codes of a pair of positions become values by, for the even and the odd columns of a lane: (h + less) * scale +
-// add, and what the addend's rounding left out.
+// The codes of four neighbouring columns of two positions, from their words: pairs over the positions, as binary16 numbers
+// c 2^-24, and 16 c 2^-24 where a nibble stays where it is (4 bits: v[1] and v[3]). quarter: of a word of 4-bit codes, its half.
 template <int BITS>
-struct ValueTerms {
-    __half2 scale, add[2];
-    uint32_t left[2];
-    // first, second: (scale, bias) of the two positions
-    __device__ __forceinline__ ValueTerms(uint32_t first, uint32_t second, bool centred) {
-        scale = half2_of(__byte_perm(first, second, 0x5410));
-        const __half2 bias = half2_of(__byte_perm(first, second, 0x7632));
-        if (centred) {
-            add[0] = add[1] = __hfma2(half2_of(BITS == 8 ? kHalf128 : kHalf8), scale, bias);
-            left[0] = left[1] = 0u;
-            return;
-        }
-        auto set = [&](int i, uint32_t minus) {   // -1024 or -64
-            const __half2 m = half2_of(minus);
-            add[i] = __hfma2(m, scale, bias);
-            left[i] = bits_of(__hadd2(bias, __hfma2(m, scale, __hneg2(add[i]))));   // b - (b - 1024 s - add's error)
-        };
-        set(0, kHalf1024 | 0x80008000u);
-        if constexpr (BITS == 4) set(1, kHalf64 | 0x80008000u);
-        else add[1] = add[0], left[1] = left[0];
-    }
-};
-
-// The values of four neighbouring columns of two positions, from their codes' words: pairs over the positions. quarter: of a
-// word of 4-bit codes, its half.
-template <int BITS>
-__device__ __forceinline__ void value_pairs(uint32_t first, uint32_t second, int quarter, const ValueTerms<BITS>& t, bool centred,
-                                            uint32_t (&v)[4]) {
-    __half2 h[4];
+__device__ __forceinline__ void code_pairs(uint32_t first, uint32_t second, int quarter, uint32_t (&v)[4]) {
     if constexpr (BITS == 8) {
         const uint32_t x = __byte_perm(first, second, 0x5140), y = __byte_perm(first, second, 0x7362);
-        h[0] = half2_of(__byte_perm(x, 0x64646464u, 0x4140));
-        h[1] = half2_of(__byte_perm(x, 0x64646464u, 0x4342));
-        h[2] = half2_of(__byte_perm(y, 0x64646464u, 0x4140));
-        h[3] = half2_of(__byte_perm(y, 0x64646464u, 0x4342));
+        v[0] = __byte_perm(x, 0u, 0x4140);
+        v[1] = __byte_perm(x, 0u, 0x4342);
+        v[2] = __byte_perm(y, 0u, 0x4140);
+        v[3] = __byte_perm(y, 0u, 0x4342);
     } else {
         const uint32_t x = __byte_perm(first, second, quarter == 0 ? 0x5410 : 0x7632), y = x >> 8;
-        h[0] = half2_of(and_or(x, 0x000F000Fu, kHalf1024));
-        h[1] = half2_of(and_or(x, 0x00F000F0u, kHalf64));
-        h[2] = half2_of(and_or(y, 0x000F000Fu, kHalf1024));
-        h[3] = half2_of(and_or(y, 0x00F000F0u, kHalf64));
+        v[0] = x & 0x000F000Fu;
+        v[1] = x & 0x00F000F0u;
+        v[2] = y & 0x000F000Fu;
+        v[3] = y & 0x00F000F0u;
     }
-    if (centred) {
+}
+
+// The same as values: s (c - middle) + (b + s middle).
+template <int BITS>
+__device__ __forceinline__ void value_pairs(uint32_t first, uint32_t second, int quarter, uint32_t scale, uint32_t bias, uint32_t (&v)[4]) {
+    const __half2 s = half2_of(scale), add = __hfma2(half2_of(BITS == 8 ? kHalf128 : kHalf8), s, half2_of(bias));
+    code_pairs<BITS>(first, second, quarter, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __hsub2(h[i], half2_of(BITS == 8 ? kHalf1152 : i & 1 ? kHalf72 : kHalf1032));
+    for (int i = 0; i < 4; ++i) {
+        const bool high = BITS == 4 && i & 1;   // 64 + c, and of the others 1024 + c
+        const __half2 c = __hsub2(half2_of(v[i] | (high ? kHalf64 : kHalf1024)), half2_of(BITS == 8 ? kHalf1152 : high ? kHalf72 : kHalf1032));
+        v[i] = bits_of(__hfma2(c, s, add));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = bits_of(__hfma2(h[i], t.scale, t.add[i & 1]));
 }
 
 template <int D, int ROWS8, int BITS>
@@ -180,8 +171,9 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
     constexpr int kPartRows = 16 * kTiles;         // positions of a warp's part of a step
     constexpr int kThreads = 32 * Cfg::kCompute;   // computing threads
     constexpr int kGroups = D / 64;
-    constexpr int kEach = D == 64 ? 8 : 16;        // neighbouring columns of a lane
-    constexpr int kSets = D / (8 * kEach);         // sets of them
+    constexpr int kEach = 8;                       // neighbouring columns of a lane in each group of 64
+    constexpr int kSets = D / 64;
+    constexpr int kBiases = kSets < 2 ? 1 : kSets / 2;   // products of two groups' biases
     constexpr int kPairsAt = kStep * Cfg::kRowBytes;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* const full = reinterpret_cast<uint64_t*>(smem + Cfg::kBarsAt);
@@ -235,7 +227,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
         value_at[c] = Cfg::kSideBytes + part * kPartRows * Cfg::kRowBytes + Cfg::value_place(2 * quad, byte >> 4) + (byte & 15);
     }
     const uint32_t key_pair_at = kPairsAt + (part * kPartRows + gid) * Cfg::kPairBytes;
-    const uint32_t value_pair_at = Cfg::kSideBytes + kPairsAt + (part * kPartRows + 2 * quad) * Cfg::kPairBytes + gid * kEach / 64 * 4;
+    const uint32_t value_pair_at = Cfg::kSideBytes + kPairsAt + (part * kPartRows + 2 * quad) * Cfg::kPairBytes;
 
     uint64_t* const my_full = full + team * Cfg::kSlots;
     uint64_t* const my_empty = empty + team * Cfg::kSlots;
@@ -348,7 +340,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                 l[n][j] = 0.0f;
             }
 
-        float o[D / 16][ROWS8][4], left[kSets][ROWS8][4];   // columns by rows; what the values' rounding left out
+        float o[D / 16][ROWS8][4], ob[kBiases][ROWS8][4];   // columns by rows of scaled codes; of biases, two groups of 64
 #pragma unroll
         for (int n = 0; n < ROWS8; ++n)
 #pragma unroll
@@ -356,7 +348,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) o[c][n][j] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < kSets; ++c) left[c][n][j] = 0.0f;
+                for (int c = 0; c < kBiases; ++c) ob[c][n][j] = 0.0f;
             }
 
         for (int i = team; i < it.steps; i += Cfg::kTeams) {
@@ -380,7 +372,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
             for (int c = 0; c < kPartRows * kGroups; c += 32) {
                 if (kPartRows * kGroups < 32 && lane >= kPartRows * kGroups) break;
                 const uint32_t pair = lds32(side + (Cfg::kSideBytes + kPairsAt + part * kPartRows * Cfg::kPairBytes) + (c + lane) * 4);
-                slow |= (pair & 0x7FFFu) > 0x5380u;   // 60
+                slow |= (pair & 0x7FFFu) > Cfg::kMostScale;
                 if (!whole && p.rows > 1) {
                     const float2 sb = __half22float2(half2_of(pair));
                     slow |= !(fabsf(sb.y) + ((1 << BITS) - 1) * fabsf(sb.x) < 65504.0f);
@@ -389,6 +381,9 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
                 float part_sc[kTiles][ROWS8][4];
+                uint4 q_sums[ROWS8];   // sum and more of the two rows
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n) q_sums[n] = *reinterpret_cast<const uint4*>(sums + (k * kRows + n * 8 + quad * 2) * 8);
 #pragma unroll
                 for (int s = 0; s < kTiles; ++s) {
                     uint32_t codes[2][BITS / 2];   // of positions gid and gid + 8
@@ -417,14 +412,11 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                                 const uint2 v = lds64(q_smem + ((n * (D / 16) + k * 4 + w) * 32 + lane) * 8);
                                 b0 = v.x, b1 = v.y;
                             }
-                            if (w == 0) mma_f16_zc(part_sc[s][n], a[0], a[1], a[2], a[3], b0, b1);
+                            if (w == 0) mma_f16_from(part_sc[s][n], a, b0, b1, -__uint_as_float(q_sums[n].y), -__uint_as_float(q_sums[n].w));
                             else mma_f16(part_sc[s][n], a[0], a[1], a[2], a[3], b0, b1);
                         }
                     }
                 }
-                uint4 q_sums[ROWS8];   // sum and more of the two rows
-#pragma unroll
-                for (int n = 0; n < ROWS8; ++n) q_sums[n] = *reinterpret_cast<const uint4*>(sums + (k * kRows + n * 8 + quad * 2) * 8);
 #pragma unroll
                 for (int s = 0; s < kTiles; ++s)
 #pragma unroll
@@ -434,9 +426,8 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                         for (int n = 0; n < ROWS8; ++n) {
                             float(&x)[4] = sc[s][n];
                             const float(&a)[4] = part_sc[s][n];
-                            x[2 * h] = fmaf(sb.x, a[2 * h] - __uint_as_float(q_sums[n].y), fmaf(sb.y, __uint_as_float(q_sums[n].x), x[2 * h]));
-                            x[2 * h + 1] = fmaf(sb.x, a[2 * h + 1] - __uint_as_float(q_sums[n].w),
-                                                fmaf(sb.y, __uint_as_float(q_sums[n].z), x[2 * h + 1]));
+                            x[2 * h] = fmaf(sb.x, a[2 * h], fmaf(sb.y, __uint_as_float(q_sums[n].x), x[2 * h]));
+                            x[2 * h + 1] = fmaf(sb.x, a[2 * h + 1], fmaf(sb.y, __uint_as_float(q_sums[n].z), x[2 * h + 1]));
                         }
                     }
             }
@@ -468,7 +459,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
                     // The maximum is one of scores before their unit, which is above 0 and keeps the order: a difference to it
-                    // is exact to a rounding of its own, so that no weight passes 2^15, and becomes an infinity, however large
+                    // is exact to a rounding of its own, so that no weight passes its bits, and becomes an infinity, however large
                     // the scores.
                     const float m_new = fmaxf(m[n][j], top);
                     const float ref = m_new == -INFINITY ? 0.0f : m_new;
@@ -480,7 +471,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     for (int s = 0; s < kTiles; ++s) {
                         float &x = sc[s][n][j], &y = sc[s][n][2 + j];
                         add_x2(x, y, x, y, -ref, -ref);
-                        fma_x2(x, y, x, y, unit[n][j], unit[n][j], kWeightBits, kWeightBits);
+                        fma_x2(x, y, x, y, unit[n][j], unit[n][j], Cfg::kWeightBits, Cfg::kWeightBits);
                         x = exp2_approx(x), y = exp2_approx(y);
                         sum += x;
                         sum += y;
@@ -496,60 +487,88 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) o[c][n][j] *= alpha[n][j & 1];
 #pragma unroll
-                        for (int c = 0; c < kSets; ++c) left[c][n][j] *= alpha[n][j & 1];
+                        for (int c = 0; c < kBiases; ++c) ob[c][n][j] *= alpha[n][j & 1];
                     }
             }
 
-            // Products of a tile's values; kSlow: with codes centred, for the rows of the token at `rp` alone, with what `keep`
-            // leaves of the pairs of positions.
+            // Products of a tile's values: of the codes with weights times scales, and of the biases with the weights. kSlow: of
+            // the values themselves, for the rows of the token at `rp` alone, with what `keep` leaves of the pairs of positions.
             auto values = [&](int s, auto slowly, const uint32_t (&pb)[ROWS8][2], const uint32_t (&keep)[2], int rp) {
                 constexpr bool kSlow = decltype(slowly)::value;
                 constexpr int kWords = kEach * BITS / 32, kPerWord = 32 / BITS;   // of a lane's codes
-                auto product = [&](float(&to)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int n) {
-                    if constexpr (!kSlow) {
-                        mma_f16(to, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                    } else {
-                        float x[4];
-                        mma_f16_zc(x, a0 & keep[0], a1 & keep[0], a2 & keep[1], a3 & keep[1], pb[n][0], pb[n][1]);
+                uint32_t pairs[4][kSets];   // of positions 2 quad + {0, 1, 8, 9}
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (row_pos[n][j & 1] == rp) to[j] += x[j];
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t at = side + value_pair_at + (s * 16 + (j & 1) + (j >> 1) * 8) * Cfg::kPairBytes;
+                    if constexpr (kSets == 1) {
+                        pairs[j][0] = lds32(at);
+                    } else if constexpr (kSets == 2) {
+                        const uint2 v = lds64(at);
+                        pairs[j][0] = v.x, pairs[j][1] = v.y;
+                    } else {
+                        const uint4 v = lds128(at);
+                        pairs[j][0] = v.x, pairs[j][1] = v.y, pairs[j][2] = v.z, pairs[j][3] = v.w;
                     }
-                };
+                }
+                auto scales = [&](int c, int h) { return __byte_perm(pairs[2 * h][c], pairs[2 * h + 1][c], 0x5410); };
+                auto biases = [&](int c, int h) { return __byte_perm(pairs[2 * h][c], pairs[2 * h + 1][c], 0x7632); };
 #pragma unroll
                 for (int c = 0; c < kSets; ++c) {
-                    uint32_t codes[4][kWords];   // of positions 2 quad + {0, 1, 8, 9}
+                    uint32_t codes[4][kWords];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         // (the odd positions of eight lie four rows behind the even ones)
                         const uint32_t at = side + value_at[c] + (s * 16 + (j & 1) * 4 + (j >> 1) * 8) * Cfg::kRowBytes;
-                        if constexpr (kWords == 4) {
-                            const uint4 v = lds128(at);
-                            codes[j][0] = v.x, codes[j][1] = v.y, codes[j][2] = v.z, codes[j][3] = v.w;
-                        } else if constexpr (kWords == 2) {
+                        if constexpr (kWords == 2) {
                             const uint2 v = lds64(at);
                             codes[j][0] = v.x, codes[j][1] = v.y;
                         } else {
                             codes[j][0] = lds32(at);
                         }
                     }
-                    const uint32_t at = side + value_pair_at + s * 16 * Cfg::kPairBytes + c * kEach / 8 * 4;
-                    const ValueTerms<BITS> t0(lds32(at), lds32(at + Cfg::kPairBytes), kSlow);
-                    const ValueTerms<BITS> t1(lds32(at + 8 * Cfg::kPairBytes), lds32(at + 9 * Cfg::kPairBytes), kSlow);
+                    uint32_t ps[ROWS8][2];   // weights times scales
                     if constexpr (!kSlow) {
 #pragma unroll
-                        for (int n = 0; n < ROWS8; ++n) product(left[c][n], t0.left[0], t0.left[1], t1.left[0], t1.left[1], n);
+                        for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) ps[n][h] = bits_of(__hmul2(half2_of(pb[n][h]), half2_of(scales(c, h))));
                     }
 #pragma unroll
                     for (int e = 0; e < kEach; e += 4) {
                         uint32_t v0[4], v1[4];
-                        value_pairs<BITS>(codes[0][e / kPerWord], codes[1][e / kPerWord], e % kPerWord / 4, t0, kSlow, v0);
-                        value_pairs<BITS>(codes[2][e / kPerWord], codes[3][e / kPerWord], e % kPerWord / 4, t1, kSlow, v1);
+                        const int word = e / kPerWord, quarter = e % kPerWord / 4;
+                        if constexpr (kSlow) {
+                            value_pairs<BITS>(codes[0][word], codes[1][word], quarter, scales(c, 0), biases(c, 0), v0);
+                            value_pairs<BITS>(codes[2][word], codes[3][word], quarter, scales(c, 1), biases(c, 1), v1);
+                        } else {
+                            code_pairs<BITS>(codes[0][word], codes[1][word], quarter, v0);
+                            code_pairs<BITS>(codes[2][word], codes[3][word], quarter, v1);
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; k += 2)
 #pragma unroll
-                            for (int n = 0; n < ROWS8; ++n)
-                                product(o[(c * kEach + e + k) / 2][n], v0[k], v0[k + 1], v1[k], v1[k + 1], n);
+                            for (int n = 0; n < ROWS8; ++n) {
+                                float(&to)[4] = o[(c * kEach + e + k) / 2][n];
+                                if constexpr (!kSlow) {
+                                    mma_f16(to, v0[k], v0[k + 1], v1[k], v1[k + 1], ps[n][0], ps[n][1]);
+                                } else {
+                                    float x[4];
+                                    mma_f16_zc(x, v0[k] & keep[0], v0[k + 1] & keep[0], v1[k] & keep[1], v1[k + 1] & keep[1], pb[n][0],
+                                               pb[n][1]);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        if (row_pos[n][j & 1] == rp) to[j] += x[j] * (j < 2 ? 1.0f / Cfg::kEven : 1.0f / Cfg::kOdd);
+                                }
+                            }
+                    }
+                }
+                if constexpr (!kSlow) {
+#pragma unroll
+                    for (int c = 0; c < kBiases; ++c) {
+                        const int other = kSets > 1 ? 2 * c + 1 : 0;
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n)
+                            mma_f16(ob[c][n], biases(2 * c, 0), biases(other, 0), biases(2 * c, 1), biases(other, 1), pb[n][0], pb[n][1]);
                     }
                 }
             };
@@ -597,7 +616,8 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                 for (int k = 0; k < 4; k += 2) {
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) o[c][n][k + j] += left[c / (kEach / 2)][n][k + j];
+                    for (int c = 0; c < D / 16; ++c)   // four of a group of 64
+                        o[c][n][k + j] = fmaf(o[c][n][k + j], k == 0 ? Cfg::kEven : Cfg::kOdd, ob[c / 8][n][(c / 4 & 1) * 2 + j]);
                 }
             }
         named_barrier(1, kThreads);
