@@ -8,17 +8,20 @@
 //     64 + c, by masks), the queries q f with a power of two f of their row. A group of 64 elements adds
 //       s (sum q f (1024 + c) - 1024 sum q f) + b sum q f
 //     to f times the score, in float32.
-//   - A value becomes s (1024 + c) + r, one fused multiply-add with r = f16(b - 1024 s). What that rounding left out,
-//     e = b - 1024 s - r, is the same for a whole group of a position: sum P e is one more row of the product. Where |s| is
-//     so large that 1024 s is no binary16 number the codes are centred first.
-//   - The weights P are binary16 numbers of up to 2^15: one product, where the kernel of bfloat16 caches has two.
+//   - A value's code becomes the binary16 number c 2^-24 (or 16 c 2^-24, of nibbles that stay where they are), which has no
+//     offset to take off again; its scale goes into the weight, P s, for each group of 64 columns; the biases are one more
+//     product of the weights themselves: O = 2^24 sum (P s) (c 2^-24) + sum P b.
+//   - The weights P are binary16 numbers of up to 2^15 (4 bits: 2^13), so that with scales below 2 (8) P s is one too: one
+//     product, where the kernel of bfloat16 caches has two. Larger scales take the values themselves, s (c - 128) + (b + 128 s).
 //
-// What bounds it: with 8-bit codes bytes, with 4-bit codes the computing warps' instructions (about 890 of a warp for 32
-// positions of a 128-wide head), and of short sequences latency. One sequence of 131,072 positions with 8 heads of 128: 52.5 us
-// with 8 bits (5.4 TB/s; 50 without the products), 48.0 with 4 (3.1 TB/s); 64 ragged sequences, 8 bits: 119 us (5.0 TB/s).
-// About 7 us of each are start and join. Tried, in us of the two long ones of 4 bits (one sequence, 64 of them, now 48.0 and
-// 111): a step's key products before the last one's softmax 59 and 127; 12 computing warps in one CTA 52 and 158; four warps
-// a step slower in both, one warp a step 47 and 120. Codes made numbers in shared memory first, as for more rows, took 82.
+// What bounds it: with 8-bit codes bytes, with 4-bit codes the computing warps, of which registers allow two a scheduler, with
+// a step's chain of products, maximum, exponentials, transposition and products. One sequence of 131,072 positions with 8 heads
+// of 128: 52.8 us with 8 bits (5.4 TB/s; 50 without the products), 44.9 with 4 (3.4 TB/s); 64 ragged sequences: 113 us (5.3 TB/s)
+// and 103. About 7 us of each are start and join. A branch that the compiler does not know to be the whole warp's costs: masks
+// in one block for all rows, one for the slow path and votes before both took 48.1 us of 4 bits to 44.9. Tried before that, in
+// us of the two long forms of 4 bits (then 48 and 111): values as numbers, by a multiply-add each, the same; a step's key
+// products before the last one's softmax 59 and 127; 12 computing warps in one CTA 52 and 158; four warps a step slower in
+// both, one warp a step 47 and 120. Codes made numbers in shared memory first, as for more rows, took 82.
 #pragma once
 
 #include <type_traits>
@@ -361,22 +364,20 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sc[s][n][j] = 0.0f;
             const uint32_t side = slot_full();
-            // positions that every row sees need no mask
-            const bool whole = pos0 + kPartRows <= min(first_pos + 1, p.positions) &&
-                               (p.window == 0 || first_pos + p.rows - 1 - pos0 < p.window || pos0 + kPartRows <= p.sinks);
-            // Scales whose multiples may leave binary16 take the values' codes centred. A position that only some rows see
-            // weighs nothing in the others, but 0 * inf is not 0: where the values of such a one may not be binary16 numbers,
-            // each token's rows get a product of their own without what they do not see. Both are rare, and one path.
+            // positions that every row sees need no mask (the vote tells the compiler that the warp takes one way)
+            const bool whole = __all_sync(
+                0xFFFFFFFFu, pos0 + kPartRows <= min(first_pos + 1, p.positions) &&
+                                 (p.window == 0 || first_pos + p.rows - 1 - pos0 < p.window || pos0 + kPartRows <= p.sinks));
+            // Scales that weights leave binary16 with, infinities and NaN take a slow path: the values themselves, and for each
+            // token's rows a product of their own without what they do not see, for a position that only some rows see weighs
+            // nothing in the others, but 0 * inf is not 0.
             bool slow = false;
 #pragma unroll
             for (int c = 0; c < kPartRows * kGroups; c += 32) {
                 if (kPartRows * kGroups < 32 && lane >= kPartRows * kGroups) break;
                 const uint32_t pair = lds32(side + (Cfg::kSideBytes + kPairsAt + part * kPartRows * Cfg::kPairBytes) + (c + lane) * 4);
                 slow |= (pair & 0x7FFFu) > Cfg::kMostScale;
-                if (!whole && p.rows > 1) {
-                    const float2 sb = __half22float2(half2_of(pair));
-                    slow |= !(fabsf(sb.y) + ((1 << BITS) - 1) * fabsf(sb.x) < 65504.0f);
-                }
+                slow |= (pair & 0x7FFF0000u) >= 0x7C000000u;   // the bias
             }
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
@@ -431,13 +432,11 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                         }
                     }
             }
-            float alpha[ROWS8][2];
-            bool same = true;
+            if (!whole) {
 #pragma unroll
-            for (int n = 0; n < ROWS8; ++n)
+                for (int n = 0; n < ROWS8; ++n)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (!whole) {
+                    for (int j = 0; j < 2; ++j) {
                         // position s * 16 + h * 8 of the lane's lies after its row or the table's end, or before the window
                         // and past the sinks
                         const int own = row_pos[n][j] - pos0 - gid;
@@ -453,6 +452,13 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                                 if (at > last || (at <= out && at >= sink)) sc[s][n][2 * h + j] = -INFINITY;
                             }
                     }
+            }
+            float alpha[ROWS8][2];
+            bool same = true;
+#pragma unroll
+            for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
                     float top = -INFINITY;
 #pragma unroll
                     for (int s = 0; s < kTiles; ++s) top = fmaxf(top, fmaxf(sc[s][n][j], sc[s][n][2 + j]));
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     // the scores.
                     const float m_new = fmaxf(m[n][j], top);
                     const float ref = m_new == -INFINITY ? 0.0f : m_new;
-                    alpha[n][j] = m_new == m[n][j] ? 1.0f : exp2_approx((m[n][j] - ref) * unit[n][j]);
+                    alpha[n][j] = exp2_approx((m[n][j] - ref) * unit[n][j]);
                     same &= m_new == m[n][j];
                     m[n][j] = m_new;
                     float sum = 0.0f;
@@ -572,16 +578,19 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     }
                 }
             };
+            uint32_t pb[kTiles][ROWS8][2], keep[2] = {};
 #pragma unroll
-            for (int s = 0; s < kTiles; ++s) {
-                uint32_t pb[ROWS8][2], keep[2] = {};
+            for (int s = 0; s < kTiles; ++s)
 #pragma unroll
                 for (int n = 0; n < ROWS8; ++n)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) pb[n][h] = transposed(pack_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1]));
-                if (!slow) {
-                    values(s, std::false_type(), pb, keep, 0);
-                } else {
+                    for (int h = 0; h < 2; ++h) pb[s][n][h] = transposed(pack_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1]));
+            if (__builtin_expect(!slow, 1)) {
+#pragma unroll
+                for (int s = 0; s < kTiles; ++s) values(s, std::false_type(), pb[s], keep, 0);
+            } else {
+#pragma unroll
+                for (int s = 0; s < kTiles; ++s) {
 #pragma unroll 1
                     for (int r = 0; r < p.rows; ++r) {
                         const int rp = first_pos + r;
@@ -595,7 +604,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                                 if (back >= 0 && (p.window == 0 || back < p.window || pos < p.sinks)) keep[w] |= 0xFFFFu << (16 * j);
                             }
                         }
-                        values(s, std::true_type(), pb, keep, rp);
+                        values(s, std::true_type(), pb[s], keep, rp);
                     }
                 }
             }

@@ -462,12 +462,15 @@ int qmm_kvq_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, con
 /*
  * qmm_attention over a cache of codes. The same plan, arguments and checks. Each
  * query row enters as binary16 numbers of a power of two that brings its largest
- * element to 2^14..2^15 (elements down to 2^-28 of that keep all bits). Values
- * enter as binary16, s c + b within 2^-11 of its value and of |b| + 128 |s| (8 |s|
- * for 4 bits), and so do keys where rows * q_heads / kv_heads is more than 16; of
- * fewer, scores are products with the codes themselves, scaled in float32. The
- * softmax's weights are binary16 (within 2^-11); sums and maxima are float32.
- * s c + b beyond binary16 is infinite.
+ * element to 2^14..2^15 (elements down to 2^-28 of that keep all bits). Where rows *
+ * q_heads / kv_heads is up to 16, scores are products with the codes themselves,
+ * scaled in float32, and the values' scales enter with the softmax's weights P, so
+ * that a position's share of an output is off by up to 2^-10 P (|s| c + |b|) + 2^-32.
+ * Of more, keys and values enter as binary16, s c + b within 2^-11 of its value and of
+ * |b| + 128 |s| (8 |s| for 4 bits), and weights within 2^-11; so do values of 32
+ * neighbouring positions where an |s| is 2 or more (8 for 4 bits). Sums and maxima
+ * are float32.
+ * s c + b beyond binary16 may be infinite.
  */
 int qmm_check_kvq_attention_args(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_attention_args* a);
 int qmm_kvq_attention(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, const qmm_attention_args* a, void* stream);
