@@ -443,6 +443,32 @@ def test_sizes_of_keys_and_values(q, bits, d, rows, size):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,rows", [(64, 2), (128, 1), (128, 9), (256, 3)])
+@pytest.mark.parametrize("size", [12.0, 20.0, 28.0, 60.0, 80.0, 100.0])
+def test_sizes_of_values_about_the_largest_scales_of_weights(q, bits, d, rows, size):
+    """Scales on both sides of 2 and 8, some of each in a step."""
+    _fits(*_attend(q, [150, 70], 4, 1, d, bits, rows=rows, q_size=1.0 / size, size=size, seed=d + rows + 1)[:4])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("scale", [0x3FFF, 0x4000, 0x47FF, 0x4800, 0xBFFF, 0xC000, 0xC7FF, 0xC800, 0x0001, 0x8001])
+@pytest.mark.parametrize("n,d,rows", [(1, 128, 1), (2, 64, 2), (40, 256, 1), (9, 128, 4)])
+def test_scales_at_the_edges_of_binary16(q, bits, scale, n, d, rows):
+    """The largest scales that weights are multiplied by, the next ones, negative ones and the smallest: the last position's."""
+    import torch
+    of = torch.tensor([scale], dtype=torch.int32).to(torch.int16).view(torch.float16)
+
+    def change(pool):
+        page, slot = pool.place(0, n - 1)
+        pool.va[page, :, slot, :, 0] = of
+        pool.parts[0][1][1][n - 1, :, :, 0] = of
+
+    got, want, tol, flags, _ = _attend(q, [n], 4, 1, d, bits, rows=rows, seed=n + d, change=change)
+    assert flags == 0 and np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol + 2.0 ** -10 * abs(float(of)) * 2 ** bits).all()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("rows,window,told", [(1, 0, 100), (3, 0, 98), (3, 20, 100), (2, 0, 5000)])
 def test_lengths_past_the_page_table(q, bits, rows, window, told):
     """Rows stand where the length says; what is past the table is not seen."""
