@@ -12,7 +12,7 @@
 //     offset to take off again; its scale goes into the weight, P s, for each group of 64 columns; the biases are one more
 //     product of the weights themselves: O = 2^24 sum (P s) (c 2^-24) + sum P b.
 //   - The weights P are binary16 numbers of up to 2^15 (4 bits: 2^13), so that with scales below 2 (8) P s is one too: one
-//     product, where the kernel of bfloat16 caches has two. Larger scales take the values themselves, s (c - 128) + (b + 128 s).
+//     product, where the kernel of bfloat16 caches has two. Larger scales take the values themselves, s c + b rounded once.
 //
 // What bounds it: with 8-bit codes bytes, with 4-bit codes the computing warps, of which registers allow two a scheduler, with
 // a step's chain of products, maximum, exponentials, transposition and products. One sequence of 131,072 positions with 8 heads
@@ -152,16 +152,15 @@ __device__ __forceinline__ void code_pairs(uint32_t first, uint32_t second, int 
     }
 }
 
-// The same as values: s (c - middle) + (b + s middle).
+// The same as values, s c + b rounded once.
 template <int BITS>
 __device__ __forceinline__ void value_pairs(uint32_t first, uint32_t second, int quarter, uint32_t scale, uint32_t bias, uint32_t (&v)[4]) {
-    const __half2 s = half2_of(scale), add = __hfma2(half2_of(BITS == 8 ? kHalf128 : kHalf8), s, half2_of(bias));
     code_pairs<BITS>(first, second, quarter, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const bool high = BITS == 4 && i & 1;   // 64 + c, and of the others 1024 + c
-        const __half2 c = __hsub2(half2_of(v[i] | (high ? kHalf64 : kHalf1024)), half2_of(BITS == 8 ? kHalf1152 : high ? kHalf72 : kHalf1032));
-        v[i] = bits_of(__hfma2(c, s, add));
+        const __half2 zero = half2_of(high ? kHalf64 : kHalf1024);
+        v[i] = bits_of(__hfma2(__hsub2(half2_of(v[i] | bits_of(zero)), zero), half2_of(scale), half2_of(bias)));
     }
 }
 

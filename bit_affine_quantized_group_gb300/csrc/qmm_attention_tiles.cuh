@@ -116,8 +116,8 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     else mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
-// The codes of a side as binary16 numbers (c - 128) s + (b + 128 s), or with 8 in the place of 128 for 4 bits, laid out as a
-// side of bfloat16 is. By the 128 threads of a team.
+// The codes of a side as binary16 numbers s c + b, each rounded once (c is exact), laid out as a side of bfloat16 is. By the 128
+// threads of a team.
 template <class Cfg>
 __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
     constexpr int kChunks = Cfg::kRowBytes / 16, kElems = 128 / Cfg::kBits;   // of a row; elements of a chunk
@@ -129,18 +129,16 @@ __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         const uint32_t pair = lds32(side + kStep * Cfg::kRowBytes + row * Cfg::kPairBytes + chunk * kElems / 64 * 4);
         const __half2 scale = half2_of(__byte_perm(pair, pair, 0x1010)), bias = half2_of(__byte_perm(pair, pair, 0x3232));
-        const __half2 mid = __hfma2(half2_of(Cfg::kBits == 8 ? kHalf128 : kHalf8), scale, bias);
 #pragma unroll
         for (int u = 0; u < kElems / 8; ++u) {   // eight elements each
             __half2 h[4];
             if constexpr (Cfg::kBits == 8) {
-                const __half2 middle = half2_of(kHalf1152);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    h[i] = __hsub2(half2_of(__byte_perm(w[2 * u + (i >> 1)], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), middle);
+                    h[i] = __hsub2(half2_of(__byte_perm(w[2 * u + (i >> 1)], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), half2_of(kHalf1024));
             } else {
                 const uint32_t x = w[u], y = x >> 8;
-                const __half2 low = half2_of(kHalf1032), high = half2_of(kHalf72);
+                const __half2 low = half2_of(kHalf1024), high = half2_of(kHalf64);
                 const uint32_t e0 = bits_of(__hsub2(half2_of(and_or(x, 0x000F000Fu, 0x64006400u)), low));    // 0, 4
                 const uint32_t e1 = bits_of(__hsub2(half2_of(and_or(x, 0x00F000F0u, 0x54005400u)), high));   // 1, 5
                 const uint32_t e2 = bits_of(__hsub2(half2_of(and_or(y, 0x000F000Fu, 0x64006400u)), low));    // 2, 6
@@ -150,7 +148,7 @@ __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
             }
             uint32_t r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = bits_of(__hfma2(h[i], scale, mid));
+            for (int i = 0; i < 4; ++i) r[i] = bits_of(__hfma2(h[i], scale, bias));
             const int unit = chunk * (kElems / 8) + u;
             sts128(tile + (unit >> 3) * (kStep * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
         }

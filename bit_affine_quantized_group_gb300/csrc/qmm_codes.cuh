@@ -8,8 +8,7 @@ namespace qmmk {
 
 namespace {
 
-constexpr uint32_t kHalf1152 = 0x64806480u, kHalf1032 = 0x64086408u, kHalf1024 = 0x64006400u;   // pairs of binary16 numbers
-constexpr uint32_t kHalf128 = 0x58005800u, kHalf72 = 0x54805480u, kHalf64 = 0x54005400u, kHalf8 = 0x48004800u;
+constexpr uint32_t kHalf1024 = 0x64006400u, kHalf64 = 0x54005400u;   // pairs of binary16 numbers
 constexpr float kWeightBits = 15.0f;   // weights are binary16 numbers of up to 2^15, so that those from 2^-29 on keep their bits
 
 __device__ __forceinline__ uint32_t bits_of(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }

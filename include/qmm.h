@@ -466,8 +466,8 @@ int qmm_kvq_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, con
  * q_heads / kv_heads is up to 16, scores are products with the codes themselves,
  * scaled in float32, and the values' scales enter with the softmax's weights P, so
  * that a position's share of an output is off by up to 2^-10 P (|s| c + |b|) + 2^-32.
- * Of more, keys and values enter as binary16, s c + b within 2^-11 of its value and of
- * |b| + 128 |s| (8 |s| for 4 bits), and weights within 2^-11; so do values of 32
+ * Of more, keys and values enter as binary16, s c + b rounded once (within 2^-11 of it
+ * or 2^-25), and weights within 2^-11 or, of the largest, 2^-40; so do values of 32
  * neighbouring positions where an |s| is 2 or more (8 for 4 bits). Sums and maxima
  * are float32.
  * s c + b beyond binary16 may be infinite.

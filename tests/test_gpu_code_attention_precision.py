@@ -1,0 +1,81 @@
+"""Attention over a cache of codes where terms of an output cancel, so that the precision of weights and sums shows.
+
+Keys have the scale 0, so that a score is its position's bias: the products' sums are exact, and a weight is off by the rounding
+of its exponent (|score| 2^-23, and 2^-24 of 15 for the power that weights are held at) and by ex2.approx (2^-22), 2^-18 in all
+for scores down to -10. With weights P relative to the largest a position's share of an output of up to 16 rows is off by
+    (2^-19 P + 2^-37) (|s| top + |b|) + 2^-30
+with top = 255 or 15: the weight's two binary16 terms (2^-21 of it, or 2^-24 where the largest weight is 2^15 or, of 4 bits, 2^13),
+its product with the scale in two terms (2^-21 and three roundings of subnormal numbers, 2^-25 each, times a code), and products
+that the tensor cores cut at 2^-24 of the largest of 16, codes being subnormal numbers. The output is rounded once (2^-8)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def q():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_affine_quantized_group_gb300 import _build
+    _build.build()
+    import bit_affine_quantized_group_gb300 as q
+    return q
+
+
+def _run(q, bits, d, group, scores, code, scale, bias, page=64):
+    """One token of every sequence, with `group` equal query heads of ones. scores: [seqs, n, heads]; code, scale, bias: of the
+    values, [seqs, n, heads, d / 64], the same for all 64 columns of a group. Returns the outputs [seqs, heads, group, d / 64]
+    of the groups, and what they should be, and by how much they may be off."""
+    import torch
+    S, n, H = scores.shape
+    G, pages = d // 64, -(-n // page)
+    half = lambda x: x.astype(np.float16)  # noqa: E731
+    scores, scale, bias = half(scores), half(scale), half(bias)
+
+    def paged(x):   # [seqs, n, heads, ...] to pages
+        y = np.zeros((S, pages * page, *x.shape[2:]), x.dtype)
+        y[:, :n] = x
+        return torch.from_numpy(np.ascontiguousarray(y.reshape(S * pages, page, *x.shape[2:]).swapaxes(1, 2))).to(DEV)
+
+    byte = (code if bits == 8 else code | code << 4).astype(np.uint8)
+    k = torch.zeros((S * pages, H, page, d * bits // 8), dtype=torch.uint8, device=DEV)
+    v = paged(np.repeat(byte, 64 * bits // 8, 3))
+    ka = paged(np.stack((np.zeros((S, n, H, G), np.float16), np.repeat(scores[..., None], G, 3)), 4))
+    va = paged(np.stack((scale, bias), 4))
+    plan = q.KVPlan(H * group, H, d, page, max_seqs=S, max_rows=1, max_pages=pages, rot_dim=0, scale=1.0 / d)
+    cache = q.QuantKVCache(k, v, ka, va, bits)
+    table = torch.arange(S * pages, dtype=torch.int32, device=DEV).view(S, pages)
+    out = torch.empty((S, H * group, d), dtype=torch.bfloat16, device=DEV)
+    q.attention(plan, torch.ones_like(out), cache, table, torch.full((S,), n, dtype=torch.int32, device=DEV), out)
+    torch.cuda.synchronize()
+    assert plan.error_flags() == 0
+    got = out.double().cpu().numpy().reshape(S, H, group, G, 64)
+    assert (got == got[..., :1]).all()
+    a = scores.astype(np.float64)
+    P = np.exp(a - a.max(1, keepdims=True))[..., None]
+    s, b, top = scale.astype(np.float64), bias.astype(np.float64), 2 ** bits - 1
+    L = P.sum(1)
+    want = (P * (s * code + b)).sum(1) / L
+    size = np.abs(s) * top + np.abs(b)
+    off = (2.0 ** -17 * (P * np.abs(s * code + b)).sum(1) + ((2.0 ** -19 * P + 2.0 ** -37) * size + 2.0 ** -30).sum(1)) / L
+    return got[..., 0], want[:, :, None], (off + 2.0 ** -8 * np.abs(want))[:, :, None]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,group", [(64, 20), (128, 32), (256, 17), (128, 64)])
+def test_more_rows_round_keys_and_values_once(q, bits, d, group):
+    """Of more than 16 rows s c + b is a binary16 number, and so is the weight: each rounded once (2^-11), whatever the group's
+    middle: values of groups far from zero, in which small ones stand out."""
+    rng = np.random.default_rng(bits + d + group)
+    S, n, H, G, top = 8, 1, 3, d // 64, 2 ** bits - 1
+    code = rng.integers(0, 2, (S, n, H, G))
+    scale = (0.5 + rng.random((S, n, H, G))) * 60 / top
+    bias = 2.0 ** -7 * (0.1 + rng.random((S, n, H, G)))
+    got, want, _ = _run(q, bits, d, group, np.zeros((S, n, H)), code, scale, bias)
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -19) * np.abs(want)).all(), np.max(np.abs(got - want) / np.abs(want))
