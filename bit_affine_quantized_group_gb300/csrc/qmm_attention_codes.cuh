@@ -8,20 +8,24 @@
 //     64 + c, by masks), the queries q f with a power of two f of their row. A group of 64 elements adds
 //       s (sum q f (1024 + c) - 1024 sum q f) + b sum q f
 //     to f times the score, in float32.
-//   - A value's code becomes the binary16 number c 2^-24 (or 16 c 2^-24, of nibbles that stay where they are), which has no
-//     offset to take off again; its scale goes into the weight, P s, for each group of 64 columns; the biases are one more
-//     product of the weights themselves: O = 2^24 sum (P s) (c 2^-24) + sum P b.
+//   - A value's code becomes the binary16 number c 2^-24 (c 2^-20 of 4 bits), which has no offset to take off again; its scale
+//     goes into the weight, P s, for each group of 64 columns; the biases are one more product of the weights themselves:
+//     O = 2^24 sum (P s) (c 2^-24) + sum P b.
+//   - The tensor cores cut what they add at about 2^-24 of the largest term, always to the same side, and a subnormal number
+//     counts as one of 2^-14. Where codes and biases cancel, sums of all steps kept there lost more the longer the sequence was;
+//     so only a step's are, and the steps are added up by float32 additions, which round. 4-bit codes are held as high as a
+//     nibble's place allows for the same reason.
 //   - The weights P are binary16 numbers of up to 2^15 (4 bits: 2^13), so that with scales below 2 (8) P s is one too: one
 //     product, where the kernel of bfloat16 caches has two. Larger scales take the values themselves, s c + b rounded once.
 //
 // What bounds it: with 8-bit codes bytes, with 4-bit codes the computing warps, of which registers allow two a scheduler, with
 // a step's chain of products, maximum, exponentials, transposition and products. One sequence of 131,072 positions with 8 heads
-// of 128: 52.8 us with 8 bits (5.4 TB/s; 50 without the products), 44.9 with 4 (3.4 TB/s); 64 ragged sequences: 113 us (5.3 TB/s)
-// and 103. About 7 us of each are start and join. A branch that the compiler does not know to be the whole warp's costs: masks
-// in one block for all rows, one for the slow path and votes before both took 48.1 us of 4 bits to 44.9. Tried before that, in
-// us of the two long forms of 4 bits (then 48 and 111): values as numbers, by a multiply-add each, the same; a step's key
-// products before the last one's softmax 59 and 127; 12 computing warps in one CTA 52 and 158; four warps a step slower in
-// both, one warp a step 47 and 120. Codes made numbers in shared memory first, as for more rows, took 82.
+// of 128: 54.7 us with 8 bits (5.2 TB/s), 48.5 with 4 (3.1 TB/s); 64 ragged sequences: 117 us (5.1 TB/s) and 110 (52.4, 44.6, 114
+// and 102 with sums of all steps in the tensor cores). About 7 us of each are start and join. A branch that the compiler does not
+// know to be the whole warp's costs: masks in one block for all rows, one for the slow path and votes before both took 48.1 us of
+// 4 bits to 44.9. Tried before that, in us of the two long forms of 4 bits (then 48 and 111): values as numbers, by a multiply-add
+// each, the same; a step's key products before the last one's softmax 59 and 127; 12 computing warps in one CTA 52 and 158; four
+// warps a step slower in both, one warp a step 47 and 120. Codes made numbers in shared memory first, as for more rows, took 82.
 #pragma once
 
 #include <type_traits>
@@ -45,8 +49,9 @@ struct CodesCfg {
     static constexpr int kTiles = 4 / kTeamWarps;                  // 16-position tiles of a warp
     static constexpr int kThreads = 32 * (kCompute + 4);           // and a group of four that starts the copies
     static constexpr int kLaunchRegs = D == 256 ? 168 : 128;
-    static constexpr int kComputeRegs = D == 256 ? (ROWS8 == 1 ? 200 : 216) : ROWS8 == 1 ? 152 : 176;
-    static constexpr int kCopyRegs = ROWS8 == 1 ? 104 : D == 256 ? 72 : 80;
+    // (heads of 128 in 152 and 104: 64 ragged sequences of 8 bits a twelfth slower)
+    static constexpr int kComputeRegs = D == 256 ? (ROWS8 == 1 ? 200 : 216) : D == 64 && ROWS8 == 1 ? 152 : 176;
+    static constexpr int kCopyRegs = ROWS8 == 1 && D != 128 ? 104 : D == 256 ? 72 : 80;
     static_assert(kCompute * kComputeRegs + 4 * kCopyRegs <= (kCompute + 4) * kLaunchRegs, "registers of a CTA");
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
     static constexpr int kShortShare = D < 256 ? 4 : 2;            // steps of the shortest share
@@ -59,7 +64,7 @@ struct CodesCfg {
     // still are.
     static constexpr float kWeightBits = BITS == 8 ? 15.0f : 13.0f;
     static constexpr uint32_t kMostScale = BITS == 8 ? 0x3FFFu : 0x47FFu;
-    static constexpr float kEven = 0x1p24f, kOdd = BITS == 8 ? 0x1p24f : 0x1p20f;   // what outputs of codes count by, by columns
+    static constexpr float kUnit = BITS == 8 ? 0x1p24f : 0x1p20f;  // what products with codes count by
     static constexpr bool kQueryRegs = D < 256;                    // else the queries stay in shared memory
     static constexpr int kQueryBytes = kQueryRegs ? 0 : D * kRows * 2;
     static constexpr int kSumBytes = kRows * (D / 64 * 8 + 4);     // of the queries' groups, and their rows' units
@@ -134,7 +139,7 @@ __device__ __forceinline__ void key_fragment(const uint32_t (&codes)[BITS / 2], 
 }
 
 // The codes of four neighbouring columns of two positions, from their words: pairs over the positions, as binary16 numbers
-// c 2^-24, and 16 c 2^-24 where a nibble stays where it is (4 bits: v[1] and v[3]). quarter: of a word of 4-bit codes, its half.
+// c 2^-24, or c 2^-20 of 4 bits. quarter: of a word of 4-bit codes, its half.
 template <int BITS>
 __device__ __forceinline__ void code_pairs(uint32_t first, uint32_t second, int quarter, uint32_t (&v)[4]) {
     if constexpr (BITS == 8) {
@@ -144,24 +149,21 @@ __device__ __forceinline__ void code_pairs(uint32_t first, uint32_t second, int 
         v[2] = __byte_perm(y, 0u, 0x4140);
         v[3] = __byte_perm(y, 0u, 0x4342);
     } else {
-        const uint32_t x = __byte_perm(first, second, quarter == 0 ? 0x5410 : 0x7632), y = x >> 8;
-        v[0] = x & 0x000F000Fu;
+        const uint32_t x = __byte_perm(first, second, quarter == 0 ? 0x5410 : 0x7632);
+        v[0] = (x << 4) & 0x00F000F0u;
         v[1] = x & 0x00F000F0u;
-        v[2] = y & 0x000F000Fu;
-        v[3] = y & 0x00F000F0u;
+        v[2] = (x >> 4) & 0x00F000F0u;
+        v[3] = (x >> 8) & 0x00F000F0u;
     }
 }
 
 // The same as values, s c + b rounded once.
 template <int BITS>
 __device__ __forceinline__ void value_pairs(uint32_t first, uint32_t second, int quarter, uint32_t scale, uint32_t bias, uint32_t (&v)[4]) {
+    constexpr uint32_t kZero = BITS == 8 ? kHalf1024 : kHalf64;   // the number whose last bits the code's are
     code_pairs<BITS>(first, second, quarter, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool high = BITS == 4 && i & 1;   // 64 + c, and of the others 1024 + c
-        const __half2 zero = half2_of(high ? kHalf64 : kHalf1024);
-        v[i] = bits_of(__hfma2(__hsub2(half2_of(v[i] | bits_of(zero)), zero), half2_of(scale), half2_of(bias)));
-    }
+    for (int i = 0; i < 4; ++i) v[i] = bits_of(__hfma2(__hsub2(half2_of(v[i] | kZero), half2_of(kZero)), half2_of(scale), half2_of(bias)));
 }
 
 template <int D, int ROWS8, int BITS>
@@ -496,12 +498,14 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     }
             }
 
-            // Products of a tile's values: of the codes with weights times scales, and of the biases with the weights. kSlow: of
-            // the values themselves, for the rows of the token at `rp` alone, with what `keep` leaves of the pairs of positions.
-            auto values = [&](int s, auto slowly, const uint32_t (&pb)[ROWS8][2], const uint32_t (&keep)[2], int rp) {
-                constexpr bool kSlow = decltype(slowly)::value;
-                constexpr int kWords = kEach * BITS / 32, kPerWord = 32 / BITS;   // of a lane's codes
-                uint32_t pairs[4][kSets];   // of positions 2 quad + {0, 1, 8, 9}
+            uint32_t pb[kTiles][ROWS8][2];   // the weights, as right operands
+#pragma unroll
+            for (int s = 0; s < kTiles; ++s)
+#pragma unroll
+                for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) pb[s][n][h] = transposed(pack_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1]));
+            auto load_pairs = [&](int s, uint32_t (&pairs)[4][kSets]) {   // of a tile's values, positions 2 quad + {0, 1, 8, 9}
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t at = side + value_pair_at + (s * 16 + (j & 1) + (j >> 1) * 8) * Cfg::kPairBytes;
@@ -515,84 +519,93 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                         pairs[j][0] = v.x, pairs[j][1] = v.y, pairs[j][2] = v.z, pairs[j][3] = v.w;
                     }
                 }
-                auto scales = [&](int c, int h) { return __byte_perm(pairs[2 * h][c], pairs[2 * h + 1][c], 0x5410); };
-                auto biases = [&](int c, int h) { return __byte_perm(pairs[2 * h][c], pairs[2 * h + 1][c], 0x7632); };
+            };
+            auto scales = [](const uint32_t (&pairs)[4][kSets], int c, int h) { return __byte_perm(pairs[2 * h][c], pairs[2 * h + 1][c], 0x5410); };
+            auto biases = [](const uint32_t (&pairs)[4][kSets], int c, int h) { return __byte_perm(pairs[2 * h][c], pairs[2 * h + 1][c], 0x7632); };
+            constexpr int kWords = kEach * BITS / 32, kPerWord = 32 / BITS;   // of a lane's codes
+            auto load_codes = [&](int s, int c, uint32_t (&codes)[4][kWords]) {   // of a tile's group, of those positions
 #pragma unroll
-                for (int c = 0; c < kSets; ++c) {
-                    uint32_t codes[4][kWords];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // (the odd positions of eight lie four rows behind the even ones)
-                        const uint32_t at = side + value_at[c] + (s * 16 + (j & 1) * 4 + (j >> 1) * 8) * Cfg::kRowBytes;
-                        if constexpr (kWords == 2) {
-                            const uint2 v = lds64(at);
-                            codes[j][0] = v.x, codes[j][1] = v.y;
-                        } else {
-                            codes[j][0] = lds32(at);
-                        }
-                    }
-                    uint32_t ps[ROWS8][2];   // weights times scales
-                    if constexpr (!kSlow) {
-#pragma unroll
-                        for (int n = 0; n < ROWS8; ++n)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) ps[n][h] = bits_of(__hmul2(half2_of(pb[n][h]), half2_of(scales(c, h))));
-                    }
-#pragma unroll
-                    for (int e = 0; e < kEach; e += 4) {
-                        uint32_t v0[4], v1[4];
-                        const int word = e / kPerWord, quarter = e % kPerWord / 4;
-                        if constexpr (kSlow) {
-                            value_pairs<BITS>(codes[0][word], codes[1][word], quarter, scales(c, 0), biases(c, 0), v0);
-                            value_pairs<BITS>(codes[2][word], codes[3][word], quarter, scales(c, 1), biases(c, 1), v1);
-                        } else {
-                            code_pairs<BITS>(codes[0][word], codes[1][word], quarter, v0);
-                            code_pairs<BITS>(codes[2][word], codes[3][word], quarter, v1);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2)
-#pragma unroll
-                            for (int n = 0; n < ROWS8; ++n) {
-                                float(&to)[4] = o[(c * kEach + e + k) / 2][n];
-                                if constexpr (!kSlow) {
-                                    mma_f16(to, v0[k], v0[k + 1], v1[k], v1[k + 1], ps[n][0], ps[n][1]);
-                                } else {
-                                    float x[4];
-                                    mma_f16_zc(x, v0[k] & keep[0], v0[k + 1] & keep[0], v1[k] & keep[1], v1[k + 1] & keep[1], pb[n][0],
-                                               pb[n][1]);
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        if (row_pos[n][j & 1] == rp) to[j] += x[j] * (j < 2 ? 1.0f / Cfg::kEven : 1.0f / Cfg::kOdd);
-                                }
-                            }
-                    }
-                }
-                if constexpr (!kSlow) {
-#pragma unroll
-                    for (int c = 0; c < kBiases; ++c) {
-                        const int other = kSets > 1 ? 2 * c + 1 : 0;
-#pragma unroll
-                        for (int n = 0; n < ROWS8; ++n)
-                            mma_f16(ob[c][n], biases(2 * c, 0), biases(other, 0), biases(2 * c, 1), biases(other, 1), pb[n][0], pb[n][1]);
+                for (int j = 0; j < 4; ++j) {
+                    // (the odd positions of eight lie four rows behind the even ones)
+                    const uint32_t at = side + value_at[c] + (s * 16 + (j & 1) * 4 + (j >> 1) * 8) * Cfg::kRowBytes;
+                    if constexpr (kWords == 2) {
+                        const uint2 v = lds64(at);
+                        codes[j][0] = v.x, codes[j][1] = v.y;
+                    } else {
+                        codes[j][0] = lds32(at);
                     }
                 }
             };
-            uint32_t pb[kTiles][ROWS8][2], keep[2] = {};
-#pragma unroll
-            for (int s = 0; s < kTiles; ++s)
-#pragma unroll
-                for (int n = 0; n < ROWS8; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) pb[s][n][h] = transposed(pack_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1]));
             if (__builtin_expect(!slow, 1)) {
+                uint32_t pairs[kTiles][4][kSets];
 #pragma unroll
-                for (int s = 0; s < kTiles; ++s) values(s, std::false_type(), pb[s], keep, 0);
+                for (int s = 0; s < kTiles; ++s) load_pairs(s, pairs[s]);
+#pragma unroll
+                for (int c = 0; c < kBiases; ++c) {
+                    const int other = kSets > 1 ? 2 * c + 1 : 0;
+                    float sum[ROWS8][4];   // of the step
+#pragma unroll
+                    for (int s = 0; s < kTiles; ++s)
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n) {
+                            const uint32_t b[4] = {biases(pairs[s], 2 * c, 0), biases(pairs[s], other, 0), biases(pairs[s], 2 * c, 1), biases(pairs[s], other, 1)};
+                            if (s == 0) mma_f16_zc(sum[n], b[0], b[1], b[2], b[3], pb[s][n][0], pb[s][n][1]);
+                            else mma_f16(sum[n], b[0], b[1], b[2], b[3], pb[s][n][0], pb[s][n][1]);
+                        }
+#pragma unroll
+                    for (int n = 0; n < ROWS8; ++n) {
+                        add_x2(ob[c][n][0], ob[c][n][1], ob[c][n][0], ob[c][n][1], sum[n][0], sum[n][1]);
+                        add_x2(ob[c][n][2], ob[c][n][3], ob[c][n][2], ob[c][n][3], sum[n][2], sum[n][3]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < kSets; ++c) {
+                    float sum[kEach / 2][ROWS8][4];   // of the step: columns by rows
+#pragma unroll
+                    for (int s = 0; s < kTiles; ++s) {
+                        uint32_t codes[4][kWords];
+                        load_codes(s, c, codes);
+                        uint32_t ph[ROWS8][2];   // weights times scales
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) ph[n][h] = bits_of(__hmul2(half2_of(pb[s][n][h]), half2_of(scales(pairs[s], c, h))));
+#pragma unroll
+                        for (int e = 0; e < kEach; e += 4) {
+                            uint32_t v0[4], v1[4];
+                            const int word = e / kPerWord, quarter = e % kPerWord / 4;
+                            code_pairs<BITS>(codes[0][word], codes[1][word], quarter, v0);
+                            code_pairs<BITS>(codes[2][word], codes[3][word], quarter, v1);
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2)
+#pragma unroll
+                                for (int n = 0; n < ROWS8; ++n) {
+                                    float(&to)[4] = sum[(e + k) / 2][n];
+                                    if (s == 0) mma_f16_zc(to, v0[k], v0[k + 1], v1[k], v1[k + 1], ph[n][0], ph[n][1]);
+                                    else mma_f16(to, v0[k], v0[k + 1], v1[k], v1[k + 1], ph[n][0], ph[n][1]);
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kEach / 2; ++k)
+#pragma unroll
+                        for (int n = 0; n < ROWS8; ++n) {
+                            float(&to)[4] = o[c * (kEach / 2) + k][n];
+                            float(&x)[4] = sum[k][n];
+                            add_x2(to[0], to[1], to[0], to[1], x[0], x[1]);
+                            add_x2(to[2], to[3], to[2], to[3], x[2], x[3]);
+                        }
+                }
             } else {
+                // Products of the values themselves, for the rows of one token at a time, without what they do not see.
 #pragma unroll
                 for (int s = 0; s < kTiles; ++s) {
+                    uint32_t pairs[4][kSets];
+                    load_pairs(s, pairs);
 #pragma unroll 1
                     for (int r = 0; r < p.rows; ++r) {
                         const int rp = first_pos + r;
+                        uint32_t keep[2];
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {   // the halves of a fragment word whose position token r sees
                             keep[w] = 0u;
@@ -603,7 +616,29 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                                 if (back >= 0 && (p.window == 0 || back < p.window || pos < p.sinks)) keep[w] |= 0xFFFFu << (16 * j);
                             }
                         }
-                        values(s, std::true_type(), pb[s], keep, rp);
+#pragma unroll
+                        for (int c = 0; c < kSets; ++c) {
+                            uint32_t codes[4][kWords];
+                            load_codes(s, c, codes);
+#pragma unroll
+                            for (int e = 0; e < kEach; e += 4) {
+                                uint32_t v0[4], v1[4];
+                                const int word = e / kPerWord, quarter = e % kPerWord / 4;
+                                value_pairs<BITS>(codes[0][word], codes[1][word], quarter, scales(pairs, c, 0), biases(pairs, c, 0), v0);
+                                value_pairs<BITS>(codes[2][word], codes[3][word], quarter, scales(pairs, c, 1), biases(pairs, c, 1), v1);
+#pragma unroll
+                                for (int k = 0; k < 4; k += 2)
+#pragma unroll
+                                    for (int n = 0; n < ROWS8; ++n) {
+                                        const uint32_t a[4] = {v0[k] & keep[0], v0[k + 1] & keep[0], v1[k] & keep[1], v1[k + 1] & keep[1]};
+                                        float x[4];
+                                        mma_f16_zc(x, a[0], a[1], a[2], a[3], pb[s][n][0], pb[s][n][1]);
+#pragma unroll
+                                        for (int j = 0; j < 4; ++j)
+                                            if (row_pos[n][j & 1] == rp) o[(c * kEach + e + k) / 2][n][j] += x[j] * (1.0f / Cfg::kUnit);
+                                    }
+                            }
+                        }
                     }
                 }
             }
@@ -625,7 +660,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                 for (int k = 0; k < 4; k += 2) {
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)   // four of a group of 64
-                        o[c][n][k + j] = fmaf(o[c][n][k + j], k == 0 ? Cfg::kEven : Cfg::kOdd, ob[c / 8][n][(c / 4 & 1) * 2 + j]);
+                        o[c][n][k + j] = fmaf(o[c][n][k + j], Cfg::kUnit, ob[c / 8][n][(c / 4 & 1) * 2 + j]);
                 }
             }
         named_barrier(1, kThreads);

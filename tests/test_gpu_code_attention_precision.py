@@ -68,6 +68,22 @@ def _run(q, bits, d, group, scores, code, scale, bias, page=64):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,group,n", [(128, 4, 4000), (64, 4, 4000), (256, 4, 4000), (128, 12, 3000)])
+def test_long_sums_of_codes_and_biases(q, bits, d, group, n):
+    """Equal weights, and values whose code and bias cancel: their sums are as long as a sequence, and the outputs hundreds of
+    times smaller. The tensor cores cut what they add at 2^-24 of their largest term, always to the same side: of a step's 32
+    positions that is 2^-20 of a code's share at most, of sums over all steps it grew with them."""
+    rng = np.random.default_rng(bits + d + n)
+    S, H, G, top = 80, 4, d // 64, 2 ** bits - 1
+    code = rng.integers(top // 2, top + 1, (S, n, H, G))
+    scale = np.full((S, n, H, G), (1.5 if bits == 8 else 6.0) * 2.0 / top)
+    bias = -scale * code * (1.0 + 2.0 ** -6 * (rng.random((S, n, H, G)) - 0.5))
+    got, want, off = _run(q, bits, d, group, np.zeros((S, n, H)), code, scale, bias)
+    size = 2 * np.abs(bias).mean(1)[:, :, None]   # weights are powers of two, exact
+    assert (np.abs(got - want) <= 2.0 ** -20 * size + 2.0 ** -8 * np.abs(want)).all(), np.max(np.abs(got - want) / size) * 2.0 ** 20
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("d,group", [(64, 20), (128, 32), (256, 17), (128, 64)])
 def test_more_rows_round_keys_and_values_once(q, bits, d, group):
     """Of more than 16 rows s c + b is a binary16 number, and so is the weight: each rounded once (2^-11), whatever the group's
