@@ -15,17 +15,20 @@
 //     counts as one of 2^-14. Where codes and biases cancel, sums of all steps kept there lost more the longer the sequence was;
 //     so only a step's are, and the steps are added up by float32 additions, which round. 4-bit codes are held as high as a
 //     nibble's place allows for the same reason.
-//   - The weights P are binary16 numbers of up to 2^15 (4 bits: 2^13), so that with scales below 2 (8) P s is one too: one
-//     product, where the kernel of bfloat16 caches has two. Larger scales take the values themselves, s c + b rounded once.
+//   - The weights P are two binary16 terms, the first of up to 2^15 (4 bits: 2^13), so that with scales below 2 (8) P s is as well:
+//     two products, as in the kernel of bfloat16 caches, for one term rounds values that cancel by more than the output's own
+//     rounding. Larger scales take the values themselves, s c + b rounded once.
 //
 // What bounds it: with 8-bit codes bytes, with 4-bit codes the computing warps, of which registers allow two a scheduler, with
 // a step's chain of products, maximum, exponentials, transposition and products. One sequence of 131,072 positions with 8 heads
-// of 128: 54.7 us with 8 bits (5.2 TB/s), 48.5 with 4 (3.1 TB/s); 64 ragged sequences: 117 us (5.1 TB/s) and 110 (52.4, 44.6, 114
-// and 102 with sums of all steps in the tensor cores). About 7 us of each are start and join. A branch that the compiler does not
-// know to be the whole warp's costs: masks in one block for all rows, one for the slow path and votes before both took 48.1 us of
-// 4 bits to 44.9. Tried before that, in us of the two long forms of 4 bits (then 48 and 111): values as numbers, by a multiply-add
-// each, the same; a step's key products before the last one's softmax 59 and 127; 12 computing warps in one CTA 52 and 158; four
-// warps a step slower in both, one warp a step 47 and 120. Codes made numbers in shared memory first, as for more rows, took 82.
+// of 128: 54.5 us with 8 bits (5.2 TB/s), 51.3 with 4 (2.9 TB/s); 64 ragged sequences: 122 us (4.9 TB/s) and 116. About 7 us of
+// each are start and join. (Weights of one term: 54.7, 48.5, 117 and 110; sums of all steps in the tensor cores besides: 52.4, 44.6,
+// 114 and 102. Added late, with the next step's: no gain; begun with the biases' products: 53.5 and 121 of 4 bits.) A branch
+// that the compiler does not know to be the whole warp's costs: masks in one block for all rows, one for the slow path and votes
+// before both took 48.1 us of 4 bits to 44.9. Tried before all that, in us of the two long forms of 4 bits (then 48 and 111): values
+// as numbers, by a multiply-add each, the same; a step's key products before the last one's softmax 59 and 127; 12 computing warps
+// in one CTA 52 and 158; four warps a step slower in both, one warp a step 47 and 120. Codes made numbers in shared memory first,
+// as for more rows, took 82.
 #pragma once
 
 #include <type_traits>
@@ -60,7 +63,7 @@ struct CodesCfg {
     static constexpr int kSideBytes = kStep * (kRowBytes + kPairBytes);
     static constexpr int kJoinCols = D == 256 && ROWS8 == 2 ? 32 : 64;   // columns of all rows that the warps join at once
     static constexpr int kJoinBytes = kCompute * kRows * kJoinCols * 4;
-    // Weights are binary16 numbers of up to 2^kWeightBits. Times a scale of up to kMostScale (2 or 8, as a binary16 number) they
+    // Weights are binary16 terms of up to 2^kWeightBits. Times a scale of up to kMostScale (2 or 8, as a binary16 number) they
     // still are.
     static constexpr float kWeightBits = BITS == 8 ? 15.0f : 13.0f;
     static constexpr uint32_t kMostScale = BITS == 8 ? 0x3FFFu : 0x47FFu;
@@ -498,13 +501,17 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     }
             }
 
-            uint32_t pb[kTiles][ROWS8][2];   // the weights, as right operands
+            uint32_t pb[kTiles][ROWS8][2], pl[kTiles][ROWS8][2];   // the weights' terms, as right operands
 #pragma unroll
             for (int s = 0; s < kTiles; ++s)
 #pragma unroll
                 for (int n = 0; n < ROWS8; ++n)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) pb[s][n][h] = transposed(pack_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1]));
+                    for (int h = 0; h < 2; ++h) {
+                        split_f16(sc[s][n][2 * h], sc[s][n][2 * h + 1], pb[s][n][h], pl[s][n][h]);
+                        pb[s][n][h] = transposed(pb[s][n][h]);
+                        pl[s][n][h] = transposed(pl[s][n][h]);
+                    }
             auto load_pairs = [&](int s, uint32_t (&pairs)[4][kSets]) {   // of a tile's values, positions 2 quad + {0, 1, 8, 9}
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -551,6 +558,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                             const uint32_t b[4] = {biases(pairs[s], 2 * c, 0), biases(pairs[s], other, 0), biases(pairs[s], 2 * c, 1), biases(pairs[s], other, 1)};
                             if (s == 0) mma_f16_zc(sum[n], b[0], b[1], b[2], b[3], pb[s][n][0], pb[s][n][1]);
                             else mma_f16(sum[n], b[0], b[1], b[2], b[3], pb[s][n][0], pb[s][n][1]);
+                            mma_f16(sum[n], b[0], b[1], b[2], b[3], pl[s][n][0], pl[s][n][1]);
                         }
 #pragma unroll
                     for (int n = 0; n < ROWS8; ++n) {
@@ -565,11 +573,15 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                     for (int s = 0; s < kTiles; ++s) {
                         uint32_t codes[4][kWords];
                         load_codes(s, c, codes);
-                        uint32_t ph[ROWS8][2];   // weights times scales
+                        uint32_t ph[ROWS8][2], pr[ROWS8][2];   // weights times scales, in two terms as well
 #pragma unroll
                         for (int n = 0; n < ROWS8; ++n)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) ph[n][h] = bits_of(__hmul2(half2_of(pb[s][n][h]), half2_of(scales(pairs[s], c, h))));
+                            for (int h = 0; h < 2; ++h) {
+                                const __half2 hi = half2_of(pb[s][n][h]), of = half2_of(scales(pairs[s], c, h)), first = __hmul2(hi, of);
+                                ph[n][h] = bits_of(first);
+                                pr[n][h] = bits_of(__hfma2(half2_of(pl[s][n][h]), of, __hfma2(hi, of, __hneg2(first))));
+                            }
 #pragma unroll
                         for (int e = 0; e < kEach; e += 4) {
                             uint32_t v0[4], v1[4];
@@ -584,6 +596,11 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                                     if (s == 0) mma_f16_zc(to, v0[k], v0[k + 1], v1[k], v1[k + 1], ph[n][0], ph[n][1]);
                                     else mma_f16(to, v0[k], v0[k + 1], v1[k], v1[k + 1], ph[n][0], ph[n][1]);
                                 }
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2)
+#pragma unroll
+                                for (int n = 0; n < ROWS8; ++n)
+                                    mma_f16(sum[(e + k) / 2][n], v0[k], v0[k + 1], v1[k], v1[k + 1], pr[n][0], pr[n][1]);
                         }
                     }
 #pragma unroll
@@ -602,6 +619,10 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                 for (int s = 0; s < kTiles; ++s) {
                     uint32_t pairs[4][kSets];
                     load_pairs(s, pairs);
+#pragma unroll
+                    for (int n = 0; n < ROWS8; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) pl[s][n][h] = some_left(pb[s][n][h], pl[s][n][h]);
 #pragma unroll 1
                     for (int r = 0; r < p.rows; ++r) {
                         const int rp = first_pos + r;
@@ -633,6 +654,7 @@ __global__ void __launch_bounds__(CodesCfg<D, ROWS8, BITS>::kThreads, CodesCfg<D
                                         const uint32_t a[4] = {v0[k] & keep[0], v0[k + 1] & keep[0], v1[k] & keep[1], v1[k + 1] & keep[1]};
                                         float x[4];
                                         mma_f16_zc(x, a[0], a[1], a[2], a[3], pb[s][n][0], pb[s][n][1]);
+                                        mma_f16(x, a[0], a[1], a[2], a[3], pl[s][n][0], pl[s][n][1]);
 #pragma unroll
                                         for (int j = 0; j < 4; ++j)
                                             if (row_pos[n][j & 1] == rp) o[(c * kEach + e + k) / 2][n][j] += x[j] * (1.0f / Cfg::kUnit);

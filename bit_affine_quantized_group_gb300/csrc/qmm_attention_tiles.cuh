@@ -1,6 +1,7 @@
 // Attention over a paged cache for tiles of 16 query rows: the kernel of bfloat16 caches, and of caches of codes for more
 // than 16 rows, where the team of a step first writes its codes into shared memory as binary16 numbers, for all row tiles
-// read them. (With fewer rows the numbers stay in registers: qmm_attention_codes.cuh.)
+// read them. (With fewer rows the numbers stay in registers: qmm_attention_codes.cuh.) Beside keys and values of 11 bits weights
+// are one binary16 number: a second term took 38.9 us for the form below and left its error as it was.
 //
 // Four sequences of up to 16,001 positions with 8 tokens each, 64 rows a cache head: 33.6 us from bfloat16, 35.5 from 8-bit and
 // 34.6 from 4-bit codes, at a half and a quarter of the bytes: no kind is bound by them, but by a step's chain of products,

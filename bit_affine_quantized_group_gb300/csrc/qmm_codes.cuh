@@ -15,6 +15,19 @@ __device__ __forceinline__ uint32_t bits_of(__half2 v) { return *reinterpret_cas
 __device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return bits_of(__floats2half2_rn(a, b)); }
 
+// Weights a and b, at least 0, as pairs of binary16 numbers: their upper 11 bits, and the rounded remainders. hi + lo is within
+// 2^-21 of a weight, or within 2^-24 where that is more.
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const float x = __uint_as_float(__float_as_uint(a) & 0xFFFFE000u), y = __uint_as_float(__float_as_uint(b) & 0xFFFFE000u);
+    hi = pack_f16(x, y);
+    lo = pack_f16(a - x, b - y);
+}
+// Remainders of 2^-24 at least, where hi is not 0: a remainder of 0 times an infinite value were NaN, where the weight times it
+// is infinite.
+__device__ __forceinline__ uint32_t some_left(uint32_t hi, uint32_t lo) {
+    return bits_of(__hmax2(half2_of(lo), __hmin2(half2_of(hi), half2_of(0x00010001u))));
+}
+
 // (x & mask) | bits in one instruction (of two constants the compiler makes two).
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
     uint32_t d;

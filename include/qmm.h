@@ -464,8 +464,10 @@ int qmm_kvq_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, con
  * query row enters as binary16 numbers of a power of two that brings its largest
  * element to 2^14..2^15 (elements down to 2^-28 of that keep all bits). Where rows *
  * q_heads / kv_heads is up to 16, scores are products with the codes themselves,
- * scaled in float32, and the values' scales enter with the softmax's weights P, so
- * that a position's share of an output is off by up to 2^-10 P (|s| c + |b|) + 2^-32.
+ * scaled in float32, and the values' scales enter with the softmax's weights, which
+ * are two binary16 terms. With P a position's weight relative to the row's largest (or
+ * the largest among 32 neighbours, where that is more) and top 255 or 15, its share of
+ * an output is off by up to (2^-19 P + 2^-37) (|s| top + |b|) + 2^-30.
  * Of more, keys and values enter as binary16, s c + b rounded once (within 2^-11 of it
  * or 2^-25), and weights within 2^-11 or, of the largest, 2^-40; so do values of 32
  * neighbouring positions where an |s| is 2 or more (8 for 4 bits). Sums and maxima

@@ -68,6 +68,42 @@ def _run(q, bits, d, group, scores, code, scale, bias, page=64):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 4), (128, 12), (256, 8), (256, 16), (64, 16)])
+def test_weights_keep_more_bits_than_the_output(q, bits, d, group):
+    """The last of three positions takes off what the first two add, to 11 bits: what is left is 2^-11 of the terms, and weights
+    of one binary16 number would be off by as much."""
+    rng = np.random.default_rng(bits + d + group)
+    S, H, G, top = 24, 4, d // 64, 2 ** bits - 1
+    scores = -8.0 * rng.random((S, 3, H))
+    scores[:, 2] = -1.0 * rng.random((S, H))
+    code = rng.integers(0, top + 1, (S, 3, H, G))
+    scale = (0.2 + rng.random((S, 3, H, G))) * 4 / top
+    bias = -2.0 + rng.random((S, 3, H, G))
+    scale[:, 2] = 0
+    a = scores.astype(np.float16).astype(np.float64)[..., None]
+    v = scale.astype(np.float16).astype(np.float64) * code + bias.astype(np.float16)
+    bias[:, 2] = -(np.exp(a[:, :2] - a[:, 2:]) * v[:, :2]).sum(1)
+    got, want, off = _run(q, bits, d, group, scores, code, scale, bias)
+    assert (np.abs(got - want) <= off).all(), np.max(np.abs(got - want) / off)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,group", [(64, 2), (128, 4), (128, 16), (256, 1)])
+def test_small_weights_on_large_values(q, bits, d, group):
+    """The likeliest position has the value 0, the others weights down to 2^-45 of its and values of up to 65,000."""
+    rng = np.random.default_rng(bits * d + group)
+    S, n, H, G, top = 8, 7, 3, d // 64, 2 ** bits - 1
+    scores = -31.0 * rng.random((S, n, H))
+    code = rng.integers(0, top + 1, (S, n, H, G))
+    scale = np.where(rng.random((S, n, H, G)) < 0.5, 0.0, (1.0 if bits == 8 else 7.0) * rng.random((S, n, H, G)))
+    bias = 6.0e4 * rng.random((S, n, H, G))
+    scores[:, 0], code[:, 0], scale[:, 0], bias[:, 0] = 0.0, 0, 0.0, 0.0
+    got, want, off = _run(q, bits, d, group, scores, code, scale, bias)
+    # (scores down to -31: their exponents round to |score| 2^-23 more)
+    assert (np.abs(got - want) <= off + 2.0 ** -18 * np.abs(want)).all(), np.max(np.abs(got - want) / off)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("d,group,n", [(128, 4, 4000), (64, 4, 4000), (256, 4, 4000), (128, 12, 3000)])
 def test_long_sums_of_codes_and_biases(q, bits, d, group, n):
     """Equal weights, and values whose code and bias cancel: their sums are as long as a sequence, and the outputs hundreds of
