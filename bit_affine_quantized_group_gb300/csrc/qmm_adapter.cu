@@ -12,7 +12,11 @@
 //   - out: each warp takes a run of a tile's columns, 32 at a time. low enters as
 //     two bfloat16 terms (high + low within 2^-17), for float32 outputs as three
 //     (2^-26): one would round more than bfloat16 outputs do. Tiles, y and B are
-//     read while the first kernel still runs.
+//     read while the first kernel still runs. That one lets the second start only
+//     behind its own wait, when all that came before the call is complete; but
+//     sight of it is promised behind the second's wait alone. So ids and the first
+//     y are read from L2, where a completed kernel's writes are, past any older
+//     line of an SM's own cache.
 // In both a lane of a quad has 8 neighbouring elements of the 32 that two
 // products sum over, so that loads are whole 16-byte vectors of whole sectors.
 // K 4096, N 6144, a row for each of 16 adapters of rank 16: 7.0 us, of which 4.2
@@ -100,7 +104,7 @@ __device__ __forceinline__ void find_tiles(const AdapterParams& p, int row0, Til
     if (tid < kBlock) {
         int id = 0x7FFFFFFF;   // behind all others
         if (tid < rows) {
-            id = p.ids[row0 + tid];
+            id = __ldcg(p.ids + row0 + tid);
             if (id < -1 || id >= p.adapters) {
                 atomicOr(p.err, static_cast<uint32_t>(QMM_ADAPTER_BAD_ID));
                 id = -1;
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
     const int group = static_cast<int>(blockIdx.x % groups), row0 = static_cast<int>(blockIdx.x / groups) * kBlock;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, quad = lane & 3;
     griddep_launch_dependents();
-    find_tiles(p, row0, t);
+    find_tiles(p, row0, t);   // (before the wait, as the first y and B: what is read there was complete when the first kernel began)
     const uint32_t columns = static_cast<uint32_t>((p.N + 31) / 32);
     const uint32_t units = t.tiles * columns;   // (2^31 at most)
     const uint32_t all = groups * kWarps, mine = group * kWarps + warp, each = units / all, rest = units - each * all;
@@ -331,12 +335,15 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
         uint4 l[kStage ? 1 : STEPS][kTerms][2];
         bool loaded = false;
         uint4 wy[2][F32 ? 2 : 1], wb[STEPS][4];   // y and B of a unit
-        auto load_y = [&](int ahead, int left) {
+        auto load_y = [&](int ahead, int left, bool early) {   // early: before the wait
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int k = 0; k < (F32 ? 2 : 1); ++k)
-                    if (WIDE && in[h] && quad * 8 + 8 <= left) wy[h][k] = *reinterpret_cast<const uint4*>(y[h] + ahead + 4 * k);
+                    if (WIDE && in[h] && quad * 8 + 8 <= left) {
+                        const uint4* const from = reinterpret_cast<const uint4*>(y[h] + ahead + 4 * k);
+                        wy[h][k] = F32 && !early ? *from : __ldcg(from);   // (of float32 two loads share a sector)
+                    }
         };
         auto load_b = [&](const uint16_t* from, int left) {
             if (all_rank && left == 32) {
@@ -353,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
         };
         auto columns_of = [&](uint32_t c) { return static_cast<int>(min(p.N - static_cast<int64_t>(c) * 32, static_cast<int64_t>(32))); };
         int left = columns_of(column);
-        if constexpr (kStage) load_y(0, left), load_b(b, left);
+        if constexpr (kStage) load_y(0, left, !waited), load_b(b, left);
 #pragma unroll 1
         for (; column < end; ++column, b += 16 * b_next, y[0] += 32, y[1] += 32, out[0] += 32, out[1] += 32) {
             const bool whole = WIDE && quad * 8 + 8 <= left;
             const bool more = column + 1 < end;
             const int left_next = more ? columns_of(column + 1) : 0;
             const bool roll = kStage && more && all_rank && left_next == 32;
-            if constexpr (!kStage) load_y(0, left), load_b(b, left);
+            if constexpr (!kStage) load_y(0, left, !waited), load_b(b, left);
             if (!waited) {
                 griddep_wait();
                 waited = true;
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
                     }
                 }
             }
-            if (kStage && more) load_y(32, left_next);
+            if (kStage && more) load_y(32, left_next, false);
             left = left_next;
         }
     }

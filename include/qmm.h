@@ -562,7 +562,10 @@ typedef struct qmm_adapter_args {
  * may be 0, and 0 times an infinity of B is NaN, so that an infinite element of B
  * makes its column of the adapter's rows NaN. The order of the sums is fixed: a
  * call gives the same bits for the same inputs. out may be y itself (rows at the
- * same places) and otherwise overlaps nothing. Two launches. rows = 0 is a no-op.
+ * same places) and otherwise overlaps nothing. Two launches, of which the second
+ * reads ids, y and b while the first still runs: they are written by nothing but
+ * what came before the call on its stream (or was waited for there), and by nothing
+ * while the call runs but the call itself. rows = 0 is a no-op.
  */
 int qmm_check_adapter_args(const qmm_adapter_desc* d, const qmm_adapter_args* a);
 int qmm_add_adapters(const qmm_adapter_plan_t* p, const qmm_adapter_args* a, void* stream);
