@@ -169,9 +169,10 @@ __device__ __forceinline__ void split(float v, uint32_t (&term)[TERMS]) {
 
 __device__ __forceinline__ uint4 load16(const uint16_t* p, bool in) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (in) v = __ldg(reinterpret_cast<const uint4*>(p));
+    if (in) v = load_written(p);
     return v;
 }
+__device__ __forceinline__ uint4 load_weights(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
 // Two products of fragments that hold 8 neighbouring elements a lane: rows a0 (gid) and a1 (gid + 8), column gid of b.
 __device__ __forceinline__ void mma_32(float (&d)[4], const uint4& a0, const uint4& a1, const uint4& b) {
@@ -198,6 +199,8 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
     cluster_arrive();   // this CTA has started, and its memory may be written
     griddep_wait();
     griddep_launch_dependents();   // not before: the second kernel reads what came before this one without waiting
+    const uint16_t* const p_a = behind_wait(p.a);
+    const uint16_t* const p_x = behind_wait(p.x);
     find_tiles(p, row0, t);
     float scale = 1.0f;   // (on its way while the products run)
     if (p.scale != nullptr && threadIdx.x < t.tiles && t.tile_id[threadIdx.x] >= 0) scale = __ldg(p.scale + t.tile_id[threadIdx.x]);
@@ -212,14 +215,14 @@ __global__ void __launch_bounds__(kThreads, 2) qmm_adapter_low_kernel(const __gr
         if (id < 0) continue;
         const int first = t.first[tile], size = t.size[tile];
         const bool two = column + 8 < p.rank;
-        const uint16_t* const a = p.a + (static_cast<int64_t>(id) * p.rank + column + gid) * p.K + s0 * kStep + quad * 8;
+        const uint16_t* const a = p_a + (static_cast<int64_t>(id) * p.rank + column + gid) * p.K + s0 * kStep + quad * 8;
         const int64_t a_next = 8 * p.K;
         const uint16_t* x[2];
         bool in[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             in[h] = gid + 8 * h < size;
-            x[h] = p.x + static_cast<int64_t>(row0 + (in[h] ? t.row[first + gid + 8 * h] : 0)) * p.x_stride + s0 * kStep + quad * 8;
+            x[h] = p_x + static_cast<int64_t>(row0 + (in[h] ? t.row[first + gid + 8 * h] : 0)) * p.x_stride + s0 * kStep + quad * 8;
         }
         float acc[2][4] = {};
         for (int k0 = 0; k0 < count; k0 += kAhead) {
@@ -350,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wb[k][j] = __ldg(reinterpret_cast<const uint4*>(from + j * b_next + k * 32));
+                    for (int j = 0; j < 4; ++j) wb[k][j] = load_weights(from + j * b_next + k * 32);
             } else {
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wb[k][j] = load16(from + j * b_next + k * 32, in_rank[k] && own + 2 * j < left);
+                    for (int j = 0; j < 4; ++j) wb[k][j] = in_rank[k] && own + 2 * j < left ? load_weights(from + j * b_next + k * 32) : make_uint4(0u, 0u, 0u, 0u);
             }
         };
         auto columns_of = [&](uint32_t c) { return static_cast<int>(min(p.N - static_cast<int64_t>(c) * 32, static_cast<int64_t>(32))); };
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 1 && !F32 ? 3 : 2) qmm_adap
                     for (int i = 0; i < kTerms; ++i) mma_32(acc[j], lk[i][0], lk[i][1], wb[k][j]);
                 if (roll) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wb[k][j] = __ldg(reinterpret_cast<const uint4*>(b + 16 * b_next + j * b_next + k * 32));
+                    for (int j = 0; j < 4; ++j) wb[k][j] = load_weights(b + 16 * b_next + j * b_next + k * 32);
                 }
             }
             if (kStage && more && !roll) load_b(b + 16 * b_next, left_next);

@@ -87,16 +87,17 @@ __device__ __forceinline__ Pairs pairs_of(const float4& x, const float4& y) {
 template <bool F32, bool NEAR>
 struct Raw {
     uint4 w[F32 ? 2 : 1];
-    // the elements at `first`, and four more at `second` bytes from there
+    // the elements at `first`, and four more at `second` bytes from there (plain loads: the kernel before may still write them when
+    // this one starts, which __ldg does not allow)
     __device__ __forceinline__ void load(const uint8_t* first, int second) {
         if constexpr (F32) {
-            w[0] = __ldg(reinterpret_cast<const uint4*>(first));
-            w[1] = __ldg(reinterpret_cast<const uint4*>(first + second));
+            w[0] = *reinterpret_cast<const uint4*>(first);
+            w[1] = *reinterpret_cast<const uint4*>(first + second);
         } else if constexpr (NEAR) {
-            w[0] = __ldg(reinterpret_cast<const uint4*>(first));
+            w[0] = *reinterpret_cast<const uint4*>(first);
         } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(first));
-            const uint2 y = __ldg(reinterpret_cast<const uint2*>(first + second));
+            const uint2 x = *reinterpret_cast<const uint2*>(first);
+            const uint2 y = *reinterpret_cast<const uint2*>(first + second);
             w[0] = make_uint4(x.x, x.y, y.x, y.y);
         }
     }

@@ -45,6 +45,19 @@ __device__ __forceinline__ unsigned long long global_timer_ns() {
 
 // ---- programmatic dependent launch ----------------------------------------
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A pointer to what earlier kernels wrote, for load_written: behind griddep_wait, so that no load through it is made before.
+template <class T>
+__device__ __forceinline__ const T* behind_wait(const T* p) {
+    asm volatile("" : "+l"(p));
+    return p;
+}
+// 16 bytes that this kernel does not write. A load as any other, and not one of memory that is read-only for the whole life of
+// the kernel (__ldg), which the kernel before may still be writing when this one starts; but it may pass this kernel's stores.
+__device__ __forceinline__ uint4 load_written(const void* p) {
+    uint4 v;
+    asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

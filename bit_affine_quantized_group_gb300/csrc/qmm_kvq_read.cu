@@ -5,8 +5,11 @@
 // instructions are few enough: with indexes and pages looked up for every 16
 // bytes they were 174 for those, 81 % of the issue slots at 4.5 TB/s. A thread
 // has the same 16 bytes of four positions of a page; neighbours write neighbours.
-// 16 sequences of up to 8191 positions of 8 heads of 128, 8 bits to bfloat16: 66.6
-// us, 6.3 TB/s; two of 100 positions: 2.2 us, a launch.
+// 16 sequences of up to 8191 positions of 8 heads of 128, 8 bits to bfloat16: 67.2
+// us, 6.2 TB/s, 4 bits 65.8 (51.5 of bytes); two of 100 positions: 2.2 us, a launch.
+// The loads are plain ones, for the append before may still be writing when this
+// kernel starts; held to the registers of eight CTAs an SM, without which they took
+// 72.4 us. (66.6 with loads of memory that nobody writes, which it is not.)
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -57,7 +60,7 @@ __device__ __forceinline__ uint4 values_of(const Word& word, uint32_t pair) {
 }
 
 template <int D, bool F32, int BITS>
-__global__ void __launch_bounds__(kReadThreads) qmm_kvq_read_kernel(const __grid_constant__ ReadParams p, uint32_t tiles) {
+__global__ void __launch_bounds__(kReadThreads, 8) qmm_kvq_read_kernel(const __grid_constant__ ReadParams p, uint32_t tiles) {
     constexpr int kElems = F32 ? 4 : 8;                // of an output of 16 bytes
     constexpr int kUnits = D / kElems;                 // of a head
     constexpr int kBytes = kElems * BITS / 8;          // of their codes: 2, 4 or 8
@@ -102,8 +105,8 @@ __global__ void __launch_bounds__(kReadThreads) qmm_kvq_read_kernel(const __grid
         uint32_t pair[kReadRows];
 #pragma unroll
         for (int i = 0; i < kReadRows; ++i, src += codes.slot, src_pair += pairs.slot) {
-            word[i] = __ldg(reinterpret_cast<const Word*>(src));
-            pair[i] = __ldg(src_pair);
+            word[i] = *reinterpret_cast<const Word*>(src);
+            pair[i] = *src_pair;
         }
 #pragma unroll
         for (int i = 0; i < kReadRows; ++i, to += row_stride) *reinterpret_cast<uint4*>(to) = values_of<F32, BITS>(word[i], pair[i]);
@@ -117,8 +120,8 @@ __global__ void __launch_bounds__(kReadThreads) qmm_kvq_read_kernel(const __grid
         uint32_t pair = 0;
         if (pg >= 0) {
             const int64_t slot = (at + i) & mask;
-            word = __ldg(reinterpret_cast<const Word*>(from + pg * codes.page + slot * codes.slot));
-            pair = __ldg(from_pairs + pg * pairs.page + slot * pairs.slot);
+            word = *reinterpret_cast<const Word*>(from + pg * codes.page + slot * codes.slot);
+            pair = from_pairs[pg * pairs.page + slot * pairs.slot];
         }
         *reinterpret_cast<uint4*>(to) = values_of<F32, BITS>(word, pair);
     }

@@ -113,7 +113,7 @@ struct Row {
     // chunk c, elements outside the row as -infinity
     __device__ __forceinline__ uint4 load(int c) const {
         const int e = first(c);
-        if (whole(c)) return __ldg(reinterpret_cast<const uint4*>(base + e));
+        if (whole(c)) return *reinterpret_cast<const uint4*>(base + e);
         uint32_t w[4] = {};
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) qmm_logprobs_kernel(c
             for (int i = warp; i < count; i += kWarps) {
                 const int of = static_cast<int>(s.again[i]), seen = all ? -1 : s.at[of];
                 for (int c = w0 + of + lane * kThreads; c < w1; c += 32 * kThreads)
-                    if (c != seen) look(c, __ldg(chunks + c), f);
+                    if (c != seen) look(c, chunks[c], f);
                 if (lane == 0 && of == 0 && c0 < w0 && c0 < c1 && c0 != seen) look(c0, r.load(c0), f);
                 if (lane == 0 && of == 1 && w1 < c1 && w1 >= w0 && w1 != seen) look(w1, r.load(w1), f);
             }

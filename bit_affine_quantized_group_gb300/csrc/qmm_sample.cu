@@ -209,7 +209,7 @@ struct RowSampler {
         return x;
     }
     __device__ __forceinline__ bool inside(int c) const { return c * kVec >= lo && (c + 1) * kVec <= hi; }
-    __device__ __forceinline__ uint4 raw(int c) const { return __ldg(reinterpret_cast<const uint4*>(src + shift + c * kVec)); }
+    __device__ __forceinline__ uint4 raw(int c) const { return *reinterpret_cast<const uint4*>(src + shift + c * kVec); }
     __device__ __forceinline__ static void unpack(const uint4& r, float (&v)[kVec]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
