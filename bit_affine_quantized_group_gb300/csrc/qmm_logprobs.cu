@@ -1,7 +1,11 @@
 // Log probabilities of given tokens, entropy and the largest alternatives, in
 // one pass over the logits:
 //   m' = max(m, l),  d = m - m',  t = (t + s d) e^d + sum e^(l - m') (l - m'),  s = s e^d + sum e^(l - m'),
-//   lse = m + log s,   entropy = log s - t / s   (every term of -t is positive, so that nothing cancels).
+//   lse = m + log s,   entropy = log s - t / s.
+// For m stands a logit of the row that the largest lies less than 6 above, so that m changes seldom. Terms of -t then cancel only
+// where that logit has e^-6 of the probability, and the entropy 0.017, or more; what is lost is 2^-21. (With 16 in its place
+// entropies of 2e-6 were off by a fifth, and those of 512 rows by 3.9e-7 of their norm, 7.7e-8 now; 1 row took 7.3 us, with 4 7.6
+// and 512 rows 25.9.) Where nothing cancels the rounding of s, 2^-24, remains.
 //
 // A thread keeps m, s, t, the chunk of 16 bytes that its largest logit came from
 // and the largest logit of its other chunks. The `top` best (logit, index) of a
@@ -10,10 +14,11 @@
 // them where a second one reaches as far. Each CTA of a row ranks what it finds by
 // counting, the first one of the cluster ranks the CTAs' lists.
 //
-// One row of 151,936 float32 logits with 5 alternatives: 7.3 us, latency of the
+// One row of 151,936 float32 logits with 5 alternatives: 7.5 us, latency of the
 // launch (2.2), of 10 chunks a thread, of bound, list and cluster. 512 rows of
-// 100,277 bfloat16 logits with 20: 25.3 us, 4.1 TB/s, bound by the bytes on their
-// way and by the 4 us of a row's steps behind the pass (21.5 without alternatives).
+// 100,277 bfloat16 logits with 20: 25.4 us, 4.0 TB/s, and 4 of them a row's steps
+// behind the pass (21.6 without alternatives). Rows are whole: some SMs have four
+// of the 512, the mean is 3.4, and four rows' instructions are about 16 us of an SM.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -32,11 +37,11 @@ namespace cg = cooperative_groups;
 constexpr int kTop = QMM_LOGPROBS_MAX_TOP;
 constexpr int kList = 1024;            // candidates that are ranked by counting
 constexpr int kRanks = 8;              // CTAs of a row at most
-// Chunks that a thread has on their way. Of 512 rows at once the pass is bound by how many bytes are: four in registers came to
-// 3.4 TB/s, and more left no room for the CTAs.
+// Chunks that a thread has on their way. (512 rows: four in registers 3.4 TB/s; eight here, with as many CTAs on an SM, 27.1 us, and
+// twelve 32.8.)
 constexpr int kAhead = 5;
 constexpr int kSome = 8;               // threads that may be looked at beyond the needed ones
-constexpr float kRise = 16.0f;         // that logits may lie above a thread's reference before its sums are brought to a new one
+constexpr float kRise = 6.0f;          // that logits may lie above a thread's reference before its sums are brought to a new one
 constexpr float kLeast = -1000.0f;     // differences are brought to it: e^-1000 is 0, and no infinity meets a 0
 constexpr float kLog2E = 1.4426950408889634f;
 
