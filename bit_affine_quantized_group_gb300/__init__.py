@@ -605,10 +605,11 @@ def qk_norm_rope(plan: KVPlan, q, k, v, q_weight, k_weight, rope, lengths, page_
         rope.data_ptr() if plan.rot_dim else 0, rope_len, lengths.data_ptr(),
         0 if positions is None else positions.data_ptr(), page_table.data_ptr(), out.data_ptr(),
         _rows(out, tokens, plan.q_width, _BF16, "out"), seqs, rows, QMM_IN_F32 if dtype is _F32 else QMM_IN_BF16)
-    call = _LIB.qmm_kvq_qk_norm_rope if isinstance(cache, QuantKVCache) else _LIB.qmm_qk_norm_rope
+    coded = isinstance(cache, QuantKVCache)
+    call = _LIB.qmm_kvq_qk_norm_rope if coded else _LIB.qmm_qk_norm_rope
     st = call(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
-        raise QmmError(st, "qmm_qk_norm_rope")
+        raise QmmError(st, "qmm_kvq_qk_norm_rope" if coded else "qmm_qk_norm_rope")
 
 
 def attention(plan: KVPlan, q, cache, page_table, lengths, out, stream=None) -> None:
@@ -620,10 +621,11 @@ def attention(plan: KVPlan, q, cache, page_table, lengths, out, stream=None) -> 
     args = _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(), lengths.data_ptr(), page_table.data_ptr(),
                                 _rows(q, tokens, plan.q_width, _BF16, "q"), _rows(out, tokens, plan.q_width, _BF16, "out"),
                                 seqs, rows)
-    call = _LIB.qmm_kvq_attention if isinstance(cache, QuantKVCache) else _LIB.qmm_attention
+    coded = isinstance(cache, QuantKVCache)
+    call = _LIB.qmm_kvq_attention if coded else _LIB.qmm_attention
     st = call(plan._handle, cache.ref, args, _stream_on(stream, plan._device_index))
     if st != QMM_OK:
-        raise QmmError(st, "qmm_attention")
+        raise QmmError(st, "qmm_kvq_attention" if coded else "qmm_attention")
 
 
 def _dense(t, seqs, plan, dtype, what):
