@@ -29,6 +29,8 @@
 // 48 us, 4.0 TB/s, a quarter of it start and join.
 #include "qmm_attention_tiles.cuh"
 
+#include <atomic>
+
 namespace qmmk {
 
 namespace {
@@ -54,8 +56,17 @@ cudaError_t configure_attention() {
     cudaError_t e = configure_dim<64>();
     if (e == cudaSuccess) e = configure_dim<128>();
     if (e == cudaSuccess) e = configure_dim<256>();
-    if (e == cudaSuccess) e = configure_attention_codes8();
-    if (e == cudaSuccess) e = configure_attention_codes4();
+    return e;
+}
+
+// Once for each device and kind of codes, by the first call: a plan does not know its calls' caches, and what is configured is
+// loaded.
+cudaError_t configure_attention_codes(int bits, int device) {
+    static std::atomic<uint64_t> done[2];   // of 8 and of 4 bits: one bit for each device
+    std::atomic<uint64_t>& of = done[bits == 8 ? 0 : 1];
+    if (device < 64 && of.load(std::memory_order_acquire) >> device & 1) return cudaSuccess;
+    const cudaError_t e = bits == 8 ? configure_attention_codes8() : configure_attention_codes4();
+    if (e == cudaSuccess && device < 64) of.fetch_or(1ull << device, std::memory_order_release);
     return e;
 }
 

@@ -93,7 +93,8 @@ constexpr AttnWorkspace attn_workspace(int head_dim, int rows) {
     return w;
 }
 
-cudaError_t configure_attention();
+cudaError_t configure_attention();   // of bfloat16 caches, for the current device
+cudaError_t configure_attention_codes(int bits, int device);   // which is the current one
 // bits: of a cache of codes; 16 for one of bfloat16
 cudaError_t launch_attention(int head_dim, int bits, const AttnParams& p, int num_sms, cudaStream_t stream);
 cudaError_t configure_attention_codes8();

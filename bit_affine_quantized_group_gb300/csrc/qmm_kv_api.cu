@@ -267,6 +267,7 @@ int attend(const qmm_kv_plan_t* p, const Cache* cache, const qmm_attention_args*
     // a scale of 0 would make masked scores of -infinity NaN; one that moves no score does not
     // (over codes, whose queries come to 2^15, the kernel sees to that)
     ap.scale_log2 = std::fmax(std::fabs(d.scale), bits == 16 ? 1e-30f : 0.0f) * 1.4426950408889634f;
+    if (bits != 16 && configure_attention_codes(bits, p->device) != cudaSuccess) return QMM_ERR_CUDA;
     pthread_mutex_lock(&p->launches);
     const cudaError_t e = launch_attention(d.head_dim, bits, ap, p->num_sms, static_cast<cudaStream_t>(stream));
     pthread_mutex_unlock(&p->launches);
