@@ -21,9 +21,10 @@
 // products sum over, so that loads are whole 16-byte vectors of whole sectors.
 // K 4096, N 6144, a row for each of 16 adapters of rank 16: 7.0 us, of which 4.2
 // are the first kernel and 2.2 a launch. 64 rows of 16 adapters of rank 64, K
-// 5120, N 17408, float32: 18.8 us. 2048 rows, rank 32, K 5120, N 6144: 22.9 us
+// 5120, N 17408, float32: 19.1 us. 2048 rows, rank 32, K 5120, N 6144: 23.2 us
 // (3.2 TB/s), 11.3 of them the first kernel: both wait for loads, of which a
-// lane's registers hold no more. (Tried there: loads of the step five on as soon
+// lane's registers hold no more, and which are more than the operands, for A and
+// B are read again for every tile of 16 rows. (Tried there: loads of the step five on as soon
 // as a step's products run, y through a ring of asynchronous copies, no gain;
 // 32 columns of rank a unit, with two warps on a unit's K: 1 us more, 5 % less
 // for 16,000 rows of rank 64.)

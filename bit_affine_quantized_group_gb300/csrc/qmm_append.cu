@@ -17,9 +17,9 @@
 // which a lane has eight neighbours and eight lanes a group of 64, whose least
 // and largest they find by shuffles:
 //   b = f16(lo),  s = f16((hi - lo) / top),  c = round((x - b) (1 / s)).
-// The same 4 x 2048 tokens: 40 us, bound by instructions (35.0 M of warps, 28.5 M
-// for the bfloat16 cache) with seven CTAs on an SM, as many as their registers
-// leave room for.
+// The same 4 x 2048 tokens: 40 us, bound by instructions (34.2 M of warps, 28.5 M
+// for the bfloat16 cache), of which spills and values' trip through shared memory,
+// as if they were to be rotated, are a part, with seven CTAs on an SM.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) qmm_append_kernel(const __g
     append<D, F32, NEAR, 16>(p, span);
 }
 
-// Registers are held to seven CTAs an SM: 4 x 2048 tokens 40 us, with six 44 and with eight 42.
+// Registers are held to seven CTAs an SM, though all but four kernels spill 24 to 108 bytes then: 4 x 2048 tokens 40 us, with six
+// 44 and with eight 42.
 template <int D, bool F32, bool NEAR, int BITS>
 __global__ void __launch_bounds__(32 * kAppendWarps, 7) qmm_append_codes_kernel(const __grid_constant__ AppendParams p, int span) {
     append<D, F32, NEAR, BITS>(p, span);
