@@ -1,11 +1,13 @@
 // Attention over a paged cache for tiles of 16 query rows: the kernel of bfloat16 caches, and of caches of codes for more
 // than 16 rows, where the team of a step first writes its codes into shared memory as binary16 numbers, for all row tiles
-// read them. (With fewer rows the numbers stay in registers: qmm_attention_codes.cuh.) Beside keys and values of 11 bits weights
-// are one binary16 number: a second term took 38.9 us for the form below and left its error as it was.
+// read them: of keys the codes themselves, whose products each group's scale and bias then turn into scores, of values s c + b.
+// (With fewer rows the numbers stay in registers: qmm_attention_codes.cuh.) Weights are one binary16 number: beside values of 11
+// bits a second term took 3.3 us more for the form below and left its error as it was.
 //
-// Four sequences of up to 16,001 positions with 8 tokens each, 64 rows a cache head: 33.6 us from bfloat16, 35.5 from 8-bit and
-// 34.6 from 4-bit codes, at a half and a quarter of the bytes: no kind is bound by them, but by a step's chain of products,
-// softmax and products (with codes, and of numbers made before).
+// Four sequences of up to 16,001 positions with 8 tokens each, 64 rows a cache head: 33.6 us from bfloat16, 39.1 from 8-bit and
+// 38.4 from 4-bit codes, at a half and a quarter of the bytes: no kind is bound by them, but by a step's chain of products,
+// softmax and products (with codes, and of numbers made before). Keys as binary16 numbers s c + b took 35.7 and 34.7 us, but where
+// they lie 4 of their spreads from zero outputs were off by 0.0047 of their norm, 0.0016 of it their own rounding.
 #pragma once
 
 #include "qmm_attention_shared.cuh"
@@ -55,20 +57,21 @@ struct AttnCfg {
     static constexpr int kTileCount = BITS == 16 ? 0 : D == 256 ? 1 : 2;
     static constexpr int kRoom = D == 256 ? 227 * 1024 : 113 * 1024;   // of a CTA
     static constexpr int kMostSides = 12;
+    static constexpr int kRowFloats = 1 + D / 64;                  // of a query row over codes: its unit, and its groups' sums
     static constexpr int kFixedBytes = kTeams * kTileCount * kTileBytes + kJoinBytes + RW * (kQueryRegs ? 0 : kQueryBytes) +
-                                       (kGroups + 1) * 16 * RW * 8 + 2 * kMostSides * 8 + RW * 64 + 16;
+                                       (kGroups + 1) * 16 * RW * 8 + 2 * kMostSides * 8 + RW * 64 * kRowFloats + 16;
     // A slot of the ring of codes has both sides of a step.
     static constexpr int kSlotBytes = 2 * kSideBytes;
     static constexpr int kFit = (kRoom - kFixedBytes) / (kTeams * kSlotBytes);
     static constexpr int kSlots = kFit < kMostSides / 2 / kTeams ? kFit : kMostSides / 2 / kTeams;
     static constexpr int kSides = BITS == 16 ? (D == 64 ? 12 : 6) / kTeams - (D > 64 && RW == 4 ? 1 : 0) : 2 * kSlots;
     static constexpr int kRingBytes = kSides * kSideBytes;         // of a team
-    // shared memory: rings, tiles, join, queries, their rows' units, maxima and sums, barriers
+    // shared memory: rings, tiles, join, queries, their rows' units and sums, maxima and sums, barriers
     static constexpr int kTilesAt = kTeams * kRingBytes;
     static constexpr int kJoinAt = kTilesAt + kTeams * kTileCount * kTileBytes;
     static constexpr int kQueryAt = kJoinAt + kJoinBytes;
     static constexpr int kUnitAt = kQueryAt + (kQueryRegs ? 0 : RW * kQueryBytes);
-    static constexpr int kMlAt = kUnitAt + (kQueryRegs || BITS == 16 ? 0 : RW * 64);
+    static constexpr int kMlAt = kUnitAt + (kQueryRegs || BITS == 16 ? 0 : RW * 64 * kRowFloats);
     static constexpr int kSumAt = kMlAt + kGroups * 16 * RW * 8;
     static constexpr int kBarsAt = kSumAt + (kScaled ? 16 * RW * 8 : 0);
     static constexpr int kLastAt = kBarsAt + 2 * kTeams * kSides * 8;
@@ -117,9 +120,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     else mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
-// The codes of a side as binary16 numbers s c + b, each rounded once (c is exact), laid out as a side of bfloat16 is. By the 128
-// threads of a team.
-template <class Cfg>
+// The codes of a side as binary16 numbers, laid out as a side of bfloat16 is: keys as c, values as s c + b, each rounded once.
+// By the 128 threads of a team.
+template <class Cfg, bool KEYS>
 __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
     constexpr int kChunks = Cfg::kRowBytes / 16, kElems = 128 / Cfg::kBits;   // of a row; elements of a chunk
     static_assert(Cfg::kTeamWarps == 4, "a thread has every 128th chunk");
@@ -128,7 +131,7 @@ __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
         const int at = c * 128 + tid, row = at / kChunks, chunk = at % kChunks;
         const uint4 v = lds128(side + at * 16);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t pair = lds32(side + kStep * Cfg::kRowBytes + row * Cfg::kPairBytes + chunk * kElems / 64 * 4);
+        const uint32_t pair = KEYS ? 0u : lds32(side + kStep * Cfg::kRowBytes + row * Cfg::kPairBytes + chunk * kElems / 64 * 4);
         const __half2 scale = half2_of(__byte_perm(pair, pair, 0x1010)), bias = half2_of(__byte_perm(pair, pair, 0x3232));
 #pragma unroll
         for (int u = 0; u < kElems / 8; ++u) {   // eight elements each
@@ -149,7 +152,7 @@ __device__ __forceinline__ void widen(uint32_t side, uint32_t tile, int tid) {
             }
             uint32_t r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = bits_of(__hfma2(h[i], scale, bias));
+            for (int i = 0; i < 4; ++i) r[i] = bits_of(KEYS ? h[i] : __hfma2(h[i], scale, bias));
             const int unit = chunk * (kElems / 8) + u;
             sts128(tile + (unit >> 3) * (kStep * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
         }
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
             const uint32_t tile = ring + Cfg::kTilesAt + (team * Cfg::kTileCount + (Cfg::kTileCount == 2 ? which : 0)) * Cfg::kTileBytes;
             // in one tile, the other side has been read; of two, a barrier has passed since this one's was
             if (Cfg::kTileCount == 1) named_barrier(4 + team, 32 * Cfg::kTeamWarps);
-            widen<Cfg>(side, tile, (warp % Cfg::kTeamWarps) * 32 + lane);
+            if (which == 0) widen<Cfg, true>(side, tile, (warp % Cfg::kTeamWarps) * 32 + lane);
+            else widen<Cfg, false>(side, tile, (warp % Cfg::kTeamWarps) * 32 + lane);
             if (which == 1) side_done();
             named_barrier(4 + team, 32 * Cfg::kTeamWarps);
             return tile;
@@ -274,6 +278,7 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
         };
         uint32_t qf[Cfg::kQueryRegs ? D / 16 : 1][4];
         float unit[2] = {p.scale_log2, p.scale_log2};   // what a score of the lane's two rows counts, in powers of two
+        float q_sum[2][D / 64];   // over codes: the sums of their queries, by groups of 64
         int row_pos[2];   // the positions of the lane's two rows; -1 for none
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -300,6 +305,14 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
                         qf[kk][h] = size.f16(qf[kk][h]);
                         qf[kk][h + 2] = size.f16(qf[kk][h + 2]);
                     }
+#pragma unroll
+                    for (int g = 0; g < D / 64; ++g) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int kk = 4 * g; kk < 4 * g + 4; ++kk) sum += sum_f16(qf[kk][h]) + sum_f16(qf[kk][h + 2]);
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                        q_sum[h][g] = sum + __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                    }
                 }
             }
         }
@@ -325,14 +338,24 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
                     for (int o = 1; o < D / 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
                     const QuerySize size(most, p.scale_log2);
                     v[k].x = size.f16(v[k].x), v[k].y = size.f16(v[k].y), v[k].z = size.f16(v[k].z), v[k].w = size.f16(v[k].w);
-                    if (c == 0 && r < 16) reinterpret_cast<float*>(smem + Cfg::kUnitAt)[wr * 16 + r] = size.unit;
+                    float* const of_row = reinterpret_cast<float*>(smem + Cfg::kUnitAt) + (wr * 16 + r) * Cfg::kRowFloats;
+                    if (c == 0 && r < 16) of_row[0] = size.unit;
+                    float sum = (sum_f16(v[k].x) + sum_f16(v[k].y)) + (sum_f16(v[k].z) + sum_f16(v[k].w));
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    if (c % 8 == 0 && r < 16) of_row[1 + c / 8] = sum;
                 }
                 if (r < 16) sts128(q_smem + r * (D * 2) + ((c ^ (r & 7)) << 4), v[k]);
             }
             named_barrier(1, kThreads);
             if constexpr (BITS != 16) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) unit[h] = reinterpret_cast<const float*>(smem + Cfg::kUnitAt)[wr * 16 + h * 8 + gid];
+                for (int h = 0; h < 2; ++h) {
+                    const float* const of_row = reinterpret_cast<const float*>(smem + Cfg::kUnitAt) + (wr * 16 + h * 8 + gid) * Cfg::kRowFloats;
+                    unit[h] = of_row[0];
+#pragma unroll
+                    for (int g = 0; g < D / 64; ++g) q_sum[h][g] = of_row[1 + g];
+                }
             }
         }
 
@@ -373,22 +396,73 @@ __global__ void __launch_bounds__(AttnCfg<D, RW, BITS>::kThreads, AttnCfg<D, RW,
             };
             // the fragments of the next products are read before the present ones
             constexpr int kAhead = Cfg::kAhead ? 1 : 0;
-            uint32_t kb[kAhead + 1][kTiles][4], qa[kAhead + 1][4];
-            if constexpr (kAhead) {
-                load_keys(0, kb[0]);
-                load_query(0, qa[0]);
-            }
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                if (kk + kAhead < D / 16) {
-                    load_keys(kk + kAhead, kb[(kk + 1) & kAhead]);
-                    load_query(kk + kAhead, qa[(kk + 1) & kAhead]);
+            if constexpr (BITS == 16) {
+                uint32_t kb[kAhead + 1][kTiles][4], qa[kAhead + 1][4];
+                if constexpr (kAhead) {
+                    load_keys(0, kb[0]);
+                    load_query(0, qa[0]);
                 }
 #pragma unroll
-                for (int s = 0; s < kTiles; ++s) {
-                    const uint32_t(&b)[4] = kb[kk & kAhead][s];
-                    mma<BITS>(sc[kk % kChains][2 * s], qa[kk & kAhead], b[0], b[1]);
-                    mma<BITS>(sc[kk % kChains][2 * s + 1], qa[kk & kAhead], b[2], b[3]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    if (kk + kAhead < D / 16) {
+                        load_keys(kk + kAhead, kb[(kk + 1) & kAhead]);
+                        load_query(kk + kAhead, qa[(kk + 1) & kAhead]);
+                    }
+#pragma unroll
+                    for (int s = 0; s < kTiles; ++s) {
+                        const uint32_t(&b)[4] = kb[kk & kAhead][s];
+                        mma<BITS>(sc[kk % kChains][2 * s], qa[kk & kAhead], b[0], b[1]);
+                        mma<BITS>(sc[kk % kChains][2 * s + 1], qa[kk & kAhead], b[2], b[3]);
+                    }
+                }
+            } else {
+                // Products of the codes, two tiles at a time; each group of 64 then adds s (sum q f c) + b sum q f in float32, so that
+                // keys are not rounded: those far from zero, of which only differences count, would lose the differences.
+                constexpr int kPair = 2;
+                static_assert(kTiles % kPair == 0 && kChains == 1, "tiles by twos");
+                const uint32_t pairs = ring + (team * kPlaces + slot) * kPlaceBytes + kStep * Cfg::kRowBytes +
+                                       (part * kPartRows + quad * 2) * Cfg::kPairBytes;
+#pragma unroll
+                for (int s0 = 0; s0 < kTiles; s0 += kPair) {
+                    uint32_t kb[kAhead + 1][kPair][4], qa[kAhead + 1][4];
+                    auto load_pair = [&](int kk, uint32_t(&b)[kPair][4]) {
+#pragma unroll
+                        for (int s = 0; s < kPair; ++s)
+                            ldmatrix_x4(kst + k_at[kk & 3] + (kk >> 2) * (kStep * 128) + (s0 + s) * (16 * 128), b[s][0], b[s][1], b[s][2],
+                                        b[s][3]);
+                    };
+                    if constexpr (kAhead) {
+                        load_pair(0, kb[0]);
+                        load_query(0, qa[0]);
+                    }
+                    float sum[2 * kPair][4];   // of a group
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        if (kk + kAhead < D / 16) {
+                            load_pair(kk + kAhead, kb[(kk + 1) & kAhead]);
+                            load_query(kk + kAhead, qa[(kk + 1) & kAhead]);
+                        }
+                        const uint32_t(&q)[4] = qa[kk & kAhead];
+#pragma unroll
+                        for (int n = 0; n < 2 * kPair; ++n) {
+                            const uint32_t(&b)[4] = kb[kk & kAhead][n >> 1];
+                            if (kk % 4 == 0) mma_f16_zc(sum[n], q[0], q[1], q[2], q[3], b[2 * (n & 1)], b[2 * (n & 1) + 1]);
+                            else mma_f16(sum[n], q[0], q[1], q[2], q[3], b[2 * (n & 1)], b[2 * (n & 1) + 1]);
+                        }
+                        if (kk % 4 != 3) continue;
+#pragma unroll
+                        for (int n = 0; n < 2 * kPair; ++n) {   // positions 2 quad and 2 quad + 1 of eight
+                            const uint32_t at = pairs + (s0 * 16 + n * 8) * Cfg::kPairBytes + kk / 4 * 4;
+                            const float2 first = __half22float2(half2_of(lds32(at))), second = __half22float2(half2_of(lds32(at + Cfg::kPairBytes)));
+                            float(&x)[4] = sc[0][2 * s0 + n];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float of_row = q_sum[h][kk / 4];
+                                fma_x2(x[2 * h], x[2 * h + 1], first.y, second.y, of_row, of_row, x[2 * h], x[2 * h + 1]);
+                                fma_x2(x[2 * h], x[2 * h + 1], sum[n][2 * h], sum[n][2 * h + 1], first.x, second.x, x[2 * h], x[2 * h + 1]);
+                            }
+                        }
+                    }
                 }
             }
             side_end();

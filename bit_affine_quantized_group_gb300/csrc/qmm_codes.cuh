@@ -15,6 +15,11 @@ __device__ __forceinline__ uint32_t bits_of(__half2 v) { return *reinterpret_cas
 __device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return bits_of(__floats2half2_rn(a, b)); }
 
+__device__ __forceinline__ float sum_f16(uint32_t pair) {
+    const float2 v = __half22float2(half2_of(pair));
+    return v.x + v.y;
+}
+
 // Weights a and b, at least 0, as pairs of binary16 numbers: their upper 11 bits, and the rounded remainders. hi + lo is within
 // 2^-21 of a weight, or within 2^-24 where that is more.
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {

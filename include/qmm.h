@@ -462,16 +462,15 @@ int qmm_kvq_qk_norm_rope(const qmm_kv_plan_t* p, const qmm_kvq_cache* cache, con
 /*
  * qmm_attention over a cache of codes. The same plan, arguments and checks. Each
  * query row enters as binary16 numbers of a power of two that brings its largest
- * element to 2^14..2^15 (elements down to 2^-28 of that keep all bits). Where rows *
- * q_heads / kv_heads is up to 16, scores are products with the codes themselves,
- * scaled in float32, and the values' scales enter with the softmax's weights, which
+ * element to 2^14..2^15 (elements down to 2^-28 of that keep all bits). Scores are
+ * products with the codes themselves, scaled in float32. Where rows * q_heads /
+ * kv_heads is up to 16, the values' scales enter with the softmax's weights, which
  * are two binary16 terms. With P a position's weight relative to the row's largest (or
  * the largest among 32 neighbours, where that is more) and top 255 or 15, its share of
  * an output is off by up to (2^-19 P + 2^-37) (|s| top + |b|) + 2^-30.
- * Of more, keys and values enter as binary16, s c + b rounded once (within 2^-11 of it
- * or 2^-25), and weights within 2^-11 or, of the largest, 2^-40; so do values of 32
- * neighbouring positions where an |s| is 2 or more (8 for 4 bits). Sums and maxima
- * are float32.
+ * Of more, values enter as binary16, s c + b rounded once (within 2^-11 of it or 2^-25),
+ * and weights within 2^-11 or, of the largest, 2^-40; so do values of 32 neighbouring
+ * positions where an |s| is 2 or more (8 for 4 bits). Sums and maxima are float32.
  * s c + b beyond binary16 may be infinite.
  */
 int qmm_check_kvq_attention_args(const qmm_kv_desc* d, const qmm_kvq_cache* cache, const qmm_attention_args* a);

@@ -131,3 +131,37 @@ def test_more_rows_round_keys_and_values_once(q, bits, d, group):
     bias = 2.0 ** -7 * (0.1 + rng.random((S, n, H, G)))
     got, want, _ = _run(q, bits, d, group, np.zeros((S, n, H)), code, scale, bias)
     assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -19) * np.abs(want)).all(), np.max(np.abs(got - want) / np.abs(want))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d,group,rows", [(64, 5, 1), (128, 4, 4), (128, 10, 2), (128, 8, 8), (64, 16, 4), (256, 6, 4), (256, 8, 8)])
+@pytest.mark.parametrize("q_shift,k_shift", [(0.0, 0.0), (2.0, 4.0), (0.0, 8.0)])
+def test_keys_far_from_zero(q, bits, d, group, rows, q_shift, k_shift):
+    """Keys whose groups lie far from zero, of which scores have only the differences. Over all outputs roundings to bfloat16 come to
+    2^-7 / sqrt(12) of the numbers' powers of two, 0.0017 of the norm; of more than 16 rows weights and values are binary16
+    numbers besides (2^-11 / sqrt(3) each): 2^-9 in all, and no more where keys are shifted, for they are not rounded."""
+    import torch
+    from tests._codes import quantise, pack, values
+    gen = torch.Generator().manual_seed(bits + d + group)
+    S, H, page, n = 2, 2, 64, 700
+    pages = -(-n // page)
+    shift = k_shift * torch.sign(torch.randn(d, generator=gen))
+    parts = []
+    for off in (shift, torch.zeros(d)):
+        parts.append(quantise(torch.randn((S * pages, H, page, d), generator=gen) + off, bits))
+    (kc, ka), (vc, va) = parts
+    cache = q.QuantKVCache(*(t.to(DEV) for t in (pack(kc, bits), pack(vc, bits), ka, va)), bits)
+    plan = q.KVPlan(H * group, H, d, page, max_seqs=S, max_rows=rows, max_pages=pages, rot_dim=0)
+    x = (1.5 * torch.randn((S * rows, H * group, d), generator=gen) + q_shift * torch.sign(shift + 0.5)).to(torch.bfloat16)
+    out = torch.empty_like(x, device=DEV)
+    table = torch.arange(S * pages, dtype=torch.int32, device=DEV).view(S, pages)
+    q.attention(plan, x.to(DEV), cache, table, torch.full((S,), n, dtype=torch.int32, device=DEV), out)
+    k, v = (values(c, a).view(S, pages, H, page, d).transpose(2, 3).reshape(S, pages * page, H, d)[:, :n] for c, a in parts)
+    xx = x.double().view(S, rows, H, group, d)
+    a = torch.einsum("srhgd,sjhd->srhgj", xx, k) * d ** -0.5
+    seen = torch.arange(n)[None] <= (n - rows + torch.arange(rows))[:, None]
+    a = a.masked_fill(~seen[None, :, None, None], float("-inf"))
+    want = torch.einsum("srhgj,sjhd->srhgd", torch.softmax(a, 4), v).reshape(S * rows, H * group, d)
+    error = float((out.double().cpu() - want).norm() / want.norm())
+    assert plan.error_flags() == 0
+    assert error <= 2.0 ** -9, error
